@@ -81,6 +81,27 @@ typedef struct {
 } pa_pool;
 
 /*
+ * An 8-bit pool: the same block-paged K and V as e4m3 codes, one byte each, and one power-of-two
+ * scale for every (block, kv head) of K and of V:
+ *   K[block, h, t, d] = e4m3(k_cache[block, h, t, d]) * 2^(exps[block, h, 0] - 127)
+ *   V likewise with exps[block, h, 1].
+ * exps holds values 27 .. 246 (2^-100 .. 2^119), in which every product is a normal bf16 number,
+ * so reading the pool rounds nothing.  Half the bytes of a bf16 pool (and 2 per block and kv
+ * head): half the time of a decode, and twice the blocks of a memory budget
+ * (pa_kv_block_bytes with dtype_bytes = 1).  The caller owns the three tensors and zeroes
+ * them, or at least writes a block's offset 0 before its other rows.
+ */
+typedef struct {
+    void *k_cache;        /* [num_blocks, num_kv_heads, 16, head_dim] e4m3, 16-byte aligned */
+    void *v_cache;
+    void *exps;           /* [num_blocks, num_kv_heads, 2] uint8, 2-byte aligned */
+    int32_t num_blocks;
+    int32_t block_size;   /* must be 16 */
+    int32_t num_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+} pa_pool8;
+
+/*
  * pa_kv_append -- write new K/V rows into their pool slots.
  * Defines: for t in [0, num_tokens) with slot_mapping[t] >= 0,
  *   k_cache[slot / 16, h, slot % 16, :] = k_new[t, h, :]  (and v likewise), every kv head h.
@@ -114,6 +135,24 @@ int pa_kv_copy(const pa_pool *pool, const int64_t *src_slots, const int64_t *dst
                pa_stream_t stream);
 
 /*
+ * pa_kv_append8 -- pa_kv_append into an 8-bit pool: rows are rounded to e4m3 (to nearest even)
+ * under their block's scale.  Per (block, kv head, K or V), with k(a) the smallest exponent
+ * in [-100, 119] for which a <= 448 * 2^k(a), and a the new rows' largest finite magnitude:
+ *   * when the call writes offset 0 of the block, the block begins anew: k = k(a), and the bytes
+ *     of the rows it does not write stay as they are;
+ *   * otherwise k = max(k_old, k(a)); if that is larger than k_old, the codes of the rows it does
+ *     not write are multiplied by 2^(k_old - k) and rounded again, which loses bits only
+ *     below 2^-6 * 2^k.
+ * Infinities and values past 448 * 2^k saturate, a NaN stays one.  The rows a block receives
+ * must be consecutive entries of slot_mapping (negative entries between them do not count), as
+ * the tokens of a sequence are; a block that comes up again later in the same call is a caller
+ * error, and so are calls that write the same block at the same time.  Of entries with the same
+ * slot the last counts.  Arguments and errors otherwise as pa_kv_append.
+ */
+int pa_kv_append8(const pa_pool8 *pool, const void *k_new, const void *v_new, const int64_t *slot_mapping,
+                  int32_t num_tokens, pa_stream_t stream);
+
+/*
  * pa_decode -- one query token per sequence attends to keys [0, seq_lens[b]).
  * ("Qwen3-4B / 8B / 32B", "Architecture Notes": GQA over a paged KV cache; the query is
  * the newest token, already appended.)
@@ -126,6 +165,65 @@ int pa_kv_copy(const pa_pool *pool, const int64_t *src_slots, const int64_t *dst
 int pa_decode(const pa_pool *pool, const void *q, const int32_t *block_tables, int32_t max_blocks,
               const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale, void *out,
               pa_stream_t stream);
+
+/*
+ * pa_decode8 -- pa_decode over an 8-bit pool (same arguments, errors and splitting).  K and V are
+ * taken exactly as stored; q enters the tensor core as f16 after each row is brought to a
+ * maximum in [2^14, 2^15) by a power of two (exact for elements above 2^-29 of the row's
+ * maximum), the softmax weights as f16, each with its block's V scale, under a running
+ * maximum of their products; sums are fp32.
+ */
+int pa_decode8(const pa_pool8 *pool, const void *q, const int32_t *block_tables, int32_t max_blocks,
+               const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale, void *out,
+               pa_stream_t stream);
+
+/* Workspace of pa_decode_weights and pa_decode8_weights, in bytes (a float per block and query
+ * head of a group, the group rounded up to 8 or 16).  Host-only, no CUDA call. */
+size_t pa_weights_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t max_blocks);
+
+/*
+ * pa_decode_weights, pa_decode8_weights -- pa_decode / pa_decode8 that also add up the attention
+ * weight every block got, for pa_kv_evict.  With p the softmax weights of the call,
+ *   weights[b, h, j] = decay * weights[b, h, j] + sum of p over the query heads of kv head h and
+ *                      the keys of logical block j          for j < ceil(seq_lens[b] / 16);
+ * other entries stay as they are.  A sequence's row starts at zero.  Each entry is added up by
+ * one thread in a fixed order, so a repeated call gives the same bits.  A query head whose
+ * scores hold a NaN adds nothing.
+ *   weights    [batch, num_kv_heads, max_blocks] fp32, updated in place
+ *   decay      finite; 1 keeps the plain sum
+ *   workspace  pa_weights_workspace_bytes(...) bytes, 4-byte aligned, not shared by calls that
+ *              may run at the same time; nothing in it outlives the call
+ */
+int pa_decode_weights(const pa_pool *pool, const void *q, const int32_t *block_tables, int32_t max_blocks,
+                      const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale, float decay,
+                      float *weights, float *workspace, void *out, pa_stream_t stream);
+int pa_decode8_weights(const pa_pool8 *pool, const void *q, const int32_t *block_tables, int32_t max_blocks,
+                       const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale, float decay,
+                       float *weights, float *workspace, void *out, pa_stream_t stream);
+
+/*
+ * pa_kv_evict -- evict the blocks with the lowest accumulated weight, so that no sequence keeps
+ * more than keep_blocks.  Per sequence, nb = ceil(seq_len / 16) and e = max(0, nb - keep_blocks):
+ * of the logical blocks [sink_blocks, nb - recent_blocks) the e with the lowest
+ * W_j = sum_h weights[b, h, j] (fp64, rounded to fp32) leave, of equal ones the lower index first,
+ * a NaN before all.  Then
+ *   block_tables_out  the row without the e entries, in order, reserved entries past nb included;
+ *                     the last e entries are -1
+ *   weights_out       the rows likewise; the last e entries are 0
+ *   seq_lens_out      seq_len - 16 e: later tokens are appended at the shortened positions (their
+ *                     rotary positions, which K already carries, are the caller's)
+ *   evicted           [batch, max_blocks] the ids that left, in order of their position, -1 behind
+ *                     them (for pa_bm_evict); num_evicted [batch] = e
+ * K and V do not move and no block is written, so blocks shared with other sequences are safe.
+ * Any of the three outputs may be its input; otherwise the arrays must not overlap.  A seq_len
+ * outside [0, max_blocks * 16] is clamped and sets PA_DEV_OUT_OF_RANGE.
+ * sink_blocks >= 0, recent_blocks >= 1 (the block being filled stays), their sum at most
+ * keep_blocks; max_blocks at most 49152, else PA_ERR_UNSUPPORTED.
+ */
+int pa_kv_evict(const int32_t *block_tables, const int32_t *seq_lens, const float *weights, int32_t batch,
+                int32_t max_blocks, int32_t num_kv_heads, int32_t keep_blocks, int32_t sink_blocks,
+                int32_t recent_blocks, int32_t *block_tables_out, int32_t *seq_lens_out, float *weights_out,
+                int32_t *evicted, int32_t *num_evicted, pa_stream_t stream);
 
 /*
  * pa_append_decode -- pa_kv_append of one new row per sequence followed by pa_decode, in
@@ -195,6 +293,15 @@ int pa_combine(const float *ws_o, const float *ws_lse, int32_t batch, int32_t nu
 int pa_prefill_chunked(const pa_pool *pool, const void *q, const int32_t *cu_q_lens, const int32_t *block_tables,
                        int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads,
                        int32_t max_chunk, float scale, void *out, pa_stream_t stream);
+
+/*
+ * pa_prefill_chunked8 -- pa_prefill_chunked over an 8-bit pool: same arguments, errors, kernels by
+ * shape and arithmetic, on the pool's exact bf16 values (chunks of at most 16 / group queries
+ * as pa_decode8).
+ */
+int pa_prefill_chunked8(const pa_pool8 *pool, const void *q, const int32_t *cu_q_lens, const int32_t *block_tables,
+                        int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads,
+                        int32_t max_chunk, float scale, void *out, pa_stream_t stream);
 
 /*
  * pa_device_status -- synchronise `stream`, then read the device status word of the
@@ -317,6 +424,16 @@ int pa_bm_admit_cow(pa_blockmgr *bm, int64_t request_id, const int32_t *tokens, 
  * are full within those tokens enter the prefix cache (one entry per distinct content).
  */
 int pa_bm_commit(pa_blockmgr *bm, int64_t request_id, const int32_t *new_tokens, int32_t n_new, int32_t computed);
+
+/*
+ * pa_bm_evict -- blocks block_ids[0, n) leave the request (one row of pa_kv_evict's `evicted`): its
+ * table closes up as the device's does, they lose a user, and the request's tokens, positions
+ * and reserved lifetime shrink by n blocks.  Nothing the request computes afterwards enters the
+ * prefix cache (its K/V saw only part of the prompt); blocks that are cached already stay.
+ * The ids must be full blocks of the request in the order of its table, else PA_ERR_INVALID_ARG
+ * and nothing changes.
+ */
+int pa_bm_evict(pa_blockmgr *bm, int64_t request_id, const int32_t *block_ids, int32_t n);
 
 /* Release the request: its blocks lose a user; cached ones stay reusable until the allocator
  * needs them (the one released longest ago first), the rest are free at once. */

@@ -6,7 +6,9 @@ kernels of libpagedattn.so.  There is no CPU or PyTorch fallback -- if the
 library is not built, loading it raises.
 
 Names follow the C ABI: pa_kv_append, pa_decode, pa_decode_splitkv,
-pa_combine, pa_prefill_chunked, pa_device_status.  Tensors must be CUDA,
+pa_combine, pa_prefill_chunked, pa_device_status; on an 8-bit pool (PaPool8) pa_kv_append8,
+pa_decode8, pa_prefill_chunked8; pa_decode_weights / pa_decode8_weights and pa_kv_evict for
+eviction by accumulated attention weight.  Tensors must be CUDA,
 contiguous, and of the dtypes the header states (bf16 data, int32 tables,
 int64 slot mapping, fp32 split-KV workspace).  Calls are asynchronous on the
 given stream (default: torch's current stream).
@@ -20,7 +22,8 @@ from typing import Optional, Tuple
 
 import torch
 
-__all__ = ["PaPool", "pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decode", "pa_decode_splitkv",
+__all__ = ["PaPool", "PaPool8", "pa_kv_append8", "pa_decode8", "pa_prefill_chunked8", "pa_decode_weights",
+           "pa_decode8_weights", "pa_weights_workspace_bytes", "pa_kv_evict", "pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decode", "pa_decode_splitkv",
            "pa_combine", "pa_prefill_chunked",
            "pa_device_status", "pa_selftest_wait_timeout", "pa_splitkv_workspace_bytes", "pa_decode_num_splits", "pa_splitkv_num_partitions",
            "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes", "PagedAttnError",
@@ -30,7 +33,8 @@ __all__ = ["PaPool", "pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decod
 BLOCK_SIZE = 16
 PKG = Path(__file__).resolve().parent
 _LIB_PATH = PKG / "libpagedattn.so"
-EXPORTED_SYMBOLS = ("pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decode", "pa_splitkv_workspace_bytes",
+EXPORTED_SYMBOLS = ("pa_kv_append8", "pa_decode8", "pa_prefill_chunked8", "pa_decode_weights", "pa_decode8_weights",
+                    "pa_weights_workspace_bytes", "pa_kv_evict", "pa_bm_evict", "pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decode", "pa_splitkv_workspace_bytes",
                     "pa_decode_splitkv", "pa_combine",
                     "pa_prefill_chunked", "pa_device_status", "pa_decode_num_splits", "pa_splitkv_num_partitions",
                     "pa_status_str", "pa_version", "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes",
@@ -61,6 +65,12 @@ class _PaPoolC(ctypes.Structure):
                 ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class _PaPool8C(ctypes.Structure):
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("exps", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -79,7 +89,17 @@ def library() -> ctypes.CDLL:
     lib = ctypes.CDLL(str(_LIB_PATH))
     P, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     pool = ctypes.POINTER(_PaPoolC)
+    pool8 = ctypes.POINTER(_PaPool8C)
+    weights_args = [P, P, I32, P, I32, I32, F32, F32, P, P, P, P]
     sig = {
+        "pa_kv_append8": (ctypes.c_int, [pool8, P, P, P, I32, P]),
+        "pa_decode8": (ctypes.c_int, [pool8, P, P, I32, P, I32, I32, F32, P, P]),
+        "pa_prefill_chunked8": (ctypes.c_int, [pool8, P, P, P, I32, P, I32, I32, I32, F32, P, P]),
+        "pa_decode_weights": (ctypes.c_int, [pool, *weights_args]),
+        "pa_decode8_weights": (ctypes.c_int, [pool8, *weights_args]),
+        "pa_weights_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "pa_kv_evict": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
+        "pa_bm_evict": (ctypes.c_int, [P, ctypes.c_int64, P, I32]),
         "pa_kv_append": (ctypes.c_int, [pool, P, P, P, I32, P]),
         "pa_kv_copy": (ctypes.c_int, [pool, P, P, I32, P]),
         "pa_decode": (ctypes.c_int, [pool, P, P, I32, P, I32, I32, F32, P, P]),
@@ -313,6 +333,196 @@ def pa_prefill_chunked(pool: PaPool, q: torch.Tensor, cu_q_lens: torch.Tensor, b
     return out
 
 
+# ----------------------------------------------------------------------------- 8-bit pool, weights, eviction
+def _arg(t: torch.Tensor, dtype, name: str, device: int) -> int:
+    """Address of a contiguous CUDA tensor of `dtype` on the call's device."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors are on cuda:{device}")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, device: int, stream) -> torch.Tensor:
+    """A result tensor, allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+
+
+def _call(what: str, device: int, stream, *args) -> None:
+    """The library's call on `device` (its current stream unless one is given)."""
+    fn = getattr(library(), what)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != PA_OK:
+        raise PagedAttnError(what, rc)
+
+
+class PaPool8:
+    """The 8-bit paged KV pool: k_cache, v_cache = [num_blocks, num_kv_heads, 16, head_dim] e4m3 codes
+    (torch.uint8 or torch.float8_e4m3fn), exps = [num_blocks, num_kv_heads, 2] uint8, all on one GPU:
+    K = code * 2^(exps[..., 0] - 127), V = code * 2^(exps[..., 1] - 127)."""
+
+    def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor, exps: torch.Tensor):
+        if k_cache.shape != v_cache.shape or k_cache.dim() != 4 or k_cache.dtype != v_cache.dtype:
+            raise ValueError("k_cache and v_cache must both be [num_blocks, num_kv_heads, block_size, head_dim]")
+        if k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise ValueError(f"k_cache and v_cache: need uint8 or float8_e4m3fn codes, got {k_cache.dtype}")
+        nb, hkv, bs, d = k_cache.shape
+        if tuple(exps.shape) != (nb, hkv, 2):
+            raise ValueError(f"exps: need shape {(nb, hkv, 2)}, got {tuple(exps.shape)}")
+        self.k_cache, self.v_cache, self.exps = k_cache, v_cache, exps
+        self.device = k_cache.get_device()
+        self.c = _PaPool8C(_arg(k_cache, k_cache.dtype, "k_cache", self.device),
+                           _arg(v_cache, k_cache.dtype, "v_cache", self.device),
+                           _arg(exps, torch.uint8, "exps", self.device), nb, bs, hkv, d)
+        self.ref = ctypes.byref(self.c)
+        self.num_kv_heads, self.head_dim = hkv, d
+
+    @classmethod
+    def zeros(cls, num_blocks: int, num_kv_heads: int, head_dim: int, device="cuda") -> "PaPool8":
+        shape = (num_blocks, num_kv_heads, BLOCK_SIZE, head_dim)
+        return cls(torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros((num_blocks, num_kv_heads, 2), dtype=torch.uint8, device=device))
+
+
+def pa_kv_append8(pool: PaPool8, k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                  stream=None) -> None:
+    """Quantise new bf16 rows into the pool; the rows of one block are consecutive entries."""
+    T = slot_mapping.numel()
+    _rows(k_new, v_new, pool, T)
+    if T == 0:
+        return
+    d = pool.device
+    _call("pa_kv_append8", d, stream, pool.ref, _arg(k_new, torch.bfloat16, "k_new", d),
+          _arg(v_new, torch.bfloat16, "v_new", d), _arg(slot_mapping, torch.int64, "slot_mapping", d), T)
+
+
+def _query(pool, q: torch.Tensor, out: Optional[torch.Tensor], device: int, stream) -> torch.Tensor:
+    """Check q against the pool; the output tensor (the caller's, checked, or a new one)."""
+    if q.dim() != 3 or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q: need [rows, num_heads, {pool.head_dim}], got {tuple(q.shape)}")
+    if out is None:
+        return _new(q.shape, torch.bfloat16, device, stream)
+    if out.shape != q.shape:
+        raise ValueError(f"out: need shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def pa_decode8(pool: PaPool8, q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    d = pool.device
+    out = _query(pool, q, out, d, stream)
+    B = q.shape[0]
+    _tables(block_tables, seq_lens, B)
+    _call("pa_decode8", d, stream, pool.ref, _arg(q, torch.bfloat16, "q", d),
+          _arg(block_tables, torch.int32, "block_tables", d), block_tables.shape[1],
+          _arg(seq_lens, torch.int32, "seq_lens", d), B, q.shape[1], float(scale),
+          _arg(out, torch.bfloat16, "out", d))
+    return out
+
+
+def pa_prefill_chunked8(pool: PaPool8, q: torch.Tensor, cu_q_lens: torch.Tensor, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, scale: float, max_chunk: int, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    d = pool.device
+    out = _query(pool, q, out, d, stream)
+    B = seq_lens.numel()
+    _tables(block_tables, seq_lens, B)
+    if cu_q_lens.numel() != B + 1:
+        raise ValueError(f"cu_q_lens: need {B + 1} entries, got {cu_q_lens.numel()}")
+    _call("pa_prefill_chunked8", d, stream, pool.ref, _arg(q, torch.bfloat16, "q", d),
+          _arg(cu_q_lens, torch.int32, "cu_q_lens", d), _arg(block_tables, torch.int32, "block_tables", d),
+          block_tables.shape[1], _arg(seq_lens, torch.int32, "seq_lens", d), B, q.shape[1], int(max_chunk),
+          float(scale), _arg(out, torch.bfloat16, "out", d))
+    return out
+
+
+def pa_weights_workspace_bytes(batch: int, num_heads: int, num_kv_heads: int, max_blocks: int) -> int:
+    return int(library().pa_weights_workspace_bytes(batch, num_heads, num_kv_heads, max_blocks))
+
+
+def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weights, decay, workspace, out, stream):
+    out = _query(pool, q, out, device, stream)
+    B, Hq, _ = q.shape
+    _tables(block_tables, seq_lens, B)
+    width = block_tables.shape[1]
+    if weights.shape != (B, pool.num_kv_heads, width):
+        raise ValueError(f"weights: need shape {(B, pool.num_kv_heads, width)}, got {tuple(weights.shape)}")
+    if B == 0:
+        return out
+    need = B * pool.num_kv_heads * width * (16 if Hq // pool.num_kv_heads > 8 else 8)
+    if workspace is None:
+        workspace = _new((need,), torch.float32, device, stream)
+    elif workspace.numel() < need:
+        raise ValueError(f"workspace: need {need} floats, got {workspace.numel()}")
+    _call(what, device, stream, pool.ref, _arg(q, torch.bfloat16, "q", device),
+          _arg(block_tables, torch.int32, "block_tables", device), width,
+          _arg(seq_lens, torch.int32, "seq_lens", device), B, Hq, float(scale), float(decay),
+          _arg(weights, torch.float32, "weights", device), _arg(workspace, torch.float32, "workspace", device),
+          _arg(out, torch.bfloat16, "out", device))
+    return out
+
+
+def pa_decode_weights(pool: PaPool, q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                      scale: float, weights: torch.Tensor, decay: float = 1.0,
+                      workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """pa_decode that also does weights[b, kvh, j] = decay * weights[b, kvh, j] + the attention weight
+    that logical block j got from the query heads of kv head kvh (fp32, in place)."""
+    return _decode_weights("pa_decode_weights", pool, pool.k_cache.get_device(), q, block_tables, seq_lens, scale,
+                           weights, decay, workspace, out, stream)
+
+
+def pa_decode8_weights(pool: PaPool8, q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                       scale: float, weights: torch.Tensor, decay: float = 1.0,
+                       workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """pa_decode8 with the accumulated block weights of pa_decode_weights."""
+    return _decode_weights("pa_decode8_weights", pool, pool.device, q, block_tables, seq_lens, scale, weights, decay,
+                           workspace, out, stream)
+
+
+def pa_kv_evict(block_tables: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor, keep_blocks: int,
+                sink_blocks: int = 1, recent_blocks: int = 1, in_place: bool = False, stream=None):
+    """Evict each sequence's blocks past `keep_blocks` with the lowest accumulated weight, but none of
+    the first sink_blocks and last recent_blocks.  Returns (block_tables, seq_lens, weights, evicted,
+    num_evicted): new tensors, or with in_place the given ones updated; evicted [batch, max_blocks]
+    lists the ids that left (-1 behind them) for BlockManager.evict."""
+    if weights.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("need block_tables [batch, max_blocks] and weights [batch, num_kv_heads, max_blocks]")
+    B, hkv, width = weights.shape
+    if block_tables.shape != (B, width) or seq_lens.shape != (B,):
+        raise ValueError(f"block_tables / seq_lens: need shapes {(B, width)} / {(B,)}, got "
+                         f"{tuple(block_tables.shape)} / {tuple(seq_lens.shape)}")
+    d = weights.get_device()
+    if in_place:
+        new_tables, new_lens, new_weights = block_tables, seq_lens, weights
+    else:
+        new_tables = _new((B, width), torch.int32, d, stream)
+        new_lens = _new((B,), torch.int32, d, stream)
+        new_weights = _new((B, hkv, width), torch.float32, d, stream)
+    evicted = _new((B, width), torch.int32, d, stream)
+    num = _new((B,), torch.int32, d, stream)
+    _call("pa_kv_evict", d, stream, _arg(block_tables, torch.int32, "block_tables", d),
+          _arg(seq_lens, torch.int32, "seq_lens", d), _arg(weights, torch.float32, "weights", d), B, width, hkv,
+          int(keep_blocks), int(sink_blocks), int(recent_blocks), new_tables.data_ptr(), new_lens.data_ptr(),
+          new_weights.data_ptr(), evicted.data_ptr(), num.data_ptr())
+    return new_tables, new_lens, new_weights, evicted, num
+
+
 def pa_device_status(clear: bool = True, stream=None) -> int:
     """Synchronise the stream and return the device status bits (0 = clean)."""
     flags = ctypes.c_uint32(0)
@@ -417,6 +627,15 @@ class BlockManager:
 
     def release(self, request_id: int):
         _check(library().pa_bm_release(self._h, request_id), "pa_bm_release")
+
+    def evict(self, request_id: int, block_ids):
+        """The given blocks (one row of pa_kv_evict's `evicted`; negative entries do not count) leave the
+        request; its table, positions and reserved lifetime shrink by them."""
+        np = self._np
+        ids = np.ascontiguousarray(block_ids, dtype=np.int32)
+        ids = np.ascontiguousarray(ids[ids >= 0])
+        _check(library().pa_bm_evict(self._h, request_id, ids.ctypes.data if len(ids) else None, len(ids)),
+               "pa_bm_evict")
 
     def slots(self, request_id: int, start: int, n: int):
         np = self._np

@@ -60,6 +60,7 @@ struct Request {
     std::vector<int32_t> blocks;         // block table: the whole lifetime, reserved at admission
     int32_t registered = 0;              // leading blocks already in the prefix cache (or matched)
     int32_t capacity = 0;                // tokens the reservation covers
+    bool evicted = false;                // blocks have left: what follows is not a cacheable prefix
     int32_t pinned = -1;                 // copy-on-write source block held for the request, or -1
 };
 
@@ -147,7 +148,8 @@ struct pa_blockmgr {
     }
 
     void register_full_blocks(Request& r, int32_t computed) {
-        if (!prefix_cache) return;
+        // K/V computed after an eviction saw only part of the tokens before it
+        if (!prefix_cache || r.evicted) return;
         const int32_t full = std::min<int32_t>(computed, (int32_t)r.tokens.size()) / block_size;
         for (int32_t i = r.registered; i < full; ++i) {
             const int32_t id = r.blocks[i];
@@ -316,6 +318,42 @@ int pa_bm_commit(pa_blockmgr* m, int64_t request_id, const int32_t* new_tokens, 
     if (len > r.capacity || computed < 0 || computed > len) return PA_ERR_INVALID_ARG;
     r.tokens.insert(r.tokens.end(), new_tokens, new_tokens + n_new);
     m->register_full_blocks(r, computed);
+    return PA_OK;
+}
+
+int pa_bm_evict(pa_blockmgr* m, int64_t request_id, const int32_t* block_ids, int32_t n) {
+    if (!m || n < 0 || (n > 0 && !block_ids)) return PA_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(m->mu);
+    auto it = m->requests.find(request_id);
+    if (it == m->requests.end()) return PA_ERR_INVALID_ARG;
+    if (n == 0) return PA_OK;
+    Request& r = it->second;
+    const int32_t bs = m->block_size;
+    // the ids in the order of the request's table; only blocks whose every token is there may leave
+    const int32_t full = (int32_t)r.tokens.size() / bs;
+    std::vector<char> leaves(r.blocks.size(), 0);
+    int32_t at = 0;
+    for (int32_t i = 0; i < full && at < n; ++i)
+        if (r.blocks[i] == block_ids[at]) {
+            leaves[i] = 1;
+            ++at;
+        }
+    if (at < n) return PA_ERR_INVALID_ARG;  // not the request's, not full, out of order, or twice
+    std::vector<int32_t> blocks, tokens;
+    blocks.reserve(r.blocks.size() - n);
+    tokens.reserve(r.tokens.size() - (size_t)n * bs);
+    for (size_t i = 0; i < r.blocks.size(); ++i) {
+        if (leaves[i]) continue;
+        blocks.push_back(r.blocks[i]);
+        const size_t t0 = std::min(r.tokens.size(), i * bs), t1 = std::min(r.tokens.size(), (i + 1) * bs);
+        tokens.insert(tokens.end(), r.tokens.begin() + t0, r.tokens.begin() + t1);
+    }
+    for (size_t i = r.blocks.size(); i-- > 0;)  // later blocks first, as at a release
+        if (leaves[i]) m->drop_ref(r.blocks[i]);
+    r.blocks.swap(blocks);
+    r.tokens.swap(tokens);
+    r.capacity -= n * bs;
+    r.evicted = true;
     return PA_OK;
 }
 

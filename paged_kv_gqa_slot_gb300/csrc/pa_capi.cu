@@ -129,8 +129,21 @@ int check_pool(const pa_pool* p, PoolView* v, bool need_maps) {
     return PA_OK;
 }
 
-int check_heads(const PoolView& v, int num_heads) {
-    if (num_heads <= 0 || num_heads % v.num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+int check_pool8(const pa_pool8* p, Pool8View* v) {
+    if (!p || !p->k_cache || !p->v_cache || !p->exps) return PA_ERR_INVALID_ARG;
+    if (p->num_blocks <= 0 || p->num_kv_heads <= 0 || p->block_size <= 0 || p->head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (p->block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+    if (p->head_dim != 64 && p->head_dim != 128) return PA_ERR_UNSUPPORTED;
+    if (!aligned16(p->k_cache) || !aligned16(p->v_cache) || (reinterpret_cast<uintptr_t>(p->exps) & 1u))
+        return PA_ERR_INVALID_ARG;
+    if (p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension
+    v->k = static_cast<uint8_t*>(p->k_cache);
+    v->v = static_cast<uint8_t*>(p->v_cache);
+    v->exps = static_cast<uint8_t*>(p->exps);
+    v->num_blocks = p->num_blocks;
+    v->num_kv_heads = p->num_kv_heads;
+    v->head_dim = p->head_dim;
     return PA_OK;
 }
 
@@ -238,18 +251,47 @@ int pa_kv_copy(const pa_pool* pool, const int64_t* src_slots, const int64_t* dst
     return from_cuda(launch_kv_copy(v, src_slots, dst_slots, n, st, (cudaStream_t)stream));
 }
 
-static int check_attn(const pa_pool* pool, PoolView* v, const void* q, const int32_t* block_tables,
-                      int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale,
-                      const void* out) {
-    int rc = check_pool(pool, v, false);
-    if (rc) return rc;
-    rc = check_heads(*v, num_heads);
-    if (rc) return rc;
+// What every attention call checks besides its pool.
+static int check_call(int num_kv_heads, const void* q, const int32_t* block_tables, int32_t max_blocks,
+                      const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, const void* out) {
+    if (num_heads <= 0 || num_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
     if (batch < 0 || batch > 65535) return PA_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
     if (batch == 0) return PA_OK;
     if (!q || !block_tables || !seq_lens || !out || !aligned16(q) || !aligned16(out)) return PA_ERR_INVALID_ARG;
     if (max_blocks <= 0 || (long long)max_blocks * kBlockSize > 0x7fffffffLL) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+static int check_attn(const pa_pool* pool, PoolView* v, const void* q, const int32_t* block_tables,
+                      int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale,
+                      const void* out) {
+    const int rc = check_pool(pool, v, false);
+    return rc ? rc
+              : check_call(v->num_kv_heads, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+}
+
+// The pointers and factor of a decode that adds up weights, on top of check_attn / check_call.
+static int check_weights(const float* weights, const float* workspace, float decay) {
+    if (!weights || !workspace || !std::isfinite(decay)) return PA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(workspace)) & 3u)
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+// The arguments every decode sets; PA_ERR_CUDA without a device status word.
+static int decode_args(AttnArgs* a, const void* q, const int32_t* block_tables, int32_t max_blocks,
+                       const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, void* out) {
+    a->q = q;
+    a->block_tables = block_tables;
+    a->seq_lens = seq_lens;
+    a->out = out;
+    a->status = device_status_ptr();
+    if (!a->status) return PA_ERR_CUDA;
+    a->batch = batch;
+    a->num_heads = num_heads;
+    a->max_blocks = max_blocks;
+    a->scale = scale;
     return PA_OK;
 }
 
@@ -376,6 +418,129 @@ int pa_prefill_chunked(const pa_pool* pool, const void* q, const int32_t* cu_q_l
     a.max_chunk = max_chunk;
     a.scale = scale;
     return from_cuda(launch_prefill(v, a, (cudaStream_t)stream));
+}
+
+size_t pa_weights_workspace_bytes(int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t max_blocks) {
+    if (batch < 0 || max_blocks < 0 || num_kv_heads <= 0 || num_heads <= 0) return 0;
+    const size_t columns = num_heads / num_kv_heads > 8 ? 16 : 8;
+    return (size_t)batch * num_kv_heads * max_blocks * columns * sizeof(float);
+}
+
+int pa_decode_weights(const pa_pool* pool, const void* q, const int32_t* block_tables, int32_t max_blocks,
+                      const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, float decay,
+                      float* weights, float* workspace, void* out, pa_stream_t stream) {
+    PoolView v;
+    int rc = check_attn(pool, &v, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc || batch == 0) return rc;
+    if (num_heads / v.num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+    rc = check_weights(weights, workspace, decay);
+    AttnArgs a{};
+    if (!rc) rc = decode_args(&a, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc) return rc;
+    a.weights = weights;
+    a.ws_weights = workspace;
+    a.decay = decay;
+    return from_cuda(launch_decode_weights(v, a, (cudaStream_t)stream));
+}
+
+int pa_kv_append8(const pa_pool8* pool, const void* k_new, const void* v_new, const int64_t* slot_mapping,
+                  int32_t num_tokens, pa_stream_t stream) {
+    Pool8View v;
+    int rc = check_pool8(pool, &v);
+    if (rc) return rc;
+    if (num_tokens < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new)) return PA_ERR_INVALID_ARG;
+    if ((long long)num_tokens * 2 * v.num_kv_heads * (v.head_dim / 8) >= (1LL << 31)) return PA_ERR_INVALID_ARG;
+    unsigned* st = device_status_ptr();
+    if (!st) return PA_ERR_CUDA;
+    return from_cuda(launch_kv_append8(v, k_new, v_new, slot_mapping, num_tokens, st, (cudaStream_t)stream));
+}
+
+static int decode8(const pa_pool8* pool, const void* q, const int32_t* block_tables, int32_t max_blocks,
+                   const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, float decay,
+                   float* weights, float* workspace, void* out, pa_stream_t stream) {
+    Pool8View v;
+    int rc = check_pool8(pool, &v);
+    if (!rc) rc = check_call(v.num_kv_heads, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc || batch == 0) return rc;
+    if (num_heads / v.num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+    AttnArgs a{};
+    rc = decode_args(&a, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc) return rc;
+    a.weights = weights;
+    a.ws_weights = workspace;
+    a.decay = decay;
+    return from_cuda(launch_decode8(v, a, (cudaStream_t)stream));
+}
+
+int pa_decode8(const pa_pool8* pool, const void* q, const int32_t* block_tables, int32_t max_blocks,
+               const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, void* out,
+               pa_stream_t stream) {
+    return decode8(pool, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, 1.f, nullptr, nullptr, out,
+                   stream);
+}
+
+int pa_decode8_weights(const pa_pool8* pool, const void* q, const int32_t* block_tables, int32_t max_blocks,
+                       const int32_t* seq_lens, int32_t batch, int32_t num_heads, float scale, float decay,
+                       float* weights, float* workspace, void* out, pa_stream_t stream) {
+    if (batch > 0) {
+        const int rc = check_weights(weights, workspace, decay);
+        if (rc) return rc;
+    }
+    return decode8(pool, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, decay, weights, workspace,
+                   out, stream);
+}
+
+int pa_prefill_chunked8(const pa_pool8* pool, const void* q, const int32_t* cu_q_lens, const int32_t* block_tables,
+                        int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t num_heads,
+                        int32_t max_chunk, float scale, void* out, pa_stream_t stream) {
+    Pool8View v;
+    int rc = check_pool8(pool, &v);
+    if (!rc) rc = check_call(v.num_kv_heads, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc) return rc;
+    if (max_chunk < 0) return PA_ERR_INVALID_ARG;
+    if (batch == 0 || max_chunk == 0) return PA_OK;
+    if (!cu_q_lens) return PA_ERR_INVALID_ARG;
+    if ((long long)max_chunk * (num_heads / v.num_kv_heads) > 0x3fffffffLL) return PA_ERR_INVALID_ARG;
+    AttnArgs a{};
+    rc = decode_args(&a, q, block_tables, max_blocks, seq_lens, batch, num_heads, scale, out);
+    if (rc) return rc;
+    a.cu_q_lens = cu_q_lens;
+    a.max_chunk = max_chunk;
+    return from_cuda(launch_prefill8(v, a, (cudaStream_t)stream));
+}
+
+int pa_kv_evict(const int32_t* block_tables, const int32_t* seq_lens, const float* weights, int32_t batch,
+                int32_t max_blocks, int32_t num_kv_heads, int32_t keep_blocks, int32_t sink_blocks,
+                int32_t recent_blocks, int32_t* block_tables_out, int32_t* seq_lens_out, float* weights_out,
+                int32_t* evicted, int32_t* num_evicted, pa_stream_t stream) {
+    if (batch < 0 || batch > 65535 || num_kv_heads <= 0 || max_blocks <= 0) return PA_ERR_INVALID_ARG;
+    if (sink_blocks < 0 || recent_blocks < 1 || (long long)sink_blocks + recent_blocks > keep_blocks)
+        return PA_ERR_INVALID_ARG;
+    if (max_blocks > kEvictMaxBlocks) return PA_ERR_UNSUPPORTED;
+    if (batch == 0) return PA_OK;
+    const void* all[] = {block_tables, seq_lens, weights, block_tables_out, seq_lens_out, weights_out, evicted,
+                         num_evicted};
+    for (const void* p : all)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return PA_ERR_INVALID_ARG;
+    EvictArgs a;
+    a.tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.weights = weights;
+    a.tables_out = block_tables_out;
+    a.seq_lens_out = seq_lens_out;
+    a.weights_out = weights_out;
+    a.evicted = evicted;
+    a.num_evicted = num_evicted;
+    a.status = device_status_ptr();
+    if (!a.status) return PA_ERR_CUDA;
+    a.max_blocks = max_blocks;
+    a.num_kv_heads = num_kv_heads;
+    a.keep = keep_blocks;
+    a.sink = sink_blocks;
+    a.recent = recent_blocks;
+    return from_cuda(launch_evict(a, batch, (cudaStream_t)stream));
 }
 
 int pa_device_status(uint32_t* flags, int32_t clear, pa_stream_t stream) {

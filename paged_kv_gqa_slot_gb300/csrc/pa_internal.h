@@ -30,6 +30,17 @@ struct PoolView {
     CUtensorMap tile_v;
 };
 
+// A validated 8-bit pool: e4m3 codes [num_blocks, num_kv_heads, 16, head_dim] for K and for V,
+// and the biased exponents of their scales [num_blocks, num_kv_heads, 2] (pa_kv8.cuh).
+struct Pool8View {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* exps;
+    int num_blocks;
+    int num_kv_heads;
+    int head_dim;
+};
+
 struct DeviceInfo {
     int device;
     int num_sms;
@@ -57,6 +68,25 @@ struct AttnArgs {
     const void* k_new;
     const void* v_new;
     const int64_t* slots;
+    // decode with the blocks' accumulated weight (null: without): [B, Hkv, max_blocks], the factor
+    // on what it holds, and the workspace (pa_weights_workspace_bytes)
+    float* weights;
+    float* ws_weights;
+    float decay;
+};
+
+// Arguments of the eviction (pa_kv_evict); outputs may be their inputs.
+struct EvictArgs {
+    const int32_t* tables;    // [B, max_blocks]
+    const int32_t* seq_lens;  // [B]
+    const float* weights;     // [B, Hkv, max_blocks]
+    int32_t* tables_out;
+    int32_t* seq_lens_out;
+    float* weights_out;
+    int32_t* evicted;         // [B, max_blocks] ids, -1 behind the last
+    int32_t* num_evicted;     // [B]
+    unsigned* status;
+    int max_blocks, num_kv_heads, keep, sink, recent;
 };
 
 const DeviceInfo& device_info();
@@ -116,6 +146,16 @@ cudaError_t launch_decode_splitkv(const PoolView& pool, const AttnArgs& a, cudaS
 // decode kernel (columns = query x head), when max_chunk x group <= 16.
 bool decode_mq_supported(int group, int max_chunk);
 cudaError_t launch_decode_mq(const PoolView& pool, const AttnArgs& a, cudaStream_t stream);
+// pa_decode with the blocks' accumulated weight
+cudaError_t launch_decode_weights(const PoolView& pool, const AttnArgs& a, cudaStream_t stream);
+// the 8-bit pool: quantising append, decode (with weights if a.weights), multi-query decode
+cudaError_t launch_kv_append8(const Pool8View& pool, const void* k_new, const void* v_new, const int64_t* slots,
+                              int num_tokens, unsigned* status, cudaStream_t stream);
+cudaError_t launch_decode8(const Pool8View& pool, const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_decode8_mq(const Pool8View& pool, const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill8(const Pool8View& pool, const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream);
+constexpr int kEvictMaxBlocks = 49152;  // table width of an eviction: a word of shared memory each
 cudaError_t launch_combine(const float* ws_o, const float* ws_lse, int batch, int num_heads, int head_dim,
                            int num_partitions, void* out, cudaStream_t stream);
 cudaError_t launch_prefill(const PoolView& pool, const AttnArgs& a, cudaStream_t stream);
