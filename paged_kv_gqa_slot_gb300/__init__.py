@@ -343,14 +343,14 @@ def _arg(t: torch.Tensor, dtype, name: str, device: int) -> int:
     return t.data_ptr()
 
 
-def _new(shape, dtype, device: int, stream) -> torch.Tensor:
-    """A result tensor, allocated for the stream that writes it."""
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A result tensor of t's shape, type and device, allocated for the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _call(what: str, device: int, stream, *args) -> None:
@@ -410,12 +410,12 @@ def pa_kv_append8(pool: PaPool8, k_new: torch.Tensor, v_new: torch.Tensor, slot_
           _arg(v_new, torch.bfloat16, "v_new", d), _arg(slot_mapping, torch.int64, "slot_mapping", d), T)
 
 
-def _query(pool, q: torch.Tensor, out: Optional[torch.Tensor], device: int, stream) -> torch.Tensor:
+def _query(pool, q: torch.Tensor, out: Optional[torch.Tensor], stream) -> torch.Tensor:
     """Check q against the pool; the output tensor (the caller's, checked, or a new one)."""
     if q.dim() != 3 or q.shape[2] != pool.head_dim:
         raise ValueError(f"q: need [rows, num_heads, {pool.head_dim}], got {tuple(q.shape)}")
     if out is None:
-        return _new(q.shape, torch.bfloat16, device, stream)
+        return _like(q, stream)
     if out.shape != q.shape:
         raise ValueError(f"out: need shape {tuple(q.shape)}, got {tuple(out.shape)}")
     return out
@@ -424,7 +424,7 @@ def _query(pool, q: torch.Tensor, out: Optional[torch.Tensor], device: int, stre
 def pa_decode8(pool: PaPool8, q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     d = pool.device
-    out = _query(pool, q, out, d, stream)
+    out = _query(pool, q, out, stream)
     B = q.shape[0]
     _tables(block_tables, seq_lens, B)
     _call("pa_decode8", d, stream, pool.ref, _arg(q, torch.bfloat16, "q", d),
@@ -438,7 +438,7 @@ def pa_prefill_chunked8(pool: PaPool8, q: torch.Tensor, cu_q_lens: torch.Tensor,
                         seq_lens: torch.Tensor, scale: float, max_chunk: int, out: Optional[torch.Tensor] = None,
                         stream=None) -> torch.Tensor:
     d = pool.device
-    out = _query(pool, q, out, d, stream)
+    out = _query(pool, q, out, stream)
     B = seq_lens.numel()
     _tables(block_tables, seq_lens, B)
     if cu_q_lens.numel() != B + 1:
@@ -455,17 +455,17 @@ def pa_weights_workspace_bytes(batch: int, num_heads: int, num_kv_heads: int, ma
 
 
 def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weights, decay, workspace, out, stream):
-    out = _query(pool, q, out, device, stream)
+    out = _query(pool, q, out, stream)
     B, Hq, _ = q.shape
     _tables(block_tables, seq_lens, B)
     width = block_tables.shape[1]
     if weights.shape != (B, pool.num_kv_heads, width):
         raise ValueError(f"weights: need shape {(B, pool.num_kv_heads, width)}, got {tuple(weights.shape)}")
-    if B == 0:
+    if B == 0 or width == 0:
         return out
     need = B * pool.num_kv_heads * width * (16 if Hq // pool.num_kv_heads > 8 else 8)
     if workspace is None:
-        workspace = _new((need,), torch.float32, device, stream)
+        workspace = _like(weights.expand(need // weights.numel(), *weights.shape), stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace: need {need} floats, got {workspace.numel()}")
     _call(what, device, stream, pool.ref, _arg(q, torch.bfloat16, "q", device),
@@ -511,11 +511,8 @@ def pa_kv_evict(block_tables: torch.Tensor, seq_lens: torch.Tensor, weights: tor
     if in_place:
         new_tables, new_lens, new_weights = block_tables, seq_lens, weights
     else:
-        new_tables = _new((B, width), torch.int32, d, stream)
-        new_lens = _new((B,), torch.int32, d, stream)
-        new_weights = _new((B, hkv, width), torch.float32, d, stream)
-    evicted = _new((B, width), torch.int32, d, stream)
-    num = _new((B,), torch.int32, d, stream)
+        new_tables, new_lens, new_weights = _like(block_tables, stream), _like(seq_lens, stream), _like(weights, stream)
+    evicted, num = _like(block_tables, stream), _like(seq_lens, stream)
     _call("pa_kv_evict", d, stream, _arg(block_tables, torch.int32, "block_tables", d),
           _arg(seq_lens, torch.int32, "seq_lens", d), _arg(weights, torch.float32, "weights", d), B, width, hkv,
           int(keep_blocks), int(sink_blocks), int(recent_blocks), new_tables.data_ptr(), new_lens.data_ptr(),

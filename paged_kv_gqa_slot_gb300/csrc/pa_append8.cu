@@ -33,32 +33,32 @@ struct Append8Args {
     int num_tokens, num_kv_heads, window;
 };
 
-// Largest finite magnitude of the 8 bf16 values of a chunk (NaN and infinities do not count).
-__device__ __forceinline__ float chunk_amax(const uint4& v) {
-    float m = 0.f;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = fabsf(bf16_lo(w[i])), b = fabsf(bf16_hi(w[i]));
-        m = fmaxf(m, a < INFINITY ? a : 0.f);
-        m = fmaxf(m, b < INFINITY ? b : 0.f);
-    }
-    return m;
+// Larger of the magnitudes, bf16 pair by pair, as unsigned integers (their order is the
+// magnitudes'; infinities and NaN come last).
+__device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
+    return d;
+}
+
+// A bf16 pair's magnitudes with infinities and NaN as zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    w &= 0x7fff7fffu;
+    return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | (w >> 16 < 0x7f80u ? w & 0xffff0000u : 0u);
 }
 
 // 8 bf16 values times s, as 8 codes.
 __device__ __forceinline__ uint2 chunk_codes(const uint4& v, float s) {
-    auto word = [&](uint32_t a, uint32_t b) {
-        return to_e4m3x2(bf16_lo(a) * s, bf16_hi(a) * s) | (to_e4m3x2(bf16_lo(b) * s, bf16_hi(b) * s) << 16);
-    };
-    return make_uint2(word(v.x, v.y), word(v.z, v.w));
+    return make_uint2(to_e4m3x4(bf16_lo(v.x) * s, bf16_hi(v.x) * s, bf16_lo(v.y) * s, bf16_hi(v.y) * s),
+                      to_e4m3x4(bf16_lo(v.z) * s, bf16_hi(v.z) * s, bf16_lo(v.w) * s, bf16_hi(v.w) * s));
 }
 
 // 4 codes times s, rounded again.
 __device__ __forceinline__ uint32_t shift_codes(uint32_t w, float s) {
-    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(w & 0xffffu));
-    const float2 b = f16x2_to_float2(e4m3x2_to_f16x2(w >> 16));
-    return to_e4m3x2(a.x * s, a.y * s) | (to_e4m3x2(b.x * s, b.y * s) << 16);
+    uint32_t lo, hi;
+    e4m3x4_to_f16x4(w, lo, hi);
+    const float2 a = f16x2_to_float2(lo), b = f16x2_to_float2(hi);
+    return to_e4m3x4(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
 template <int D>
@@ -76,43 +76,51 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append8_kernel(const __grid_co
     const int t1 = static_cast<int>(min((long long)a.num_tokens, (long long)t0 + a.window));
     const int kvh = head >> 1, is_v = head & 1;
 
-    for (int t = t0; t < t1; ++t) {
-        const int64_t slot = __ldg(a.slots + t);
-        if (slot < 0) continue;
-        if (slot >= a.pool_slots) {
-            if (head == 0 && lane == 0) atomicOr(a.status, kDevOutOfRange);
-            continue;
-        }
-        const int64_t block = slot / kBlockSize;
-        // the entry before this one that names a slot: of the same block, and this unit is done there
-        auto in_pool = [&](int64_t s) { return s >= 0 && s < a.pool_slots; };
+    // the window's entries, one a lane, and which of them is its block's first: the entry before
+    // it that names a slot is of another block
+    __shared__ int tokens[kWarps][kBlockSize];
+    int* token_at = tokens[threadIdx.x >> 5];
+    const auto in_pool = [&](int64_t s) { return s >= 0 && s < a.pool_slots; };
+    const int64_t mine = t0 + lane < t1 ? __ldg(a.slots + t0 + lane) : -1;
+    if (mine >= a.pool_slots && head == 0) atomicOr(a.status, kDevOutOfRange);
+    const bool named = in_pool(mine);
+    const int64_t my_block = named ? mine / kBlockSize : -1;
+    const unsigned all_named = __ballot_sync(0xffffffffu, named);
+    if (!all_named) return;
+    const unsigned before = all_named & ((1u << lane) - 1u);
+    const int64_t prev = __shfl_sync(0xffffffffu, my_block, before ? 31 - __clz(before) : 0);
+    unsigned firsts = __ballot_sync(0xffffffffu, named && before && prev != my_block);
+    {
+        // the window's first named entry: look back past it
+        const int f = __ffs(all_named) - 1;
+        const int64_t block = __shfl_sync(0xffffffffu, my_block, f);
         bool first = true;
-        for (int p = t - 1; p >= 0; p -= 32) {
+        for (int p = t0 - 1; p >= 0; p -= 32) {
             const int64_t s = p - lane >= 0 ? __ldg(a.slots + p - lane) : -1;
-            const unsigned named = __ballot_sync(0xffffffffu, in_pool(s));
-            if (!named) continue;
-            const int64_t last = __shfl_sync(0xffffffffu, s, __ffs(named) - 1);
-            first = last / kBlockSize != block;
+            const unsigned some = __ballot_sync(0xffffffffu, in_pool(s));
+            if (!some) continue;
+            first = __shfl_sync(0xffffffffu, s, __ffs(some) - 1) / kBlockSize != block;
             break;
         }
-        if (!first) continue;
-        // the block's entries: lane o keeps the token whose row goes to offset o (-1: none); of
+        if (first) firsts |= 1u << f;
+    }
+
+    for (; firsts; firsts &= firsts - 1) {
+        const int f = __ffs(firsts) - 1, t = t0 + f;
+        const int64_t block = __shfl_sync(0xffffffffu, my_block, f);
+        // the block's entries: token_at[o] is the token whose row goes to offset o (-1: none); of
         // entries with the same slot the last counts
-        int token = -1;
+        if (lane < kBlockSize) token_at[lane] = -1;
+        __syncwarp();
         for (int p = t; p < a.num_tokens; p += 32) {
             const int64_t s = p + lane < a.num_tokens ? __ldg(a.slots + p + lane) : -1;
-            const bool named = in_pool(s);
-            const unsigned other = __ballot_sync(0xffffffffu, named && s / kBlockSize != block);
-            unsigned mine = __ballot_sync(0xffffffffu, named && s / kBlockSize == block);
-            if (other) mine &= (1u << (__ffs(other) - 1)) - 1;  // entries before the next block's
-            while (mine) {
-                const int src = __ffs(mine) - 1;
-                mine &= mine - 1;
-                const int off = static_cast<int>(__shfl_sync(0xffffffffu, s, src) % kBlockSize);
-                if (lane == off) token = p + src;
-            }
+            const bool here = in_pool(s);
+            const unsigned other = __ballot_sync(0xffffffffu, here && s / kBlockSize != block);
+            if (here && lane < (other ? __ffs(other) - 1 : 32)) atomicMax(&token_at[s % kBlockSize], p + lane);
             if (other) break;
         }
+        __syncwarp();
+        const int token = lane < kBlockSize ? token_at[lane] : -1;
         const unsigned written = __ballot_sync(0xffffffffu, token >= 0);
         const int sub = lane / kLanes, c = lane % kLanes;
         const size_t tile = (size_t)block * a.num_kv_heads + kvh;
@@ -120,20 +128,28 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append8_kernel(const __grid_co
         uint8_t* rows = a.codes[is_v] + tile * kBlockSize * D;
 
         uint4 x[kSteps];
-        float amax = 0.f;
+        uint32_t mag = 0u;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int src = __shfl_sync(0xffffffffu, token, i * kPar + sub);
             x[i] = make_uint4(0u, 0u, 0u, 0u);
             if (src >= 0) x[i] = __ldg(a.rows[is_v] + ((size_t)src * a.num_kv_heads + kvh) * kLanes + c);
         }
+        const int k_old = static_cast<int>(*exp_at) - kExpBias;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) amax = fmaxf(amax, chunk_amax(x[i]));
+        for (int i = 0; i < kSteps; ++i)
+            mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, x[i].x), x[i].y), x[i].z), x[i].w);
+        mag = __reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16));
+        if (mag >= 0x7f80u) {  // infinities and NaN do not count
+            mag = 0u;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        int k = scale_exponent(amax);
+            for (int i = 0; i < kSteps; ++i)
+                mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, finite2(x[i].x)), finite2(x[i].y)), finite2(x[i].z)),
+                               finite2(x[i].w));
+            mag = __reduce_max_sync(0xffffffffu, max(mag & 0xffffu, mag >> 16));
+        }
+        int k = scale_exponent(__uint_as_float(mag << 16));
         if (!(written & 1u)) {
-            const int k_old = static_cast<int>(*exp_at) - kExpBias;
             if (k > k_old) {
                 const float s = exp2_int(k_old - k);
 #pragma unroll

@@ -2,6 +2,7 @@
 // word, the per-device launch facts and the cache of TMA descriptors over the pool.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -46,14 +47,16 @@ struct MapKey {
     int d;
     int kind;   // 0: 2-D half-tile boxes, 1: 4-D whole-tile boxes, 2: 3-D (d, head, token) rows
     int extra;  // kind 2: heads * 65536 + box heads
+    long long stride = 0;  // kind 3: distance of the two planes (0: one plane)
     bool operator==(const MapKey& o) const {
-        return base == o.base && rows == o.rows && d == o.d && kind == o.kind && extra == o.extra;
+        return base == o.base && rows == o.rows && d == o.d && kind == o.kind && extra == o.extra &&
+               stride == o.stride;
     }
 };
 struct MapKeyHash {
     size_t operator()(const MapKey& k) const {
         return std::hash<const void*>()(k.base) ^ (std::hash<long long>()(k.rows) * 31u) ^ (size_t)k.d ^
-               ((size_t)k.kind << 20) ^ ((size_t)k.extra << 24);
+               ((size_t)k.kind << 20) ^ ((size_t)k.extra << 24) ^ std::hash<long long>()(k.stride);
     }
 };
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash>& map_cache() {
@@ -138,6 +141,8 @@ int check_pool8(const pa_pool8* p, Pool8View* v) {
     if (!aligned16(p->k_cache) || !aligned16(p->v_cache) || (reinterpret_cast<uintptr_t>(p->exps) & 1u))
         return PA_ERR_INVALID_ARG;
     if (p->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;  // a grid dimension
+    if ((long long)p->num_blocks * p->num_kv_heads * kBlockSize > 0x7fffffffLL)
+        return PA_ERR_UNSUPPORTED;  // TMA row coordinates are int32
     v->k = static_cast<uint8_t*>(p->k_cache);
     v->v = static_cast<uint8_t*>(p->v_cache);
     v->exps = static_cast<uint8_t*>(p->exps);
@@ -184,6 +189,62 @@ bool rows_map(CUtensorMap* out, const void* base, long long tokens, int heads, i
     cache[key] = m;
     *out = m;
     return true;
+}
+
+// One map of kind 3: bytes as (64 or 128, rows, row_bytes / 128 halves, planes), the halves dimension
+// only for rows of 256 bytes; box: one tile of every plane.
+static bool plane_map(CUtensorMap* out, const void* base, long long rows, int row_bytes, long long stride) {
+    auto& cache = map_cache();
+    MapKey key{base, rows, row_bytes, 3, 0};
+    key.stride = stride;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        auto it = cache.find(key);
+        if (it != cache.end()) {
+            *out = it->second;
+            return true;
+        }
+    }
+    auto fn = encode_fn();
+    if (!fn) return false;
+    CUtensorMap m;
+    const int halves = row_bytes / 128, planes = stride ? 2 : 1;
+    const int rank = halves > 1 ? 4 : 3;
+    const cuuint64_t inner = std::min(row_bytes, 128);
+    cuuint64_t dims[4] = {inner, (cuuint64_t)rows, 0, 0}, strides[3] = {(cuuint64_t)row_bytes, 0, 0};
+    cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)kBlockSize, 0, 0};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const cuuint64_t between = stride ? (cuuint64_t)stride : (cuuint64_t)rows * row_bytes;
+    int i = 2;
+    if (halves > 1) {
+        dims[i] = halves;
+        strides[i - 1] = 128;
+        box[i++] = halves;
+    }
+    dims[i] = planes;
+    strides[i - 1] = between;
+    box[i] = planes;
+    const CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return false;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (cache.size() > 256) cache.clear();
+    cache[key] = m;
+    *out = m;
+    return true;
+}
+
+bool plane_maps(PlaneMaps* out, const void* k, const void* v, long long rows, int row_bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(k), b = reinterpret_cast<uintptr_t>(v);
+    const unsigned long long gap = a < b ? b - a : a - b;
+    out->k_second = a > b;
+    // a plane stride is a multiple of 16 below 2^40; pools that overlap are not two planes
+    out->paired = gap >= (unsigned long long)rows * row_bytes && gap < (1ull << 40);
+    if (!out->paired) out->k_second = 0;
+    if (out->paired) return plane_map(&out->k, out->k_second ? v : k, rows, row_bytes, (long long)gap);
+    return plane_map(&out->k, k, rows, row_bytes, 0) && plane_map(&out->v, v, rows, row_bytes, 0);
 }
 
 const DeviceInfo& device_info() {

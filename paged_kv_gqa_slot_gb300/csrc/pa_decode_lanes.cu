@@ -4,7 +4,7 @@
 //
 //   o = sum_t softmax_t(scale <q, K_t>) V_t,   8-bit: K_t = codeK_t 2^kK(block), V_t = codeV_t 2^kV(block)
 //
-// One CTA serves one (sequence, kv head, split); its four warps, and the splits of a sequence
+// One CTA serves one (sequence, kv head, split); its warps, and the splits of a sequence
 // (one thread-block cluster, merged through distributed shared memory), take the blocks
 // round-robin, so a warp's block indices do not depend on the sequence's length.
 //
@@ -13,25 +13,25 @@
 // per block and head).  q enters as f16 too, after its row is brought to a maximum in
 // [2^14, 2^15) by a power of two that joins the same factor: an element loses bits only below
 // 2^-29 of the row's maximum.  V's scale joins the exponent: with x = log2(e) scale <q, K> the
-// weight the V product takes is u = 2^(x + kV - my), my the running maximum of x + kV, so
-// u <= 1 fits f16 whatever the blocks' scales, and the largest contributions, not the largest
+// weight the V product takes is u = 2^(x + kV - base), base following the maximum of x + kV, so
+// u fits f16 whatever the blocks' scales, and the largest contributions, not the largest
 // probabilities, set its range.  u is rounded to f16's 11 bits (an eighth of the rounding of the
 // bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.
 // 16 bits: the same with kK = kV = 0 on bf16 MMAs, u carried as two bf16 parts.
 //
-// Loads.  A thread's MMA fragments want, per 16-token block, 16-byte pieces of a few rows --
-// since which d values make one MMA step is free as long as q (or the output) agrees.  So every
-// lane copies (cp.async) just the pieces its own fragments take into its own 16-byte columns of
-// a ring in shared memory: every byte is copied once and read once, with no bank conflict, no
-// ldmatrix, and no barrier between warps or lanes, and kStages blocks a warp are in flight.
+// Loads.  Which d values make one MMA step, and which token is which MMA row, is free as long as q,
+// u and the output agree, so every lane takes 16-byte pieces of a few rows as its fragments, with
+// no ldmatrix and no exchange between lanes.  Each warp fetches its own blocks by TMA, K and V of a
+// block in one box (their pools are two planes of one tensor map), into a private ring of
+// swizzled slots, in which the pieces are chosen so that an access has no bank conflict: no
+// barrier between warps, and one copy instruction a block.
 //
 // Weights.  A block's sum of 2^x per head goes to a workspace as it is computed; once the
 // sequence's maximum and normaliser are known (after the merge) the CTA that read the block turns
 // the sums into weights, adds the group's heads in order and updates its own entry: no
 // atomics, no second launch.
 #include <algorithm>
-#include <cmath>
-#include <cstdlib>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -43,24 +43,30 @@ namespace cg = cooperative_groups;
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int BITS, int D>
 struct Lanes {
     static constexpr int kRowBytes = D * BITS / 8;
     static constexpr int kBlockBytes = 2 * kBlockSize * kRowBytes;  // K and V of one (block, kv head)
-    static constexpr int kStages = 3 * 4096 / (kBlockBytes < 4096 ? kBlockBytes : 4096);  // blocks in flight per warp
-    static constexpr int kPieces = kBlockBytes / 512;               // 16-byte pieces of a block a lane takes
+    static constexpr int kPlane = kBlockSize * kRowBytes;  // K or V of one (block, kv head)
     static constexpr int kKChunks = kRowBytes / 64;                 // of a K row
-    static constexpr int kVChunks = kRowBytes >= 128 ? kRowBytes / 128 : 1;  // of a V row (half of one at 64 bytes)
-    static constexpr int kRing = kWarps * kStages * kBlockBytes;
-    // merge scratch over the ring: per warp, and for the CTA, m[16], l[16], O[16][kRow]
+    static constexpr int kVChunks = kRowBytes > 128 ? 2 : 1;                 // of a V row (half of one at 64 bytes)
+    // merge scratch: per warp, and for the CTA, m[16], l[16], O[16][kRow]
     static constexpr int kRow = D + 4;
     static constexpr int kPart = 32 + 16 * kRow;
-    static constexpr int kMerge = (kWarps + 1) * kPart * 4;
-    static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+    static constexpr int merge_bytes(int warps) { return (warps + 1) * kPart * 4; }
+    // blocks in flight per warp: what an SM's shared memory holds for the warps that run on it
+    __host__ __device__ static constexpr int stages(int warps, int ctas) {
+        return 196608 / (ctas * warps * kBlockBytes);
+    }
+    __host__ __device__ static constexpr int ring_bytes(int warps, int ctas) {
+        return stages(warps, ctas) * warps * kBlockBytes;
+    }
+    static constexpr int smem(int warps, int ctas) {
+        const int ring = ring_bytes(warps, ctas) + stages(warps, ctas) * warps * 8;
+        return ring > merge_bytes(warps) ? ring : merge_bytes(warps);
+    }
     static constexpr int kQuads = D / 32;  // 4-float groups of O a lane holds per head
     // which group of a head's row (d / 4) the lane's MMA tiles 2 w, 2 w + 1 hold
     __device__ static constexpr int quad(int gid, int w) {
@@ -82,25 +88,79 @@ struct LanesArgs {
     unsigned* status;
     int max_blocks, num_heads, num_kv_heads, num_blocks, group;
     float scale_log2, decay;
+    // one box brings K and V of a block (their pools as two planes of one map), and whether
+    // K is the second plane; else a box each
+    int paired, k_second;
 };
 
-// CTAs an SM is to hold: as many as the rings leave room for, one fewer where two n-tiles need
-// more than 128 registers
-__host__ __device__ constexpr int resident_ctas(int bits, int d, int nt) {
-    return bits == 16 ? 2 : d == 128 && nt == 2 ? 3 : 4;
+// Warps of a CTA: 4, or 3 where a thread needs more than 128 registers, so that four CTAs fit an
+// SM in either case: 512 CTAs (64 sequences of 8 kv heads) are then one wave.  WIDE: twice as
+// many, two CTAs an SM, where even 16 splits of every sequence leave SMs empty.
+__host__ __device__ constexpr bool fits128(int bits, int d, int nt) { return d == 64 || (bits == 8 && nt == 1); }
+__host__ __device__ constexpr int warps_of(int bits, int d, int nt, bool wide) {
+    return (fits128(bits, d, nt) ? 4 : 3) * (wide ? 2 : 1);
+}
+__host__ __device__ constexpr int ctas_of(bool wide) { return wide ? 2 : 4; }
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+// One box of a pool map: x = 0, row, then for 16-bit rows their 128-byte halves, then K and V.
+template <bool HALVES>
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar, uint64_t policy) {
+    if constexpr (HALVES)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %2, %2}], [%4], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3, %2}], [%4], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar), "l"(policy)
+            : "memory");
+}
+// log2 on the special-function unit (0 gives -inf)
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A normaliser l = sum of u 2^-kV moved from one base to one 2^-d higher: l 2^d.  Its terms carry
+// 2^-kV, so l may be as large as 2^100 where u is about 1, and l 2^d matters where 2^d alone
+// is zero in fp32 (blocks of V at the two ends of the scales' range).
+__device__ __forceinline__ float rescale_sum(float l, float d) {
+    const float h = fast_exp2(0.5f * d);
+    return l * h * h;
 }
 
 // Where group `grp` (4 floats) of a head's row sits in the merge scratch: the lanes that write one
 // instruction's groups hit different banks.
 __device__ __forceinline__ int quad_at(int grp) { return grp ^ ((grp >> 2) & 1); }
 
-template <int BITS, int D, int NT, bool MQ, bool WEIGHTS>
-__global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
-    decode_lanes_kernel(const __grid_constant__ LanesArgs a) {
+template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, bool WIDE>
+__global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE))
+    decode_lanes_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ LanesArgs a) {
     using Sh = Lanes<BITS, D>;
+    constexpr int kWarps = warps_of(BITS, D, NT, WIDE), kThreads = kWarps * 32;
+    constexpr int kCtas = ctas_of(WIDE);
+    constexpr int kStages = Sh::stages(kWarps, kCtas);  // ring slots per warp
     constexpr int kSteps = D / 16;    // MMA steps over d (K), tiles of d (V)
     constexpr int kRowB = Sh::kRowBytes;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
 
     uint32_t ncl;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncl));
@@ -108,10 +168,19 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
+    // Which row of a block is which MMA row or key: neighbouring ones are kNext rows apart, which the
+    // swizzle (of 128-byte rows by their index modulo 8, of 64-byte rows by half of it) and the row
+    // length put into different banks.  trow: the row of MMA row gid (gid + 8: trow + 8).
+    constexpr int kNext = kRowB == 64 ? 1 : 4;
+    const int trow = kRowB == 64 ? gid : (gid >> 1) | ((gid & 1) << 2);
     const int g = a.group;
     const int first = rank * kWarps + warp, stride = sub * kWarps;  // this warp's blocks
     const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
     pdl_wait();
+    if (smem_u32(smem) & 1023u) {  // the swizzled slots need the declared alignment
+        if (threadIdx.x == 0) atomicOr(a.status, kDevOutOfRange);
+        return;
+    }
 
     // lane l keeps the id and exponents of the warp's block number c0 + l; the table entry does
     // not wait for the length (an entry past the sequence's blocks is not used)
@@ -149,38 +218,35 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
     id = checked(lane, id);
     int ex = exps_of(lane, id);
 
-    const uint32_t ring = smem_u32(smem) + warp * Sh::kStages * Sh::kBlockBytes;
-    const uint32_t mine = ring + lane * 16;
-    const auto issue = [&](int k, int blk) {
-        const size_t tile = ((size_t)blk * a.num_kv_heads + kvh) * (kBlockSize * kRowB);
-        uint32_t dst = mine + (k % Sh::kStages) * Sh::kBlockBytes;
-        const uint8_t* kp = a.k + tile + gid * kRowB + tig * 16;
-        const uint8_t* vp = a.v + tile + 2 * tig * kRowB + gid * (kRowB >= 128 ? 16 : 8);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)  // rows gid, gid + 8
-#pragma unroll
-            for (int c = 0; c < Sh::kKChunks; ++c, dst += 512) cp_async16(dst, kp + r * 8 * kRowB + c * 64);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {  // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-            const uint8_t* src = vp + ((r & 1) + (r >> 1) * 8) * kRowB;
-            if constexpr (kRowB >= 128) {
-#pragma unroll
-                for (int c = 0; c < Sh::kVChunks; ++c, dst += 512) cp_async16(dst, src + c * 128);
-            } else {
-                cp_async8(dst + (r >> 1) * 512 + (r & 1) * 8, src);
-            }
-        }
+    // a ring slot holds K and V of one block, [16 rows][64 or 128 B] swizzled (256-byte rows: two such
+    // halves); each warp issues and waits for its own
+    const uint32_t ring = smem_u32(smem) + warp * kStages * Sh::kBlockBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sh::ring_bytes(kWarps, kCtas)) + warp * kStages;
+    const uint64_t policy = l2_evict_first_policy();
+    const auto issue = [&](int slot, int blk) {
+        const int row = (blk * a.num_kv_heads + kvh) * kBlockSize;
+        const uint32_t dst = ring + slot * Sh::kBlockBytes, bar = smem_u32(&full[slot]);
+        mbar_arrive_expect_tx(&full[slot], Sh::kBlockBytes);
+        tma_block<(kRowB > 128)>(dst, &tm_k, row, bar, policy);
+        if (!a.paired) tma_block<(kRowB > 128)>(dst + Sh::kPlane, &tm_v, row, bar, policy);
     };
+    if (lane < kStages) mbar_init(&full[lane], 1);
+    if (lane == 0) {
+        prefetch_tensormap(&tm_k);
+        if (!a.paired) prefetch_tensormap(&tm_v);
+    }
+    fence_mbar_init();
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < Sh::kStages; ++k) {
-        if (k < n) issue(k, __shfl_sync(0xffffffffu, id, k));
-        cp_async_commit();
+    for (int k = 0; k < kStages; ++k) {
+        const int blk = __shfl_sync(0xffffffffu, id, k);
+        if (k < n && lane == 0) issue(k, blk);
     }
 
     // q as B fragments: column gid of each n-tile, the d values this lane's K pieces hold
     uint32_t qb[NT][kSteps][2];
-    int eq[NT][2];  // exponents of this thread's output columns nt * 8 + 2 tig (+1)
-    int colpos[NT][2];
+    float qf[NT][2];    // of this thread's columns nt * 8 + 2 tig (+1): factor on the raw score
+    int colpos[NT][2];  // and the last key they see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int col = nt * 8 + gid;
@@ -226,14 +292,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            eq[nt][j] = __shfl_sync(0xffffffffu, e, (2 * tig + j) * 4);
+            qf[nt][j] = a.scale_log2 * exp2_int(__shfl_sync(0xffffffffu, e, (2 * tig + j) * 4));
             const int oc = nt * 8 + 2 * tig + j;
-            colpos[nt][j] = MQ ? (oc < R ? L - C + oc / g : -1) : L - 1;
+            colpos[nt][j] = MQ ? L - C + (oc < R ? oc / g : 0) : L - 1;  // unused columns: as the first
         }
     }
 
     float ot[NT][kSteps][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];  // base and normaliser of the columns
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -242,8 +308,31 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
         for (int s = 0; s < kSteps; ++s) ot[nt][s][0] = ot[nt][s][1] = ot[nt][s][2] = ot[nt][s][3] = 0.f;
     }
 
+    const int all_see = MQ ? L - C : L - 1;  // every column sees keys up to this one
     int nid = 0, nex = 0;
-    for (int k = 0; k < n; ++k) {
+    // This lane's pieces of a slot.  K: rows trow, trow + 8, 16-byte chunks tig, tig + 4, ...  V: keys
+    // 2 tig, 2 tig + 1 (+ 8) are rows kNext apart, chunk gid (64-byte rows: half of chunk gid / 2);
+    // the lanes that would meet the others' banks take the two in the other order, and the byte
+    // permutations below put the pair right.
+    constexpr int kSlotRow = kRowB == 64 ? 64 : 128;
+    const bool swapped = kRowB == 64 ? gid >> 1 & 1 : gid & 1;
+    const int vrow = (kRowB == 64 ? 2 * tig : tig) + (swapped ? kNext : 0);
+    uint32_t k_off, v_off, v_flip;  // v_flip: row ^ kNext, and the chunk with it
+    if constexpr (kRowB == 64) {
+        k_off = trow * 64 + ((tig ^ (trow >> 1 & 3)) << 4);
+        v_off = vrow * 64 + (((gid >> 1) ^ tig) << 4) + (gid & 1) * 8;
+        v_flip = v_off ^ 64;
+    } else {
+        k_off = trow * 128 + ((tig ^ trow) << 4);
+        v_off = vrow * 128 + ((gid ^ vrow) << 4);
+        v_flip = v_off ^ (4 * 128 | 4 << 4);
+    }
+    k_off += a.k_second ? Sh::kPlane : 0;
+    v_off += a.k_second ? 0 : Sh::kPlane;
+    v_flip += a.k_second ? 0 : Sh::kPlane;
+    bool ok = true;
+    int slot = 0, parity = 0, k = 0;
+    for (; k < n; ++k) {
         const int at = k & 31;
         // the next 32 entries, then (once they have come) their exponents
         if (at == 0 && k + 32 + lane < n) nid = __ldg(bt + entry_at(k + 32 + lane));
@@ -251,122 +340,159 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
             nid = checked(k + 16 + lane, nid);
             nex = exps_of(k + 16 + lane, nid);
         }
-        cp_async_wait<Sh::kStages - 1>();
-        const int e = __shfl_sync(0xffffffffu, ex, at);
-        const int ek = (e & 255) - kExpBias, ev = (e >> 8) - kExpBias;
+        const uint32_t st_at = ring + slot * Sh::kBlockBytes;
+        ok = mbar_wait_warp(&full[slot], parity);
+        if (!ok) break;
+        float kscale = 1.f, unscale = 1.f, fev = 0.f;  // 2^kK, 2^-kV, kV
+        if constexpr (BITS == 8) {
+            const int e = __shfl_sync(0xffffffffu, ex, at);
+            kscale = __int_as_float((e & 255) << 23);
+            unscale = __int_as_float((2 * kExpBias - (e >> 8)) << 23);
+            fev = static_cast<float>((e >> 8) - kExpBias);
+        }
         const int kbase = static_cast<int>(entry_at(k)) * kBlockSize;
-        const uint4* piece = reinterpret_cast<const uint4*>(
-            smem + (warp * Sh::kStages + k % Sh::kStages) * Sh::kBlockBytes + lane * 16);
 
-        // S^T = K q^T: rows are tokens gid, gid + 8, columns the heads
-        float st[NT][4];
+        // S^T = K q^T: rows are tokens gid, gid + 8, columns the heads; two chains of MMAs (one
+        // per n-tile, or two of the one)
+        float st[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) st[nt][0] = st[nt][1] = st[nt][2] = st[nt][3] = 0.f;
+        for (int i = 0; i < 4; ++i) st[0][i] = st[1][i] = 0.f;
 #pragma unroll
         for (int c = 0; c < Sh::kKChunks; ++c) {
-            const uint4 p0 = piece[c * 32], p8 = piece[(Sh::kKChunks + c) * 32];
+            // chunk 4 (c % 2) + tig of 128-byte piece c / 2 of the rows
+            const uint32_t at16 = st_at + (k_off ^ ((c & 1) << 6)) + (c >> 1) * (kBlockSize * 128);
+            const uint4 p0 = lds16(at16), p8 = lds16(at16 + 8 * kSlotRow);
             const uint32_t w0[4] = {p0.x, p0.y, p0.z, p0.w}, w8[4] = {p8.x, p8.y, p8.z, p8.w};
             if constexpr (BITS == 8) {
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    const uint32_t a0 = e4m3x2_to_f16x2(w0[s] & 0xffffu), a2 = e4m3x2_to_f16x2(w0[s] >> 16);
-                    const uint32_t a1 = e4m3x2_to_f16x2(w8[s] & 0xffffu), a3 = e4m3x2_to_f16x2(w8[s] >> 16);
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16x4(w0[s], a0, a2);
+                    e4m3x4_to_f16x4(w8[s], a1, a3);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(st[nt], a0, a1, a2, a3, qb[nt][c * 4 + s][0], qb[nt][c * 4 + s][1]);
+                        mma_f16_16816(st[NT == 1 ? s & 1 : nt], a0, a1, a2, a3, qb[nt][c * 4 + s][0],
+                                      qb[nt][c * 4 + s][1]);
                 }
             } else {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma_16816(st[nt], w0[2 * s], w8[2 * s], w0[2 * s + 1], w8[2 * s + 1], qb[nt][c * 2 + s][0],
-                                  qb[nt][c * 2 + s][1]);
+                        mma_16816(st[NT == 1 ? s & 1 : nt], w0[2 * s], w8[2 * s], w0[2 * s + 1], w8[2 * s + 1],
+                                  qb[nt][c * 2 + s][0], qb[nt][c * 2 + s][1]);
             }
         }
-        uint32_t pb[NT][2], pl[NT][2];
-        const float unscale = exp2_int(-ev), fev = static_cast<float>(ev);
+        // u against the columns' bases as they are; the bases move only in a warp's first block, or
+        // when some u passes 2^10 (f16 ends at 2^16), then to the maximum
+        float u[NT][2][2];  // [column][token gid, gid + 8]
+        const bool whole = kbase + kBlockSize - 1 <= all_see;
+        bool move = k == 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float u[2][2];  // [column][token gid, gid + 8]
-            float alpha[2];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float f = a.scale_log2 * exp2_int(eq[nt][j] + ek);
-                const int lim = colpos[nt][j] - kbase;  // keys up to this one of the block are visible
-                const bool v0 = gid <= lim, v8 = gid + 8 <= lim;
-                const float x0 = st[nt][j] * f, x8 = st[nt][2 + j] * f;
-                float mx = fmaxf(v0 ? x0 : -INFINITY, v8 ? x8 : -INFINITY);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float mn = fmaxf(m[nt][j], mx + fev);
-                const float base = mn == -INFINITY ? 0.f : mn;  // nothing visible so far
-                alpha[j] = fast_exp2(m[nt][j] - base);
-                m[nt][j] = mn;
-                const float off = fev - base;
-                u[j][0] = v0 ? fast_exp2(fmaf(st[nt][j], f, off)) : 0.f;
-                u[j][1] = v8 ? fast_exp2(fmaf(st[nt][2 + j], f, off)) : 0.f;
-                float sum = (u[j][0] + u[j][1]) * unscale;
-                l[nt][j] = l[nt][j] * alpha[j] + sum;
-                if (WEIGHTS) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                    if (gid == j)
-                        a.ws[(((size_t)b * a.num_kv_heads + kvh) * a.max_blocks + entry_at(k)) * (8 * NT) + nt * 8 +
-                             2 * tig + j] = sum > 0.f ? log2f(sum) + base : -INFINITY;
-                }
+                const float f = qf[nt][j] * kscale, off = fev - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+                st[nt][j] = (NT == 1 ? st[0][j] + st[1][j] : st[nt][j]) * f;
+                st[nt][2 + j] = (NT == 1 ? st[0][2 + j] + st[1][2 + j] : st[nt][2 + j]) * f;
+                u[nt][j][0] = fast_exp2(st[nt][j] + off);
+                u[nt][j][1] = fast_exp2(st[nt][2 + j] + off);
             }
+        if (!whole) {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                ot[nt][s][0] *= alpha[0];
-                ot[nt][s][2] *= alpha[0];
-                ot[nt][s][1] *= alpha[1];
-                ot[nt][s][3] *= alpha[1];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int lim = colpos[nt][j] - kbase;  // keys up to this one of the block are visible
+                    if (trow > lim) u[nt][j][0] = 0.f, st[nt][j] = -INFINITY;
+                    if (trow + 8 > lim) u[nt][j][1] = 0.f, st[nt][2 + j] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) move |= !(u[nt][j][0] <= 1024.f) || !(u[nt][j][1] <= 1024.f);
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(st[nt][j], st[nt][2 + j]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float mn = fmaxf(m[nt][j], mx + fev);
+                    const float base = mn == -INFINITY ? 0.f : mn;  // nothing visible so far
+                    const float alpha = fast_exp2(m[nt][j] - base);
+                    l[nt][j] = rescale_sum(l[nt][j], m[nt][j] - base);
+                    m[nt][j] = mn;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        ot[nt][s][j] *= alpha;
+                        ot[nt][s][2 + j] *= alpha;
+                    }
+                    u[nt][j][0] = fast_exp2(st[nt][j] + (fev - base));
+                    u[nt][j][1] = fast_exp2(st[nt][2 + j] + (fev - base));
+                }
+        }
+        uint32_t pb[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float sum[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sum[j] = (u[nt][j][0] + u[nt][j][1]) * unscale;
+                l[nt][j] += sum[j];
+            }
+            if (WEIGHTS) {
+                // over the 8 lanes of a column: lanes of odd gid end with column 1, the others with 0
+                const bool odd = gid & 1;
+                float t = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                if (gid < 2)
+                    a.ws[(((size_t)b * a.num_kv_heads + kvh) * a.max_blocks + entry_at(k)) * (8 * NT) + nt * 8 +
+                         2 * tig + gid] = fast_log2(t) + (odd ? m[nt][1] : m[nt][0]);
             }
             // rows (tokens) x columns (heads) -> transposed: the B operand of the V product
             if constexpr (BITS == 8) {
-                pb[nt][0] = movmatrix_t(pack_f16x2(u[0][0], u[1][0]));
-                pb[nt][1] = movmatrix_t(pack_f16x2(u[0][1], u[1][1]));
+                pb[nt][0] = movmatrix_t(pack_f16x2(u[nt][0][0], u[nt][1][0]));
+                pb[nt][1] = movmatrix_t(pack_f16x2(u[nt][0][1], u[nt][1][1]));
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t hi = pack_bf16x2(u[0][i], u[1][i]);
+                    const uint32_t hi = pack_bf16x2(u[nt][0][i], u[nt][1][i]);
                     pb[nt][i] = movmatrix_t(hi);
-                    pl[nt][i] = movmatrix_t(pack_bf16x2(u[0][i] - bf16_lo(hi), u[1][i] - bf16_hi(hi)));
+                    pl[nt][i] = movmatrix_t(pack_bf16x2(u[nt][0][i] - bf16_lo(hi), u[nt][1][i] - bf16_hi(hi)));
                 }
             }
         }
-        // O^T += V^T u^T: keys 2 tig, 2 tig + 1 (+8); tile rows gid, gid + 8 are neighbouring d
-        constexpr int kVWords = kRowB / 32;  // of each of the lane's four V rows
+        // O^T += V^T u^T: tile rows gid, gid + 8 are neighbouring d
+        constexpr int kVWords = kRowB / 32;  // words of each of the lane's four V rows
         uint32_t vw[4][kVWords];
-        if constexpr (kRowB >= 128) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t from = st_at + (r & 1 ? v_flip : v_off) + (r >> 1) * (8 * kSlotRow);
+            if constexpr (kRowB == 64) {
+                const uint2 p = lds8(from);
+                vw[r][0] = p.x;
+                vw[r][1] = p.y;
+            } else {
 #pragma unroll
                 for (int c = 0; c < Sh::kVChunks; ++c) {
-                    const uint4 p = piece[(2 * Sh::kKChunks + r * Sh::kVChunks + c) * 32];
+                    const uint4 p = lds16(from + c * (kBlockSize * 128));
                     vw[r][4 * c] = p.x;
                     vw[r][4 * c + 1] = p.y;
                     vw[r][4 * c + 2] = p.z;
                     vw[r][4 * c + 3] = p.w;
                 }
-        } else {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint4 p = piece[(2 * Sh::kKChunks + r) * 32];
-                vw[2 * r][0] = p.x;
-                vw[2 * r][1] = p.y;
-                vw[2 * r + 1][0] = p.z;
-                vw[2 * r + 1][1] = p.w;
             }
         }
         if (kbase + kBlockSize > L) {
             // rows past the sequence's end: whatever they hold (NaN times u = 0 is NaN)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (kbase + 2 * tig + (r & 1) + (r >> 1) * 8 >= L) {
+                if (kbase + (vrow ^ (r & 1 ? kNext : 0)) + (r >> 1) * 8 >= L) {
 #pragma unroll
                     for (int w = 0; w < kVWords; ++w) vw[r][w] = 0u;
                 }
@@ -375,24 +501,27 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
         for (int w = 0; w < kVWords; ++w) {
             if constexpr (BITS == 8) {
                 // codes of d, d+1 (then d+2, d+3) paired over keys 2 tig, 2 tig + 1 and over the next 8
-                const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-                const uint32_t hi = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-                const uint32_t lo8 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-                const uint32_t hi8 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-                const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16);
-                const uint32_t a2 = e4m3x2_to_f16x2(lo8 & 0xffffu), a3 = e4m3x2_to_f16x2(lo8 >> 16);
-                const uint32_t c0 = e4m3x2_to_f16x2(hi & 0xffffu), c1 = e4m3x2_to_f16x2(hi >> 16);
-                const uint32_t c2 = e4m3x2_to_f16x2(hi8 & 0xffffu), c3 = e4m3x2_to_f16x2(hi8 >> 16);
+                const uint32_t sel_lo = swapped ? 0x1504u : 0x5140u, sel_hi = swapped ? 0x3726u : 0x7362u;
+                const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel_lo);
+                const uint32_t hi = __byte_perm(vw[0][w], vw[1][w], sel_hi);
+                const uint32_t lo8 = __byte_perm(vw[2][w], vw[3][w], sel_lo);
+                const uint32_t hi8 = __byte_perm(vw[2][w], vw[3][w], sel_hi);
+                uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                e4m3x4_to_f16x4(lo, a0, a1);
+                e4m3x4_to_f16x4(lo8, a2, a3);
+                e4m3x4_to_f16x4(hi, c0, c1);
+                e4m3x4_to_f16x4(hi8, c2, c3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_f16_16816(ot[nt][2 * w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
                     mma_f16_16816(ot[nt][2 * w + 1], c0, c1, c2, c3, pb[nt][0], pb[nt][1]);
                 }
             } else {
-                const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410);
-                const uint32_t a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-                const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410);
-                const uint32_t a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+                const uint32_t sel_lo = swapped ? 0x1054u : 0x5410u, sel_hi = swapped ? 0x3276u : 0x7632u;
+                const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], sel_lo);
+                const uint32_t a1 = __byte_perm(vw[0][w], vw[1][w], sel_hi);
+                const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], sel_lo);
+                const uint32_t a3 = __byte_perm(vw[2][w], vw[3][w], sel_hi);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_16816(ot[nt][w], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -400,20 +529,25 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
                 }
             }
         }
-        // refill the slot just read
         if (at == 31) {  // on to the next 32 blocks
             id = nid;
             ex = nex;
         }
-        const int next = k + Sh::kStages;
-        if (next < n) {
-            // its id is among the current 32, or (its entries not yet moved up) among the next
-            const bool ahead = (next >> 5) != ((k + 1) >> 5);
-            issue(next, __shfl_sync(0xffffffffu, ahead ? nid : id, next & 31));
-        }
-        cp_async_commit();
+        // refill the slot: the block's id is among the current 32, or (entries not yet moved up) the next
+        const int next = k + kStages;
+        const int next_id = __shfl_sync(0xffffffffu, (next >> 5) != ((k + 1) >> 5) ? nid : id, next & 31);
+        __syncwarp();  // every lane has its pieces
+        if (next < n && lane == 0) issue(slot, next_id);
+        if (++slot == kStages) slot = 0, parity ^= 1;
     }
-    cp_async_wait<0>();
+    if (!ok) {
+        // a wait ran out: the copies in flight must still land before their memory is used again
+        for (int left = min(n - k, kStages); left > 0; --left) {
+            mbar_wait_warp(&full[slot], parity);
+            if (++slot == kStages) slot = 0, parity ^= 1;
+        }
+        if (lane == 0) atomicOr(a.status, kDevTimeout);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -469,13 +603,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float* pm = part + w * Sh::kPart;
-            const float wt = pm[col] == -INFINITY ? 0.f : fast_exp2(pm[col] - M);
+            if (pm[col] == -INFINITY) continue;
+            const float wt = fast_exp2(pm[col] - M);
             const float4 v = *reinterpret_cast<const float4*>(pm + 32 + col * Sh::kRow + 4 * quad_at(grp));
             acc.x += wt * v.x;
             acc.y += wt * v.y;
             acc.z += wt * v.z;
             acc.w += wt * v.w;
-            den += wt * pm[16 + col];
+            den += rescale_sum(pm[16 + col], pm[col] - M);
         }
         if (sub == 1) store(qd, acc, den > 0.f ? 1.f / den : 0.f);
         *reinterpret_cast<float4*>(cta + 32 + col * Sh::kRow + 4 * grp) = acc;
@@ -508,9 +643,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
             for (int r = 0; r < sub; ++r) M = fmaxf(M, wgt[r * 16 + col]);
             for (int r = 0; r < sub; ++r) {
                 const float mr = wgt[r * 16 + col];
-                const float w = mr == -INFINITY ? 0.f : fast_exp2(mr - M);
-                wgt[r * 16 + col] = w;
-                den += w * lsum[r * 16 + col];
+                wgt[r * 16 + col] = mr == -INFINITY ? 0.f : fast_exp2(mr - M);
+                if (mr != -INFINITY) den += rescale_sum(lsum[r * 16 + col], mr - M);
             }
             col_m[col] = M;
             col_l[col] = den;
@@ -534,16 +668,20 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(BITS, D, NT))
     }
     if (WEIGHTS) {
         // this CTA's blocks: the columns' shares of the whole sequence's weight, added up
+        float* lse = part + 576;  // log2 of a column's whole sum of 2^x; a NaN column adds nothing
+        if (threadIdx.x < R) {
+            const float den = col_l[threadIdx.x];
+            lse[threadIdx.x] = den > 0.f ? col_m[threadIdx.x] + log2f(den) : INFINITY;
+        }
+        __syncthreads();
         const int own = nb > rank * kWarps ? nb - rank * kWarps : 0;
         for (int t = threadIdx.x; t < (own + stride - 1) / stride * kWarps; t += kThreads) {
             const int blk = rank * kWarps + t % kWarps + t / kWarps * stride;
             if (blk >= nb) continue;
             const float* lb = a.ws + (((size_t)b * a.num_kv_heads + kvh) * a.max_blocks + blk) * (8 * NT);
             float sum = 0.f;
-            for (int col = 0; col < R; ++col) {
-                const float den = col_l[col];
-                if (den > 0.f) sum += fast_exp2(lb[col] - col_m[col]) / den;
-            }
+            for (int col = 0; col < R; ++col)
+                if (lse[col] < INFINITY) sum += fast_exp2(lb[col] - lse[col]);
             float* w = a.weights + ((size_t)b * a.num_kv_heads + kvh) * a.max_blocks + blk;
             *w = *w * a.decay + sum;
         }
@@ -557,13 +695,14 @@ struct LanesPool {
     int num_blocks, num_kv_heads, head_dim;
 };
 
-template <int BITS, int D, int NT, bool MQ, bool WEIGHTS>
-cudaError_t launch_one(const LanesPool& pool, const AttnArgs& a, int splits, cudaStream_t stream) {
+template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, bool WIDE>
+cudaError_t launch_as(const LanesPool& pool, const AttnArgs& a, int splits, cudaStream_t stream) {
     using Sh = Lanes<BITS, D>;
-    auto kern = decode_lanes_kernel<BITS, D, NT, MQ, WEIGHTS>;
+    auto kern = decode_lanes_kernel<BITS, D, NT, MQ, WEIGHTS, WIDE>;
+    constexpr int kWarps = warps_of(BITS, D, NT, WIDE);
     static OncePerDevice configured;  // per instantiation
     cudaError_t se = configured.run([&] {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::smem(kWarps, ctas_of(WIDE)));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return e;
@@ -588,10 +727,16 @@ cudaError_t launch_one(const LanesPool& pool, const AttnArgs& a, int splits, cud
     d.group = a.num_heads / pool.num_kv_heads;
     d.scale_log2 = a.scale * kLog2e;
     d.decay = a.decay;
+    PlaneMaps maps = {};
+    if (!plane_maps(&maps, pool.k, pool.v, (long long)pool.num_blocks * pool.num_kv_heads * kBlockSize,
+                                Sh::kRowBytes))
+        return cudaErrorInvalidValue;
+    d.paired = maps.paired;
+    d.k_second = maps.k_second;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, pool.num_kv_heads, a.batch);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = Sh::smem(kWarps, ctas_of(WIDE));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
     cfg.attrs = attr;
@@ -603,17 +748,84 @@ cudaError_t launch_one(const LanesPool& pool, const AttnArgs& a, int splits, cud
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, kern, d);
+    return cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, d);
+}
+
+// How many clusters of `splits` CTAs (four an SM, or two wide ones) the device runs at once; asked
+// once per device.
+int cluster_capacity(bool wide, int splits) {
+    static std::atomic<int> cached[64][2][17];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (const int c = cached[dev][wide][splits].load(std::memory_order_relaxed)) return c - 1;
+    const auto ask = [&](auto kern, int warps, int smem) {
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess ||
+            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(splits * 64);
+        cfg.blockDim = dim3(warps * 32);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = splits;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
+    };
+    using Sh = Lanes<8, 128>;
+    const int n = wide ? ask(decode_lanes_kernel<8, 128, 1, false, false, true>, 8, Sh::smem(8, 2))
+                       : ask(decode_lanes_kernel<8, 128, 1, false, false, false>, 4, Sh::smem(4, 4));
+    cudaGetLastError();
+    cached[dev][wide][splits].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+struct Split {
+    int splits;
+    bool wide;
+};
+
+// Splits of every (sequence, kv head), as CTAs of a cluster.  Measured on GB300, us a call:
+//   * as many as run at once: 16 x ~4000 tokens, 8 kv heads (128 items) 24 at 4 splits against 33 at
+//     1; one cluster too many costs a second wave (32 items: wide at 8 splits 16, at 9 23);
+//   * but at least ten blocks a warp once every SM has a CTA: 30 x 1000 (240 items) 13.9 at 1,
+//     15.4 at 2; 24 x ~1500 21.9 at 1, 17.5 at 3;
+//   * wide where even 16 splits leave room, at four blocks a warp: 1 x 32768 (8 items) 20.7 wide at
+//     12 splits, 25.9 at 16 of the others; 4 x 8192 15.9 wide at 8, 17.2;
+//   * two in a grid of over three CTAs an SM with long sequences, whose CTAs end far apart: 64 x 8192
+//     152 against 159, but 64 x 2048 47 against 44.
+Split split_for(int batch, int num_kv_heads, int max_blocks, int warps) {
+    const int items = batch * num_kv_heads, sms = device_info().num_sms;
+    if (items >= 3 * sms) return {max_blocks >= 320 ? 2 : 1, false};
+    if (items <= cluster_capacity(false, 16)) {
+        int s = 12;
+        while (s > 1 && items > cluster_capacity(true, s)) --s;
+        if (s > 1 && max_blocks >= 4 * s * 2 * warps) return {s, true};
+    }
+    const int least = items >= sms ? 10 * warps : 4;  // blocks of a CTA
+    int s = std::min(16, std::max(1, max_blocks / least));
+    while (s > 1 && items > cluster_capacity(false, s)) --s;
+    return {s, false};
+}
+
+template <int BITS, int D, int NT, bool MQ, bool WEIGHTS>
+cudaError_t launch_one(const LanesPool& pool, const AttnArgs& a, cudaStream_t stream) {
+    const Split s = split_for(a.batch, pool.num_kv_heads, a.max_blocks, warps_of(BITS, D, NT, false));
+    return s.wide ? launch_as<BITS, D, NT, MQ, WEIGHTS, true>(pool, a, s.splits, stream)
+                  : launch_as<BITS, D, NT, MQ, WEIGHTS, false>(pool, a, s.splits, stream);
 }
 
 template <int BITS, bool MQ, bool WEIGHTS>
 cudaError_t dispatch(const LanesPool& pool, const AttnArgs& a, int columns, cudaStream_t stream) {
-    const int splits = decode_splits_for(a.batch, pool.num_kv_heads, a.max_blocks);
     if (pool.head_dim == 128)
-        return columns > 8 ? launch_one<BITS, 128, 2, MQ, WEIGHTS>(pool, a, splits, stream)
-                           : launch_one<BITS, 128, 1, MQ, WEIGHTS>(pool, a, splits, stream);
-    return columns > 8 ? launch_one<BITS, 64, 2, MQ, WEIGHTS>(pool, a, splits, stream)
-                       : launch_one<BITS, 64, 1, MQ, WEIGHTS>(pool, a, splits, stream);
+        return columns > 8 ? launch_one<BITS, 128, 2, MQ, WEIGHTS>(pool, a, stream)
+                           : launch_one<BITS, 128, 1, MQ, WEIGHTS>(pool, a, stream);
+    return columns > 8 ? launch_one<BITS, 64, 2, MQ, WEIGHTS>(pool, a, stream)
+                       : launch_one<BITS, 64, 1, MQ, WEIGHTS>(pool, a, stream);
 }
 
 LanesPool lanes_pool(const Pool8View& p) {

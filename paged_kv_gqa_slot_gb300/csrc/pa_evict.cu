@@ -7,12 +7,16 @@
 // leave, so no K or V moves, the pool is only ever read by others, and a block that several
 // sequences share is dropped from one table only.
 //
-// A few KB per sequence: latency is all there is.  One CTA per sequence sums the heads into
-// order-preserving 32-bit keys in shared memory, finds the e-th smallest by four 8-bit radix
-// passes, ranks ties and survivors with two block scans, and gathers through the resulting
-// source list.  W_j is summed in 64 bits and rounded once, so it does not depend on the order
-// of the heads.  Every source index is >= its destination and the gather runs in ascending
-// tiles, each read before it is written, so outputs may be their inputs.
+// A few KB per sequence: latency is all there is.  One CTA per sequence copies its rows into
+// shared memory (while they fit; else it reads them twice), sums the heads into
+// order-preserving 32-bit keys, which its threads keep in registers, finds the e-th smallest by
+// bisection -- two bits a round, a count and one barrier each, which beat radix histograms,
+// whose shared-memory atomics pile up on the few exponents that weights have -- ranks ties and
+// survivors with two block scans, and gathers through the resulting source list.  W_j is summed
+// in 64 bits and rounded once, so it does not depend on the order of the heads.  Rows in shared
+// memory are read whole before any output is written; the others are gathered in
+// ascending tiles, each read before it is written, from sources at or past it: outputs may be
+// their inputs.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -21,8 +25,8 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kFewBlocks = 256;    // tables up to this width: 128 threads, else 1024
+constexpr int kResident = 200 * 1024;  // bytes of rows and keys a CTA keeps in shared memory
 
 // float order as unsigned order; -0 as +0, NaN below everything
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -31,8 +35,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive sum of v over the block's threads in order; `total` is the sum of all.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+// Exclusive sum of v over the block's threads in order.
+template <int T>
+__device__ __forceinline__ int block_scan(int v, int* warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = v;
 #pragma unroll
@@ -43,30 +48,40 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     __syncthreads();  // warp_sums may still be read from the call before
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const int s = warp_sums[w];
-        before += w < warp ? s : 0;
-        total += s;
-    }
-    return before + incl - v;
+    const int below = lane < warp ? warp_sums[lane] : 0;  // at most 32 warps
+    return __reduce_add_sync(0xffffffffu, below) + incl - v;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__ EvictArgs a) {
-    extern __shared__ uint32_t src[];  // keys first, then the source index of every new entry
-    __shared__ int hist[256];
-    __shared__ int warp_sums[kWarps];
-    __shared__ uint32_t s_prefix;
-    __shared__ int s_left;
+template <int T>
+__global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictArgs a, int resident) {
+    extern __shared__ uint32_t src[];  // keys, then the source index of every new entry
+    __shared__ int warp_sums[32];
+    __shared__ int counts[2][3];
     const int b = blockIdx.x, width = a.max_blocks, tid = threadIdx.x;
-    const int lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
     const int32_t* table = a.tables + (size_t)b * width;
     const float* weights = a.weights + (size_t)b * a.num_kv_heads * width;
     int L = a.seq_lens[b];
+    if (resident) {
+        float* rows = reinterpret_cast<float*>(src + width);
+        int32_t* ids = reinterpret_cast<int32_t*>(rows + a.num_kv_heads * width);
+        const int cells = a.num_kv_heads * width;
+        int i = tid;
+        for (; i + 7 * T < cells; i += 8 * T) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = weights[i + k * T];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) rows[i + k * T] = v[k];
+        }
+        for (; i < cells; i += T) rows[i] = weights[i];
+        for (int j = tid; j < width; j += T) ids[j] = table[j];
+        weights = rows;
+        table = ids;
+    }
+    if (tid < 6) (&counts[0][0])[tid] = 0;
+    __syncthreads();
     if (L < 0 || L > width * kBlockSize) {
         if (tid == 0) atomicOr(a.status, kDevOutOfRange);
         L = L < 0 ? 0 : width * kBlockSize;
@@ -75,58 +90,60 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     const int e = max(0, nb - a.keep);
     const int lo = a.sink, hi = nb - a.recent;  // candidates [lo, hi): at least e of them, as sink + recent <= keep
 
-    // this thread's run of entries
-    const int per = (width + kThreads - 1) / kThreads;
-    const int j0 = min(width, tid * per), j1 = min(width, j0 + per);
     if (e > 0) {
-        for (int j = lo + tid; j < hi; j += kThreads) {
+        for (int j = lo + tid; j < hi; j += T) {
             double w = 0.0;
+#pragma unroll 8
             for (int h = 0; h < a.num_kv_heads; ++h) w += (double)weights[(size_t)h * width + j];
             src[j] = order_key((float)w);
         }
-        // the e-th smallest key, a digit at a time: `prefix` its upper digits, `left` how many of
-        // the keys that share them still leave
-        uint32_t prefix = 0;
-        int left = e;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-            __syncthreads();
-            for (int j = lo + tid; j < hi; j += kThreads) {
-                const uint32_t key = src[j];
-                if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[key >> shift & 255u], 1);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                int v[8], sum = 0;
+        __syncthreads();
+        // The e-th smallest key T: the largest value with fewer than e keys below it, two bits at a
+        // time.  `left` of the keys equal to it leave too.  A thread keeps up to 4 keys at hand.
+        constexpr int kHand = 4;
+        uint32_t hand[kHand];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += v[i] = hist[lane * 8 + i];
-                int incl = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += up;
-                }
-                int below = incl - sum;
-                if (below < left && left <= incl) {  // the digit is one of this lane's
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (below < left && left <= below + v[i]) {
-                            s_prefix = prefix | (uint32_t)(lane * 8 + i) << shift;
-                            s_left = left - below;
-                        }
-                        below += v[i];
-                    }
-                }
-            }
-            __syncthreads();
-            prefix = s_prefix;
-            left = s_left;
+        for (int i = 0; i < kHand; ++i) {
+            const int j = lo + tid + i * T;
+            hand[i] = j < hi ? src[j] : 0xffffffffu;  // counts as below no trial value
         }
-        // keys below `prefix` leave, and the first `left` equal to it
+        uint32_t prefix = 0;
+        int below = 0;  // keys below prefix
+        for (int shift = 30, round = 0; shift >= 0; shift -= 2, ++round) {
+            // keys below prefix + 1, 2, 3 steps
+            int c[3] = {0, 0, 0};
+            const auto count = [&](uint32_t key) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) c[i] += key < (prefix | ((uint32_t)(i + 1) << shift));
+            };
+#pragma unroll
+            for (int i = 0; i < kHand; ++i) count(hand[i]);
+            for (int j = lo + tid + kHand * T; j < hi; j += T) count(src[j]);
+            int* to = counts[round & 1];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int sum = __reduce_add_sync(0xffffffffu, c[i]);
+                if ((tid & 31) == i && sum) atomicAdd(&to[i], sum);
+            }
+            __syncthreads();
+            int digit = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (to[i] < e) {
+                    digit = i + 1;
+                    below = to[i];
+                }
+            prefix |= (uint32_t)digit << shift;
+            if (tid < 3) counts[(round + 1) & 1][tid] = 0;
+            __syncthreads();
+        }
+        const int left = e - below;
+        // this thread's run of entries
+        const int per = (width + T - 1) / T;
+        const int j0 = min(width, tid * per), j1 = min(width, j0 + per);
         int ties = 0;
         for (int j = j0; j < j1; ++j) ties += j >= lo && j < hi && src[j] == prefix;
-        int total;
-        int tie = block_scan(ties, warp_sums, total);
+        int tie = block_scan<T>(ties, warp_sums);
         int gone = 0;
         for (int j = j0; j < j1; ++j) {
             const bool cand = j >= lo && j < hi;
@@ -136,26 +153,22 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
             gone += out;
             src[j] = out ? 1u : 0u;
         }
-        int before = block_scan(gone, warp_sums, total);
-        // evicted entries in order; the survivors' source list is built in place: entry
-        // j - before <= j, and no thread's run is overwritten before it is read (the sync below)
-        uint32_t out_bits[(kEvictMaxBlocks / kThreads + 31) / 32];
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof out_bits / 4); ++i) out_bits[i] = 0u;
+        int before = block_scan<T>(gone, warp_sums);
+        // the survivors' source list, in place: entry j - before <= j, which may lie in another
+        // thread's run, so the flags move to registers first
+        uint32_t flags[(kEvictMaxBlocks / 1024 + 31) / 32] = {};
         for (int j = j0; j < j1; ++j) {
-            const int i = j - j0;
 #pragma unroll
-            for (int w = 0; w < (int)(sizeof out_bits / 4); ++w)
-                if (i >> 5 == w) out_bits[w] |= src[j] << (i & 31);
+            for (int w = 0; w < (int)(sizeof flags / 4); ++w)
+                if ((j - j0) >> 5 == w) flags[w] |= src[j] << ((j - j0) & 31);
         }
         __syncthreads();
         for (int j = j0; j < j1; ++j) {
-            const int i = j - j0;
             uint32_t bits = 0;
 #pragma unroll
-            for (int w = 0; w < (int)(sizeof out_bits / 4); ++w)
-                if (i >> 5 == w) bits = out_bits[w];
-            if (bits >> (i & 31) & 1u) {
+            for (int w = 0; w < (int)(sizeof flags / 4); ++w)
+                if ((j - j0) >> 5 == w) bits = flags[w];
+            if (bits >> ((j - j0) & 31) & 1u) {
                 a.evicted[(size_t)b * width + before] = table[j];
                 ++before;
             } else {
@@ -164,16 +177,16 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
         }
         __syncthreads();
     }
-    for (int j = e + tid; j < width; j += kThreads) a.evicted[(size_t)b * width + j] = -1;
+    for (int j = e + tid; j < width; j += T) a.evicted[(size_t)b * width + j] = -1;
     if (tid == 0) {
         a.num_evicted[b] = e;
         a.seq_lens_out[b] = L - kBlockSize * e;
     }
-    // close up: ascending tiles, read before written
+    // close up
     int32_t* table_out = a.tables_out + (size_t)b * width;
     float* weights_out = a.weights_out + (size_t)b * a.num_kv_heads * width;
-    const bool in_place = a.tables_out == a.tables || a.weights_out == a.weights;
-    for (int i0 = 0; i0 < width; i0 += kThreads) {
+    const bool in_place = !resident && (a.tables_out == a.tables || a.weights_out == a.weights);
+    for (int i0 = 0; i0 < width; i0 += T) {
         const int i = i0 + tid;
         const bool in = i < width, kept = i < width - e;
         const int from = kept ? (e > 0 ? (int)src[i] : i) : 0;
@@ -193,23 +206,30 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     }
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream) {
+template <int T>
+cudaError_t launch(const EvictArgs& a, int batch, cudaStream_t stream) {
     static OncePerDevice configured;
     const cudaError_t e = configured.run([] {
-        return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxBlocks * 4);
+        return cudaFuncSetAttribute(evict_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kResident);
     });
     if (e != cudaSuccess) return e;
+    const long long all = (long long)a.max_blocks * (a.num_kv_heads + 2) * 4;
+    const int resident = all <= kResident;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(batch);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)a.max_blocks * 4;
+    cfg.blockDim = dim3(T);
+    cfg.dynamicSmemBytes = resident ? (size_t)all : (size_t)a.max_blocks * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<T>, a, resident);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream) {
+    return a.max_blocks <= kFewBlocks ? launch<128>(a, batch, stream) : launch<1024>(a, batch, stream);
 }
 
 }  // namespace pa

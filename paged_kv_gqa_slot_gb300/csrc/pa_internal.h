@@ -93,6 +93,15 @@ const DeviceInfo& device_info();
 // 3-D TMA map (d, head, token) over a [tokens, heads, d] bf16 tensor (d = 128), 128-byte
 // swizzled, box (64, box_heads, box_tokens); false if it cannot be encoded.
 bool rows_map(CUtensorMap* out, const void* base, long long tokens, int heads, int d, int box_heads, int box_tokens);
+// TMA maps of a pool's K and V for boxes of one whole (block, head) tile: rows of 64 bytes (64-byte
+// swizzle), of 128 (128-byte swizzle), or of 256 as two such halves.  paired: `k` brings K and V in one box, as the
+// two planes of one tensor whose plane stride is the distance of the pools (K the second plane
+// when V lies first); else a box each.  False if they cannot be encoded.
+struct PlaneMaps {
+    CUtensorMap k, v;
+    int paired, k_second;
+};
+bool plane_maps(PlaneMaps* out, const void* k, const void* v, long long rows, int row_bytes);
 unsigned* device_status_ptr();
 
 // One-time set-up of a kernel (function attributes, occupancy queries) on each device:

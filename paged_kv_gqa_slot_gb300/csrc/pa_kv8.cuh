@@ -34,19 +34,23 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return min(max(k, kExpMin), kExpMax);
 }
 
-// Two e4m3 codes as f16 (exact; a NaN code gives NaN).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair16) {
-    uint32_t d;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(pair16));
-    return d;
+// The four e4m3 codes of a word as f16 pairs: lo the two low bytes, hi the others (exact; a NaN
+// code gives NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
-// lo and hi rounded to nearest even e4m3 (magnitudes past 448 saturate, NaN stays NaN).
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+// Four values rounded to nearest even e4m3, lowest byte first (magnitudes past 448 saturate, NaN
+// stays NaN).
+__device__ __forceinline__ uint32_t to_e4m3x4(float x0, float x1, float x2, float x3) {
     uint32_t d;
-    asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}"
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
         : "=r"(d)
-        : "f"(lo), "f"(hi));
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
     return d;
 }
 
@@ -59,14 +63,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The four codes of a word times `s` as four bf16 (two packed words).  With s = 2^k of an
-// 8-bit pool the products are bf16 numbers, so nothing is rounded.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, float s) {
-    const float2 a = f16x2_to_float2(e4m3x2_to_f16x2(w & 0xffffu));
-    const float2 b = f16x2_to_float2(e4m3x2_to_f16x2(w >> 16));
-    return make_uint2(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(b.x * s, b.y * s));
-}
-
 // D[16x8] += A[16x16] * B[16x8], f16 in, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -74,20 +70,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Asynchronous copies of 16 (around L1) or 8 bytes into shared memory, completion in groups
-// that the issuing thread commits and waits for.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 }  // namespace pa

@@ -109,39 +109,48 @@ __device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pr
     using P = Pre8<D>;
     const int lane = threadIdx.x & 31;
     const int total = 2 * nst * kParts;
-    uint4 codes[P::kLoads];
-    const auto load = [&](int u) {
+    // entries of blocks c0 + lane and the 32 after them; units walk the blocks of K one stage ahead
+    // of V's, and the loads run up to kAhead units ahead of that
+    constexpr int kAhead = 3;
+    uint4 codes[kAhead][P::kLoads];
+    int c0 = 0;
+    const auto entry = [&](int blk) -> int {
+        if (blk >= nblk) return -1;
+        const int id = __ldg(bt + blk);
+        if (id >= 0 && id < a.num_blocks) return id;
+        atomicOr(a.status, kDevOutOfRange);
+        return 0;  // read inside the pool; the status word reports the bad id
+    };
+    int cur = entry(lane), nxt = entry(32 + lane);
+    const auto load = [&](uint4 (&to)[P::kLoads], int u) {
         const Unit n = unit_of(u, nst);
         const int lb = n.stage * kParts + n.part;
 #pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) codes[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (lb >= nblk) return;  // past the keys the tile needs: zeros
-        int id = __ldg(bt + lb);
-        if (id < 0 || id >= a.num_blocks) {
-            if (lane == 0) atomicOr(a.status, kDevOutOfRange);
-            id = 0;
+        for (int i = 0; i < P::kLoads; ++i) to[i] = make_uint4(0u, 0u, 0u, 0u);
+        // V units trail, so the window moves on once V has left it
+        if (n.is_v && lb >= c0 + 32) {
+            c0 += 32;
+            cur = nxt;
+            nxt = entry(c0 + 32 + lane);
         }
+        const int id = __shfl_sync(0xffffffffu, lb < c0 + 32 ? cur : nxt, lb & 31);
+        if (id < 0) return;  // past the keys the tile needs: zeros
         const size_t tile = ((size_t)id * a.num_kv_heads + kvh) * (kBlockSize * D);
         const uint4* src = reinterpret_cast<const uint4*>((n.is_v ? a.v : a.k) + tile) + lane;
 #pragma unroll
         for (int i = 0; i < P::kLoads; ++i) {
             // V rows past the sequence's end count as zeros (u is 0 there, but 0 times NaN is NaN)
             const int row = (i * 32 + lane) / (D / 16);
-            if (!n.is_v || lb * kBlockSize + row < L) codes[i] = __ldg(src + i * 32);
+            if (!n.is_v || lb * kBlockSize + row < L) to[i] = __ldg(src + i * 32);
         }
     };
     bool ok = true;
-    if (w < total) load(w);
-    for (int u = w; u < total; u += kCvtWarps) {
+    const auto store = [&](const uint4 (&from)[P::kLoads], int u) {
         const Unit n = unit_of(u, nst);
-        uint4 now[P::kLoads];
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) now[i] = codes[i];
-        if (u + kCvtWarps < total) load(u + kCvtWarps);
         const int nslots = n.is_v ? kVStages : kKStages, slot = n.stage % nslots;
         uint64_t* empty = n.is_v ? bars->v_empty : bars->k_empty;
         if (n.stage >= nslots) ok = mbar_wait_warp(&empty[slot], ((n.stage / nslots) & 1) ^ 1);
-        if (!ok) break;
+        if (!ok) return;
         uint8_t* dst = smem + (n.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + n.part * (kBlockSize * 128);
 #pragma unroll
         for (int i = 0; i < P::kLoads; ++i) {
@@ -149,11 +158,12 @@ __device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pr
             // store them in the other order, so that the lanes of one row hit different banks
             const int piece = i * 32 + lane, row = piece / (D / 16), c = piece % (D / 16);
             const int h = c >> 2, ch = (c & 3) * 2;
-            const auto half2 = [&](uint32_t x, uint32_t y) {
-                return make_uint4(e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y & 0xffffu),
-                                  e4m3x2_to_f16x2(y >> 16));
-            };
-            const uint4 lo = half2(now[i].x, now[i].y), hi = half2(now[i].z, now[i].w);
+            const uint4 now = from[i];
+            uint4 lo, hi;
+            e4m3x4_to_f16x4(now.x, lo.x, lo.y);
+            e4m3x4_to_f16x4(now.y, lo.z, lo.w);
+            e4m3x4_to_f16x4(now.z, hi.x, hi.y);
+            e4m3x4_to_f16x4(now.w, hi.z, hi.w);
             uint8_t* at = dst + h * P::kKVHalf;
             *reinterpret_cast<uint4*>(at + swz128(row, ch + h)) = h ? hi : lo;
             *reinterpret_cast<uint4*>(at + swz128(row, ch + 1 - h)) = h ? lo : hi;
@@ -161,7 +171,18 @@ __device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pr
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(n.is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (w + i * kCvtWarps < total) load(codes[i], w + i * kCvtWarps);
+    for (int u0 = w; u0 < total && ok; u0 += kAhead * kCvtWarps)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int u = u0 + i * kCvtWarps;
+            if (u >= total || !ok) break;
+            store(codes[i], u);
+            if (u + kAhead * kCvtWarps < total) load(codes[i], u + kAhead * kCvtWarps);
+        }
     if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
 }
 
@@ -369,12 +390,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
         const int pos = valid ? L - C + qi : -1;  // last key the row sees
         const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
         // exponents of blocks c0 + lane: a word a lane, the next 32 read ahead
-        const auto exps_at = [&](int blk) -> int {
+        const auto entry = [&](int blk) { return blk < nblk ? __ldg(bt + blk) : -1; };
+        const auto exps_of = [&](int blk, int id) -> int {
             if (blk >= nblk) return kExpBias * 257;
-            const int id = __ldg(bt + blk);
             return __ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh);
         };
-        int ex = exps_at(lane), next_ex = 0;
+        int ex = exps_of(lane, entry(lane)), next_id = entry(32 + lane), next_ex = 0;
         int eq;
         {
             // the row of q, normalised, into the swizzled layout (zeros past the chunk); a
@@ -411,7 +432,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
         // tcgen05.ld / st are warp-collective: what leads to one is decided by the whole warp
         for (int j = 0; j < nst; ++j) {
             const int at = (j * kParts) & 31;
-            if (at == 0 && j > 0) ex = next_ex;
+            if (at == 0 && j > 0) {
+                ex = next_ex;
+                next_id = entry(j * kParts + 32 + lane);
+            }
             StageScales sc;
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
@@ -419,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
                 sc.f[i] = sl * exp2_int(eq + (e & 255) - kExpBias);
                 sc.kv[i] = static_cast<float>((e >> 8) - kExpBias);
             }
-            if (at == 0) next_ex = exps_at(j * kParts + 32 + lane);
+            if (at == 16) next_ex = exps_of(j * kParts + 16 + lane, next_id);
             const uint32_t buf = tm + kTmemS + 64 * (j & 1);
             ok = mbar_wait_warp(&bars->s_full[j & 1], (j >> 1) & 1);
             if (!ok) break;
@@ -455,7 +479,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
                     scale_o<D>(tm + kTmemO, f);
                 }
                 if (move) {
-                    l *= f;
+                    // in two steps: l, whose terms carry 2^-kV, may count where f alone is zero
+                    if (rescale) {
+                        const float h = fast_exp2(0.5f * (base - top));
+                        l = l * h * h;
+                    }
                     base = top;
                 }
                 weigh(lsum);
