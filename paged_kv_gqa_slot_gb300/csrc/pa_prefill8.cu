@@ -3,9 +3,9 @@
 //
 // Query i of sequence s's chunk of C_s tokens sits at position L_s - C_s + i and attends causally
 // to keys 0 .. that position.  The (query, head of the group) pairs of a (sequence, kv head)
-// are the rows r = i g + h of its query tiles, 128 to a tile, whatever g is.  One CTA holds
-// one tile, two CTAs share an SM (256 columns of tensor memory each), and the longest
-// tiles launch first.
+// are the rows r = i g + h of its query tiles, 128 to a tile, whatever g is.  One CTA an SM
+// holds two tiles (one where that leaves SMs empty), which share every K and V it widens, and
+// the CTAs with the most keys launch first.
 //
 // Arithmetic: f16 operands and fp32 sums, as in pa_decode_lanes.cu.  A code is an f16 number, so K and V
 // widen with one conversion per two codes and no multiplication; q is brought to a maximum in
@@ -16,17 +16,18 @@
 // second part even where a few weights dominate a row.
 //
 // Per stage of 64 keys (four pool blocks):
-//   warps 5-7  read codes, 16 bytes a lane, widen them and store them in the 128-byte swizzled
-//              layout of the MMA operands (rows past the sequence's end as zeros); a unit is one
-//              block's K or V, units go to the three warps in turn, K one stage ahead of V, and a
-//              warp's next unit is loaded before it waits for the slot of the one in hand
-//   warp 4     S[128 x 64] = Q K^T into one of two 64-column buffers, O[128 x D] += u V with u
-//              from tensor memory; per stage u V(j), then S(j + 2), which reuses u(j)'s buffer
-//   warps 0-3  softmax, one row a thread: reads S, writes u over it.  The base is set by a row's
-//              first visible stage and moves only when a stage's sum passes 2^15 (f16 ends at
-//              2^16), then to the maximum, if that is more than 2^8 above; O is rescaled in
-//              tensor memory by all rows of a warp together.
-// At the end all eight warps normalise and store, a quarter of the rows and half the columns each.
+//   warp 9       copies the codes, a contiguous 1 or 2 KB a block, into a ring of raw tiles
+//   warps 10-15  widen them into the 128-byte swizzled layout of the MMA operands (rows past the
+//                sequence's end as zeros); a unit is one block's K or V, units go to the six
+//                warps in turn, K one stage ahead of V
+//   warp 8       per tile, S[128 x 64] = Q K^T into one of two 64-column buffers and
+//                O[128 x D] += u V with u from tensor memory; per stage u V(j), then S(j + 2), which
+//                reuses u(j)'s buffer, of the one tile while the other's softmax runs
+//   warps 0-7    softmax, one row a thread: reads S, writes u over it.  The base is set by a row's
+//                first visible stage and moves only when a stage's sum passes 2^15 (f16 ends at
+//                2^16), then to the maximum, if that is more than 2^8 above; O is rescaled in
+//                tensor memory by all rows of a warp together.
+// At the end all warps normalise, stage the rows in the free Q buffer and store them coalesced.
 #include <algorithm>
 #include <cmath>
 
@@ -39,11 +40,12 @@ namespace {
 constexpr int kRows = 128;                 // MMA M: rows of a query tile
 constexpr int kKeys = 64;                  // keys of a stage
 constexpr int kParts = kKeys / kBlockSize;  // pool blocks of a stage
-constexpr int kKStages = 3, kVStages = 2;
-constexpr int kMmaWarp = 4, kCvtWarp = 5, kCvtWarps = 3;
-constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 2;
-constexpr int kTmemCols = 256;
+constexpr int kKStages = 3, kVStages = 3;
+constexpr int kRawGroups = 4;              // raw ring, in groups of K or V of one stage
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kCvtWarp = 10, kCvtWarps = 6;
+constexpr int kThreads = 512;
+constexpr int kTmemCols = 512;             // per tile: two 64-column score buffers, then O
+constexpr uint32_t kTmemTile = 256;
 constexpr uint32_t kTmemS = 0, kTmemO = 128;
 constexpr float kSumLimit = 32768.f;      // a stage sum of u past this takes the maximum path
 constexpr float kRebase = 8.f;            // log2 units a maximum must exceed the base by to move it
@@ -53,24 +55,28 @@ template <int D>
 struct Pre8 {
     static constexpr int kHalves = D / 64;            // 64-column (128-byte) pieces of a row
     static constexpr int kQHalf = kRows * 128;
+    static constexpr int kQTile = kHalves * kQHalf;
     static constexpr int kKVHalf = kKeys * 128;
     static constexpr int kStage = kHalves * kKVHalf;  // K or V of a stage
-    static constexpr int kOffK = kHalves * kQHalf;
+    static constexpr int kRawBlock = kBlockSize * D;  // one block's codes of K or V
+    static constexpr int kRawGroup = kParts * kRawBlock;
+    static constexpr int kOffK = 2 * kQTile;
     static constexpr int kOffV = kOffK + kKStages * kStage;
-    static constexpr int kOffBars = kOffV + kVStages * kStage;
-    static constexpr int kOffInv = kOffBars + 256;     // [128] 1 / l, then whether every wait ended
-    static constexpr int kSmem = kOffInv + kRows * 4 + 16;
+    static constexpr int kOffRaw = kOffV + kVStages * kStage;
+    static constexpr int kOffBars = kOffRaw + kRawGroups * kRawGroup;
+    static constexpr int kOffInv = kOffBars + 512;     // [2][128] 1 / l, then whether every wait ended
+    static constexpr int kSmem = kOffInv + 2 * kRows * 4 + 16;
     static constexpr int kLoads = kBlockSize * D / 512;  // 16-byte pieces of a block a lane takes
 };
-static_assert(kCtasPerSm * (Pre8<128>::kSmem + 1024) <= 228 * 1024, "shared memory of two resident CTAs");
-static_assert(kCtasPerSm * kTmemCols <= 512, "tensor memory of two resident CTAs");
+static_assert(Pre8<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct Bars8 {
+    uint64_t raw_full[kRawGroups], raw_empty[kRawGroups];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t q_full, s_full[2], p_full[2], o_done, o_final, drain;
+    uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2], o_final[2], drain;  // [tile][buffer]
     uint32_t tmem_base;
 };
-static_assert(sizeof(Bars8) <= 256, "barrier block");
+static_assert(sizeof(Bars8) <= 512, "barrier block");
 
 struct Pre8Args {
     const __nv_bfloat16* q;
@@ -79,7 +85,9 @@ struct Pre8Args {
     const int32_t *block_tables, *seq_lens, *cu_q_lens;
     __nv_bfloat16* out;
     unsigned* status;
-    int max_blocks, num_heads, num_kv_heads, num_blocks, group, batch, tiles;
+    int max_blocks, num_heads, num_kv_heads, num_blocks, group, batch;
+    int ctas_per_pair;   // CTAs the grid holds per (sequence, kv head)
+    int tiles_per_cta;   // 1 or 2
     float scale_log2;
 };
 
@@ -87,32 +95,36 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
     return tc_idesc_bf16(kRows, n, b_mn_major) & ~((1u << 7) | (1u << 10));  // f16 A and B
 }
 
-// Unit u of the stream K(0), then K(j + 1), V(j) for j = 0, 1, ..., each kParts units (the last
-// stage has no K(j + 1)).
-struct Unit {
-    int stage, part;
+// Group grp of the stream K(0), then K(j + 1), V(j) for j = 0, 1, ..., each the kParts blocks of
+// one stage (the last stage has no K(j + 1)).
+struct Group {
+    int stage;
     bool is_v;
 };
-__device__ __forceinline__ Unit unit_of(int u, int nst) {
-    const int grp = u / kParts;
-    Unit r;
-    r.part = u % kParts;
+__device__ __forceinline__ Group group_of(int grp, int nst) {
+    Group r;
     const bool last = grp == 2 * nst - 1;
     r.is_v = last || (grp > 0 && grp % 2 == 0);
     r.stage = last ? nst - 1 : r.is_v ? grp / 2 - 1 : (grp + 1) / 2;
     return r;
 }
 
+// Contiguous copy into this CTA's shared memory, completing on its mbarrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The loader warp: lanes 0-3 each copy one block of a group.
 template <int D>
-__device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pre8Args& a, const int32_t* bt, int kvh,
-                                            int L, int nst, int nblk, int w) {
+__device__ __forceinline__ void load_groups(uint8_t* smem, Bars8* bars, const Pre8Args& a, const int32_t* bt, int kvh,
+                                            int nst, int nblk) {
     using P = Pre8<D>;
     const int lane = threadIdx.x & 31;
-    const int total = 2 * nst * kParts;
-    // entries of blocks c0 + lane and the 32 after them; units walk the blocks of K one stage ahead
-    // of V's, and the loads run up to kAhead units ahead of that
-    constexpr int kAhead = 3;
-    uint4 codes[kAhead][P::kLoads];
+    const int total = 2 * nst;
+    // entries of blocks c0 + lane and of the 32 after them; V trails K, so the window moves with V
     int c0 = 0;
     const auto entry = [&](int blk) -> int {
         if (blk >= nblk) return -1;
@@ -122,48 +134,78 @@ __device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pr
         return 0;  // read inside the pool; the status word reports the bad id
     };
     int cur = entry(lane), nxt = entry(32 + lane);
-    const auto load = [&](uint4 (&to)[P::kLoads], int u) {
-        const Unit n = unit_of(u, nst);
-        const int lb = n.stage * kParts + n.part;
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) to[i] = make_uint4(0u, 0u, 0u, 0u);
-        // V units trail, so the window moves on once V has left it
-        if (n.is_v && lb >= c0 + 32) {
+    bool ok = true;
+    int issued = 0;
+    for (int grp = 0; grp < total && ok; ++grp) {
+        const Group n = group_of(grp, nst);
+        const int lb = n.stage * kParts + (lane & (kParts - 1));
+        if (n.is_v && n.stage * kParts >= c0 + 32) {
             c0 += 32;
             cur = nxt;
             nxt = entry(c0 + 32 + lane);
         }
-        const int id = __shfl_sync(0xffffffffu, lb < c0 + 32 ? cur : nxt, lb & 31);
-        if (id < 0) return;  // past the keys the tile needs: zeros
-        const size_t tile = ((size_t)id * a.num_kv_heads + kvh) * (kBlockSize * D);
-        const uint4* src = reinterpret_cast<const uint4*>((n.is_v ? a.v : a.k) + tile) + lane;
+        const int from_cur = __shfl_sync(0xffffffffu, cur, lb & 31), from_nxt = __shfl_sync(0xffffffffu, nxt, lb & 31);
+        const int id = lb < c0 + 32 ? from_cur : from_nxt;
+        const int slot = grp % kRawGroups;
+        if (grp >= kRawGroups) ok = mbar_wait_warp(&bars->raw_empty[slot], ((grp / kRawGroups) & 1) ^ 1);
+        if (!ok) break;
+        const int there = min(kParts, nblk - n.stage * kParts);  // blocks of the group the tile needs
+        if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], max(there, 0) * P::kRawBlock);
+        __syncwarp();
+        if (lane < there)
+            bulk_load(smem + P::kOffRaw + slot * P::kRawGroup + lane * P::kRawBlock,
+                      (n.is_v ? a.v : a.k) + ((size_t)id * a.num_kv_heads + kvh) * P::kRawBlock, P::kRawBlock,
+                      &bars->raw_full[slot]);
+        ++issued;
+    }
+    // before the CTA may leave: every copy has landed
+    for (int grp = max(0, issued - kRawGroups); grp < issued; ++grp)
+        if (!mbar_wait_warp(&bars->raw_full[grp % kRawGroups], (grp / kRawGroups) & 1)) ok = false;
+    if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
+}
+
+// Converter warp w of kCvtWarps.
+template <int D>
+__device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pre8Args& a, int L, int nst, int nblk,
+                                            int w) {
+    using P = Pre8<D>;
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    for (int u = w; u < 2 * nst * kParts; u += kCvtWarps) {
+        const int grp = u / kParts, part = u % kParts;
+        const Group n = group_of(grp, nst);
+        const int raw = grp % kRawGroups;
+        ok = mbar_wait_warp(&bars->raw_full[raw], (grp / kRawGroups) & 1);
+        if (!ok) break;
+        const int lb = n.stage * kParts + part;
+        const uint4* src = reinterpret_cast<const uint4*>(smem + P::kOffRaw + raw * P::kRawGroup + part * P::kRawBlock) + lane;
+        uint4 codes[P::kLoads];
 #pragma unroll
         for (int i = 0; i < P::kLoads; ++i) {
-            // V rows past the sequence's end count as zeros (u is 0 there, but 0 times NaN is NaN)
+            // past the keys the tile needs, and V past the sequence's end: zeros (u is 0 there, but 0
+            // times NaN is NaN)
             const int row = (i * 32 + lane) / (D / 16);
-            if (!n.is_v || lb * kBlockSize + row < L) to[i] = __ldg(src + i * 32);
+            const bool in = lb < nblk && (!n.is_v || lb * kBlockSize + row < L);
+            codes[i] = in ? src[i * 32] : make_uint4(0u, 0u, 0u, 0u);
         }
-    };
-    bool ok = true;
-    const auto store = [&](const uint4 (&from)[P::kLoads], int u) {
-        const Unit n = unit_of(u, nst);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->raw_empty[raw]);
         const int nslots = n.is_v ? kVStages : kKStages, slot = n.stage % nslots;
-        uint64_t* empty = n.is_v ? bars->v_empty : bars->k_empty;
-        if (n.stage >= nslots) ok = mbar_wait_warp(&empty[slot], ((n.stage / nslots) & 1) ^ 1);
-        if (!ok) return;
-        uint8_t* dst = smem + (n.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + n.part * (kBlockSize * 128);
+        if (n.stage >= nslots)
+            ok = mbar_wait_warp(n.is_v ? &bars->v_empty[slot] : &bars->k_empty[slot], ((n.stage / nslots) & 1) ^ 1);
+        if (!ok) break;
+        uint8_t* dst = smem + (n.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + part * (kBlockSize * 128);
 #pragma unroll
         for (int i = 0; i < P::kLoads; ++i) {
             // 16 codes: the 16-byte chunks ch, ch + 1 of column half h; lanes of the second half
             // store them in the other order, so that the lanes of one row hit different banks
             const int piece = i * 32 + lane, row = piece / (D / 16), c = piece % (D / 16);
             const int h = c >> 2, ch = (c & 3) * 2;
-            const uint4 now = from[i];
             uint4 lo, hi;
-            e4m3x4_to_f16x4(now.x, lo.x, lo.y);
-            e4m3x4_to_f16x4(now.y, lo.z, lo.w);
-            e4m3x4_to_f16x4(now.z, hi.x, hi.y);
-            e4m3x4_to_f16x4(now.w, hi.z, hi.w);
+            e4m3x4_to_f16x4(codes[i].x, lo.x, lo.y);
+            e4m3x4_to_f16x4(codes[i].y, lo.z, lo.w);
+            e4m3x4_to_f16x4(codes[i].z, hi.x, hi.y);
+            e4m3x4_to_f16x4(codes[i].w, hi.z, hi.w);
             uint8_t* at = dst + h * P::kKVHalf;
             *reinterpret_cast<uint4*>(at + swz128(row, ch + h)) = h ? hi : lo;
             *reinterpret_cast<uint4*>(at + swz128(row, ch + 1 - h)) = h ? lo : hi;
@@ -171,24 +213,13 @@ __device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pr
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(n.is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (w + i * kCvtWarps < total) load(codes[i], w + i * kCvtWarps);
-    for (int u0 = w; u0 < total && ok; u0 += kAhead * kCvtWarps)
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int u = u0 + i * kCvtWarps;
-            if (u >= total || !ok) break;
-            store(codes[i], u);
-            if (u + kAhead * kCvtWarps < total) load(codes[i], u + kAhead * kCvtWarps);
-        }
+    }
     if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
 }
 
 // The scales of a stage's four blocks as one row's softmax takes them.
 struct StageScales {
-    float f[kParts], kv[kParts];  // factor on s; exponent of V
+    float f[kParts], kv[kParts], back[kParts];  // factor on s; kV; 2^-kV
 };
 
 // Largest s f + kV of the stage's visible keys c <= lim (all of them with kAll).
@@ -246,7 +277,7 @@ __device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, co
         }
         const float sum = (a0 + a1) + (a2 + a3);
         all += sum;
-        lsum = fmaf(sum, exp2_int(-(int)sc.kv[i]), lsum);
+        lsum = fmaf(sum, sc.back[i], lsum);
         tmem_st8_nowait(dst + 8 * i, pw[0], pw[1], pw[2], pw[3], pw[4], pw[5], pw[6], pw[7]);
     }
     return all;
@@ -267,14 +298,14 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float f) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __grid_constant__ Pre8Args a) {
+__global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_constant__ Pre8Args a) {
     using P = Pre8<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars8* bars = reinterpret_cast<Bars8*>(smem + P::kOffBars);
     float* row_inv = reinterpret_cast<float*>(smem + P::kOffInv);
-    int* all_ok = reinterpret_cast<int*>(row_inv + kRows);
+    int* all_ok = reinterpret_cast<int*>(row_inv + 2 * kRows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // blockIdx.x = (rank * batch + b) * num_kv_heads + kvh: rank 0 is every chunk's last tile
+    // blockIdx.x = (rank * batch + b) * num_kv_heads + kvh: rank 0 is every chunk's last CTA
     const int kvh = (int)(blockIdx.x % (unsigned)a.num_kv_heads);
     const int rb = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
     const int b = rb % a.batch, rank = rb / a.batch;
@@ -292,19 +323,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
         return;
     }
     const long long rows = (long long)C * g;
-    const long long need = (rows + kRows - 1) / kRows;
-    // a chunk longer than max_chunk: the grid covers its first tiles, the rest is reported
-    if (rank == 0 && kvh == 0 && threadIdx.x == 0 && need > a.tiles) atomicOr(a.status, kDevOutOfRange);
-    const int covered = (int)min(need, (long long)a.tiles);
+    const int cta_rows = a.tiles_per_cta * kRows;
+    const long long need = (rows + cta_rows - 1) / cta_rows;
+    // a chunk longer than max_chunk: the grid covers its first rows, the rest is reported
+    if (rank == 0 && kvh == 0 && threadIdx.x == 0 && need > a.ctas_per_pair) atomicOr(a.status, kDevOutOfRange);
+    const int covered = (int)min(need, (long long)a.ctas_per_pair);
     if (rank >= covered) return;
-    const int row0 = (covered - 1 - rank) * kRows;
-    const int live = (int)min((long long)kRows, rows - row0);
-    const int nkeys = L - C + (row0 + live - 1) / g + 1;  // keys the tile's last query sees
-    const int nst = (nkeys + kKeys - 1) / kKeys;
+    const int row0 = (covered - 1 - rank) * cta_rows;
+    // rows of either tile, and its stages: up to the key its last query sees
+    const auto live_of = [&](int t) {
+        return t < a.tiles_per_cta ? (int)max(0ll, min((long long)kRows, rows - row0 - t * kRows)) : 0;
+    };
+    const auto keys_of = [&](int t) {
+        const int live = live_of(t);
+        return live ? L - C + (row0 + t * kRows + live - 1) / g + 1 : 0;
+    };
+    const int nkeys = max(keys_of(0), keys_of(1));
+    const int nst0 = (keys_of(0) + kKeys - 1) / kKeys, nst1 = (keys_of(1) + kKeys - 1) / kKeys;
+    const int nst = max(nst0, nst1);
     const int nblk = (nkeys + kBlockSize - 1) / kBlockSize;
     const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
 
     if (threadIdx.x == 0) {
+        for (int s = 0; s < kRawGroups; ++s) {
+            mbar_init(&bars->raw_full[s], 1);
+            mbar_init(&bars->raw_empty[s], kParts);
+        }
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bars->k_full[s], kParts);
             mbar_init(&bars->k_empty[s], 1);
@@ -313,13 +357,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
             mbar_init(&bars->v_full[s], kParts);
             mbar_init(&bars->v_empty[s], 1);
         }
-        mbar_init(&bars->q_full, kRows);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], kRows);
+        mbar_init(&bars->q_full, 2 * kRows);
+        for (int t = 0; t < 2; ++t) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&bars->s_full[t][i], 1);
+                mbar_init(&bars->p_full[t][i], kRows);
+            }
+            mbar_init(&bars->o_done[t], 1);
+            mbar_init(&bars->o_final[t], 1);
         }
-        mbar_init(&bars->o_done, 1);
-        mbar_init(&bars->o_final, 1);
         mbar_init(&bars->drain, 1);
         *all_ok = 1;
         fence_mbar_init();
@@ -334,49 +380,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
     const uint32_t tmem = bars->tmem_base;
 
     if (warp >= kCvtWarp) {
-        widen_units<D>(smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp);
+        widen_units<D>(smem, bars, a, L, nst, nblk, warp - kCvtWarp);
+    } else if (warp == kLoadWarp) {
+        load_groups<D>(smem, bars, a, bt, kvh, nst, nblk);
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
         constexpr uint32_t idesc_s = idesc_f16(kKeys, false), idesc_o = idesc_f16(D, true);
-        const uint64_t qd = smem_desc_sw128(smem_u32(smem), 0, 1024);
+        const uint64_t qd0 = smem_desc_sw128(smem_u32(smem), 0, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + P::kOffK), 0, 1024);
         const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + P::kOffV), P::kKVHalf, 1024);
-        const auto issue_s = [&](int j) {  // S(j) into buffer j % 2
+        const auto issue_s = [&](int t, int j) {  // S(j) of tile t into its buffer j % 2
+            const uint64_t qd = qd0 + (uint64_t)((t * P::kQTile) >> 4);
             const uint64_t kd = kd0 + (uint64_t)(((j % kKStages) * P::kStage) >> 4);
-            const uint32_t d = tmem + kTmemS + 64 * (j & 1);
+            const uint32_t d = tmem + t * kTmemTile + kTmemS + 64 * (j & 1);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 tc_mma_ew(d, qd + (uint64_t)(((kk >> 2) * P::kQHalf + (kk & 3) * 32) >> 4),
                           kd + (uint64_t)(((kk >> 2) * P::kKVHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-            tc_commit_ew(&bars->s_full[j & 1]);
-            tc_commit_ew(&bars->k_empty[j % kKStages]);
+            tc_commit_ew(&bars->s_full[t][j & 1]);
         };
-        const auto issue_o = [&](int j) {  // O += u(j) V(j), u(j) in buffer j % 2
+        const auto issue_o = [&](int t, int j) {  // O += u(j) V(j) of tile t
             const uint64_t vd = vd0 + (uint64_t)(((j % kVStages) * P::kStage) >> 4);
-            const uint32_t p = tmem + kTmemS + 64 * (j & 1);
+            const uint32_t p = tmem + t * kTmemTile + kTmemS + 64 * (j & 1);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc_mma_ts_ew(tmem + kTmemO, p + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
+                tc_mma_ts_ew(tmem + t * kTmemTile + kTmemO, p + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
                              (j > 0 || kk > 0) ? 1u : 0u);
-            tc_commit_ew(&bars->o_done);
-            tc_commit_ew(&bars->v_empty[j % kVStages]);
-            if (j + 1 == nst) tc_commit_ew(&bars->o_final);
+            tc_commit_ew(&bars->o_done[t]);
+            if (j + 1 == (t ? nst1 : nst0)) tc_commit_ew(&bars->o_final[t]);
         };
         bool ok = mbar_wait_warp(&bars->q_full, 0);
         for (int j = 0; j < 2 && j < nst && ok; ++j) {
             ok = mbar_wait_warp(&bars->k_full[j], 0);
             if (!ok) break;
             tc_fence_after();
-            issue_s(j);
+            if (j < nst0) issue_s(0, j);
+            if (j < nst1) issue_s(1, j);
+            tc_commit_ew(&bars->k_empty[j]);
         }
         for (int j = 0; j < nst && ok; ++j) {
             ok = mbar_wait_warp(&bars->v_full[j % kVStages], (j / kVStages) & 1);
             if (ok && j + 2 < nst) ok = mbar_wait_warp(&bars->k_full[(j + 2) % kKStages], ((j + 2) / kKStages) & 1);
-            if (ok) ok = mbar_wait_warp(&bars->p_full[j & 1], (j >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(j);
-            if (j + 2 < nst) issue_s(j + 2);  // after u V(j), whose u sits in its buffer
+            // per tile: u V(j), then S(j + 2) into the buffer that u(j) sits in
+            if (ok && j < nst0) {
+                ok = mbar_wait_warp(&bars->p_full[0][j & 1], (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_o(0, j);
+                if (j + 2 < nst0) issue_s(0, j + 2);
+            }
+            if (ok && j < nst1) {
+                ok = mbar_wait_warp(&bars->p_full[1][j & 1], (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_o(1, j);
+            }
+            tc_commit_ew(&bars->v_empty[j % kVStages]);
+            if (j + 2 < nst1) issue_s(1, j + 2);
+            if (j + 2 < nst) tc_commit_ew(&bars->k_empty[(j + 2) % kKStages]);
         }
         // every MMA issued here has finished before the tensor memory is released
         tc_commit_ew(&bars->drain);
@@ -384,11 +445,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
         if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
     } else {
         // ---------------------------------------------------------------- softmax: one row a thread
-        const int r = threadIdx.x;
-        const bool valid = r < live;
-        const int qi = (row0 + r) / g, h = (row0 + r) % g;
+        const int t = warp >> 2, r = threadIdx.x & (kRows - 1);  // tile, and its row: tensor memory lane
+        const int myst = t ? nst1 : nst0;
+        const bool valid = r < live_of(t);
+        const int cr = row0 + t * kRows + r;
+        const int qi = cr / g, h = cr % g;
         const int pos = valid ? L - C + qi : -1;  // last key the row sees
-        const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t tm = tmem + t * kTmemTile + ((uint32_t)((warp & 3) * 32) << 16);
         // exponents of blocks c0 + lane: a word a lane, the next 32 read ahead
         const auto entry = [&](int blk) { return blk < nblk ? __ldg(bt + blk) : -1; };
         const auto exps_of = [&](int blk, int id) -> int {
@@ -396,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
             return __ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh);
         };
         int ex = exps_of(lane, entry(lane)), next_id = entry(32 + lane), next_ex = 0;
-        int eq;
+        float qf;  // log2(e) |scale| 2^eq, eq the power of two taken out of the row of q
         {
             // the row of q, normalised, into the swizzled layout (zeros past the chunk); a
             // negative scale enters as -q, so that maxima are of the scores as they are
@@ -415,22 +478,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
                     amax = fmaxf(amax, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
                 }
             }
-            eq = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -110);
+            const int eq = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -110);
+            qf = fabsf(a.scale_log2) * exp2_int(eq);
             const float s = a.scale_log2 < 0.f ? -exp2_int(-eq) : exp2_int(-eq);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 const auto w = [&](uint32_t x) { return pack_f16x2(bf16_lo(x) * s, bf16_hi(x) * s); };
-                *reinterpret_cast<uint4*>(smem + (c >> 3) * P::kQHalf + swz128(r, c & 7)) =
+                *reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7)) =
                     make_uint4(w(v[c].x), w(v[c].y), w(v[c].z), w(v[c].w));
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars->q_full);
         }
-        const float sl = fabsf(a.scale_log2);
         float base = -INFINITY, l = 0.f;
         bool ok = true;
         // tcgen05.ld / st are warp-collective: what leads to one is decided by the whole warp
-        for (int j = 0; j < nst; ++j) {
+        for (int j = 0; j < myst; ++j) {
             const int at = (j * kParts) & 31;
             if (at == 0 && j > 0) {
                 ex = next_ex;
@@ -440,12 +503,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
 #pragma unroll
             for (int i = 0; i < kParts; ++i) {
                 const int e = __shfl_sync(0xffffffffu, ex, at + i);
-                sc.f[i] = sl * exp2_int(eq + (e & 255) - kExpBias);
+                sc.f[i] = qf * __int_as_float((e & 255) << 23);
                 sc.kv[i] = static_cast<float>((e >> 8) - kExpBias);
+                sc.back[i] = __int_as_float((2 * kExpBias - (e >> 8)) << 23);
             }
             if (at == 16) next_ex = exps_of(j * kParts + 16 + lane, next_id);
             const uint32_t buf = tm + kTmemS + 64 * (j & 1);
-            ok = mbar_wait_warp(&bars->s_full[j & 1], (j >> 1) & 1);
+            ok = mbar_wait_warp(&bars->s_full[t][j & 1], (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const int lim = pos - j * kKeys;
@@ -469,20 +533,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
                 const float top = fmaxf(base, mx);
                 const bool move = top > base + kRebase;  // always at a row's first visible key
                 const bool rescale = move && base != -INFINITY;
-                const float f = rescale ? fast_exp2(base - top) : 1.f;
                 if (__any_sync(0xffffffffu, rescale)) {
                     // O changes once u V(j - 1) has finished: phase j - 1 of o_done (phases up to
                     // j - 2 are over, as S(j) followed u V(j - 2), and u V(j) waits for this u)
-                    if (j > 0) ok = mbar_wait_warp(&bars->o_done, (j - 1) & 1);
+                    if (j > 0) ok = mbar_wait_warp(&bars->o_done[t], (j - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    scale_o<D>(tm + kTmemO, f);
+                    scale_o<D>(tm + kTmemO, rescale ? fast_exp2(base - top) : 1.f);
                 }
                 if (move) {
-                    // in two steps: l, whose terms carry 2^-kV, may count where f alone is zero
+                    // in two steps: l, whose terms carry 2^-kV, may count where the factor is zero
                     if (rescale) {
-                        const float h = fast_exp2(0.5f * (base - top));
-                        l = l * h * h;
+                        const float half = fast_exp2(0.5f * (base - top));
+                        l = l * half * half;
                     }
                     base = top;
                 }
@@ -491,10 +554,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
             l += lsum;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bars->p_full[j & 1]);
+            mbar_arrive(&bars->p_full[t][j & 1]);
         }
-        if (ok) ok = mbar_wait_warp(&bars->o_final, 0);
-        row_inv[r] = l > 0.f ? 1.f / l : 0.f;
+        if (ok && myst > 0) ok = mbar_wait_warp(&bars->o_final[t], 0);
+        row_inv[t * kRows + r] = l > 0.f ? 1.f / l : 0.f;
         if (!ok && lane == 0) {
             *all_ok = 0;
             atomicOr(a.status, kDevTimeout);
@@ -503,26 +566,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
     __syncthreads();
     tc_fence_after();
     // ---------------------------------------------------------------- epilogue
+    // Warp: a quarter of a tile's rows and half of the columns, normalised, as 16-byte chunks into
+    // the Q buffer ([row][chunk ^ row % 8]: no bank conflicts either way), then coalesced.
+    constexpr int kChunks = D / 8;
     if (*all_ok) {
-        const int r = (warp & 3) * 32 + lane;
-        const bool valid = r < live;
-        const int qi = (row0 + r) / g, h = (row0 + r) % g;
-        __nv_bfloat16* dst =
-            a.out + ((size_t)(q0 + (valid ? qi : 0)) * a.num_heads + (size_t)kvh * g + h) * D;
-        const float inv = row_inv[r];
-        const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kTmemO;
-        const int c0 = (warp >> 2) * (D / 2);
+        const int t = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, c0 = (warp >> 3) * (D / 2);
+        if (live_of(t)) {
+            const float inv = row_inv[t * kRows + r];
+            const uint32_t tm = tmem + t * kTmemTile + ((uint32_t)((warp & 3) * 32) << 16) + kTmemO;
 #pragma unroll
-        for (int c = 0; c < D / 2; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tm + c0 + c, o);
-            if (valid) {
+            for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tm + c0 + c, o);
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     const auto w = [&](int i) {
                         return pack_bf16x2(__uint_as_float(o[e + i]) * inv, __uint_as_float(o[e + i + 1]) * inv);
                     };
-                    *reinterpret_cast<uint4*>(dst + c0 + c + e) = make_uint4(w(0), w(2), w(4), w(6));
+                    const int ch = (c0 + c + e) >> 3;
+                    *reinterpret_cast<uint4*>(smem + t * P::kQTile + (r * kChunks + (ch ^ (r & 7))) * 16) =
+                        make_uint4(w(0), w(2), w(4), w(6));
                 }
             }
         }
@@ -533,6 +596,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) prefill8_kernel(const __
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+    if (*all_ok) {
+        const int live = live_of(0) + live_of(1);
+        for (int i = threadIdx.x; i < live * kChunks; i += kThreads) {
+            const int cr = i / kChunks, ch = i % kChunks;
+            const int r = cr & (kRows - 1);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + (cr / kRows) * P::kQTile +
+                                                            (r * kChunks + (ch ^ (r & 7))) * 16);
+            const int qi = (row0 + cr) / g, h = (row0 + cr) % g;
+            *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + h) * D + ch * 8) = v;
+        }
     }
 }
 
@@ -581,9 +655,13 @@ cudaError_t launch_prefill8(const Pool8View& pool, const AttnArgs& a, cudaStream
     p.num_blocks = pool.num_blocks;
     p.group = g;
     p.batch = a.batch;
-    p.tiles = (int)(((long long)a.max_chunk * g + kRows - 1) / kRows);
     p.scale_log2 = a.scale * kLog2e;
-    const long long ctas = (long long)p.tiles * a.batch * pool.num_kv_heads;
+    // two tiles to a CTA, unless the tiles, one to an SM, all run at once
+    const long long pairs = (long long)a.batch * pool.num_kv_heads;
+    const long long tiles = ((long long)a.max_chunk * g + kRows - 1) / kRows;
+    p.tiles_per_cta = tiles * pairs <= device_info().num_sms ? 1 : 2;
+    p.ctas_per_pair = (int)((tiles + p.tiles_per_cta - 1) / p.tiles_per_cta);
+    const long long ctas = p.ctas_per_pair * pairs;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;  // more CTAs than a grid holds
     return pool.head_dim == 128 ? launch<128>(p, (unsigned)ctas, stream) : launch<64>(p, (unsigned)ctas, stream);
 }
