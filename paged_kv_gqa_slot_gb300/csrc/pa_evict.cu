@@ -7,14 +7,15 @@
 // leave, so no K or V moves, the pool is only ever read by others, and a block that several
 // sequences share is dropped from one table only.
 //
-// A few KB per sequence: latency is all there is.  One CTA per sequence copies its rows into
-// shared memory (while they fit; else it reads them twice), sums the heads into
-// order-preserving 32-bit keys, which its threads keep in registers, finds the e-th smallest by
-// bisection -- two bits a round, a count and one barrier each, which beat radix histograms,
-// whose shared-memory atomics pile up on the few exponents that weights have -- ranks ties and
-// survivors with two block scans, and gathers through the resulting source list.  W_j is summed
-// in 64 bits and rounded once, so it does not depend on the order of the heads.  Rows in shared
-// memory are read whole before any output is written; the others are gathered in
+// A few KB per sequence: latency is all there is.  One CTA per sequence reads its rows once, summing
+// the heads into order-preserving 32-bit keys on the way into shared memory (where the rows fit;
+// else it reads them again for the copy), finds the e-th smallest key by four 8-bit radix passes,
+// ranks ties and survivors with two block scans, and gathers through the resulting source list.  The
+// weights of a sequence share a few exponents, so the lanes of a warp that hold the same digit
+// count together before they add to a bin.  W_j is the sum in 64 bits rounded once, so it does not
+// depend on the order of the heads; it is formed from fp32 sums and their exact errors (fp64
+// arithmetic, of which an SM does two operations a cycle, took half the kernel's time).  Rows in
+// shared memory are read whole before any output is written; the others are gathered in
 // ascending tiles, each read before it is written, from sources at or past it: outputs may be
 // their inputs.
 #include <algorithm>
@@ -25,7 +26,7 @@
 namespace pa {
 namespace {
 
-constexpr int kFewBlocks = 256;    // tables up to this width: 128 threads, else 1024
+constexpr int kFewBlocks = 256;    // tables up to this width: 128 threads, else 512
 constexpr int kResident = 200 * 1024;  // bytes of rows and keys a CTA keeps in shared memory
 
 // float order as unsigned order; -0 as +0, NaN below everything
@@ -34,6 +35,23 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+// W_j of one entry: the sum over heads of col[h * width], rounded once.  s + err is the sum to
+// 48 bits: every addition's error is exact and added up on its own.
+struct WeightSum {
+    float s = 0.f, err = 0.f;
+    __device__ __forceinline__ void add(float w) {
+        const float t = s + w, z = t - s;
+        err += (s - (t - z)) + (w - z);
+        s = t;
+    }
+    __device__ __forceinline__ float value(const float* col, int heads, int width) const {
+        if (fabsf(s) < INFINITY) return s + err;
+        double d = 0.0;  // infinities, NaN, sums past the fp32 range
+        for (int h = 0; h < heads; ++h) d += (double)col[(size_t)h * width];
+        return (float)d;
+    }
+};
 
 // Exclusive sum of v over the block's threads in order.
 template <int T>
@@ -56,31 +74,38 @@ template <int T>
 __global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictArgs a, int resident) {
     extern __shared__ uint32_t src[];  // keys, then the source index of every new entry
     __shared__ int warp_sums[32];
-    __shared__ int counts[2][3];
-    const int b = blockIdx.x, width = a.max_blocks, tid = threadIdx.x;
+    __shared__ int hist[256];
+    __shared__ uint32_t s_prefix;
+    __shared__ int s_left;
+    const int b = blockIdx.x, width = a.max_blocks, heads = a.num_kv_heads, tid = threadIdx.x;
+    const int lane = tid & 31;
     pdl_trigger();
     pdl_wait();
     const int32_t* table = a.tables + (size_t)b * width;
-    const float* weights = a.weights + (size_t)b * a.num_kv_heads * width;
+    const float* weights = a.weights + (size_t)b * heads * width;
     int L = a.seq_lens[b];
-    if (resident) {
-        float* rows = reinterpret_cast<float*>(src + width);
-        int32_t* ids = reinterpret_cast<int32_t*>(rows + a.num_kv_heads * width);
-        const int cells = a.num_kv_heads * width;
-        int i = tid;
-        for (; i + 7 * T < cells; i += 8 * T) {
+    float* rows = reinterpret_cast<float*>(src + width);             // resident: the weights
+    int32_t* ids = reinterpret_cast<int32_t*>(rows + heads * width);  // and the table
+    for (int j = tid; j < width; j += T) {
+        const int32_t id = resident ? table[j] : 0;
+        WeightSum w;
+        for (int h0 = 0; h0 < heads; h0 += 8) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = weights[i + k * T];
+            for (int h = 0; h < 8; ++h) v[h] = h0 + h < heads ? weights[(size_t)(h0 + h) * width + j] : 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) rows[i + k * T] = v[k];
+            for (int h = 0; h < 8; ++h) {
+                w.add(v[h]);
+                if (resident && h0 + h < heads) rows[(h0 + h) * width + j] = v[h];
+            }
         }
-        for (; i < cells; i += T) rows[i] = weights[i];
-        for (int j = tid; j < width; j += T) ids[j] = table[j];
+        src[j] = order_key(w.value(weights + j, heads, width));
+        if (resident) ids[j] = id;
+    }
+    if (resident) {
         weights = rows;
         table = ids;
     }
-    if (tid < 6) (&counts[0][0])[tid] = 0;
     __syncthreads();
     if (L < 0 || L > width * kBlockSize) {
         if (tid == 0) atomicOr(a.status, kDevOutOfRange);
@@ -91,53 +116,47 @@ __global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictA
     const int lo = a.sink, hi = nb - a.recent;  // candidates [lo, hi): at least e of them, as sink + recent <= keep
 
     if (e > 0) {
-        for (int j = lo + tid; j < hi; j += T) {
-            double w = 0.0;
-#pragma unroll 8
-            for (int h = 0; h < a.num_kv_heads; ++h) w += (double)weights[(size_t)h * width + j];
-            src[j] = order_key((float)w);
-        }
-        __syncthreads();
-        // The e-th smallest key T: the largest value with fewer than e keys below it, two bits at a
-        // time.  `left` of the keys equal to it leave too.  A thread keeps up to 4 keys at hand.
-        constexpr int kHand = 4;
-        uint32_t hand[kHand];
-#pragma unroll
-        for (int i = 0; i < kHand; ++i) {
-            const int j = lo + tid + i * T;
-            hand[i] = j < hi ? src[j] : 0xffffffffu;  // counts as below no trial value
-        }
+        // the e-th smallest key, a digit at a time: `prefix` its upper digits, `left` how many of the
+        // keys that share them still leave
         uint32_t prefix = 0;
-        int below = 0;  // keys below prefix
-        for (int shift = 30, round = 0; shift >= 0; shift -= 2, ++round) {
-            // keys below prefix + 1, 2, 3 steps
-            int c[3] = {0, 0, 0};
-            const auto count = [&](uint32_t key) {
-#pragma unroll
-                for (int i = 0; i < 3; ++i) c[i] += key < (prefix | ((uint32_t)(i + 1) << shift));
-            };
-#pragma unroll
-            for (int i = 0; i < kHand; ++i) count(hand[i]);
-            for (int j = lo + tid + kHand * T; j < hi; j += T) count(src[j]);
-            int* to = counts[round & 1];
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const int sum = __reduce_add_sync(0xffffffffu, c[i]);
-                if ((tid & 31) == i && sum) atomicAdd(&to[i], sum);
+        int left = e;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 256; i += T) hist[i] = 0;
+            __syncthreads();
+            for (int j0 = lo; j0 < hi; j0 += T) {
+                const int j = j0 + tid;
+                const uint32_t key = j < hi ? src[j] : 0u;
+                const bool in = j < hi && (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8));
+                const unsigned peers = __match_any_sync(0xffffffffu, in ? (int)(key >> shift & 255u) : -1);
+                if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[key >> shift & 255u], __popc(peers));
             }
             __syncthreads();
-            int digit = 0;
+            if (tid < 32) {
+                int v[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (to[i] < e) {
-                    digit = i + 1;
-                    below = to[i];
+                for (int i = 0; i < 8; ++i) sum += v[i] = hist[lane * 8 + i];
+                int incl = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
                 }
-            prefix |= (uint32_t)digit << shift;
-            if (tid < 3) counts[(round + 1) & 1][tid] = 0;
+                int below = incl - sum;
+                if (below < left && left <= incl) {  // the digit is one of this lane's
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (below < left && left <= below + v[i]) {
+                            s_prefix = prefix | (uint32_t)(lane * 8 + i) << shift;
+                            s_left = left - below;
+                        }
+                        below += v[i];
+                    }
+                }
+            }
             __syncthreads();
+            prefix = s_prefix;
+            left = s_left;
         }
-        const int left = e - below;
         // this thread's run of entries
         const int per = (width + T - 1) / T;
         const int j0 = min(width, tid * per), j1 = min(width, j0 + per);
@@ -156,7 +175,7 @@ __global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictA
         int before = block_scan<T>(gone, warp_sums);
         // the survivors' source list, in place: entry j - before <= j, which may lie in another
         // thread's run, so the flags move to registers first
-        uint32_t flags[(kEvictMaxBlocks / 1024 + 31) / 32] = {};
+        uint32_t flags[(kEvictMaxBlocks / 512 + 31) / 32] = {};
         for (int j = j0; j < j1; ++j) {
 #pragma unroll
             for (int w = 0; w < (int)(sizeof flags / 4); ++w)
@@ -184,7 +203,7 @@ __global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictA
     }
     // close up
     int32_t* table_out = a.tables_out + (size_t)b * width;
-    float* weights_out = a.weights_out + (size_t)b * a.num_kv_heads * width;
+    float* weights_out = a.weights_out + (size_t)b * heads * width;
     const bool in_place = !resident && (a.tables_out == a.tables || a.weights_out == a.weights);
     for (int i0 = 0; i0 < width; i0 += T) {
         const int i = i0 + tid;
@@ -229,7 +248,7 @@ cudaError_t launch(const EvictArgs& a, int batch, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream) {
-    return a.max_blocks <= kFewBlocks ? launch<128>(a, batch, stream) : launch<1024>(a, batch, stream);
+    return a.max_blocks <= kFewBlocks ? launch<128>(a, batch, stream) : launch<512>(a, batch, stream);
 }
 
 }  // namespace pa

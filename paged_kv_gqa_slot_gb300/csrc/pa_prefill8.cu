@@ -16,18 +16,29 @@
 // second part even where a few weights dominate a row.
 //
 // Per stage of 64 keys (four pool blocks):
-//   warp 9       copies the codes, a contiguous 1 or 2 KB a block, into a ring of raw tiles
-//   warps 10-15  widen them into the 128-byte swizzled layout of the MMA operands (rows past the
-//                sequence's end as zeros); a unit is one block's K or V, units go to the six
-//                warps in turn, K one stage ahead of V
+//   warps 9-15   read codes, each lane its own 16-byte pieces by cp.async kAhead units ahead, and
+//                widen them into the 128-byte swizzled layout of the MMA operands (rows past the
+//                sequence's end as zeros); a unit is one block's K or V, units go to the seven
+//                warps in turn, K one stage ahead of V.  (One warp that copied the blocks in bulk took
+//                over 400 cycles to issue a stage's K or V, which bounded the kernel.)
 //   warp 8       per tile, S[128 x 64] = Q K^T into one of two 64-column buffers and
 //                O[128 x D] += u V with u from tensor memory; per stage u V(j), then S(j + 2), which
 //                reuses u(j)'s buffer, of the one tile while the other's softmax runs
 //   warps 0-7    softmax, one row a thread: reads S, writes u over it.  The base is set by a row's
 //                first visible stage and moves only when a stage's sum passes 2^15 (f16 ends at
 //                2^16), then to the maximum, if that is more than 2^8 above; O is rescaled in
-//                tensor memory by all rows of a warp together.
+//                tensor memory by all rows of a warp together.  (The maximum in every stage instead
+//                cost 6 us of 52.)
 // At the end all warps normalise, stage the rows in the free Q buffer and store them coalesced.
+//
+// Measured on GB300 (32 q / 8 kv heads, d 128): 8 x 256 over 768 cached tokens 53 us (the bf16 pool's
+// kernel on the same values 59), 8 x 1024 over 1024 250 us (305), 1.20 us a stage of two tiles.  What
+// bounds a stage is shared memory: Q K^T reads Q and K (768 cycles for the two tiles), u V reads V
+// (256), and the codes are written, read and stored widened (512), 1536 of its 2280 cycles; the
+// MMA warp spends 1660 of them in issuing.  Tried and not kept: Q in tensor memory, which leaves room
+// for one score buffer a tile (1.14 us a stage, but a single tile's chain 10% longer: 22.7 against
+// 20.5 us for 1 x 256 + 768); stages of 128 keys with one buffer (1.48 us); codes loaded into
+// registers instead of by cp.async (1.74 us).
 #include <algorithm>
 #include <cmath>
 
@@ -41,8 +52,8 @@ constexpr int kRows = 128;                 // MMA M: rows of a query tile
 constexpr int kKeys = 64;                  // keys of a stage
 constexpr int kParts = kKeys / kBlockSize;  // pool blocks of a stage
 constexpr int kKStages = 3, kVStages = 3;
-constexpr int kRawGroups = 4;              // raw ring, in groups of K or V of one stage
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kCvtWarp = 10, kCvtWarps = 6;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kCvtWarp = 9, kCvtWarps = 7;
+constexpr int kAhead = 4;                  // units a converter warp has in hand or in flight
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;             // per tile: two 64-column score buffers, then O
 constexpr uint32_t kTmemTile = 256;
@@ -58,12 +69,11 @@ struct Pre8 {
     static constexpr int kQTile = kHalves * kQHalf;
     static constexpr int kKVHalf = kKeys * 128;
     static constexpr int kStage = kHalves * kKVHalf;  // K or V of a stage
-    static constexpr int kRawBlock = kBlockSize * D;  // one block's codes of K or V
-    static constexpr int kRawGroup = kParts * kRawBlock;
+    static constexpr int kUnit = kBlockSize * D;      // codes of one block's K or V
     static constexpr int kOffK = 2 * kQTile;
     static constexpr int kOffV = kOffK + kKStages * kStage;
     static constexpr int kOffRaw = kOffV + kVStages * kStage;
-    static constexpr int kOffBars = kOffRaw + kRawGroups * kRawGroup;
+    static constexpr int kOffBars = kOffRaw + kCvtWarps * kAhead * kUnit;
     static constexpr int kOffInv = kOffBars + 512;     // [2][128] 1 / l, then whether every wait ended
     static constexpr int kSmem = kOffInv + 2 * kRows * 4 + 16;
     static constexpr int kLoads = kBlockSize * D / 512;  // 16-byte pieces of a block a lane takes
@@ -71,7 +81,6 @@ struct Pre8 {
 static_assert(Pre8<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct Bars8 {
-    uint64_t raw_full[kRawGroups], raw_empty[kRawGroups];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2], o_final[2], drain;  // [tile][buffer]
     uint32_t tmem_base;
@@ -109,122 +118,118 @@ __device__ __forceinline__ Group group_of(int grp, int nst) {
     return r;
 }
 
-// Contiguous copy into this CTA's shared memory, completing on its mbarrier.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The loader warp: lanes 0-3 each copy one block of a group.
+// Converter warp w: units w, w + kCvtWarps, ... of the stream.
 template <int D>
-__device__ __forceinline__ void load_groups(uint8_t* smem, Bars8* bars, const Pre8Args& a, const int32_t* bt, int kvh,
-                                            int nst, int nblk) {
+struct Converter {
     using P = Pre8<D>;
-    const int lane = threadIdx.x & 31;
-    const int total = 2 * nst;
-    // entries of blocks c0 + lane and of the 32 after them; V trails K, so the window moves with V
-    int c0 = 0;
-    const auto entry = [&](int blk) -> int {
-        if (blk >= nblk) return -1;
-        const int id = __ldg(bt + blk);
-        if (id >= 0 && id < a.num_blocks) return id;
-        atomicOr(a.status, kDevOutOfRange);
-        return 0;  // read inside the pool; the status word reports the bad id
-    };
-    int cur = entry(lane), nxt = entry(32 + lane);
-    bool ok = true;
-    int issued = 0;
-    for (int grp = 0; grp < total && ok; ++grp) {
-        const Group n = group_of(grp, nst);
-        const int lb = n.stage * kParts + (lane & (kParts - 1));
-        if (n.is_v && n.stage * kParts >= c0 + 32) {
-            c0 += 32;
-            cur = nxt;
-            nxt = entry(c0 + 32 + lane);
-        }
-        const int from_cur = __shfl_sync(0xffffffffu, cur, lb & 31), from_nxt = __shfl_sync(0xffffffffu, nxt, lb & 31);
-        const int id = lb < c0 + 32 ? from_cur : from_nxt;
-        const int slot = grp % kRawGroups;
-        if (grp >= kRawGroups) ok = mbar_wait_warp(&bars->raw_empty[slot], ((grp / kRawGroups) & 1) ^ 1);
-        if (!ok) break;
-        const int there = min(kParts, nblk - n.stage * kParts);  // blocks of the group the tile needs
-        if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[slot], max(there, 0) * P::kRawBlock);
-        __syncwarp();
-        if (lane < there)
-            bulk_load(smem + P::kOffRaw + slot * P::kRawGroup + lane * P::kRawBlock,
-                      (n.is_v ? a.v : a.k) + ((size_t)id * a.num_kv_heads + kvh) * P::kRawBlock, P::kRawBlock,
-                      &bars->raw_full[slot]);
-        ++issued;
-    }
-    // before the CTA may leave: every copy has landed
-    for (int grp = max(0, issued - kRawGroups); grp < issued; ++grp)
-        if (!mbar_wait_warp(&bars->raw_full[grp % kRawGroups], (grp / kRawGroups) & 1)) ok = false;
-    if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
-}
+    uint8_t* smem;
+    Bars8* bars;
+    const Pre8Args& a;
+    const int32_t* bt;
+    int kvh, L, nst, nblk, w, lane;
+    int next_id;  // of the unit to be issued next
 
-// Converter warp w of kCvtWarps.
-template <int D>
-__device__ __forceinline__ void widen_units(uint8_t* smem, Bars8* bars, const Pre8Args& a, int L, int nst, int nblk,
-                                            int w) {
-    using P = Pre8<D>;
-    const int lane = threadIdx.x & 31;
-    bool ok = true;
-    for (int u = w; u < 2 * nst * kParts; u += kCvtWarps) {
-        const int grp = u / kParts, part = u % kParts;
-        const Group n = group_of(grp, nst);
-        const int raw = grp % kRawGroups;
-        ok = mbar_wait_warp(&bars->raw_full[raw], (grp / kRawGroups) & 1);
-        if (!ok) break;
-        const int lb = n.stage * kParts + part;
-        const uint4* src = reinterpret_cast<const uint4*>(smem + P::kOffRaw + raw * P::kRawGroup + part * P::kRawBlock) + lane;
-        uint4 codes[P::kLoads];
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) {
-            // past the keys the tile needs, and V past the sequence's end: zeros (u is 0 there, but 0
-            // times NaN is NaN)
-            const int row = (i * 32 + lane) / (D / 16);
-            const bool in = lb < nblk && (!n.is_v || lb * kBlockSize + row < L);
-            codes[i] = in ? src[i * 32] : make_uint4(0u, 0u, 0u, 0u);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->raw_empty[raw]);
-        const int nslots = n.is_v ? kVStages : kKStages, slot = n.stage % nslots;
-        if (n.stage >= nslots)
-            ok = mbar_wait_warp(n.is_v ? &bars->v_empty[slot] : &bars->k_empty[slot], ((n.stage / nslots) & 1) ^ 1);
-        if (!ok) break;
-        uint8_t* dst = smem + (n.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + part * (kBlockSize * 128);
-#pragma unroll
-        for (int i = 0; i < P::kLoads; ++i) {
-            // 16 codes: the 16-byte chunks ch, ch + 1 of column half h; lanes of the second half
-            // store them in the other order, so that the lanes of one row hit different banks
-            const int piece = i * 32 + lane, row = piece / (D / 16), c = piece % (D / 16);
-            const int h = c >> 2, ch = (c & 3) * 2;
-            uint4 lo, hi;
-            e4m3x4_to_f16x4(codes[i].x, lo.x, lo.y);
-            e4m3x4_to_f16x4(codes[i].y, lo.z, lo.w);
-            e4m3x4_to_f16x4(codes[i].z, hi.x, hi.y);
-            e4m3x4_to_f16x4(codes[i].w, hi.z, hi.w);
-            uint8_t* at = dst + h * P::kKVHalf;
-            *reinterpret_cast<uint4*>(at + swz128(row, ch + h)) = h ? hi : lo;
-            *reinterpret_cast<uint4*>(at + swz128(row, ch + 1 - h)) = h ? lo : hi;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(n.is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
+    __device__ __forceinline__ int total() const { return 2 * nst * kParts; }
+    __device__ __forceinline__ uint32_t raw(int n) const {
+        return smem_u32(smem + P::kOffRaw) + (w * kAhead + n % kAhead) * P::kUnit + lane * 16;
     }
-    if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
-}
-
-// The scales of a stage's four blocks as one row's softmax takes them.
-struct StageScales {
-    float f[kParts], kv[kParts], back[kParts];  // factor on s; kV; 2^-kV
+    __device__ __forceinline__ int block_of(int u) const { return group_of(u / kParts, nst).stage * kParts + u % kParts; }
+    // id of unit u's block; -1 past the keys the CTA needs
+    __device__ __forceinline__ int entry(int u) const {
+        if (u >= total()) return -1;
+        const int lb = block_of(u);
+        return lb < nblk ? __ldg(bt + lb) : -1;
+    }
+    // n-th unit of this warp: start its copy, and load the next one's table entry
+    __device__ __forceinline__ void issue(int n) {
+        const int u = w + n * kCvtWarps;
+        if (u < total() && block_of(u) < nblk) {
+            int id = next_id;
+            if (id < 0 || id >= a.num_blocks) {
+                if (lane == 0) atomicOr(a.status, kDevOutOfRange);
+                id = 0;  // read inside the pool; the status word reports the bad id
+            }
+            const uint8_t* src = (group_of(u / kParts, nst).is_v ? a.v : a.k) +
+                                 ((size_t)id * a.num_kv_heads + kvh) * P::kUnit + lane * 16;
+#pragma unroll
+            for (int i = 0; i < P::kLoads; ++i) cp_async16(raw(n) + i * 512, src + i * 512);
+        }
+        cp_async_commit();
+        next_id = entry(u + kCvtWarps);
+    }
+    __device__ __forceinline__ void start() {
+        next_id = entry(w);
+        for (int n = 0; n < kAhead; ++n) issue(n);
+    }
+    __device__ __forceinline__ void run() {
+        bool ok = true;
+        int n = 0;
+        for (int u = w; u < total(); u += kCvtWarps, ++n) {
+            const Group grp = group_of(u / kParts, nst);
+            const int part = u % kParts, lb = grp.stage * kParts + part;
+            cp_async_wait<kAhead - 1>();
+            uint4 codes[P::kLoads];
+#pragma unroll
+            for (int i = 0; i < P::kLoads; ++i) {
+                // past the keys the CTA needs, and V past the sequence's end: zeros (u is 0 there,
+                // but 0 times NaN is NaN)
+                const int row = (i * 32 + lane) / (D / 16);
+                const bool in = lb < nblk && (!grp.is_v || lb * kBlockSize + row < L);
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
+                             : "r"(raw(n) + i * 512)
+                             : "memory");
+                if (!in) codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            const int nslots = grp.is_v ? kVStages : kKStages, slot = grp.stage % nslots;
+            if (grp.stage >= nslots)
+                ok = mbar_wait_warp(grp.is_v ? &bars->v_empty[slot] : &bars->k_empty[slot],
+                                    ((grp.stage / nslots) & 1) ^ 1);
+            if (!ok) break;
+            uint8_t* dst = smem + (grp.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + part * (kBlockSize * 128);
+#pragma unroll
+            for (int i = 0; i < P::kLoads; ++i) {
+                // 16 codes: the 16-byte chunks ch, ch + 1 of column half h; lanes of the second half
+                // store them in the other order, so that the lanes of one row hit different banks
+                const int piece = i * 32 + lane, row = piece / (D / 16), c = piece % (D / 16);
+                const int h = c >> 2, ch = (c & 3) * 2;
+                uint4 lo, hi;
+                e4m3x4_to_f16x4(codes[i].x, lo.x, lo.y);
+                e4m3x4_to_f16x4(codes[i].y, lo.z, lo.w);
+                e4m3x4_to_f16x4(codes[i].z, hi.x, hi.y);
+                e4m3x4_to_f16x4(codes[i].w, hi.z, hi.w);
+                uint8_t* at = dst + h * P::kKVHalf;
+                *reinterpret_cast<uint4*>(at + swz128(row, ch + h)) = h ? hi : lo;
+                *reinterpret_cast<uint4*>(at + swz128(row, ch + 1 - h)) = h ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(grp.is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
+            issue(n + kAhead);  // over the pieces just read
+        }
+        cp_async_wait<0>();
+        if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
+    }
 };
+
+// The scales of a block as the softmax takes them, from its word of exponents (K in the low byte):
+// the factor qf 2^kK on s, kV, and 2^-kV.
+__device__ __forceinline__ float k_factor(int e, float qf) { return qf * __int_as_float((e & 255) << 23); }
+__device__ __forceinline__ float v_exponent(int e) { return static_cast<float>((e >> 8) - kExpBias); }
+__device__ __forceinline__ float v_unscale(int e) { return __int_as_float((2 * kExpBias - (e >> 8)) << 23); }
 
 // Largest s f + kV of the stage's visible keys c <= lim (all of them with kAll).
 template <bool kAll>
-__device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, const StageScales& sc) {
+__device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf) {
     float best = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
@@ -241,29 +246,28 @@ __device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, 
             m1 = fmax3(m1, x[2], x[3]);
         }
         const float m = fmaxf(m0, m1);
-        best = fmaxf(best, m == -INFINITY ? m : fmaf(m, sc.f[i], sc.kv[i]));
+        best = fmaxf(best, m == -INFINITY ? m : fmaf(m, k_factor(ew[i], qf), v_exponent(ew[i])));
     }
     return best;
 }
 
-// u of the stage against `nbase` (= -base), as f16 pairs into the 32 columns at `dst`; returns their
-// plain sum, and adds the sum of u 2^-kV to lsum.
+// u of the stage against base -nbase, as f16 pairs into the 32 columns at `dst`; returns their plain
+// sum, and lsum gets the sum of u 2^-kV.
 template <bool kAll>
-__device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, const StageScales& sc, float nbase,
-                                         uint32_t dst, float& lsum) {
+__device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf,
+                                         float nbase, uint32_t dst, float& lsum) {
     float all = 0.f;
     lsum = 0.f;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-        const float off = sc.kv[i] + nbase;
+        const float f = k_factor(ew[i], qf), off = v_exponent(ew[i]) + nbase;
         float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
         uint32_t pw[8];
 #pragma unroll
         for (int t = 0; t < 16; t += 2) {
             const int c = i * 16 + t;
             float x0, x1;
-            fma_x2(x0, x1, __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]), sc.f[i],
-                   sc.f[i], off, off);
+            fma_x2(x0, x1, __uint_as_float(s[c >> 5][c & 31]), __uint_as_float(s[c >> 5][(c & 31) + 1]), f, f, off, off);
             if (!kAll) {
                 x0 = c > lim ? -INFINITY : x0;  // 2^-inf = 0
                 x1 = c + 1 > lim ? -INFINITY : x1;
@@ -277,7 +281,7 @@ __device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, co
         }
         const float sum = (a0 + a1) + (a2 + a3);
         all += sum;
-        lsum = fmaf(sum, sc.back[i], lsum);
+        lsum = fmaf(sum, v_unscale(ew[i]), lsum);
         tmem_st8_nowait(dst + 8 * i, pw[0], pw[1], pw[2], pw[3], pw[4], pw[5], pw[6], pw[7]);
     }
     return all;
@@ -344,11 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const int nblk = (nkeys + kBlockSize - 1) / kBlockSize;
     const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
 
+    // The first loads go out before the set-up below: a softmax thread's row of q, a converter's first
+    // units.
+    const int t_row = threadIdx.x & (kRows - 1), t_tile = (warp >> 2) & 1;  // softmax: row of its tile
+    const bool valid = warp < kSoftmaxWarps && t_row < live_of(t_tile);
+    const int cr = row0 + t_tile * kRows + t_row;
+    const int qi = cr / g, qh = cr % g;
+    uint4 qv[D / 8];
+    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane, 0};
+    if (warp < kSoftmaxWarps) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((size_t)(q0 + (valid ? qi : 0)) * a.num_heads + (size_t)kvh * g + qh) * D);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) qv[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    } else if (warp >= kCvtWarp) {
+        cvt.start();
+    }
+
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kRawGroups; ++s) {
-            mbar_init(&bars->raw_full[s], 1);
-            mbar_init(&bars->raw_empty[s], kParts);
-        }
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bars->k_full[s], kParts);
             mbar_init(&bars->k_empty[s], 1);
@@ -380,9 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const uint32_t tmem = bars->tmem_base;
 
     if (warp >= kCvtWarp) {
-        widen_units<D>(smem, bars, a, L, nst, nblk, warp - kCvtWarp);
-    } else if (warp == kLoadWarp) {
-        load_groups<D>(smem, bars, a, bt, kvh, nst, nblk);
+        cvt.run();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
         constexpr uint32_t idesc_s = idesc_f16(kKeys, false), idesc_o = idesc_f16(D, true);
@@ -445,11 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
     } else {
         // ---------------------------------------------------------------- softmax: one row a thread
-        const int t = warp >> 2, r = threadIdx.x & (kRows - 1);  // tile, and its row: tensor memory lane
+        const int t = t_tile, r = t_row;  // tile, and its row: tensor memory lane
         const int myst = t ? nst1 : nst0;
-        const bool valid = r < live_of(t);
-        const int cr = row0 + t * kRows + r;
-        const int qi = cr / g, h = cr % g;
         const int pos = valid ? L - C + qi : -1;  // last key the row sees
         const uint32_t tm = tmem + t * kTmemTile + ((uint32_t)((warp & 3) * 32) << 16);
         // exponents of blocks c0 + lane: a word a lane, the next 32 read ahead
@@ -463,15 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         {
             // the row of q, normalised, into the swizzled layout (zeros past the chunk); a
             // negative scale enters as -q, so that maxima are of the scores as they are
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((size_t)(q0 + (valid ? qi : 0)) * a.num_heads + (size_t)kvh * g + h) * D);
-            uint4 v[D / 8];
             float amax = 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = fabsf(bf16_lo(w[i])), y = fabsf(bf16_hi(w[i]));
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             for (int c = 0; c < D / 8; ++c) {
                 const auto w = [&](uint32_t x) { return pack_f16x2(bf16_lo(x) * s, bf16_hi(x) * s); };
                 *reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7)) =
-                    make_uint4(w(v[c].x), w(v[c].y), w(v[c].z), w(v[c].w));
+                    make_uint4(w(qv[c].x), w(qv[c].y), w(qv[c].z), w(qv[c].w));
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars->q_full);
@@ -499,14 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                 ex = next_ex;
                 next_id = entry(j * kParts + 32 + lane);
             }
-            StageScales sc;
+            int ew[kParts];
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                const int e = __shfl_sync(0xffffffffu, ex, at + i);
-                sc.f[i] = qf * __int_as_float((e & 255) << 23);
-                sc.kv[i] = static_cast<float>((e >> 8) - kExpBias);
-                sc.back[i] = __int_as_float((2 * kExpBias - (e >> 8)) << 23);
-            }
+            for (int i = 0; i < kParts; ++i) ew[i] = __shfl_sync(0xffffffffu, ex, at + i);
             if (at == 16) next_ex = exps_of(j * kParts + 16 + lane, next_id);
             const uint32_t buf = tm + kTmemS + 64 * (j & 1);
             ok = mbar_wait_warp(&bars->s_full[t][j & 1], (j >> 1) & 1);
@@ -519,17 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             tmem_ld32_async(buf + 32, s[1]);
             tmem_wait_ld(s[0]);
             tmem_wait_ld(s[1]);
-            const auto weigh = [&](float& lsum) {
-                const float nbase = base == -INFINITY ? 0.f : -base;
-                return unmasked ? stage_u<true>(s, lim, sc, nbase, buf, lsum)
-                                : stage_u<false>(s, lim, sc, nbase, buf, lsum);
-            };
+            // First against the row's base as it is.  The maximum, and with it a possible move of the
+            // base, is taken only for a row's first visible stage, or when the sum of u passes
+            // kSumLimit; either is the warp's decision.
             float lsum = 0.f;
+            const auto weigh = [&] {
+                const float nbase = base == -INFINITY ? 0.f : -base;
+                return unmasked ? stage_u<true>(s, lim, ew, qf, nbase, buf, lsum)
+                                : stage_u<false>(s, lim, ew, qf, nbase, buf, lsum);
+            };
             bool full = __any_sync(0xffffffffu, base == -INFINITY && lim >= 0);
-            if (!full) full = __any_sync(0xffffffffu, !(weigh(lsum) <= kSumLimit));
+            if (!full) full = __any_sync(0xffffffffu, !(weigh() <= kSumLimit));
             if (full) {
                 tmem_wait_st();  // a first attempt's u: the second goes over it
-                const float mx = unmasked ? stage_max<true>(s, lim, sc) : stage_max<false>(s, lim, sc);
+                const float mx = unmasked ? stage_max<true>(s, lim, ew, qf) : stage_max<false>(s, lim, ew, qf);
                 const float top = fmaxf(base, mx);
                 const bool move = top > base + kRebase;  // always at a row's first visible key
                 const bool rescale = move && base != -INFINITY;
@@ -540,16 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                     if (!ok) break;
                     tc_fence_after();
                     scale_o<D>(tm + kTmemO, rescale ? fast_exp2(base - top) : 1.f);
-                }
-                if (move) {
                     // in two steps: l, whose terms carry 2^-kV, may count where the factor is zero
-                    if (rescale) {
-                        const float half = fast_exp2(0.5f * (base - top));
-                        l = l * half * half;
-                    }
-                    base = top;
+                    const float half = rescale ? fast_exp2(0.5f * (base - top)) : 1.f;
+                    l = l * half * half;
                 }
-                weigh(lsum);
+                if (move) base = top;
+                weigh();
             }
             l += lsum;
             tmem_wait_st();
