@@ -360,7 +360,7 @@ def _call(what: str, device: int, stream, *args) -> None:
         raw = torch._C._cuda_getCurrentRawStream(device)
     else:
         raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):

@@ -22,6 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 7;
 
 struct Append8Args {
     uint8_t* codes[2];  // K, V
@@ -47,10 +48,16 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
     return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | (w >> 16 < 0x7f80u ? w & 0xffff0000u : 0u);
 }
 
-// 8 bf16 values times s, as 8 codes.
-__device__ __forceinline__ uint2 chunk_codes(const uint4& v, float s) {
-    return make_uint2(to_e4m3x4(bf16_lo(v.x) * s, bf16_hi(v.x) * s, bf16_lo(v.y) * s, bf16_hi(v.y) * s),
-                      to_e4m3x4(bf16_lo(v.z) * s, bf16_hi(v.z) * s, bf16_lo(v.w) * s, bf16_hi(v.w) * s));
+// 8 bf16 values times s2, a pair of equal powers of two, as 8 codes.  The product is exact in bf16
+// but for results below 2^-126, whose code is zero either way.
+__device__ __forceinline__ uint2 chunk_codes(const uint4& v, __nv_bfloat162 s2) {
+    const auto mul = [&](uint32_t w) {
+        const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), s2);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    };
+    const uint32_t x = mul(v.x), y = mul(v.y), z = mul(v.z), w = mul(v.w);
+    return make_uint2(to_e4m3x4(bf16_lo(x), bf16_hi(x), bf16_lo(y), bf16_hi(y)),
+                      to_e4m3x4(bf16_lo(z), bf16_hi(z), bf16_lo(w), bf16_hi(w)));
 }
 
 // 4 codes times s, rounded again.
@@ -61,63 +68,59 @@ __device__ __forceinline__ uint32_t shift_codes(uint32_t w, float s) {
     return to_e4m3x4(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
+// One unit: the blocks whose first entry lies in the window from t0 on, of one kv head's K or V.
+// ent, before: this lane's of the 32 entries from t0 on, and of the 32 before them.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_append8_kernel(const __grid_constant__ Append8Args a) {
+__device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int head, int64_t ent, int64_t before,
+                                            int* token_at) {
     constexpr int kLanes = D / 8;            // lanes of a row: 8 values each
     constexpr int kPar = 32 / kLanes;        // rows a warp handles at once
     constexpr int kSteps = kBlockSize / kPar;
     const int lane = threadIdx.x & 31;
-    pdl_trigger();
-    pdl_wait();
-    const int heads2 = 2 * a.num_kv_heads;
-    const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int head = static_cast<int>(unit % heads2);  // kv head, then K or V
-    const int t0 = static_cast<int>(min((long long)a.num_tokens, unit / heads2 * a.window));
-    const int t1 = static_cast<int>(min((long long)a.num_tokens, (long long)t0 + a.window));
     const int kvh = head >> 1, is_v = head & 1;
-
-    // the window's entries, one a lane, and which of them is its block's first: the entry before
-    // it that names a slot is of another block
-    __shared__ int tokens[kWarps][kBlockSize];
-    int* token_at = tokens[threadIdx.x >> 5];
+    const auto slot_at = [&](long long t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1; };
     const auto in_pool = [&](int64_t s) { return s >= 0 && s < a.pool_slots; };
-    const int64_t mine = t0 + lane < t1 ? __ldg(a.slots + t0 + lane) : -1;
-    if (mine >= a.pool_slots && head == 0) atomicOr(a.status, kDevOutOfRange);
-    const bool named = in_pool(mine);
-    const int64_t my_block = named ? mine / kBlockSize : -1;
-    const unsigned all_named = __ballot_sync(0xffffffffu, named);
-    if (!all_named) return;
-    const unsigned before = all_named & ((1u << lane) - 1u);
-    const int64_t prev = __shfl_sync(0xffffffffu, my_block, before ? 31 - __clz(before) : 0);
-    unsigned firsts = __ballot_sync(0xffffffffu, named && before && prev != my_block);
+    // an entry is its block's first if the one before it that names a slot is of another block
+    const unsigned window = (1u << a.window) - 1u;
+    if (ent >= a.pool_slots && head == 0 && window >> lane & 1u) atomicOr(a.status, kDevOutOfRange);
+    const int64_t block_of_ent = in_pool(ent) ? ent / kBlockSize : -1;
+    const unsigned named = __ballot_sync(0xffffffffu, block_of_ent >= 0);
+    if (!(named & window)) return;
+    const unsigned lower = named & ((1u << lane) - 1u);
+    const int64_t prev = __shfl_sync(0xffffffffu, block_of_ent, lower ? 31 - __clz(lower) : 0);
+    unsigned firsts = window & __ballot_sync(0xffffffffu, block_of_ent >= 0 && lower && prev != block_of_ent);
     {
-        // the window's first named entry: look back past it
-        const int f = __ffs(all_named) - 1;
-        const int64_t block = __shfl_sync(0xffffffffu, my_block, f);
+        // the window's first named entry: look back past its start, farther if need be
+        const int f = __ffs(named) - 1;
+        const int64_t block = __shfl_sync(0xffffffffu, block_of_ent, f);
         bool first = true;
+        int64_t s = before;
         for (int p = t0 - 1; p >= 0; p -= 32) {
-            const int64_t s = p - lane >= 0 ? __ldg(a.slots + p - lane) : -1;
             const unsigned some = __ballot_sync(0xffffffffu, in_pool(s));
-            if (!some) continue;
-            first = __shfl_sync(0xffffffffu, s, __ffs(some) - 1) / kBlockSize != block;
-            break;
+            if (some) {
+                first = __shfl_sync(0xffffffffu, s, __ffs(some) - 1) / kBlockSize != block;
+                break;
+            }
+            s = slot_at((long long)p - 32 - lane);
         }
-        if (first) firsts |= 1u << f;
+        if (first && f < a.window) firsts |= 1u << f;
     }
 
     for (; firsts; firsts &= firsts - 1) {
-        const int f = __ffs(firsts) - 1, t = t0 + f;
-        const int64_t block = __shfl_sync(0xffffffffu, my_block, f);
-        // the block's entries: token_at[o] is the token whose row goes to offset o (-1: none); of
-        // entries with the same slot the last counts
+        const int f = __ffs(firsts) - 1;
+        const int64_t block = __shfl_sync(0xffffffffu, block_of_ent, f);
+        // the block's entries, up to the first of another block: token_at[o] is the token whose row
+        // goes to offset o (-1: none); of entries with the same slot the last counts
         if (lane < kBlockSize) token_at[lane] = -1;
         __syncwarp();
-        for (int p = t; p < a.num_tokens; p += 32) {
-            const int64_t s = p + lane < a.num_tokens ? __ldg(a.slots + p + lane) : -1;
-            const bool here = in_pool(s);
-            const unsigned other = __ballot_sync(0xffffffffu, here && s / kBlockSize != block);
-            if (here && lane < (other ? __ffs(other) - 1 : 32)) atomicMax(&token_at[s % kBlockSize], p + lane);
-            if (other) break;
+        unsigned other = named & (~0u << f) & __ballot_sync(0xffffffffu, block_of_ent != block);
+        if (lane >= f && block_of_ent == block && lane < (other ? __ffs(other) - 1 : 32))
+            atomicMax(&token_at[ent % kBlockSize], t0 + lane);
+        for (long long p = (long long)t0 + 32; !other && p < a.num_tokens; p += 32) {
+            const int64_t s = slot_at(p + lane);
+            other = __ballot_sync(0xffffffffu, in_pool(s) && s / kBlockSize != block);
+            if (in_pool(s) && lane < (other ? __ffs(other) - 1 : 32))
+                atomicMax(&token_at[s % kBlockSize], static_cast<int>(p) + lane);
         }
         __syncwarp();
         const int token = lane < kBlockSize ? token_at[lane] : -1;
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append8_kernel(const __grid_co
             }
             k = max(k, k_old);
         }
-        const float s = exp2_int(-k);
+        const __nv_bfloat162 s = __float2bfloat162_rn(exp2_int(-k));
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int row = i * kPar + sub;
@@ -172,6 +175,21 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append8_kernel(const __grid_co
         __syncwarp();  // every lane has read the old exponent
         if (lane == 0) *exp_at = static_cast<uint8_t>(k + kExpBias);
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append8_kernel(const __grid_constant__ Append8Args a) {
+    __shared__ int tokens[kWarps][kBlockSize];
+    const int lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
+    const int heads2 = 2 * a.num_kv_heads;
+    const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long start = unit / heads2 * a.window;
+    if (start >= a.num_tokens) return;
+    const auto slot_at = [&](long long t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1; };
+    append_unit<D>(a, (int)start, (int)(unit % heads2), slot_at(start + lane), slot_at(start - 1 - lane),
+                   tokens[threadIdx.x >> 5]);
 }
 
 }  // namespace
