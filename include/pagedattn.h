@@ -89,7 +89,8 @@ typedef struct {
  * so reading the pool rounds nothing.  Half the bytes of a bf16 pool (and 2 per block and kv
  * head): half the time of a decode, and twice the blocks of a memory budget
  * (pa_kv_block_bytes with dtype_bytes = 1).  The caller owns the three tensors and zeroes
- * them, or at least writes a block's offset 0 before its other rows.
+ * them, or at least writes a block's offset 0 before its other rows; exponents outside the range
+ * (a zeroed pool's) are read as its nearer end.
  */
 typedef struct {
     void *k_cache;        /* [num_blocks, num_kv_heads, 16, head_dim] e4m3, 16-byte aligned */
@@ -147,7 +148,8 @@ int pa_kv_copy(const pa_pool *pool, const int64_t *src_slots, const int64_t *dst
  * must be consecutive entries of slot_mapping (negative entries between them do not count), as
  * the tokens of a sequence are; a block that comes up again later in the same call is a caller
  * error, and so are calls that write the same block at the same time.  Of entries with the same
- * slot the last counts.  Arguments and errors otherwise as pa_kv_append.
+ * slot the last counts.  Arguments and errors otherwise as pa_kv_append.  Rows are not copied from
+ * block to block of an 8-bit pool: admit requests with pa_bm_admit, whose hits are whole blocks.
  */
 int pa_kv_append8(const pa_pool8 *pool, const void *k_new, const void *v_new, const int64_t *slot_mapping,
                   int32_t num_tokens, pa_stream_t stream);

@@ -346,11 +346,12 @@ def _arg(t: torch.Tensor, dtype, name: str, device: int) -> int:
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
     """A result tensor of t's shape, type and device, allocated for the stream that writes it."""
     if stream is None:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return torch.empty_like(t)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return torch.empty_like(t)
 
 
 def _call(what: str, device: int, stream, *args) -> None:
@@ -465,7 +466,8 @@ def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weight
         return out
     need = B * pool.num_kv_heads * width * (16 if Hq // pool.num_kv_heads > 8 else 8)
     if workspace is None:
-        workspace = _like(weights.expand(need // weights.numel(), *weights.shape), stream)
+        workspace = torch.empty(need, dtype=torch.float32, device=weights.device) if stream is None else \
+            _like(weights.expand(need // weights.numel(), *weights.shape), stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace: need {need} floats, got {workspace.numel()}")
     _call(what, device, stream, pool.ref, _arg(q, torch.bfloat16, "q", device),

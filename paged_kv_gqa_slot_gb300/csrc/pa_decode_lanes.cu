@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
     };
     const auto exps_of = [&](int k, int blk) -> int {
         if (BITS == 16) return kExpBias * 257;
-        return k < n ? __ldg(a.exps + (size_t)blk * a.num_kv_heads + kvh) : kExpBias * 257;
+        return k < n ? valid_exps(__ldg(a.exps + (size_t)blk * a.num_kv_heads + kvh)) : kExpBias * 257;
     };
     id = checked(lane, id);
     int ex = exps_of(lane, id);

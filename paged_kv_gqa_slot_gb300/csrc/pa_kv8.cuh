@@ -25,6 +25,14 @@ __device__ __forceinline__ float exp2_int(int e) {
     return __int_as_float((min(max(e, -126), 127) + 127) << 23);
 }
 
+// A block's word of exponents (K in the low byte), each brought into the range the format has: a
+// tile that was never written may hold anything, zeros first of all.
+__device__ __forceinline__ int valid_exps(int word) {
+    const int k = min(max(word & 255, kExpMin + kExpBias), kExpMax + kExpBias);
+    const int v = min(max(word >> 8 & 255, kExpMin + kExpBias), kExpMax + kExpBias);
+    return k | v << 8;
+}
+
 // The smallest k with amax <= 448 * 2^k (amax finite, >= 0), within [kExpMin, kExpMax].
 // amax = f * 2^e with f in [1, 2), and 448 = 1.75 * 2^8.
 __device__ __forceinline__ int scale_exponent(float amax) {

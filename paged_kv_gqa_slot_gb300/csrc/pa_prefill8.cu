@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         const auto entry = [&](int blk) { return blk < nblk ? __ldg(bt + blk) : -1; };
         const auto exps_of = [&](int blk, int id) -> int {
             if (blk >= nblk) return kExpBias * 257;
-            return __ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh);
+            return valid_exps(__ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh));
         };
         int ex = exps_of(lane, entry(lane)), next_id = entry(32 + lane), next_ex = 0;
         float qf;  // log2(e) |scale| 2^eq, eq the power of two taken out of the row of q

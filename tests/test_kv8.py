@@ -466,3 +466,106 @@ def test_append_then_prefill_then_decode_follow_a_growing_sequence():
         ref, spread, _, mag = R.attention(q, k, v, [table.tolist()], [n], d ** -0.5, [0, c])
         check(out, ref, spread, n, mag)
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("how", ["k first", "v first", "one tensor", "same tensor"])
+def test_any_placement_of_the_two_pools(how, d):
+    """K and V of a block come by one copy over the distance of the pools, or by two where the pools are one."""
+    c = Case(71, [333, 50, 16], 8, 2, d)
+    nb = c.k.shape[0]
+    both = torch.empty(2 * nb + 3, *c.k.shape[1:], dtype=torch.uint8, device="cuda")
+    if how == "k first":
+        k, v = both[:nb], both[nb + 3:]
+    elif how == "v first":
+        k, v = both[nb + 1:2 * nb + 1], both[:nb]
+    elif how == "one tensor":
+        k, v = both[:2 * nb].view(2, nb, *c.k.shape[1:]).unbind(0)
+    else:
+        k = v = both[:nb]
+    k.copy_(c.k)
+    if how == "same tensor":
+        c.k, c.v = k, k
+    else:
+        v.copy_(c.v)
+    c.pool = pa.PaPool8(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), c.exps)
+    ref, spread, _, mag = c.reference()
+    check(pa.pa_decode8(c.pool, c.q, c.tables, c.lens, c.scale), ref, spread, 333, mag)
+    clean()
+
+
+@gpu
+def test_offsets_past_4_gb():
+    """Blocks whose codes lie more than 2^32 bytes into the pools."""
+    hkv, d, lens = 8, 128, [100, 777]
+    nb = (1 << 32) // (hkv * 16 * d) + 64
+    c = Case(72, lens, 16, hkv, d, [20, 17])
+    far = np.random.RandomState(1).permutation(64)[:c.k.shape[0]] + nb - 64
+    far_t = torch.tensor(far, device="cuda")
+    k, v = (torch.empty(nb, hkv, 16, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    exps = torch.zeros(nb, hkv, 2, dtype=torch.uint8, device="cuda")
+    used = len(far)
+    k[far_t], v[far_t], exps[far_t] = c.k[:used], c.v[:used], c.exps[:used]
+    remap = {old: int(far[old]) for old in range(used)}
+    tables = [[remap.get(x, -7) if x >= 0 else x for x in row] for row in c.tables_h]
+    c.tables = torch.tensor(tables, dtype=torch.int32, device="cuda")
+    ref, spread, _, mag = c.reference()
+    pool = pa.PaPool8(k, v, exps)
+    out = pa.pa_prefill_chunked8(pool, c.q, c.cu, c.tables, c.lens, c.scale, c.max_chunk)
+    check(out, ref, spread, 777, mag)
+    last = torch.stack([c.q[19], c.q[36]])
+    out = pa.pa_decode8(pool, last, c.tables, c.lens, c.scale)
+    check(out, ref[[19, 36]], spread[[19, 36]], 777, mag)
+    new = torch.randn(3, hkv, d, device="cuda").to(torch.bfloat16)
+    blk = int(far[0])
+    pa.pa_kv_append8(pool, new, new, torch.tensor([blk * 16, blk * 16 + 1, blk * 16 + 2], device="cuda"))
+    kh, eh = np.zeros((1, hkv, 16, d), np.uint8), np.zeros((1, hkv, 1), np.uint8)
+    R.append(kh, eh[:, :, 0], new.double().cpu().numpy(), [0, 1, 2])
+    assert np.array_equal(R.VALUES[k[blk, :, :3].cpu().numpy()], R.VALUES[kh[0, :, :3]])
+    assert np.array_equal(exps[blk, :, 0].cpu().numpy(), eh[0, :, 0])
+    clean()
+
+
+@gpu
+def test_blocks_of_a_zeroed_pool_that_were_never_written():
+    """A sequence over two written blocks and two of zeros (exponent byte 0) beside them."""
+    hkv, d, nb = 2, 128, 8
+    pool = pa.PaPool8.zeros(nb, hkv, d)
+    new = torch.randn(32, hkv, d, device="cuda").to(torch.bfloat16)
+    pa.pa_kv_append8(pool, new, new, torch.arange(16, 48, device="cuda"))
+    tables = torch.tensor([[0, 1, 2, 5], [4, 3, 0, 0]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([64, 30], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 8, d, device="cuda").to(torch.bfloat16)
+    k, v = R.dequant(pool.k_cache, pool.exps[..., 0]), R.dequant(pool.v_cache, pool.exps[..., 1])
+    ref, spread, _, mag = R.attention(q, k, v, tables.tolist(), [64, 30], d ** -0.5)
+    out = pa.pa_decode8(pool, q, tables, lens, d ** -0.5)
+    check(out, ref, spread, 64, mag)
+    assert (out[1] == 0).all()
+    cu = torch.tensor([0, 17, 47], dtype=torch.int32, device="cuda")
+    q = torch.randn(47, 8, d, device="cuda").to(torch.bfloat16)
+    ref, spread, _, mag = R.attention(q, k, v, tables.tolist(), [64, 30], d ** -0.5, [0, 17, 47])
+    out = pa.pa_prefill_chunked8(pool, q, cu, tables, lens, d ** -0.5, 30)
+    check(out, ref, spread, 64, mag)
+    clean()
+
+
+@gpu
+def test_other_streams_handles_and_devices():
+    c = Case(73, [100, 20], 8, 2, 128)
+    want = pa.pa_decode8(c.pool, c.q, c.tables, c.lens, c.scale)
+    torch.cuda.synchronize()
+    assert torch.equal(pa.pa_decode8(c.pool, c.q, c.tables, c.lens, c.scale, stream=0), want)  # the legacy default stream
+    with pytest.raises(ValueError):
+        pa.pa_decode8(c.pool, c.q.cpu(), c.tables, c.lens, c.scale)
+    with pytest.raises(ValueError):
+        pa.pa_decode8(c.pool, c.q, c.tables.cpu(), c.lens, c.scale)
+    with pytest.raises(ValueError):
+        pa.pa_decode8(c.pool, c.q, c.tables, c.lens, c.scale, out=want[:1])
+    with pytest.raises(ValueError):
+        pa.pa_decode8(c.pool, c.q.transpose(0, 1).contiguous().transpose(0, 1), c.tables, c.lens, c.scale)
+    with pytest.raises(ValueError):
+        pa.pa_decode8(c.pool, c.q, c.tables[:1], c.lens, c.scale)
+    with pytest.raises(ValueError):
+        pa.pa_prefill_chunked8(c.pool, c.q, c.lens, c.tables, c.lens, c.scale, 1)
+    clean()
