@@ -94,13 +94,13 @@ struct LanesArgs {
 };
 
 // Warps of a CTA: 4, or 3 where a thread needs more than 128 registers, so that four CTAs fit an
-// SM in either case: 512 CTAs (64 sequences of 8 kv heads) are then one wave.  WIDE: twice as
-// many, two CTAs an SM, where even 16 splits of every sequence leave SMs empty.
+// SM in either case: 512 CTAs (64 sequences of 8 kv heads) are then one wave.  WIDE 1, 2: twice and
+// four times as many, two CTAs and one an SM, where even the most splits leave SMs empty.
 __host__ __device__ constexpr bool fits128(int bits, int d, int nt) { return d == 64 || (bits == 8 && nt == 1); }
-__host__ __device__ constexpr int warps_of(int bits, int d, int nt, bool wide) {
-    return (fits128(bits, d, nt) ? 4 : 3) * (wide ? 2 : 1);
+__host__ __device__ constexpr int warps_of(int bits, int d, int nt, int wide) {
+    return (fits128(bits, d, nt) ? 4 : 3) << wide;
 }
-__host__ __device__ constexpr int ctas_of(bool wide) { return wide ? 2 : 4; }
+__host__ __device__ constexpr int ctas_of(int wide) { return 4 >> wide; }
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
@@ -150,7 +150,7 @@ __device__ __forceinline__ float rescale_sum(float l, float d) {
 // instruction's groups hit different banks.
 __device__ __forceinline__ int quad_at(int grp) { return grp ^ ((grp >> 2) & 1); }
 
-template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, bool WIDE>
+template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, int WIDE>
 __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE))
     decode_lanes_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ LanesArgs a) {
@@ -695,7 +695,7 @@ struct LanesPool {
     int num_blocks, num_kv_heads, head_dim;
 };
 
-template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, bool WIDE>
+template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, int WIDE>
 cudaError_t launch_as(const LanesPool& pool, const AttnArgs& a, int splits, cudaStream_t stream) {
     using Sh = Lanes<BITS, D>;
     auto kern = decode_lanes_kernel<BITS, D, NT, MQ, WEIGHTS, WIDE>;
@@ -751,10 +751,9 @@ cudaError_t launch_as(const LanesPool& pool, const AttnArgs& a, int splits, cuda
     return cudaLaunchKernelEx(&cfg, kern, maps.k, maps.v, d);
 }
 
-// How many clusters of `splits` CTAs (four an SM, or two wide ones) the device runs at once; asked
-// once per device.
-int cluster_capacity(bool wide, int splits) {
-    static std::atomic<int> cached[64][2][17];
+// How many clusters of `splits` CTAs the device runs at once; asked once per device.
+int cluster_capacity(int wide, int splits) {
+    static std::atomic<int> cached[64][3][17];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (const int c = cached[dev][wide][splits].load(std::memory_order_relaxed)) return c - 1;
@@ -777,16 +776,16 @@ int cluster_capacity(bool wide, int splits) {
         return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
     };
     using Sh = Lanes<8, 128>;
-    const int n = wide ? ask(decode_lanes_kernel<8, 128, 1, false, false, true>, 8, Sh::smem(8, 2))
-                       : ask(decode_lanes_kernel<8, 128, 1, false, false, false>, 4, Sh::smem(4, 4));
+    const int n = wide == 2   ? ask(decode_lanes_kernel<8, 128, 1, false, false, 2>, 16, Sh::smem(16, 1))
+                  : wide == 1 ? ask(decode_lanes_kernel<8, 128, 1, false, false, 1>, 8, Sh::smem(8, 2))
+                              : ask(decode_lanes_kernel<8, 128, 1, false, false, 0>, 4, Sh::smem(4, 4));
     cudaGetLastError();
     cached[dev][wide][splits].store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
 struct Split {
-    int splits;
-    bool wide;
+    int splits, wide;
 };
 
 // Splits of every (sequence, kv head), as CTAs of a cluster.  Measured on GB300, us a call:
@@ -794,29 +793,34 @@ struct Split {
 //     1; one cluster too many costs a second wave (32 items: wide at 8 splits 16, at 9 23);
 //   * but at least ten blocks a warp once every SM has a CTA: 30 x 1000 (240 items) 13.9 at 1,
 //     15.4 at 2; 24 x ~1500 21.9 at 1, 17.5 at 3;
-//   * wide where even 16 splits leave room, at four blocks a warp: 1 x 32768 (8 items) 20.7 wide at
-//     12 splits, 25.9 at 16 of the others; 4 x 8192 15.9 wide at 8, 17.2;
+//   * wide where even the most splits leave room, at four blocks a warp: 1 x 32768 (8 items) 17.6 with
+//     16 warps at 12 splits (13 would not all run at once), 20.7 with 8 warps, 25.9 with 4; 4 x 8192
+//     15.8 with 8 warps at 8 splits, 17.2 with 4 at 16;
 //   * two in a grid of over three CTAs an SM with long sequences, whose CTAs end far apart: 64 x 8192
 //     152 against 159, but 64 x 2048 47 against 44.
 Split split_for(int batch, int num_kv_heads, int max_blocks, int warps) {
     const int items = batch * num_kv_heads, sms = device_info().num_sms;
-    if (items >= 3 * sms) return {max_blocks >= 320 ? 2 : 1, false};
-    if (items <= cluster_capacity(false, 16)) {
-        int s = 12;
-        while (s > 1 && items > cluster_capacity(true, s)) --s;
-        if (s > 1 && max_blocks >= 4 * s * 2 * warps) return {s, true};
+    if (items >= 3 * sms) return {max_blocks >= 320 ? 2 : 1, 0};
+    if (items <= cluster_capacity(0, 16)) {
+        for (int wide = 2; wide; --wide) {
+            int s = wide == 2 ? 16 : 12;
+            while (s > 1 && items > cluster_capacity(wide, s)) --s;
+            if (wide == 2 && s < 12) continue;
+            if (s > 1 && max_blocks >= 4 * s * (warps << wide)) return {s, wide};
+        }
     }
     const int least = items >= sms ? 10 * warps : 4;  // blocks of a CTA
     int s = std::min(16, std::max(1, max_blocks / least));
-    while (s > 1 && items > cluster_capacity(false, s)) --s;
-    return {s, false};
+    while (s > 1 && items > cluster_capacity(0, s)) --s;
+    return {s, 0};
 }
 
 template <int BITS, int D, int NT, bool MQ, bool WEIGHTS>
 cudaError_t launch_one(const LanesPool& pool, const AttnArgs& a, cudaStream_t stream) {
-    const Split s = split_for(a.batch, pool.num_kv_heads, a.max_blocks, warps_of(BITS, D, NT, false));
-    return s.wide ? launch_as<BITS, D, NT, MQ, WEIGHTS, true>(pool, a, s.splits, stream)
-                  : launch_as<BITS, D, NT, MQ, WEIGHTS, false>(pool, a, s.splits, stream);
+    const Split s = split_for(a.batch, pool.num_kv_heads, a.max_blocks, warps_of(BITS, D, NT, 0));
+    return s.wide == 2   ? launch_as<BITS, D, NT, MQ, WEIGHTS, 2>(pool, a, s.splits, stream)
+           : s.wide == 1 ? launch_as<BITS, D, NT, MQ, WEIGHTS, 1>(pool, a, s.splits, stream)
+                         : launch_as<BITS, D, NT, MQ, WEIGHTS, 0>(pool, a, s.splits, stream);
 }
 
 template <int BITS, bool MQ, bool WEIGHTS>
