@@ -33,12 +33,15 @@
 //
 // Measured on GB300 (32 q / 8 kv heads, d 128): 8 x 256 over 768 cached tokens 53 us (the bf16 pool's
 // kernel on the same values 59), 8 x 1024 over 1024 250 us (305), 1.20 us a stage of two tiles.  What
-// bounds a stage is shared memory: Q K^T reads Q and K (768 cycles for the two tiles), u V reads V
-// (256), and the codes are written, read and stored widened (512), 1536 of its 2280 cycles; the
-// MMA warp spends 1660 of them in issuing.  Tried and not kept: Q in tensor memory, which leaves room
-// for one score buffer a tile (1.14 us a stage, but a single tile's chain 10% longer: 22.7 against
-// 20.5 us for 1 x 256 + 768); stages of 128 keys with one buffer (1.48 us); codes loaded into
-// registers instead of by cp.async (1.74 us).
+// bounds a stage is the matrix pipe with its hand-overs: its instructions read 768 cycles' worth of
+// shared memory for Q K^T of the two tiles and 256 for u V, and the codes are written, read and
+// stored widened (512), 1536 of a stage's 2280 cycles.  With half of Q K^T's instructions left out the
+// kernel took 23% less, without the converters 5%, without the softmax's arithmetic 8%.
+// Tried and not kept: Q in tensor memory, which leaves room for one score buffer a tile (1.14 us
+// a stage, but a single tile's chain 10% longer: 22.7 against 20.5 us for 1 x 256 + 768); stages of
+// 128 keys with one buffer (1.16 us; 21.9 for the single tile), and those with two threads a row
+// (1.26 us); two threads a row on the first (1.24 us; 23.2); codes loaded into registers instead of by
+// cp.async (1.74 us).
 #include <algorithm>
 #include <cmath>
 
