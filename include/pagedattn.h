@@ -297,9 +297,8 @@ int pa_prefill_chunked(const pa_pool *pool, const void *q, const int32_t *cu_q_l
                        int32_t max_chunk, float scale, void *out, pa_stream_t stream);
 
 /*
- * pa_prefill_chunked8 -- pa_prefill_chunked over an 8-bit pool: same arguments, errors, kernels by
- * shape and arithmetic, on the pool's exact bf16 values (chunks of at most 16 / group queries
- * as pa_decode8).
+ * pa_prefill_chunked8 -- pa_prefill_chunked over an 8-bit pool: same arguments and
+ * errors, arithmetic as pa_decode8.  Chunks of at most 16 / group queries run on the decode kernel.
  */
 int pa_prefill_chunked8(const pa_pool8 *pool, const void *q, const int32_t *cu_q_lens, const int32_t *block_tables,
                         int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads,
