@@ -9,14 +9,15 @@
 // round-robin, so a warp's block indices do not depend on the sequence's length.
 //
 // Products, 8 bits.  The codes enter the tensor core as f16, which holds every e4m3 value
-// exactly, at one conversion per two codes.  K's scale joins the softmax scale (one factor
-// per block and head).  q enters as f16 too, after its row is brought to a maximum in
-// [2^14, 2^15) by a power of two that joins the same factor: an element loses bits only below
-// 2^-29 of the row's maximum.  V's scale joins the exponent: with x = log2(e) scale <q, K> the
-// weight the V product takes is u = 2^(x + kV - base), base following the maximum of x + kV, so
-// u fits f16 whatever the blocks' scales, and the largest contributions, not the largest
-// probabilities, set its range.  u is rounded to f16's 11 bits (an eighth of the rounding of the
-// bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.
+// exactly, at one conversion per two codes.  (Codes as they are against q in two e4m3 parts, without a
+// conversion: 64 x ~1088 tokens 27.4 us against 25.9, 4 queries of each 42.8 against 32.4.)  K's
+// scale joins the softmax scale (one factor per block and head).  q enters as f16 too, after its
+// row is brought to a maximum in [2^14, 2^15) by a power of two that joins the same factor: an
+// element loses bits only below 2^-29 of the row's maximum.  V's scale joins the exponent: with
+// x = log2(e) scale <q, K> the weight the V product takes is u = 2^(x + kV - base), base following
+// the maximum of x + kV, so u fits f16 whatever the blocks' scales, and the largest contributions,
+// not the largest probabilities, set its range.  u is rounded to f16's 11 bits (an eighth of the
+// rounding of the bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.
 // 16 bits: the same with kK = kV = 0 on bf16 MMAs, u carried as two bf16 parts.
 //
 // Loads.  Which d values make one MMA step, and which token is which MMA row, is free as long as q,
@@ -63,8 +64,15 @@ struct Lanes {
     __host__ __device__ static constexpr int ring_bytes(int warps, int ctas) {
         return stages(warps, ctas) * warps * kBlockBytes;
     }
-    static constexpr int smem(int warps, int ctas) {
-        const int ring = ring_bytes(warps, ctas) + stages(warps, ctas) * warps * 8;
+    // behind the rings and their barriers: the q fragments, where the registers of four warps have no
+    // room for them (the same for every warp; 8 x ~2000 tokens, 16 heads a group: 14.4 us, with
+    // three warps and q in registers 15.8, with four and 112 bytes of spills 15.4)
+    __host__ __device__ static constexpr bool q_shared(int nt) { return BITS == 8 && D == 128 && nt == 2; }
+    __host__ __device__ static constexpr int q_at(int warps, int ctas) {
+        return (ring_bytes(warps, ctas) + stages(warps, ctas) * warps * 8 + 15) / 16 * 16;
+    }
+    static constexpr int smem(int warps, int ctas, int nt) {
+        const int ring = q_at(warps, ctas) + (q_shared(nt) ? D / 16 * 32 * 16 : 0);
         return ring > merge_bytes(warps) ? ring : merge_bytes(warps);
     }
     static constexpr int kQuads = D / 32;  // 4-float groups of O a lane holds per head
@@ -93,10 +101,10 @@ struct LanesArgs {
     int paired, k_second;
 };
 
-// Warps of a CTA: 4, or 3 where a thread needs more than 128 registers, so that four CTAs fit an
-// SM in either case: 512 CTAs (64 sequences of 8 kv heads) are then one wave.  WIDE 1, 2: twice and
+// Warps of a CTA: 4, or 3 where a thread needs more than 128 registers (16-bit rows of d 128), so
+// that four CTAs fit an SM in either case: 512 CTAs (64 sequences of 8 kv heads) are then one wave.  WIDE 1, 2: twice and
 // four times as many, two CTAs and one an SM, where even the most splits leave SMs empty.
-__host__ __device__ constexpr bool fits128(int bits, int d, int nt) { return d == 64 || (bits == 8 && nt == 1); }
+__host__ __device__ constexpr bool fits128(int bits, int d, int nt) { return d == 64 || bits == 8; }
 __host__ __device__ constexpr int warps_of(int bits, int d, int nt, int wide) {
     return (fits128(bits, d, nt) ? 4 : 3) << wide;
 }
@@ -109,6 +117,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
 }
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
     uint2 v;
@@ -298,6 +310,17 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
         }
     }
 
+    constexpr bool kQShared = Sh::q_shared(NT);
+    const uint32_t q_smem = smem_u32(smem) + Sh::q_at(kWarps, kCtas) + lane * 16;
+    if constexpr (kQShared) {
+        if (warp == 0) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                sts16(q_smem + s * 512, make_uint4(qb[0][s][0], qb[0][s][1], qb[NT - 1][s][0], qb[NT - 1][s][1]));
+        }
+        __syncthreads();
+    }
+
     float ot[NT][kSteps][4];
     float m[NT][2], l[NT][2];  // base and normaliser of the columns
 #pragma unroll
@@ -369,10 +392,16 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
                     uint32_t a0, a1, a2, a3;
                     e4m3x4_to_f16x4(w0[s], a0, a2);
                     e4m3x4_to_f16x4(w8[s], a1, a3);
+                    if constexpr (kQShared) {
+                        const uint4 f = lds16(q_smem + (c * 4 + s) * 512);
+                        mma_f16_16816(st[0], a0, a1, a2, a3, f.x, f.y);
+                        mma_f16_16816(st[1], a0, a1, a2, a3, f.z, f.w);
+                    } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(st[NT == 1 ? s & 1 : nt], a0, a1, a2, a3, qb[nt][c * 4 + s][0],
-                                      qb[nt][c * 4 + s][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16_16816(st[NT == 1 ? s & 1 : nt], a0, a1, a2, a3, qb[nt][c * 4 + s][0],
+                                          qb[nt][c * 4 + s][1]);
+                    }
                 }
             } else {
 #pragma unroll
@@ -702,7 +731,7 @@ cudaError_t launch_as(const LanesPool& pool, const AttnArgs& a, int splits, cuda
     constexpr int kWarps = warps_of(BITS, D, NT, WIDE);
     static OncePerDevice configured;  // per instantiation
     cudaError_t se = configured.run([&] {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::smem(kWarps, ctas_of(WIDE)));
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::smem(kWarps, ctas_of(WIDE), NT));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         return e;
@@ -736,7 +765,7 @@ cudaError_t launch_as(const LanesPool& pool, const AttnArgs& a, int splits, cuda
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, pool.num_kv_heads, a.batch);
     cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = Sh::smem(kWarps, ctas_of(WIDE));
+    cfg.dynamicSmemBytes = Sh::smem(kWarps, ctas_of(WIDE), NT);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2] = {pdl_attribute(), {}};
     cfg.attrs = attr;
@@ -776,9 +805,9 @@ int cluster_capacity(int wide, int splits) {
         return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
     };
     using Sh = Lanes<8, 128>;
-    const int n = wide == 2   ? ask(decode_lanes_kernel<8, 128, 1, false, false, 2>, 16, Sh::smem(16, 1))
-                  : wide == 1 ? ask(decode_lanes_kernel<8, 128, 1, false, false, 1>, 8, Sh::smem(8, 2))
-                              : ask(decode_lanes_kernel<8, 128, 1, false, false, 0>, 4, Sh::smem(4, 4));
+    const int n = wide == 2   ? ask(decode_lanes_kernel<8, 128, 1, false, false, 2>, 16, Sh::smem(16, 1, 1))
+                  : wide == 1 ? ask(decode_lanes_kernel<8, 128, 1, false, false, 1>, 8, Sh::smem(8, 2, 1))
+                              : ask(decode_lanes_kernel<8, 128, 1, false, false, 0>, 4, Sh::smem(4, 4, 1));
     cudaGetLastError();
     cached[dev][wide][splits].store(n + 1, std::memory_order_relaxed);
     return n;
