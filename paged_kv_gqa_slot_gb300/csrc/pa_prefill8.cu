@@ -55,8 +55,8 @@ constexpr int kRows = 128;                 // MMA M: rows of a query tile
 constexpr int kKeys = 64;                  // keys of a stage
 constexpr int kParts = kKeys / kBlockSize;  // pool blocks of a stage
 constexpr int kKStages = 3, kVStages = 3;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kCvtWarp = 9, kCvtWarps = 7;
-constexpr int kAhead = 4;                  // units a converter warp has in hand or in flight
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kMmaWarps = 2, kCvtWarp = 10, kCvtWarps = 6;
+constexpr int kAhead = 2;                  // pairs of blocks a converter warp has in hand or in flight
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;             // per tile: two 64-column score buffers, then O
 constexpr uint32_t kTmemTile = 256;
@@ -76,7 +76,7 @@ struct Pre8 {
     static constexpr int kOffK = 2 * kQTile;
     static constexpr int kOffV = kOffK + kKStages * kStage;
     static constexpr int kOffRaw = kOffV + kVStages * kStage;
-    static constexpr int kOffBars = kOffRaw + kCvtWarps * kAhead * kUnit;
+    static constexpr int kOffBars = kOffRaw + kCvtWarps * kAhead * 2 * kUnit;
     static constexpr int kOffInv = kOffBars + 512;     // [2][128] 1 / l, then whether every wait ended
     static constexpr int kSmem = kOffInv + 2 * kRows * 4 + 16;
     static constexpr int kLoads = kBlockSize * D / 512;  // 16-byte pieces of a block a lane takes
@@ -85,6 +85,7 @@ static_assert(Pre8<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct Bars8 {
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t raw_full[kCvtWarps][kAhead];
     uint64_t q_full, s_full[2][2], p_full[2][2], o_done[2], o_final[2], drain;  // [tile][buffer]
     uint32_t tmem_base;
 };
@@ -107,100 +108,94 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
     return tc_idesc_bf16(kRows, n, b_mn_major) & ~((1u << 7) | (1u << 10));  // f16 A and B
 }
 
-// Group grp of the stream K(0), then K(j + 1), V(j) for j = 0, 1, ..., each the kParts blocks of
-// one stage (the last stage has no K(j + 1)).
-struct Group {
-    int stage;
-    bool is_v;
-};
-__device__ __forceinline__ Group group_of(int grp, int nst) {
-    Group r;
-    const bool last = grp == 2 * nst - 1;
-    r.is_v = last || (grp > 0 && grp % 2 == 0);
-    r.stage = last ? nst - 1 : r.is_v ? grp / 2 - 1 : (grp + 1) / 2;
-    return r;
+// `bytes` contiguous bytes into shared memory, completing on `bar` (all multiples of 16).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Converter warp w: units w, w + kCvtWarps, ... of the stream.
+// Converter warp w: of K (the first half of the warps) or V, every kSide-th pair of blocks, whose codes
+// come into the warp's own raw slots by a bulk copy each, kAhead pairs ahead.
 template <int D>
 struct Converter {
     using P = Pre8<D>;
+    static constexpr int kSide = kCvtWarps / 2, kPairs = kParts / 2;
     uint8_t* smem;
     Bars8* bars;
     const Pre8Args& a;
     const int32_t* bt;
-    int kvh, L, nst, nblk, w, lane;
-    int next_id;  // of the unit to be issued next
+    const uint8_t* pool;  // of this warp's side, at its kv head
+    int L, nst, nblk, w, lane, first;
+    bool is_v;
+    int next_id;  // lanes 0 and 1: of the pair to be fetched next
 
-    __device__ __forceinline__ int total() const { return 2 * nst * kParts; }
+    __device__ __forceinline__ Converter(uint8_t* smem_, Bars8* bars_, const Pre8Args& a_, const int32_t* bt_, int kvh,
+                                         int L_, int nst_, int nblk_, int w_, int lane_)
+        : smem(smem_), bars(bars_), a(a_), bt(bt_), L(L_), nst(nst_), nblk(nblk_), w(w_), lane(lane_) {
+        is_v = w >= kSide;
+        first = is_v ? w - kSide : w;
+        pool = (is_v ? a.v : a.k) + (size_t)kvh * P::kUnit;
+    }
     __device__ __forceinline__ uint32_t raw(int n) const {
-        return smem_u32(smem + P::kOffRaw) + (w * kAhead + n % kAhead) * P::kUnit + lane * 16;
+        return smem_u32(smem + P::kOffRaw) + (w * kAhead + n % kAhead) * (2 * P::kUnit);
     }
-    __device__ __forceinline__ int block_of(int u) const { return group_of(u / kParts, nst).stage * kParts + u % kParts; }
-    // id of unit u's block; -1 past the keys the CTA needs
-    __device__ __forceinline__ int entry(int u) const {
-        if (u >= total()) return -1;
-        const int lb = block_of(u);
-        return lb < nblk ? __ldg(bt + lb) : -1;
-    }
-    // n-th unit of this warp: start its copy, and load the next one's table entry
+    // the warp's n-th pair: start its copies, and load the next one's table entries
     __device__ __forceinline__ void issue(int n) {
-        const int u = w + n * kCvtWarps;
-        if (u < total() && block_of(u) < nblk) {
+        const int blk = 2 * (first + n * kSide) + lane, left = nblk - (blk - lane);
+        if (left <= 0) return;
+        uint64_t* bar = &bars->raw_full[w][n % kAhead];
+        if (lane == 0) mbar_arrive_expect_tx(bar, left > 1 ? 2 * P::kUnit : P::kUnit);
+        __syncwarp();
+        if (lane < 2 && lane < left) {
             int id = next_id;
             if (id < 0 || id >= a.num_blocks) {
-                if (lane == 0) atomicOr(a.status, kDevOutOfRange);
+                atomicOr(a.status, kDevOutOfRange);
                 id = 0;  // read inside the pool; the status word reports the bad id
             }
-            const uint8_t* src = (group_of(u / kParts, nst).is_v ? a.v : a.k) +
-                                 ((size_t)id * a.num_kv_heads + kvh) * P::kUnit + lane * 16;
-#pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) cp_async16(raw(n) + i * 512, src + i * 512);
+            bulk_load(raw(n) + lane * P::kUnit, pool + (size_t)id * a.num_kv_heads * P::kUnit, P::kUnit, bar);
+            if (blk + 2 * kSide < nblk) next_id = __ldg(bt + blk + 2 * kSide);
         }
-        cp_async_commit();
-        next_id = entry(u + kCvtWarps);
     }
     __device__ __forceinline__ void start() {
-        next_id = entry(w);
+        if (lane < kAhead) mbar_init(&bars->raw_full[w][lane], 1);
+        fence_mbar_init();
+        __syncwarp();
+        next_id = lane < 2 && 2 * first + lane < nblk ? __ldg(bt + 2 * first + lane) : -1;
         for (int n = 0; n < kAhead; ++n) issue(n);
     }
     __device__ __forceinline__ void run() {
+        static_assert(kKStages == kVStages, "one slot rule for both sides");
         bool ok = true;
         int n = 0;
-        for (int u = w; u < total(); u += kCvtWarps, ++n) {
-            const Group grp = group_of(u / kParts, nst);
-            const int part = u % kParts, lb = grp.stage * kParts + part;
-            cp_async_wait<kAhead - 1>();
-            uint4 codes[P::kLoads];
+        uint64_t *full = is_v ? bars->v_full : bars->k_full, *empty = is_v ? bars->v_empty : bars->k_empty;
+        uint8_t* slots = smem + (is_v ? P::kOffV : P::kOffK);
+        // rows from here on are zeros: past the blocks the CTA needs, and V past the sequence's end (u is 0
+        // there, but 0 times NaN is NaN)
+        const int end = is_v ? min(L, nblk * kBlockSize) : nblk * kBlockSize;
+        for (int pair = first; pair < nst * kPairs; pair += kSide, ++n) {
+            const int stage = pair / kPairs, slot = stage % kKStages;
+            uint4 codes[2 * P::kLoads];
+            if (2 * pair < nblk) {
+                ok = mbar_wait_warp(&bars->raw_full[w][n % kAhead], (n / kAhead) & 1);
+                if (!ok) break;
+            }
 #pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) {
-                // past the keys the CTA needs, and V past the sequence's end: zeros (u is 0 there,
-                // but 0 times NaN is NaN)
-                const int row = (i * 32 + lane) / (D / 16);
-                const bool in = lb < nblk && (!grp.is_v || lb * kBlockSize + row < L);
+            for (int i = 0; i < 2 * P::kLoads; ++i)
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
-                             : "r"(raw(n) + i * 512)
+                             : "r"(raw(n) + lane * 16 + i * 512)
                              : "memory");
-                if (!in) codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            const int nslots = grp.is_v ? kVStages : kKStages, slot = grp.stage % nslots;
-            if (grp.stage >= nslots)
-                ok = mbar_wait_warp(grp.is_v ? &bars->v_empty[slot] : &bars->k_empty[slot],
-                                    ((grp.stage / nslots) & 1) ^ 1);
-            if (!ok) break;
-            uint8_t* dst = smem + (grp.is_v ? P::kOffV : P::kOffK) + slot * P::kStage + part * (kBlockSize * 128);
+            if ((pair + 1) * 2 * kBlockSize > end) {
 #pragma unroll
-            for (int i = 0; i < P::kLoads; ++i) {
+                for (int i = 0; i < 2 * P::kLoads; ++i)
+                    if (pair * 2 * kBlockSize + (i * 32 + lane) / (D / 16) >= end) codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (stage >= kKStages) ok = mbar_wait_warp(&empty[slot], ((stage / kKStages) & 1) ^ 1);
+            if (!ok) break;
+            uint8_t* dst = slots + slot * P::kStage + pair % kPairs * (2 * kBlockSize * 128);
+#pragma unroll
+            for (int i = 0; i < 2 * P::kLoads; ++i) {
                 // 16 codes: the 16-byte chunks ch, ch + 1 of column half h; lanes of the second half
                 // store them in the other order, so that the lanes of one row hit different banks
                 const int piece = i * 32 + lane, row = piece / (D / 16), c = piece % (D / 16);
@@ -216,11 +211,15 @@ struct Converter {
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(grp.is_v ? &bars->v_full[slot] : &bars->k_full[slot]);
-            issue(n + kAhead);  // over the pieces just read
+            if (lane == 0) mbar_arrive(&full[slot]);
+            issue(n + kAhead);  // over the codes, which every lane has read
         }
-        cp_async_wait<0>();
-        if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
+        if (!ok) {
+            // a wait ran out: the copies in flight must still land before their memory is used again
+            for (int i = n; i < n + kAhead; ++i)
+                if (2 * (first + i * kSide) < nblk) mbar_wait_warp(&bars->raw_full[w][i % kAhead], (i / kAhead) & 1);
+            if (lane == 0) atomicOr(a.status, kDevTimeout);
+        }
     }
 };
 
@@ -311,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     Bars8* bars = reinterpret_cast<Bars8*>(smem + P::kOffBars);
     float* row_inv = reinterpret_cast<float*>(smem + P::kOffInv);
     int* all_ok = reinterpret_cast<int*>(row_inv + 2 * kRows);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     // blockIdx.x = (rank * batch + b) * num_kv_heads + kvh: rank 0 is every chunk's last CTA
     const int kvh = (int)(blockIdx.x % (unsigned)a.num_kv_heads);
     const int rb = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const int cr = row0 + t_tile * kRows + t_row;
     const int qi = cr / g, qh = cr % g;
     uint4 qv[D / 8];
-    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane, 0};
+    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane};
     if (warp < kSoftmaxWarps) {
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + ((size_t)(q0 + (valid ? qi : 0)) * a.num_heads + (size_t)kvh * g + qh) * D);
@@ -370,23 +369,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kKStages; ++s) {
-            mbar_init(&bars->k_full[s], kParts);
-            mbar_init(&bars->k_empty[s], 1);
+            mbar_init(&bars->k_full[s], kParts / 2);
+            mbar_init(&bars->k_empty[s], kMmaWarps);
         }
         for (int s = 0; s < kVStages; ++s) {
-            mbar_init(&bars->v_full[s], kParts);
-            mbar_init(&bars->v_empty[s], 1);
+            mbar_init(&bars->v_full[s], kParts / 2);
+            mbar_init(&bars->v_empty[s], kMmaWarps);
         }
         mbar_init(&bars->q_full, 2 * kRows);
         for (int t = 0; t < 2; ++t) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars->s_full[t][i], 1);
-                mbar_init(&bars->p_full[t][i], kRows);
+                mbar_init(&bars->p_full[t][i], kRows / 32);
             }
             mbar_init(&bars->o_done[t], 1);
             mbar_init(&bars->o_final[t], 1);
         }
-        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->drain, kMmaWarps);
         *all_ok = 1;
         fence_mbar_init();
     }
@@ -401,61 +400,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
 
     if (warp >= kCvtWarp) {
         cvt.run();
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
         constexpr uint32_t idesc_s = idesc_f16(kKeys, false), idesc_o = idesc_f16(D, true);
-        const uint64_t qd0 = smem_desc_sw128(smem_u32(smem), 0, 1024);
+        const int t = warp - kMmaWarp, myst = t ? nst1 : nst0;  // tile, and its stages
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + t * P::kQTile), 0, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + P::kOffK), 0, 1024);
         const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + P::kOffV), P::kKVHalf, 1024);
-        const auto issue_s = [&](int t, int j) {  // S(j) of tile t into its buffer j % 2
-            const uint64_t qd = qd0 + (uint64_t)((t * P::kQTile) >> 4);
+        const uint32_t tt = tmem + t * kTmemTile;
+        const auto issue_s = [&](int j) {  // S(j) into its buffer j % 2
             const uint64_t kd = kd0 + (uint64_t)(((j % kKStages) * P::kStage) >> 4);
-            const uint32_t d = tmem + t * kTmemTile + kTmemS + 64 * (j & 1);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma_ew(d, qd + (uint64_t)(((kk >> 2) * P::kQHalf + (kk & 3) * 32) >> 4),
+                tc_mma_ew(tt + kTmemS + 64 * (j & 1), qd + (uint64_t)(((kk >> 2) * P::kQHalf + (kk & 3) * 32) >> 4),
                           kd + (uint64_t)(((kk >> 2) * P::kKVHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
             tc_commit_ew(&bars->s_full[t][j & 1]);
         };
-        const auto issue_o = [&](int t, int j) {  // O += u(j) V(j) of tile t
+        const auto issue_o = [&](int j) {  // O += u(j) V(j)
             const uint64_t vd = vd0 + (uint64_t)(((j % kVStages) * P::kStage) >> 4);
-            const uint32_t p = tmem + t * kTmemTile + kTmemS + 64 * (j & 1);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc_mma_ts_ew(tmem + t * kTmemTile + kTmemO, p + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
-                             (j > 0 || kk > 0) ? 1u : 0u);
+                tc_mma_ts_ew(tt + kTmemO, tt + kTmemS + 64 * (j & 1) + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
+                             idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
             tc_commit_ew(&bars->o_done[t]);
-            if (j + 1 == (t ? nst1 : nst0)) tc_commit_ew(&bars->o_final[t]);
+            if (j + 1 == myst) tc_commit_ew(&bars->o_final[t]);
         };
+        // a tile without this stage only passes the slots on
         bool ok = mbar_wait_warp(&bars->q_full, 0);
+        // tile 1 starts half a stage behind, and stays there: one tile's instructions run while the
+        // other's warp waits and hands over
+        if (t == 1 && nst0 > 1) ok = ok && mbar_wait_warp(&bars->s_full[0][1], 0);
         for (int j = 0; j < 2 && j < nst && ok; ++j) {
             ok = mbar_wait_warp(&bars->k_full[j], 0);
             if (!ok) break;
             tc_fence_after();
-            if (j < nst0) issue_s(0, j);
-            if (j < nst1) issue_s(1, j);
+            if (j < myst) issue_s(j);
             tc_commit_ew(&bars->k_empty[j]);
         }
         for (int j = 0; j < nst && ok; ++j) {
+            // u V(j), then S(j + 2) into the buffer that u(j) sits in
             ok = mbar_wait_warp(&bars->v_full[j % kVStages], (j / kVStages) & 1);
-            if (ok && j + 2 < nst) ok = mbar_wait_warp(&bars->k_full[(j + 2) % kKStages], ((j + 2) / kKStages) & 1);
-            // per tile: u V(j), then S(j + 2) into the buffer that u(j) sits in
-            if (ok && j < nst0) {
-                ok = mbar_wait_warp(&bars->p_full[0][j & 1], (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_o(0, j);
-                if (j + 2 < nst0) issue_s(0, j + 2);
-            }
-            if (ok && j < nst1) {
-                ok = mbar_wait_warp(&bars->p_full[1][j & 1], (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_o(1, j);
-            }
+            if (ok && j < myst) ok = mbar_wait_warp(&bars->p_full[t][j & 1], (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (j < myst) issue_o(j);
             tc_commit_ew(&bars->v_empty[j % kVStages]);
-            if (j + 2 < nst1) issue_s(1, j + 2);
-            if (j + 2 < nst) tc_commit_ew(&bars->k_empty[(j + 2) % kKStages]);
+            if (j + 2 < nst) {
+                ok = mbar_wait_warp(&bars->k_full[(j + 2) % kKStages], ((j + 2) / kKStages) & 1);
+                if (!ok) break;
+                if (j + 2 < myst) issue_s(j + 2);
+                tc_commit_ew(&bars->k_empty[(j + 2) % kKStages]);
+            }
         }
         // every MMA issued here has finished before the tensor memory is released
         tc_commit_ew(&bars->drain);
@@ -558,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             l += lsum;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bars->p_full[t][j & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[t][j & 1]);
         }
         if (ok && myst > 0) ok = mbar_wait_warp(&bars->o_final[t], 0);
         row_inv[t * kRows + r] = l > 0.f ? 1.f / l : 0.f;
