@@ -34,20 +34,6 @@ struct Append8Args {
     int num_tokens, num_kv_heads, window;
 };
 
-// Larger of the magnitudes, bf16 pair by pair, as unsigned integers (their order is the
-// magnitudes'; infinities and NaN come last).
-__device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
-    return d;
-}
-
-// A bf16 pair's magnitudes with infinities and NaN as zero.
-__device__ __forceinline__ uint32_t finite2(uint32_t w) {
-    w &= 0x7fff7fffu;
-    return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | (w >> 16 < 0x7f80u ? w & 0xffff0000u : 0u);
-}
-
 // 8 bf16 values times s2, a pair of equal powers of two, as 8 codes.  The product is exact in bf16
 // but for results below 2^-126, whose code is zero either way.
 __device__ __forceinline__ uint2 chunk_codes(const uint4& v, __nv_bfloat162 s2) {

@@ -42,6 +42,20 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return min(max(k, kExpMin), kExpMax);
 }
 
+// Larger of the magnitudes, bf16 pair by pair, as unsigned integers (their order is the
+// magnitudes'; infinities and NaN come last).
+__device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
+    return d;
+}
+
+// A bf16 pair's magnitudes with infinities and NaN as zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    w &= 0x7fff7fffu;
+    return ((w & 0xffffu) < 0x7f80u ? w & 0xffffu : 0u) | (w >> 16 < 0x7f80u ? w & 0xffff0000u : 0u);
+}
+
 // The four e4m3 codes of a word as f16 pairs: lo the two low bytes, hi the others (exact; a NaN
 // code gives NaN).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {

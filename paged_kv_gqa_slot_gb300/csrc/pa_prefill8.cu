@@ -328,41 +328,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.status, kDevOutOfRange);
         return;
     }
+    // (no division by what is a power of two, and few others: they stand before the first load)
     const long long rows = (long long)C * g;
     const int cta_rows = a.tiles_per_cta * kRows;
-    const long long need = (rows + cta_rows - 1) / cta_rows;
+    const long long need = (rows + cta_rows - 1) >> (a.tiles_per_cta == 2 ? 8 : 7);
     // a chunk longer than max_chunk: the grid covers its first rows, the rest is reported
     if (rank == 0 && kvh == 0 && threadIdx.x == 0 && need > a.ctas_per_pair) atomicOr(a.status, kDevOutOfRange);
     const int covered = (int)min(need, (long long)a.ctas_per_pair);
     if (rank >= covered) return;
     const int row0 = (covered - 1 - rank) * cta_rows;
     // rows of either tile, and its stages: up to the key its last query sees
-    const auto live_of = [&](int t) {
-        return t < a.tiles_per_cta ? (int)max(0ll, min((long long)kRows, rows - row0 - t * kRows)) : 0;
-    };
+    const int live = (int)min((long long)cta_rows, rows - row0);
+    const auto live_of = [&](int t) { return max(0, min(kRows, live - t * kRows)); };
     const auto keys_of = [&](int t) {
-        const int live = live_of(t);
-        return live ? L - C + (row0 + t * kRows + live - 1) / g + 1 : 0;
+        const int n = live_of(t);
+        return n ? L - C + (int)((unsigned)(row0 + t * kRows + n - 1) / (unsigned)g) + 1 : 0;
     };
-    const int nkeys = max(keys_of(0), keys_of(1));
-    const int nst0 = (keys_of(0) + kKeys - 1) / kKeys, nst1 = (keys_of(1) + kKeys - 1) / kKeys;
+    const int keys0 = keys_of(0), keys1 = keys_of(1), nkeys = max(keys0, keys1);
+    const int nst0 = (keys0 + kKeys - 1) / kKeys, nst1 = (keys1 + kKeys - 1) / kKeys;
     const int nst = max(nst0, nst1);
     const int nblk = (nkeys + kBlockSize - 1) / kBlockSize;
     const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
 
-    // The first loads go out before the set-up below: a softmax thread's row of q, a converter's first
-    // units.
-    const int t_row = threadIdx.x & (kRows - 1), t_tile = (warp >> 2) & 1;  // softmax: row of its tile
-    const bool valid = warp < kSoftmaxWarps && t_row < live_of(t_tile);
-    const int cr = row0 + t_tile * kRows + t_row;
-    const int qi = cr / g, qh = cr % g;
-    uint4 qv[D / 8];
+    // The first loads go out before the set-up below: a softmax warp's 32 rows of q, kLanes lanes a row,
+    // and its first table entries; a converter's first pairs.
+    constexpr int kLanes = D / 8, kPerLoad = 32 / kLanes;  // lanes of a row of q, rows of one load
+    const int t_tile = (warp >> 2) & 1, w_row = (warp & 3) * 32;
+    uint4 qv[kLanes];
+    int first_id = -1;
     Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane};
     if (warp < kSoftmaxWarps) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((size_t)(q0 + (valid ? qi : 0)) * a.num_heads + (size_t)kvh * g + qh) * D);
+        if (lane < nblk) first_id = __ldg(bt + lane);
+        const int left = live_of(t_tile) - w_row;  // of the warp's rows
+        const unsigned cr = (unsigned)(row0 + t_tile * kRows + w_row + lane / kLanes);
+        const int step_q = kPerLoad / (unsigned)g, step_h = kPerLoad - step_q * g;
+        int qi = (int)(cr / (unsigned)g), qh = (int)cr - qi * g;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) qv[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < kLanes; ++i) {
+            const __nv_bfloat16* src =
+                a.q + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + qh) * D + lane % kLanes * 8;
+            qv[i] = i * kPerLoad + lane / kLanes < left ? __ldg(reinterpret_cast<const uint4*>(src))
+                                                        : make_uint4(0u, 0u, 0u, 0u);
+            qi += step_q;
+            qh += step_h;
+            if (qh >= g) qh -= g, ++qi;
+        }
     } else if (warp >= kCvtWarp) {
         cvt.start();
     }
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             mbar_init(&bars->v_full[s], kParts / 2);
             mbar_init(&bars->v_empty[s], kMmaWarps);
         }
-        mbar_init(&bars->q_full, 2 * kRows);
+        mbar_init(&bars->q_full, kSoftmaxWarps);
         for (int t = 0; t < 2; ++t) {
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bars->s_full[t][i], 1);
@@ -458,9 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         if (!ok && lane == 0) atomicOr(a.status, kDevTimeout);
     } else {
         // ---------------------------------------------------------------- softmax: one row a thread
-        const int t = t_tile, r = t_row;  // tile, and its row: tensor memory lane
+        const int t = t_tile, r = w_row + lane;  // tile, and its row: tensor memory lane
         const int myst = t ? nst1 : nst0;
-        const int pos = valid ? L - C + qi : -1;  // last key the row sees
+        const int pos =  // last key the row sees
+            r < live_of(t) ? L - C + (int)((unsigned)(row0 + t * kRows + r) / (unsigned)g) : -1;
         const uint32_t tm = tmem + t * kTmemTile + ((uint32_t)((warp & 3) * 32) << 16);
         // exponents of blocks c0 + lane: a word a lane, the next 32 read ahead
         const auto entry = [&](int blk) { return blk < nblk ? __ldg(bt + blk) : -1; };
@@ -468,33 +479,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             if (blk >= nblk) return kExpBias * 257;
             return valid_exps(__ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh));
         };
-        int ex = exps_of(lane, entry(lane)), next_id = entry(32 + lane), next_ex = 0;
-        float qf;  // log2(e) |scale| 2^eq, eq the power of two taken out of the row of q
-        {
-            // the row of q, normalised, into the swizzled layout (zeros past the chunk); a
-            // negative scale enters as -q, so that maxima are of the scores as they are
-            float amax = 0.f;
+        int ex = exps_of(lane, first_id), next_id = entry(32 + lane), next_ex = 0;
+        int eq = 0;  // the power of two taken out of the row of q
+        // the rows of q, normalised, into the swizzled layout (zeros past the chunk); a negative scale
+        // enters as -q, so that maxima are of the scores as they are
+        uint32_t mag[kLanes];  // a row's largest magnitude, as bf16
+        bool finite = true;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x = fabsf(bf16_lo(w[i])), y = fabsf(bf16_hi(w[i]));
-                    amax = fmaxf(amax, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
-                }
-            }
-            const int eq = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -110);
-            qf = fabsf(a.scale_log2) * exp2_int(eq);
-            const float s = a.scale_log2 < 0.f ? -exp2_int(-eq) : exp2_int(-eq);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const auto w = [&](uint32_t x) { return pack_f16x2(bf16_lo(x) * s, bf16_hi(x) * s); };
-                *reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7)) =
-                    make_uint4(w(qv[c].x), w(qv[c].y), w(qv[c].z), w(qv[c].w));
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->q_full);
+        for (int i = 0; i < kLanes; ++i) {
+            mag[i] = max_mag2(max_mag2(max_mag2(max_mag2(0u, qv[i].x), qv[i].y), qv[i].z), qv[i].w);
+            finite &= max(mag[i] & 0xffffu, mag[i] >> 16) < 0x7f80u;
         }
+        if (!__all_sync(0xffffffffu, finite)) {  // infinities and NaN do not count
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i)
+                mag[i] = max_mag2(max_mag2(max_mag2(finite2(qv[i].x), finite2(qv[i].y)), finite2(qv[i].z)),
+                                  finite2(qv[i].w));
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) mag[i] = max_mag2(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], o));
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) {
+            const int e = max(static_cast<int>(max(mag[i] & 0xffffu, mag[i] >> 16) >> 7) - 127 - 14, -110);
+            const __nv_bfloat162 s = __float2bfloat162_rn(a.scale_log2 < 0.f ? -exp2_int(-e) : exp2_int(-e));
+            const auto w = [&](uint32_t x) {  // exact but for f16's own end
+                const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s);
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(&p);
+                return pack_f16x2(bf16_lo(y), bf16_hi(y));
+            };
+            const int qr = w_row + i * kPerLoad + lane / kLanes, c = lane % kLanes;
+            *reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(qr, c & 7)) =
+                make_uint4(w(qv[i].x), w(qv[i].y), w(qv[i].z), w(qv[i].w));
+            const int of = __shfl_sync(0xffffffffu, e, lane % kPerLoad * kLanes);
+            if (lane / kPerLoad == i) eq = of;
+        }
+        const float qf = fabsf(a.scale_log2) * exp2_int(eq);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
         float base = -INFINITY, l = 0.f;
         bool ok = true;
         // tcgen05.ld / st are warp-collective: what leads to one is decided by the whole warp
@@ -598,14 +622,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         tmem_dealloc(tmem, kTmemCols);
     }
     if (*all_ok) {
-        const int live = live_of(0) + live_of(1);
-        for (int i = threadIdx.x; i < live * kChunks; i += kThreads) {
-            const int cr = i / kChunks, ch = i % kChunks;
+        constexpr int kStep = kThreads / kChunks;  // rows between a thread's pieces
+        const int ch = threadIdx.x % kChunks;
+        int cr = threadIdx.x / kChunks;
+        const int step_q = kStep / (unsigned)g, step_h = kStep - step_q * g;
+        int qi = (int)((unsigned)(row0 + cr) / (unsigned)g), h = row0 + cr - qi * g;
+        for (; cr < live; cr += kStep) {
             const int r = cr & (kRows - 1);
             const uint4 v = *reinterpret_cast<const uint4*>(smem + (cr / kRows) * P::kQTile +
                                                             (r * kChunks + (ch ^ (r & 7))) * 16);
-            const int qi = (row0 + cr) / g, h = (row0 + cr) % g;
             *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + h) * D + ch * 8) = v;
+            qi += step_q;
+            h += step_h;
+            if (h >= g) h -= g, ++qi;
         }
     }
 }
