@@ -108,6 +108,16 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
     return tc_idesc_bf16(kRows, n, b_mn_major) & ~((1u << 7) | (1u << 10));  // f16 A and B
 }
 
+// 16 bytes into shared memory, zeros unless `in`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // `bytes` contiguous bytes into shared memory, completing on `bar` (all multiples of 16).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -315,69 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const int kvh = (int)(blockIdx.x % (unsigned)a.num_kv_heads);
     const int rb = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
     const int b = rb % a.batch, rank = rb / a.batch;
-    pdl_wait();
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
         if (threadIdx.x == 0) atomicOr(a.status, kDevOutOfRange);
         return;
     }
-    const int g = a.group;
-    const int q0 = a.cu_q_lens[b];
-    const int C = a.cu_q_lens[b + 1] - q0;
-    const int L = a.seq_lens[b];
-    if (C < 0 || L < C || L > a.max_blocks * kBlockSize) {
-        if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.status, kDevOutOfRange);
-        return;
-    }
-    // (no division by what is a power of two, and few others: they stand before the first load)
-    const long long rows = (long long)C * g;
-    const int cta_rows = a.tiles_per_cta * kRows;
-    const long long need = (rows + cta_rows - 1) >> (a.tiles_per_cta == 2 ? 8 : 7);
-    // a chunk longer than max_chunk: the grid covers its first rows, the rest is reported
-    if (rank == 0 && kvh == 0 && threadIdx.x == 0 && need > a.ctas_per_pair) atomicOr(a.status, kDevOutOfRange);
-    const int covered = (int)min(need, (long long)a.ctas_per_pair);
-    if (rank >= covered) return;
-    const int row0 = (covered - 1 - rank) * cta_rows;
-    // rows of either tile, and its stages: up to the key its last query sees
-    const int live = (int)min((long long)cta_rows, rows - row0);
-    const auto live_of = [&](int t) { return max(0, min(kRows, live - t * kRows)); };
-    const auto keys_of = [&](int t) {
-        const int n = live_of(t);
-        return n ? L - C + (int)((unsigned)(row0 + t * kRows + n - 1) / (unsigned)g) + 1 : 0;
-    };
-    const int keys0 = keys_of(0), keys1 = keys_of(1), nkeys = max(keys0, keys1);
-    const int nst0 = (keys0 + kKeys - 1) / kKeys, nst1 = (keys1 + kKeys - 1) / kKeys;
-    const int nst = max(nst0, nst1);
-    const int nblk = (nkeys + kBlockSize - 1) / kBlockSize;
-    const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
-
-    // The first loads go out before the set-up below: a softmax warp's 32 rows of q, kLanes lanes a row,
-    // and its first table entries; a converter's first pairs.
-    constexpr int kLanes = D / 8, kPerLoad = 32 / kLanes;  // lanes of a row of q, rows of one load
-    const int t_tile = (warp >> 2) & 1, w_row = (warp & 3) * 32;
-    uint4 qv[kLanes];
-    int first_id = -1;
-    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane};
-    if (warp < kSoftmaxWarps) {
-        if (lane < nblk) first_id = __ldg(bt + lane);
-        const int left = live_of(t_tile) - w_row;  // of the warp's rows
-        const unsigned cr = (unsigned)(row0 + t_tile * kRows + w_row + lane / kLanes);
-        const int step_q = kPerLoad / (unsigned)g, step_h = kPerLoad - step_q * g;
-        int qi = (int)(cr / (unsigned)g), qh = (int)cr - qi * g;
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            const __nv_bfloat16* src =
-                a.q + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + qh) * D + lane % kLanes * 8;
-            qv[i] = i * kPerLoad + lane / kLanes < left ? __ldg(reinterpret_cast<const uint4*>(src))
-                                                        : make_uint4(0u, 0u, 0u, 0u);
-            qi += step_q;
-            qh += step_h;
-            if (qh >= g) qh -= g, ++qi;
-        }
-    } else if (warp >= kCvtWarp) {
-        cvt.start();
-    }
-
-    if (threadIdx.x == 0) {
+    // The set-up waits for nothing of another kernel's.
+    if (warp == kMmaWarp + 1 && lane == 0) {
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bars->k_full[s], kParts / 2);
             mbar_init(&bars->k_empty[s], kMmaWarps);
@@ -407,6 +360,68 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
+
+    pdl_wait();
+    const int g = a.group;
+    const int q0 = a.cu_q_lens[b];
+    const int C = a.cu_q_lens[b + 1] - q0;
+    const int L = a.seq_lens[b];
+    const auto leave = [&] {
+        if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    };
+    if (C < 0 || L < C || L > a.max_blocks * kBlockSize) {
+        if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.status, kDevOutOfRange);
+        return leave();
+    }
+    // (no division by what is a power of two, and few others: they stand before the first load)
+    const long long rows = (long long)C * g;
+    const int cta_rows = a.tiles_per_cta * kRows;
+    const long long need = (rows + cta_rows - 1) >> (a.tiles_per_cta == 2 ? 8 : 7);
+    // a chunk longer than max_chunk: the grid covers its first rows, the rest is reported
+    if (rank == 0 && kvh == 0 && threadIdx.x == 0 && need > a.ctas_per_pair) atomicOr(a.status, kDevOutOfRange);
+    const int covered = (int)min(need, (long long)a.ctas_per_pair);
+    if (rank >= covered) return leave();
+    const int row0 = (covered - 1 - rank) * cta_rows;
+    // rows of either tile, and its stages: up to the key its last query sees
+    const int live = (int)min((long long)cta_rows, rows - row0);
+    const auto live_of = [&](int t) { return max(0, min(kRows, live - t * kRows)); };
+    const auto keys_of = [&](int t) {
+        const int n = live_of(t);
+        return n ? L - C + (int)((unsigned)(row0 + t * kRows + n - 1) / (unsigned)g) + 1 : 0;
+    };
+    const int keys0 = keys_of(0), keys1 = keys_of(1), nkeys = max(keys0, keys1);
+    const int nst0 = (keys0 + kKeys - 1) / kKeys, nst1 = (keys1 + kKeys - 1) / kKeys;
+    const int nst = max(nst0, nst1);
+    const int nblk = (nkeys + kBlockSize - 1) / kBlockSize;
+    const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
+
+    // The first loads: a softmax warp's 32 rows of q, kLanes lanes a row, into the swizzled layout (zeros
+    // past the chunk), and its first table entries; a converter's first pairs.  (Loops as they are, here and
+    // below: instructions that run once cost their fetch.)
+    constexpr int kLanes = D / 8, kPerLoad = 32 / kLanes;  // lanes of a row of q, rows of one load
+    const int t_tile = (warp >> 2) & 1, w_row = (warp & 3) * 32;
+    int first_id = -1;
+    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane};
+    if (warp < kSoftmaxWarps) {
+        if (lane < nblk) first_id = __ldg(bt + lane);
+        const int c = lane % kLanes, r0 = w_row + lane / kLanes, n = live_of(t_tile);
+        const unsigned cr = (unsigned)(row0 + t_tile * kRows + r0);
+        const int step_q = kPerLoad / (unsigned)g, step_h = kPerLoad - step_q * g;
+        int qi = (int)(cr / (unsigned)g), qh = (int)cr - qi * g;
+        const uint32_t dst = smem_u32(smem + t_tile * P::kQTile + (c >> 3) * P::kQHalf);
+        const __nv_bfloat16* src = a.q + (size_t)kvh * g * D + c * 8;
+#pragma unroll 1
+        for (int r = r0; r < w_row + 32; r += kPerLoad) {
+            const bool in = r < n;
+            cp_async16(dst + swz128(r, c & 7), in ? src + ((size_t)(q0 + qi) * a.num_heads + qh) * D : src, in);
+            qi += step_q;
+            qh += step_h;
+            if (qh >= g) qh -= g, ++qi;
+        }
+        cp_async_commit();
+    } else if (warp >= kCvtWarp) {
+        cvt.start();
+    }
 
     if (warp >= kCvtWarp) {
         cvt.run();
@@ -480,42 +495,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             return valid_exps(__ldg(a.exps + (size_t)(id < 0 || id >= a.num_blocks ? 0 : id) * a.num_kv_heads + kvh));
         };
         int ex = exps_of(lane, first_id), next_id = entry(32 + lane), next_ex = 0;
-        int eq = 0;  // the power of two taken out of the row of q
-        // the rows of q, normalised, into the swizzled layout (zeros past the chunk); a negative scale
-        // enters as -q, so that maxima are of the scores as they are
-        uint32_t mag[kLanes];  // a row's largest magnitude, as bf16
-        bool finite = true;
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            mag[i] = max_mag2(max_mag2(max_mag2(max_mag2(0u, qv[i].x), qv[i].y), qv[i].z), qv[i].w);
-            finite &= max(mag[i] & 0xffffu, mag[i] >> 16) < 0x7f80u;
+        // the row of q, normalised by a power of two, in place; a negative scale enters as -q, so that
+        // maxima are of the scores as they are
+        cp_async_wait<0>();
+        __syncwarp();
+        const auto piece = [&](int c) {
+            return reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7));
+        };
+        uint32_t mag = 0u;  // the row's largest magnitude, as bf16
+#pragma unroll 4
+        for (int c = 0; c < kLanes; ++c) {
+            const uint4 v = *piece(c);
+            mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, v.x), v.y), v.z), v.w);
         }
-        if (!__all_sync(0xffffffffu, finite)) {  // infinities and NaN do not count
-#pragma unroll
-            for (int i = 0; i < kLanes; ++i)
-                mag[i] = max_mag2(max_mag2(max_mag2(finite2(qv[i].x), finite2(qv[i].y)), finite2(qv[i].z)),
-                                  finite2(qv[i].w));
+        if (max(mag & 0xffffu, mag >> 16) >= 0x7f80u) {  // infinities and NaN do not count
+            mag = 0u;
+#pragma unroll 1
+            for (int c = 0; c < kLanes; ++c) {
+                const uint4 v = *piece(c);
+                mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, finite2(v.x)), finite2(v.y)), finite2(v.z)),
+                               finite2(v.w));
+            }
         }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < kLanes; ++i) mag[i] = max_mag2(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], o));
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            const int e = max(static_cast<int>(max(mag[i] & 0xffffu, mag[i] >> 16) >> 7) - 127 - 14, -110);
-            const __nv_bfloat162 s = __float2bfloat162_rn(a.scale_log2 < 0.f ? -exp2_int(-e) : exp2_int(-e));
+        const int eq = max(static_cast<int>(max(mag & 0xffffu, mag >> 16) >> 7) - 127 - 14, -110);
+        const float qf = fabsf(a.scale_log2) * exp2_int(eq);
+        const __nv_bfloat162 s2 = __float2bfloat162_rn(a.scale_log2 < 0.f ? -exp2_int(-eq) : exp2_int(-eq));
+#pragma unroll 4
+        for (int c = 0; c < kLanes; ++c) {
             const auto w = [&](uint32_t x) {  // exact but for f16's own end
-                const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s);
+                const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s2);
                 const uint32_t y = *reinterpret_cast<const uint32_t*>(&p);
                 return pack_f16x2(bf16_lo(y), bf16_hi(y));
             };
-            const int qr = w_row + i * kPerLoad + lane / kLanes, c = lane % kLanes;
-            *reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(qr, c & 7)) =
-                make_uint4(w(qv[i].x), w(qv[i].y), w(qv[i].z), w(qv[i].w));
-            const int of = __shfl_sync(0xffffffffu, e, lane % kPerLoad * kLanes);
-            if (lane / kPerLoad == i) eq = of;
+            const uint4 v = *piece(c);
+            *piece(c) = make_uint4(w(v.x), w(v.y), w(v.z), w(v.w));
         }
-        const float qf = fabsf(a.scale_log2) * exp2_int(eq);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full);
