@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         int qi = (int)(cr / (unsigned)g), qh = (int)cr - qi * g;
         const uint32_t dst = smem_u32(smem + t_tile * P::kQTile + (c >> 3) * P::kQHalf);
         const __nv_bfloat16* src = a.q + (size_t)kvh * g * D + c * 8;
-#pragma unroll 1
-        for (int r = r0; r < w_row + 32; r += kPerLoad) {
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+            const int r = r0 + i * kPerLoad;
             const bool in = r < n;
             cp_async16(dst + swz128(r, c & 7), in ? src + ((size_t)(q0 + qi) * a.num_heads + qh) * D : src, in);
             qi += step_q;
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             return reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7));
         };
         uint32_t mag = 0u;  // the row's largest magnitude, as bf16
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < kLanes; ++c) {
             const uint4 v = *piece(c);
             mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, v.x), v.y), v.z), v.w);
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         const int eq = max(static_cast<int>(max(mag & 0xffffu, mag >> 16) >> 7) - 127 - 14, -110);
         const float qf = fabsf(a.scale_log2) * exp2_int(eq);
         const __nv_bfloat162 s2 = __float2bfloat162_rn(a.scale_log2 < 0.f ? -exp2_int(-eq) : exp2_int(-eq));
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < kLanes; ++c) {
             const auto w = [&](uint32_t x) {  // exact but for f16's own end
                 const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s2);
@@ -641,11 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         int cr = threadIdx.x / kChunks;
         const int step_q = kStep / (unsigned)g, step_h = kStep - step_q * g;
         int qi = (int)((unsigned)(row0 + cr) / (unsigned)g), h = row0 + cr - qi * g;
-        for (; cr < live; cr += kStep) {
+#pragma unroll 4
+        for (int i = 0; i < 2 * kRows / kStep; ++i, cr += kStep) {
             const int r = cr & (kRows - 1);
             const uint4 v = *reinterpret_cast<const uint4*>(smem + (cr / kRows) * P::kQTile +
                                                             (r * kChunks + (ch ^ (r & 7))) * 16);
-            *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + h) * D + ch * 8) = v;
+            if (cr < live)
+                *reinterpret_cast<uint4*>(a.out + ((size_t)(q0 + qi) * a.num_heads + (size_t)kvh * g + h) * D + ch * 8) = v;
             qi += step_q;
             h += step_h;
             if (h >= g) h -= g, ++qi;
