@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncl));
     const int sub = static_cast<int>(ncl), rank = blockIdx.x % sub;
     const int kvh = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (by a shuffle, so that the compiler knows it is the same for all lanes and keeps what follows from it
+    // in uniform registers: 4 x 64 queries 30.7 us against 32.5, d 64 64 x ~4000 48.8 against 53.4)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
     // Which row of a block is which MMA row or key: neighbouring ones are kNext rows apart, which the
     // swizzle (of 128-byte rows by their index modulo 8, of 64-byte rows by half of it) and the row

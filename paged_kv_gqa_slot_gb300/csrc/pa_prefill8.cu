@@ -396,8 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const int32_t* bt = a.block_tables + (size_t)b * a.max_blocks;
 
     // The first loads: a softmax warp's 32 rows of q, kLanes lanes a row, into the swizzled layout (zeros
-    // past the chunk), and its first table entries; a converter's first pairs.  (Loops as they are, here and
-    // below: instructions that run once cost their fetch.)
+    // past the chunk), and its first table entries; a converter's first pairs.
     constexpr int kLanes = D / 8, kPerLoad = 32 / kLanes;  // lanes of a row of q, rows of one load
     const int t_tile = (warp >> 2) & 1, w_row = (warp & 3) * 32;
     int first_id = -1;
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             return reinterpret_cast<uint4*>(smem + t * P::kQTile + (c >> 3) * P::kQHalf + swz128(r, c & 7));
         };
         uint32_t mag = 0u;  // the row's largest magnitude, as bf16
-#pragma unroll 8
+#pragma unroll
         for (int c = 0; c < kLanes; ++c) {
             const uint4 v = *piece(c);
             mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, v.x), v.y), v.z), v.w);
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         const int eq = max(static_cast<int>(max(mag & 0xffffu, mag >> 16) >> 7) - 127 - 14, -110);
         const float qf = fabsf(a.scale_log2) * exp2_int(eq);
         const __nv_bfloat162 s2 = __float2bfloat162_rn(a.scale_log2 < 0.f ? -exp2_int(-eq) : exp2_int(-eq));
-#pragma unroll 8
+#pragma unroll
         for (int c = 0; c < kLanes; ++c) {
             const auto w = [&](uint32_t x) {  // exact but for f16's own end
                 const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), s2);
