@@ -69,22 +69,24 @@ __device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int he
     // an entry is its block's first if the one before it that names a slot is of another block
     const unsigned window = (1u << a.window) - 1u;
     if (ent >= a.pool_slots && head == 0 && window >> lane & 1u) atomicOr(a.status, kDevOutOfRange);
-    const int64_t block_of_ent = in_pool(ent) ? ent / kBlockSize : -1;
+    const auto block_of = [](int64_t s) { return static_cast<int>(s >> 4); };  // of a slot in the pool
+    static_assert(kBlockSize == 16, "block_of");
+    const int block_of_ent = in_pool(ent) ? block_of(ent) : -1;
     const unsigned named = __ballot_sync(0xffffffffu, block_of_ent >= 0);
     if (!(named & window)) return;
     const unsigned lower = named & ((1u << lane) - 1u);
-    const int64_t prev = __shfl_sync(0xffffffffu, block_of_ent, lower ? 31 - __clz(lower) : 0);
+    const int prev = __shfl_sync(0xffffffffu, block_of_ent, lower ? 31 - __clz(lower) : 0);
     unsigned firsts = window & __ballot_sync(0xffffffffu, block_of_ent >= 0 && lower && prev != block_of_ent);
     {
         // the window's first named entry: look back past its start, farther if need be
         const int f = __ffs(named) - 1;
-        const int64_t block = __shfl_sync(0xffffffffu, block_of_ent, f);
+        const int block = __shfl_sync(0xffffffffu, block_of_ent, f);
         bool first = true;
         int64_t s = before;
         for (int p = t0 - 1; p >= 0; p -= 32) {
             const unsigned some = __ballot_sync(0xffffffffu, in_pool(s));
             if (some) {
-                first = __shfl_sync(0xffffffffu, s, __ffs(some) - 1) / kBlockSize != block;
+                first = __shfl_sync(0xffffffffu, block_of(s), __ffs(some) - 1) != block;
                 break;
             }
             s = slot_at((long long)p - 32 - lane);
@@ -94,19 +96,19 @@ __device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int he
 
     for (; firsts; firsts &= firsts - 1) {
         const int f = __ffs(firsts) - 1;
-        const int64_t block = __shfl_sync(0xffffffffu, block_of_ent, f);
+        const int block = __shfl_sync(0xffffffffu, block_of_ent, f);
         // the block's entries, up to the first of another block: token_at[o] is the token whose row
         // goes to offset o (-1: none); of entries with the same slot the last counts
         if (lane < kBlockSize) token_at[lane] = -1;
         __syncwarp();
         unsigned other = named & (~0u << f) & __ballot_sync(0xffffffffu, block_of_ent != block);
         if (lane >= f && block_of_ent == block && lane < (other ? __ffs(other) - 1 : 32))
-            atomicMax(&token_at[ent % kBlockSize], t0 + lane);
+            atomicMax(&token_at[ent & 15], t0 + lane);
         for (long long p = (long long)t0 + 32; !other && p < a.num_tokens; p += 32) {
             const int64_t s = slot_at(p + lane);
-            other = __ballot_sync(0xffffffffu, in_pool(s) && s / kBlockSize != block);
+            other = __ballot_sync(0xffffffffu, in_pool(s) && block_of(s) != block);
             if (in_pool(s) && lane < (other ? __ffs(other) - 1 : 32))
-                atomicMax(&token_at[s % kBlockSize], static_cast<int>(p) + lane);
+                atomicMax(&token_at[s & 15], static_cast<int>(p) + lane);
         }
         __syncwarp();
         const int token = lane < kBlockSize ? token_at[lane] : -1;
@@ -166,16 +168,16 @@ __device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int he
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append8_kernel(const __grid_constant__ Append8Args a) {
     __shared__ int tokens[kWarps][kBlockSize];
-    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     pdl_trigger();
     pdl_wait();
     const int heads2 = 2 * a.num_kv_heads;
-    const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long unit = (long long)blockIdx.x * kWarps + warp;
     const long long start = unit / heads2 * a.window;
     if (start >= a.num_tokens) return;
     const auto slot_at = [&](long long t) { return t >= 0 && t < a.num_tokens ? __ldg(a.slots + t) : -1; };
     append_unit<D>(a, (int)start, (int)(unit % heads2), slot_at(start + lane), slot_at(start - 1 - lane),
-                   tokens[threadIdx.x >> 5]);
+                   tokens[warp]);
 }
 
 }  // namespace
