@@ -21,8 +21,6 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 7;
 
 struct Append8Args {
     uint8_t* codes[2];  // K, V
@@ -165,7 +163,7 @@ __device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int he
     }
 }
 
-template <int D>
+template <int D, int kWarps, int kCtasPerSm>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) kv_append8_kernel(const __grid_constant__ Append8Args a) {
     __shared__ int tokens[kWarps][kBlockSize];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
@@ -198,17 +196,23 @@ cudaError_t launch_kv_append8(const Pool8View& pool, const void* k_new, const vo
     const long long per_token = 2LL * pool.num_kv_heads;
     a.window = num_tokens * per_token > 16LL * 4 * device_info().num_sms ? kBlockSize : 1;
     const long long units = (num_tokens + a.window - 1) / a.window * per_token;
-    const long long ctas = (units + kWarps - 1) / kWarps;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return pool.head_dim == 128 ? cudaLaunchKernelEx(&cfg, kv_append8_kernel<128>, a)
-                                : cudaLaunchKernelEx(&cfg, kv_append8_kernel<64>, a);
+    // Many units: eight warps a CTA, four CTAs an SM; else four warps a CTA, so that few units spread over
+    // more SMs: 16k rows of 8 heads 19.0 us against 19.9, but 2k rows 4.75 against 4.40.
+    const auto launch = [&](auto kern, int warps) {
+        const long long ctas = (units + warps - 1) / warps;
+        if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)ctas);
+        cfg.blockDim = dim3(warps * 32);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1] = {pdl_attribute()};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, a);
+    };
+    if (units >= 64LL * device_info().num_sms)
+        return pool.head_dim == 128 ? launch(kv_append8_kernel<128, 8, 4>, 8) : launch(kv_append8_kernel<64, 8, 4>, 8);
+    return pool.head_dim == 128 ? launch(kv_append8_kernel<128, 4, 7>, 4) : launch(kv_append8_kernel<64, 4, 7>, 4);
 }
 
 }  // namespace pa
