@@ -18,6 +18,9 @@
 // shared memory are read whole before any output is written; the others are gathered in
 // ascending tiles, each read before it is written, from sources at or past it: outputs may be
 // their inputs.
+//
+// Measured on GB300, 8 kv heads: 64 sequences of 72 blocks 5.3 us, 16 of 2048 13.9 us, nearly all of it the
+// latency of the radix passes' barriers and the scans (the bytes would take 0.1 and 0.4 us).
 #include <algorithm>
 
 #include "pa_device.cuh"

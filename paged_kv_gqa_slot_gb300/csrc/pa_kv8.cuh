@@ -1,5 +1,5 @@
 // pa_kv8.cuh -- the 8-bit pool's number format on the device, shared by the kernels that
-// write it (pa_append8.cu) and read it (pa_decode8.cu, the prefill kernels).
+// write it (pa_append8.cu) and read it (pa_decode_lanes.cu, pa_prefill8.cu).
 //
 // A (block, kv head) tile of K or of V holds e4m3 codes and one power-of-two scale:
 //     value = e4m3(code) * 2^k,   k = exps[block, kv head, 0 (K) or 1 (V)] - 127.

@@ -16,32 +16,35 @@
 // second part even where a few weights dominate a row.
 //
 // Per stage of 64 keys (four pool blocks):
-//   warps 9-15   read codes, each lane its own 16-byte pieces by cp.async kAhead units ahead, and
-//                widen them into the 128-byte swizzled layout of the MMA operands (rows past the
-//                sequence's end as zeros); a unit is one block's K or V, units go to the seven
-//                warps in turn, K one stage ahead of V.  (One warp that copied the blocks in bulk took
-//                over 400 cycles to issue a stage's K or V, which bounded the kernel.)
-//   warp 8       per tile, S[128 x 64] = Q K^T into one of two 64-column buffers and
+//   warps 10-15  three for K, three for V, take every third pair of blocks: codes come by a bulk copy a
+//                block into the warp's own raw slots, kAhead pairs ahead, and are widened into the
+//                128-byte swizzled layout of the MMA operands (rows past the sequence's end as zeros).
+//                Pairs, because the waits, the fence and the hand-over cost as much as the widening:
+//                block by block the warps needed 1500 cycles a block and bounded the kernel.
+//   warps 8, 9   one per tile: S[128 x 64] = Q K^T into one of two 64-column buffers and
 //                O[128 x D] += u V with u from tensor memory; per stage u V(j), then S(j + 2), which
-//                reuses u(j)'s buffer, of the one tile while the other's softmax runs
+//                reuses u(j)'s buffer.  Tile 1 starts half a stage behind.  The warp index comes from a
+//                shuffle, so that descriptors and barrier addresses live in uniform registers: with
+//                them in every thread's, an instruction took 80 cycles to issue, and a stage 1750.
 //   warps 0-7    softmax, one row a thread: reads S, writes u over it.  The base is set by a row's
 //                first visible stage and moves only when a stage's sum passes 2^15 (f16 ends at
 //                2^16), then to the maximum, if that is more than 2^8 above; O is rescaled in
 //                tensor memory by all rows of a warp together.  (The maximum in every stage instead
 //                cost 6 us of 52.)
-// At the end all warps normalise, stage the rows in the free Q buffer and store them coalesced.
+// Before, they stage their rows of q by coalesced asynchronous copies and normalise them in place (rows
+// loaded by the threads that own them took 4000 cycles more).  At the end all warps normalise O, stage
+// the rows in the free Q buffer and store them coalesced.
 //
-// Measured on GB300 (32 q / 8 kv heads, d 128): 8 x 256 over 768 cached tokens 53 us (the bf16 pool's
-// kernel on the same values 59), 8 x 1024 over 1024 250 us (305), 1.20 us a stage of two tiles.  What
-// bounds a stage is the matrix pipe with its hand-overs: its instructions read 768 cycles' worth of
-// shared memory for Q K^T of the two tiles and 256 for u V, and the codes are written, read and
-// stored widened (512), 1536 of a stage's 2280 cycles.  With half of Q K^T's instructions left out the
-// kernel took 23% less, without the converters 5%, without the softmax's arithmetic 8%.
-// Tried and not kept: Q in tensor memory, which leaves room for one score buffer a tile (1.14 us
-// a stage, but a single tile's chain 10% longer: 22.7 against 20.5 us for 1 x 256 + 768); stages of
-// 128 keys with one buffer (1.16 us; 21.9 for the single tile), and those with two threads a row
-// (1.26 us); two threads a row on the first (1.24 us; 23.2); codes loaded into registers instead of by
-// cp.async (1.74 us).
+// Measured on GB300 (32 q / 8 kv heads, d 128), the bf16 pool's kernel on the same values in brackets:
+// 8 x 256 over 768 cached tokens 37.5 us (59), over 3840 107 (195), 1 x 256 over 768 15.7 (26.8),
+// 8 x 1024 over 1024 176 (304): 0.73 us a stage of two tiles, 1400 cycles, of which the matrix
+// pipe needs 1280 (Q K^T reads Q and K from shared memory for 768, u V runs for 512), and about
+// 8 us a CTA outside its stages: loads that wait for one another (lengths, table, codes) and q 4.5,
+// output 2.5.
+// Tried and not kept: Q in tensor memory, which would bring the pipe to 1024 cycles but leaves room for
+// one score buffer a tile, so that its softmax and its instructions take turns; stages of 128 keys with one
+// buffer; two threads a row; codes loaded into registers a pair ahead (115 us for 8 x 256 + 3840 became
+// 118); one call site of the two softmax attempts (121 us against 108).
 #include <algorithm>
 #include <cmath>
 
