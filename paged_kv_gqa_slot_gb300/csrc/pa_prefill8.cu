@@ -457,6 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         bool ok = mbar_wait_warp(&bars->q_full, 0);
         // tile 1 starts half a stage behind, and stays there: one tile's instructions run while the
         // other's warp waits and hands over
+        // (tile 0 cannot get to S(3), the barrier's next phase: K(3) takes the slot of a K(0) not yet released)
+        static_assert(kKStages == 3, "the phase waited for");
         if (t == 1 && nst0 > 1) ok = ok && mbar_wait_warp(&bars->s_full[0][1], 0);
         for (int j = 0; j < 2 && j < nst && ok; ++j) {
             ok = mbar_wait_warp(&bars->k_full[j], 0);

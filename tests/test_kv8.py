@@ -191,6 +191,32 @@ def test_append_is_exact(case):
 
 
 @gpu
+@pytest.mark.parametrize("hkv,d,rows", [(8, 128, 9900), (16, 64, 5100)])
+def test_append_of_many_rows_is_exact(hkv, d, rows):
+    """More units than the few-unit form takes: several sequences, the first of each ending inside a block,
+    padding between them."""
+    seed, nb = 9, rows // 16 + 8
+    k, v, exps = make_pool(seed, nb, hkv, d)
+    pool = pa.PaPool8(k, v, exps)
+    kh, vh, eh = k.cpu().numpy(), v.cpu().numpy(), exps.cpu().numpy().copy()
+    rng = np.random.RandomState(seed)
+    perm, slots = rng.permutation(nb), []
+    for i in range(4):
+        blocks = perm[i * (nb // 4):(i + 1) * (nb // 4)]
+        line = [int(b) * 16 + o for b in blocks for o in range(16)][3 + 2 * i:]
+        slots += line[:rows // 4 - 5 * i] + [-1] * (5 * i)
+    new = [torch.tensor(rng.randn(len(slots), hkv, d) * np.exp2(rng.uniform(-6, 6, size=(len(slots), hkv, 1))),
+                        dtype=torch.float32).to(torch.bfloat16) for _ in range(2)]
+    pa.pa_kv_append8(pool, new[0].cuda(), new[1].cuda(), torch.tensor(slots, device="cuda"))
+    for i, codes in enumerate((kh, vh)):
+        R.append(codes, eh[:, :, i], new[i].double().numpy(), slots)
+    assert np.array_equal(exps.cpu().numpy(), eh)
+    for got, want in ((k, kh), (v, vh)):
+        assert np.array_equal(R.VALUES[got.cpu().numpy()], R.VALUES[want], equal_nan=True)
+    clean()
+
+
+@gpu
 def test_append_special_values():
     pool = pa.PaPool8.zeros(4, 1, 64)
     x = torch.zeros(7, 1, 64)
@@ -375,6 +401,44 @@ def test_prefill_rising_scores_move_the_base(d):
     ref, spread, _, mag = c.reference()
     out = pa.pa_prefill_chunked8(c.pool, c.q, c.cu, c.tables, c.lens, c.scale, 64)
     check(out, ref, spread, 640, mag)
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_rows_of_any_size_and_with_nan(d):
+    """Rows of q down to 2^-100, zero rows, and rows with a NaN or an infinity, which concern their own
+    (query, head) alone."""
+    c = Case(56, [300, 70], 6, 2, d, [150, 70])
+    size = torch.exp2(torch.randint(-100, 3, c.q.shape[:2], device="cuda").float())
+    c.q = (c.q.float() * size[..., None]).to(torch.bfloat16)
+    c.q[5, 1] = 0
+    c.q[7, 2] *= -0.0
+    ref, spread, _, mag = c.reference()
+    q = c.q.clone()
+    bad = [(3, 0, 5, float("nan")), (149, 5, d - 1, float("inf")), (150, 2, 0, float("-inf")), (219, 4, 17, float("nan"))]
+    for r, h, i, x in bad:
+        q[r, h, i] = x
+    out = pa.pa_prefill_chunked8(c.pool, q, c.cu, c.tables, c.lens, c.scale, c.max_chunk)
+    for r, h, i, x in bad:
+        if x != x:
+            assert torch.isnan(out[r, h]).all()
+        out[r, h] = ref[r, h].to(out.dtype)
+    check(out, ref, spread, 300, mag)
+    clean()
+
+
+@gpu
+def test_prefill_many_rounds_back_to_back():
+    """Several CTAs an SM one after another, tiles of one CTA with different stage counts, and launches that
+    start before the one before them has ended."""
+    c = Case(57, [500, 1030, 64, 777, 0, 130] * 4, 32, 8, 128, [70, 130, 64, 1, 0, 129] * 4)
+    ref, spread, _, mag = c.reference()
+    outs = [torch.full_like(c.q, 7.0) for _ in range(4)]
+    for out in outs:
+        pa.pa_prefill_chunked8(c.pool, c.q, c.cu, c.tables, c.lens, c.scale, c.max_chunk, out=out)
+    for out in outs:
+        check(out, ref, spread, 1030, mag)
     clean()
 
 
