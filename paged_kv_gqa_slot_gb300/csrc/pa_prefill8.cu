@@ -94,6 +94,25 @@ struct Bars8 {
 };
 static_assert(sizeof(Bars8) <= 512, "barrier block");
 
+// Division by a number that is known at launch, for any 32-bit x (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994): a division proper is a chain of 30 instructions, and
+// half a dozen stand before a CTA's first load.
+struct Divisor {
+    unsigned d, m, s1, s2;
+    explicit Divisor(unsigned by = 1) : d(by) {
+        unsigned l = 0;
+        while ((1ull << l) < d) ++l;
+        m = static_cast<unsigned>((((1ull << l) - d) << 32) / d + 1);
+        s1 = l < 1 ? l : 1;
+        s2 = l < 1 ? 0 : l - 1;
+    }
+    __device__ __forceinline__ int div(int x) const {
+        const unsigned u = static_cast<unsigned>(x), h = __umulhi(m, u);
+        return static_cast<int>((h + ((u - h) >> s1)) >> s2);
+    }
+    __device__ __forceinline__ int mod(int x, int quotient) const { return x - quotient * static_cast<int>(d); }
+};
+
 struct Pre8Args {
     const __nv_bfloat16* q;
     const uint8_t *k, *v;
@@ -101,6 +120,7 @@ struct Pre8Args {
     const int32_t *block_tables, *seq_lens, *cu_q_lens;
     __nv_bfloat16* out;
     unsigned* status;
+    Divisor by_group, by_batch, by_heads;
     int max_blocks, num_heads, num_kv_heads, num_blocks, group, batch;
     int ctas_per_pair;   // CTAs the grid holds per (sequence, kv head)
     int tiles_per_cta;   // 1 or 2
@@ -325,9 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     int* all_ok = reinterpret_cast<int*>(row_inv + 2 * kRows);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     // blockIdx.x = (rank * batch + b) * num_kv_heads + kvh: rank 0 is every chunk's last CTA
-    const int kvh = (int)(blockIdx.x % (unsigned)a.num_kv_heads);
-    const int rb = (int)(blockIdx.x / (unsigned)a.num_kv_heads);
-    const int b = rb % a.batch, rank = rb / a.batch;
+    const int rb = a.by_heads.div((int)blockIdx.x), kvh = a.by_heads.mod((int)blockIdx.x, rb);
+    const int rank = a.by_batch.div(rb), b = a.by_batch.mod(rb, rank);
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
         if (threadIdx.x == 0) atomicOr(a.status, kDevOutOfRange);
         return;
@@ -376,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.status, kDevOutOfRange);
         return leave();
     }
-    // (no division by what is a power of two, and few others: they stand before the first load)
     const long long rows = (long long)C * g;
     const int cta_rows = a.tiles_per_cta * kRows;
     const long long need = (rows + cta_rows - 1) >> (a.tiles_per_cta == 2 ? 8 : 7);
@@ -390,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     const auto live_of = [&](int t) { return max(0, min(kRows, live - t * kRows)); };
     const auto keys_of = [&](int t) {
         const int n = live_of(t);
-        return n ? L - C + (int)((unsigned)(row0 + t * kRows + n - 1) / (unsigned)g) + 1 : 0;
+        return n ? L - C + a.by_group.div(row0 + t * kRows + n - 1) + 1 : 0;
     };
     const int keys0 = keys_of(0), keys1 = keys_of(1), nkeys = max(keys0, keys1);
     const int nst0 = (keys0 + kKeys - 1) / kKeys, nst1 = (keys1 + kKeys - 1) / kKeys;
@@ -407,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     if (warp < kSoftmaxWarps) {
         if (lane < nblk) first_id = __ldg(bt + lane);
         const int c = lane % kLanes, r0 = w_row + lane / kLanes, n = live_of(t_tile);
-        const unsigned cr = (unsigned)(row0 + t_tile * kRows + r0);
-        const int step_q = kPerLoad / (unsigned)g, step_h = kPerLoad - step_q * g;
-        int qi = (int)(cr / (unsigned)g), qh = (int)cr - qi * g;
+        const int cr = row0 + t_tile * kRows + r0;
+        const int step_q = a.by_group.div(kPerLoad), step_h = kPerLoad - step_q * g;
+        int qi = a.by_group.div(cr), qh = cr - qi * g;
         const uint32_t dst = smem_u32(smem + t_tile * P::kQTile + (c >> 3) * P::kQHalf);
         const __nv_bfloat16* src = a.q + (size_t)kvh * g * D + c * 8;
 #pragma unroll 4
@@ -478,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             if (j + 2 < nst) {
                 ok = mbar_wait_warp(&bars->k_full[(j + 2) % kKStages], ((j + 2) / kKStages) & 1);
                 if (!ok) break;
+                tc_fence_after();
                 if (j + 2 < myst) issue_s(j + 2);
                 tc_commit_ew(&bars->k_empty[(j + 2) % kKStages]);
             }
@@ -491,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         const int t = t_tile, r = w_row + lane;  // tile, and its row: tensor memory lane
         const int myst = t ? nst1 : nst0;
         const int pos =  // last key the row sees
-            r < live_of(t) ? L - C + (int)((unsigned)(row0 + t * kRows + r) / (unsigned)g) : -1;
+            r < live_of(t) ? L - C + a.by_group.div(row0 + t * kRows + r) : -1;
         const uint32_t tm = tmem + t * kTmemTile + ((uint32_t)((warp & 3) * 32) << 16);
         // exponents of blocks c0 + lane: a word a lane, the next 32 read ahead
         const auto entry = [&](int blk) { return blk < nblk ? __ldg(bt + blk) : -1; };
@@ -644,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         constexpr int kStep = kThreads / kChunks;  // rows between a thread's pieces
         const int ch = threadIdx.x % kChunks;
         int cr = threadIdx.x / kChunks;
-        const int step_q = kStep / (unsigned)g, step_h = kStep - step_q * g;
-        int qi = (int)((unsigned)(row0 + cr) / (unsigned)g), h = row0 + cr - qi * g;
+        const int step_q = a.by_group.div(kStep), step_h = kStep - step_q * g;
+        int qi = a.by_group.div(row0 + cr), h = row0 + cr - qi * g;
 #pragma unroll 4
         for (int i = 0; i < 2 * kRows / kStep; ++i, cr += kStep) {
             const int r = cr & (kRows - 1);
@@ -705,6 +724,9 @@ cudaError_t launch_prefill8(const Pool8View& pool, const AttnArgs& a, cudaStream
     p.num_blocks = pool.num_blocks;
     p.group = g;
     p.batch = a.batch;
+    p.by_group = Divisor(g);
+    p.by_batch = Divisor(a.batch);
+    p.by_heads = Divisor(pool.num_kv_heads);
     p.scale_log2 = a.scale * kLog2e;
     // two tiles to a CTA, unless the tiles, one to an SM, all run at once
     const long long pairs = (long long)a.batch * pool.num_kv_heads;
