@@ -334,13 +334,20 @@ def pa_prefill_chunked(pool: PaPool, q: torch.Tensor, cu_q_lens: torch.Tensor, b
 
 
 # ----------------------------------------------------------------------------- 8-bit pool, weights, eviction
+# (looked up once: a call's own arithmetic is a few microseconds, and so is what Python adds to it)
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_empty_like = torch.empty_like
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _arg(t: torch.Tensor, dtype, name: str, device: int) -> int:
     """Address of a contiguous CUDA tensor of `dtype` on the call's device."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and device >= 0:
+        return t.data_ptr()
     if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors are on cuda:{device}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors are on cuda:{device}")
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
@@ -354,14 +361,22 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty_like(t)
 
 
+def _width(block_tables: torch.Tensor, seq_lens: torch.Tensor, batch: int) -> int:
+    """The tables' width, once they and the lengths are known to match the batch."""
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] != batch or seq_lens.numel() != batch:
+        _tables(block_tables, seq_lens, batch)
+    return shape[1]
+
+
 def _call(what: str, device: int, stream, *args) -> None:
     """The library's call on `device` (its current stream unless one is given)."""
-    fn = getattr(library(), what)
+    fn = getattr(_lib or library(), what)
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device)
+        raw = _raw_stream(device)
     else:
         raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch._C._cuda_getDevice() == device:
+    if _current_device() == device:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -407,18 +422,19 @@ def pa_kv_append8(pool: PaPool8, k_new: torch.Tensor, v_new: torch.Tensor, slot_
     if T == 0:
         return
     d = pool.device
-    _call("pa_kv_append8", d, stream, pool.ref, _arg(k_new, torch.bfloat16, "k_new", d),
-          _arg(v_new, torch.bfloat16, "v_new", d), _arg(slot_mapping, torch.int64, "slot_mapping", d), T)
+    _call("pa_kv_append8", d, stream, pool.ref, _arg(k_new, _BF16, "k_new", d),
+          _arg(v_new, _BF16, "v_new", d), _arg(slot_mapping, _I64, "slot_mapping", d), T)
 
 
 def _query(pool, q: torch.Tensor, out: Optional[torch.Tensor], stream) -> torch.Tensor:
     """Check q against the pool; the output tensor (the caller's, checked, or a new one)."""
-    if q.dim() != 3 or q.shape[2] != pool.head_dim:
-        raise ValueError(f"q: need [rows, num_heads, {pool.head_dim}], got {tuple(q.shape)}")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pool.head_dim:
+        raise ValueError(f"q: need [rows, num_heads, {pool.head_dim}], got {tuple(shape)}")
     if out is None:
-        return _like(q, stream)
-    if out.shape != q.shape:
-        raise ValueError(f"out: need shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        return _empty_like(q) if stream is None else _like(q, stream)
+    if out.shape != shape:
+        raise ValueError(f"out: need shape {tuple(shape)}, got {tuple(out.shape)}")
     return out
 
 
@@ -426,12 +442,11 @@ def pa_decode8(pool: PaPool8, q: torch.Tensor, block_tables: torch.Tensor, seq_l
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     d = pool.device
     out = _query(pool, q, out, stream)
-    B = q.shape[0]
-    _tables(block_tables, seq_lens, B)
-    _call("pa_decode8", d, stream, pool.ref, _arg(q, torch.bfloat16, "q", d),
-          _arg(block_tables, torch.int32, "block_tables", d), block_tables.shape[1],
-          _arg(seq_lens, torch.int32, "seq_lens", d), B, q.shape[1], float(scale),
-          _arg(out, torch.bfloat16, "out", d))
+    B, heads, _ = q.shape
+    width = _width(block_tables, seq_lens, B)
+    _call("pa_decode8", d, stream, pool.ref, _arg(q, _BF16, "q", d), _arg(block_tables, _I32, "block_tables", d), width,
+          _arg(seq_lens, _I32, "seq_lens", d), B, heads, float(scale),
+          _arg(out, _BF16, "out", d))
     return out
 
 
@@ -441,13 +456,13 @@ def pa_prefill_chunked8(pool: PaPool8, q: torch.Tensor, cu_q_lens: torch.Tensor,
     d = pool.device
     out = _query(pool, q, out, stream)
     B = seq_lens.numel()
-    _tables(block_tables, seq_lens, B)
+    width = _width(block_tables, seq_lens, B)
     if cu_q_lens.numel() != B + 1:
         raise ValueError(f"cu_q_lens: need {B + 1} entries, got {cu_q_lens.numel()}")
-    _call("pa_prefill_chunked8", d, stream, pool.ref, _arg(q, torch.bfloat16, "q", d),
-          _arg(cu_q_lens, torch.int32, "cu_q_lens", d), _arg(block_tables, torch.int32, "block_tables", d),
-          block_tables.shape[1], _arg(seq_lens, torch.int32, "seq_lens", d), B, q.shape[1], int(max_chunk),
-          float(scale), _arg(out, torch.bfloat16, "out", d))
+    _call("pa_prefill_chunked8", d, stream, pool.ref, _arg(q, _BF16, "q", d),
+          _arg(cu_q_lens, _I32, "cu_q_lens", d), _arg(block_tables, _I32, "block_tables", d),
+          width, _arg(seq_lens, _I32, "seq_lens", d), B, q.shape[1], int(max_chunk),
+          float(scale), _arg(out, _BF16, "out", d))
     return out
 
 
@@ -458,8 +473,7 @@ def pa_weights_workspace_bytes(batch: int, num_heads: int, num_kv_heads: int, ma
 def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weights, decay, workspace, out, stream):
     out = _query(pool, q, out, stream)
     B, Hq, _ = q.shape
-    _tables(block_tables, seq_lens, B)
-    width = block_tables.shape[1]
+    width = _width(block_tables, seq_lens, B)
     if weights.shape != (B, pool.num_kv_heads, width):
         raise ValueError(f"weights: need shape {(B, pool.num_kv_heads, width)}, got {tuple(weights.shape)}")
     if B == 0 or width == 0:
@@ -470,11 +484,11 @@ def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weight
             _like(weights.expand(need // weights.numel(), *weights.shape), stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace: need {need} floats, got {workspace.numel()}")
-    _call(what, device, stream, pool.ref, _arg(q, torch.bfloat16, "q", device),
-          _arg(block_tables, torch.int32, "block_tables", device), width,
-          _arg(seq_lens, torch.int32, "seq_lens", device), B, Hq, float(scale), float(decay),
-          _arg(weights, torch.float32, "weights", device), _arg(workspace, torch.float32, "workspace", device),
-          _arg(out, torch.bfloat16, "out", device))
+    _call(what, device, stream, pool.ref, _arg(q, _BF16, "q", device),
+          _arg(block_tables, _I32, "block_tables", device), width,
+          _arg(seq_lens, _I32, "seq_lens", device), B, Hq, float(scale), float(decay),
+          _arg(weights, _F32, "weights", device), _arg(workspace, _F32, "workspace", device),
+          _arg(out, _BF16, "out", device))
     return out
 
 
@@ -510,13 +524,14 @@ def pa_kv_evict(block_tables: torch.Tensor, seq_lens: torch.Tensor, weights: tor
         raise ValueError(f"block_tables / seq_lens: need shapes {(B, width)} / {(B,)}, got "
                          f"{tuple(block_tables.shape)} / {tuple(seq_lens.shape)}")
     d = weights.get_device()
+    like = _empty_like if stream is None else lambda t: _like(t, stream)
     if in_place:
         new_tables, new_lens, new_weights = block_tables, seq_lens, weights
     else:
-        new_tables, new_lens, new_weights = _like(block_tables, stream), _like(seq_lens, stream), _like(weights, stream)
-    evicted, num = _like(block_tables, stream), _like(seq_lens, stream)
-    _call("pa_kv_evict", d, stream, _arg(block_tables, torch.int32, "block_tables", d),
-          _arg(seq_lens, torch.int32, "seq_lens", d), _arg(weights, torch.float32, "weights", d), B, width, hkv,
+        new_tables, new_lens, new_weights = like(block_tables), like(seq_lens), like(weights)
+    evicted, num = like(block_tables), like(seq_lens)
+    _call("pa_kv_evict", d, stream, _arg(block_tables, _I32, "block_tables", d),
+          _arg(seq_lens, _I32, "seq_lens", d), _arg(weights, _F32, "weights", d), B, width, hkv,
           int(keep_blocks), int(sink_blocks), int(recent_blocks), new_tables.data_ptr(), new_lens.data_ptr(),
           new_weights.data_ptr(), evicted.data_ptr(), num.data_ptr())
     return new_tables, new_lens, new_weights, evicted, num
