@@ -36,8 +36,8 @@
 // the rows in the free Q buffer and store them coalesced.
 //
 // Measured on GB300 (32 q / 8 kv heads, d 128), the bf16 pool's kernel on the same values in brackets:
-// 8 x 256 over 768 cached tokens 37.5 us (59), over 3840 107 (195), 1 x 256 over 768 15.7 (26.8),
-// 8 x 1024 over 1024 176 (304): 0.73 us a stage of two tiles, 1400 cycles, of which the matrix
+// 8 x 256 over 768 cached tokens 37 us (59), over 3840 105 (195), 1 x 256 over 768 15.7 (26.9),
+// 8 x 1024 over 1024 173 (304): 0.72 us a stage of two tiles, 1400 cycles, of which the matrix
 // pipe needs 1280 (Q K^T reads Q and K from shared memory for 768, u V runs for 512), and about
 // 8 us a CTA outside its stages: loads that wait for one another (lengths, table, codes) and q 4.5,
 // output 2.5.
