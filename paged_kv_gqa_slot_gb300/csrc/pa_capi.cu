@@ -47,16 +47,14 @@ struct MapKey {
     int d;
     int kind;   // 0: 2-D half-tile boxes, 1: 4-D whole-tile boxes, 2: 3-D (d, head, token) rows
     int extra;  // kind 2: heads * 65536 + box heads
-    long long stride = 0;  // kind 3: distance of the two planes (0: one plane)
     bool operator==(const MapKey& o) const {
-        return base == o.base && rows == o.rows && d == o.d && kind == o.kind && extra == o.extra &&
-               stride == o.stride;
+        return base == o.base && rows == o.rows && d == o.d && kind == o.kind && extra == o.extra;
     }
 };
 struct MapKeyHash {
     size_t operator()(const MapKey& k) const {
         return std::hash<const void*>()(k.base) ^ (std::hash<long long>()(k.rows) * 31u) ^ (size_t)k.d ^
-               ((size_t)k.kind << 20) ^ ((size_t)k.extra << 24) ^ std::hash<long long>()(k.stride);
+               ((size_t)k.kind << 20) ^ ((size_t)k.extra << 24);
     }
 };
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash>& map_cache() {
@@ -191,23 +189,12 @@ bool rows_map(CUtensorMap* out, const void* base, long long tokens, int heads, i
     return true;
 }
 
-// One map of kind 3: bytes as (64 or 128, rows, row_bytes / 128 halves, planes), the halves dimension
-// only for rows of 256 bytes; box: one tile of every plane.
+// A map of bytes as (64 or 128, rows, row_bytes / 128 halves, planes), the halves dimension only for rows
+// of 256 bytes; box: one tile of every plane.  Encoded by every call (a fraction of a microsecond): nothing
+// is kept by a pool's address.
 static bool plane_map(CUtensorMap* out, const void* base, long long rows, int row_bytes, long long stride) {
-    auto& cache = map_cache();
-    MapKey key{base, rows, row_bytes, 3, 0};
-    key.stride = stride;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        auto it = cache.find(key);
-        if (it != cache.end()) {
-            *out = it->second;
-            return true;
-        }
-    }
     auto fn = encode_fn();
     if (!fn) return false;
-    CUtensorMap m;
     const int halves = row_bytes / 128, planes = stride ? 2 : 1;
     const int rank = halves > 1 ? 4 : 3;
     const cuuint64_t inner = std::min(row_bytes, 128);
@@ -224,16 +211,9 @@ static bool plane_map(CUtensorMap* out, const void* base, long long rows, int ro
     dims[i] = planes;
     strides[i - 1] = between;
     box[i] = planes;
-    const CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return false;
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (cache.size() > 256) cache.clear();
-    cache[key] = m;
-    *out = m;
-    return true;
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool plane_maps(PlaneMaps* out, const void* k, const void* v, long long rows, int row_bytes) {
