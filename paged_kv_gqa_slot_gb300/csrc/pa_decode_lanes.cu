@@ -17,7 +17,8 @@
 // x = log2(e) scale <q, K> the weight the V product takes is u = 2^(x + kV - base), base following
 // the maximum of x + kV, so u fits f16 whatever the blocks' scales, and the largest contributions,
 // not the largest probabilities, set its range.  u is rounded to f16's 11 bits (an eighth of the
-// rounding of the bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.
+// rounding of the bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.  Where scales lie far apart
+// (far_scale) it adds 2^(x - base), each by an exponential of its own: u may be zero where that is not.
 // 16 bits: the same with kK = kV = 0 on bf16 MMAs, u carried as two bf16 parts.
 //
 // Loads.  Which d values make one MMA step, and which token is which MMA row, is free as long as q,
@@ -161,6 +162,12 @@ __device__ __forceinline__ float fast_log2(float x) {
 __device__ __forceinline__ float rescale_sum(float l, float d) {
     const float h = fast_exp2(0.5f * d);
     return l * h * h;
+}
+
+// 2^x down to fp32's last subnormal (fast_exp2 ends at 2^-126), for terms of the normaliser.
+__device__ __forceinline__ float exp2_term(float x) {
+    const float h = fast_exp2(0.5f * x);
+    return h * h;
 }
 
 // Where group `grp` (4 floats) of a head's row sits in the merge scratch: the lanes that write one
@@ -361,6 +368,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
     v_off += a.k_second ? 0 : Sh::kPlane;
     v_flip += a.k_second ? 0 : Sh::kPlane;
     bool ok = true;
+    bool far = false;  // some block so far has a far_scale
     int slot = 0, parity = 0, k = 0;
     for (; k < n; ++k) {
         const int at = k & 31;
@@ -379,6 +387,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
             kscale = __int_as_float((e & 255) << 23);
             unscale = __int_as_float((2 * kExpBias - (e >> 8)) << 23);
             fev = static_cast<float>((e >> 8) - kExpBias);
+            far = far || far_scale(e >> 8);
         }
         const int kbase = static_cast<int>(entry_at(k)) * kBlockSize;
 
@@ -478,6 +487,10 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 sum[j] = (u[nt][j][0] + u[nt][j][1]) * unscale;
+                if (far) {
+                    const float base = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+                    sum[j] = exp2_term(st[nt][j] - base) + exp2_term(st[nt][2 + j] - base);
+                }
                 l[nt][j] += sum[j];
             }
             if (WEIGHTS) {

@@ -33,6 +33,16 @@ __device__ __forceinline__ int valid_exps(int word) {
     return k | v << 8;
 }
 
+// The kernels' softmax weighs V by u = 2^(x + kV - base) and sums the normaliser's 2^(x - base) as u 2^-kV.
+// u ends at 2^-126 and the normaliser holds 2^-kB of the block that set the base, so that is right as
+// long as kB - kV stays far below 126: with every kV a row has seen within +-kNearScale, terms below
+// 2^(96 - 126) of the normaliser are lost.  From the first V exponent byte outside on, the terms
+// are taken by an exponential of their own.
+constexpr int kNearScale = 48;
+__device__ __forceinline__ bool far_scale(int byte) {
+    return static_cast<unsigned>(byte - kExpBias + kNearScale) > 2u * kNearScale;
+}
+
 // The smallest k with amax <= 448 * 2^k (amax finite, >= 0), within [kExpMin, kExpMax].
 // amax = f * 2^e with f in [1, 2), and 448 = 1.75 * 2^8.
 __device__ __forceinline__ int scale_exponent(float amax) {

@@ -11,7 +11,7 @@
 // widen with one conversion per two codes and no multiplication; q is brought to a maximum in
 // [2^14, 2^15) per row by a power of two.  The scales live in the softmax: with kK, kV the
 // exponents of a key's block, s the raw product and f = log2(e) scale 2^(eq + kK),
-//     u = 2^(s f + kV - base),   O += u codeV,   l += u 2^-kV,
+//     u = 2^(s f + kV - base),   O += u codeV,   l += u 2^-kV (or 2^(s f - base): stage_terms),
 // base following the row's maximum of s f + kV.  u is rounded to f16 (11 bits), which needs no
 // second part even where a few weights dominate a row.
 //
@@ -322,6 +322,20 @@ __device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, co
     return all;
 }
 
+// The stage's sum of 2^(s f - base), the normaliser's terms, each by an exponential of its own (far_scale),
+// in two steps, so that it ends with fp32's subnormals.
+__device__ __forceinline__ float stage_terms(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf,
+                                             float nbase) {
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) {
+        const float x = fmaf(__uint_as_float(s[c >> 5][c & 31]), k_factor(ew[c >> 4], qf), nbase);
+        const float h = fast_exp2(c > lim ? -INFINITY : 0.5f * x);
+        sum = fmaf(h, h, sum);
+    }
+    return sum;
+}
+
 // The row's D fp32 columns of O at `taddr` times f, eight at a time.
 template <int D>
 __device__ __forceinline__ void scale_o(uint32_t taddr, float f) {
@@ -558,6 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full);
         float base = -INFINITY, l = 0.f;
+        // of a stage's sum, past which it takes the maximum path; negative (every stage takes it) from a block with
+        // a far_scale on
+        float limit = kSumLimit;
         bool ok = true;
         // tcgen05.ld / st are warp-collective: what leads to one is decided by the whole warp
         for (int j = 0; j < myst; ++j) {
@@ -566,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                 ex = next_ex;
                 next_id = entry(j * kParts + 32 + lane);
             }
+            if (at == 0) limit = __any_sync(0xffffffffu, far_scale(ex >> 8)) ? -1.f : limit;
             int ew[kParts];
 #pragma unroll
             for (int i = 0; i < kParts; ++i) ew[i] = __shfl_sync(0xffffffffu, ex, at + i);
@@ -583,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             tmem_wait_ld(s[1]);
             // First against the row's base as it is.  The maximum, and with it a possible move of the
             // base, is taken only for a row's first visible stage, or when the sum of u passes
-            // kSumLimit; either is the warp's decision.
+            // the limit; either is the warp's decision.
             float lsum = 0.f;
             const auto weigh = [&] {
                 const float nbase = base == -INFINITY ? 0.f : -base;
@@ -591,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                                 : stage_u<false>(s, lim, ew, qf, nbase, buf, lsum);
             };
             bool full = __any_sync(0xffffffffu, base == -INFINITY && lim >= 0);
-            if (!full) full = __any_sync(0xffffffffu, !(weigh() <= kSumLimit));
+            if (!full) full = __any_sync(0xffffffffu, !(weigh() <= limit));
             if (full) {
                 tmem_wait_st();  // a first attempt's u: the second goes over it
                 const float mx = unmasked ? stage_max<true>(s, lim, ew, qf) : stage_max<false>(s, lim, ew, qf);
@@ -611,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                 }
                 if (move) base = top;
                 weigh();
+                if (limit < 0.f) lsum = stage_terms(s, lim, ew, qf, base == -INFINITY ? 0.f : -base);
             }
             l += lsum;
             tmem_wait_st();
