@@ -14,11 +14,12 @@
 // scale joins the softmax scale (one factor per block and head).  q enters as f16 too, after its
 // row is brought to a maximum in [2^14, 2^15) by a power of two that joins the same factor: an
 // element loses bits only below 2^-29 of the row's maximum.  V's scale joins the exponent: with
-// x = log2(e) scale <q, K> the weight the V product takes is u = 2^(x + kV - base), base following
+// x = log2(e) scale <q, K> the weight the V product takes is u = 2^(x + kV - m + 7), m following
 // the maximum of x + kV, so u fits f16 whatever the blocks' scales, and the largest contributions,
 // not the largest probabilities, set its range.  u is rounded to f16's 11 bits (an eighth of the
-// rounding of the bf16 result); the normaliser adds u 2^-kV in fp32, unrounded.  Where scales lie far apart
-// (far_scale) it adds 2^(x - base), each by an exponential of its own: u may be zero where that is not.
+// rounding of the bf16 result) where it is more than 2^-21 of the largest, to fewer below, and is zero below
+// 2^-32 (kHeadroom); the normaliser adds u 2^(-kV - 7) in fp32, unrounded.  Where scales lie far apart
+// (far_scale) it adds 2^(x - m), each by an exponential of its own: u may be zero where that is not.
 // 16 bits: the same with kK = kV = 0 on bf16 MMAs, u carried as two bf16 parts.
 //
 // Loads.  Which d values make one MMA step, and which token is which MMA row, is free as long as q,
@@ -156,8 +157,8 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
-// A normaliser l = sum of u 2^-kV moved from one base to one 2^-d higher: l 2^d.  Its terms carry
-// 2^-kV, so l may be as large as 2^100 where u is about 1, and l 2^d matters where 2^d alone
+// A normaliser l = sum of 2^(x - base) moved from one base to one 2^-d higher: l 2^d.  Its terms carry
+// 2^-kV, so l may be as large as 2^100 where x + kV is the base, and l 2^d matters where 2^d alone
 // is zero in fp32 (blocks of V at the two ends of the scales' range).
 __device__ __forceinline__ float rescale_sum(float l, float d) {
     const float h = fast_exp2(0.5f * d);
@@ -183,6 +184,9 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
     constexpr int kCtas = ctas_of(WIDE);
     constexpr int kStages = Sh::stages(kWarps, kCtas);  // ring slots per warp
     constexpr int kSteps = D / 16;    // MMA steps over d (K), tiles of d (V)
+    // u at a column's maximum is 2^kHead, and moves the base past kTop (f16 ends at 2^16)
+    constexpr int kHead = BITS == 8 ? kHeadroom : 0;
+    constexpr float kTop = BITS == 8 ? 32768.f : 1024.f;
     constexpr int kRowB = Sh::kRowBytes;
     extern __shared__ __align__(1024) uint8_t smem[];
 
@@ -381,11 +385,11 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
         const uint32_t st_at = ring + slot * Sh::kBlockBytes;
         ok = mbar_wait_warp(&full[slot], parity);
         if (!ok) break;
-        float kscale = 1.f, unscale = 1.f, fev = 0.f;  // 2^kK, 2^-kV, kV
+        float kscale = 1.f, unscale = 1.f, fev = 0.f;  // 2^kK, 2^(-kV - kHead), kV
         if constexpr (BITS == 8) {
             const int e = __shfl_sync(0xffffffffu, ex, at);
             kscale = __int_as_float((e & 255) << 23);
-            unscale = __int_as_float((2 * kExpBias - (e >> 8)) << 23);
+            unscale = __int_as_float((2 * kExpBias - kHead - (e >> 8)) << 23);
             fev = static_cast<float>((e >> 8) - kExpBias);
             far = far || far_scale(e >> 8);
         }
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
             }
         }
         // u against the columns' bases as they are; the bases move only in a warp's first block, or
-        // when some u passes 2^10 (f16 ends at 2^16), then to the maximum
+        // when some u passes kTop, then to the maximum
         float u[NT][2][2];  // [column][token gid, gid + 8]
         const bool whole = kbase + kBlockSize - 1 <= all_see;
         bool move = k == 0;
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float f = qf[nt][j] * kscale, off = fev - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
+                const float f = qf[nt][j] * kscale, off = fev + kHead - (m[nt][j] == -INFINITY ? 0.f : m[nt][j]);
                 st[nt][j] = (NT == 1 ? st[0][j] + st[1][j] : st[nt][j]) * f;
                 st[nt][2 + j] = (NT == 1 ? st[0][2 + j] + st[1][2 + j] : st[nt][2 + j]) * f;
                 u[nt][j][0] = fast_exp2(st[nt][j] + off);
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) move |= !(u[nt][j][0] <= 1024.f) || !(u[nt][j][1] <= 1024.f);
+            for (int j = 0; j < 2; ++j) move |= !(u[nt][j][0] <= kTop) || !(u[nt][j][1] <= kTop);
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -476,8 +480,8 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
                         ot[nt][s][j] *= alpha;
                         ot[nt][s][2 + j] *= alpha;
                     }
-                    u[nt][j][0] = fast_exp2(st[nt][j] + (fev - base));
-                    u[nt][j][1] = fast_exp2(st[nt][2 + j] + (fev - base));
+                    u[nt][j][0] = fast_exp2(st[nt][j] + (fev + kHead - base));
+                    u[nt][j][1] = fast_exp2(st[nt][2 + j] + (fev + kHead - base));
                 }
         }
         uint32_t pb[NT][2], pl[NT][2];
@@ -638,6 +642,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
         const size_t tok = MQ ? (size_t)q0 + col / g : (size_t)b;
         return a.out + (tok * a.num_heads + (size_t)kvh * g + (MQ ? col % g : col)) * D + qd % (D / 4) * 4;
     };
+    const auto inverse = [](float den) { return den > 0.f ? 1.f / static_cast<float>(1 << kHead) / den : 0.f; };
     const auto store = [&](int qd, const float4& v, float inv) {
         uint2 w = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         *reinterpret_cast<uint2*>(out_at(qd)) = w;
@@ -661,7 +666,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
             acc.w += wt * v.w;
             den += rescale_sum(pm[16 + col], pm[col] - M);
         }
-        if (sub == 1) store(qd, acc, den > 0.f ? 1.f / den : 0.f);
+        if (sub == 1) store(qd, acc, inverse(den));
         *reinterpret_cast<float4*>(cta + 32 + col * Sh::kRow + 4 * grp) = acc;
         if (grp == 0) {
             cta[col] = M;
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
                 acc.z += w * v.z;
                 acc.w += w * v.w;
             }
-            store(qd, acc, col_l[col] > 0.f ? 1.f / col_l[col] : 0.f);
+            store(qd, acc, inverse(col_l[col]));
         }
     }
     if (WEIGHTS) {

@@ -33,12 +33,19 @@ __device__ __forceinline__ int valid_exps(int word) {
     return k | v << 8;
 }
 
-// The kernels' softmax weighs V by u = 2^(x + kV - base) and sums the normaliser's 2^(x - base) as u 2^-kV.
+// The kernels' softmax weighs V by u = 2^(x + kV - base) (but for a constant factor) and sums the normaliser's 2^(x - base) as u 2^-kV.
 // u ends at 2^-126 and the normaliser holds 2^-kB of the block that set the base, so that is right as
 // long as kB - kV stays far below 126: with every kV a row has seen within +-kNearScale, terms below
 // 2^(96 - 126) of the normaliser are lost.  From the first V exponent byte outside on, the terms
 // are taken by an exponential of their own.
 constexpr int kNearScale = 48;
+
+// u is rounded to f16, which has 11 bits from 2^-14 on and ends at 2^16 and 2^-25.  A base kHeadroom log2
+// units below the row's maximum uses f16's upper range, so that u keeps its bits down to 2^-21 of the
+// largest and some down to 2^-32: with one key that takes 0.9998 of a row and has no value of its own, the rest
+// over 4095 others, the result is right to 2^-8 (with the base at the maximum it was 5% off).  The normaliser
+// takes u 2^(-kV - kHeadroom), a normal factor for every kV.
+constexpr int kHeadroom = 7;
 __device__ __forceinline__ bool far_scale(int byte) {
     return static_cast<unsigned>(byte - kExpBias + kNearScale) > 2u * kNearScale;
 }

@@ -11,9 +11,10 @@
 // widen with one conversion per two codes and no multiplication; q is brought to a maximum in
 // [2^14, 2^15) per row by a power of two.  The scales live in the softmax: with kK, kV the
 // exponents of a key's block, s the raw product and f = log2(e) scale 2^(eq + kK),
-//     u = 2^(s f + kV - base),   O += u codeV,   l += u 2^-kV (or 2^(s f - base): stage_terms),
-// base following the row's maximum of s f + kV.  u is rounded to f16 (11 bits), which needs no
-// second part even where a few weights dominate a row.
+//     u = 2^(s f + kV - base),   O += u codeV,   l += u 2^(-kV - 7) (or 2^(s f - base - 7): stage_terms),
+// base some log2 units below the row's maximum of s f + kV.  u is rounded to f16: 11 bits down to 2^-14, fewer
+// below, zero below 2^-25.  So the base lies kHeadroom units below a maximum that stands alone, kFlatHeadroom
+// below one that has others beside it.
 //
 // Per stage of 64 keys (four pool blocks):
 //   warps 10-15  three for K, three for V, take every third pair of blocks: codes come by a bulk copy a
@@ -27,8 +28,8 @@
 //                shuffle, so that descriptors and barrier addresses live in uniform registers: with
 //                them in every thread's, an instruction took 80 cycles to issue, and a stage 1750.
 //   warps 0-7    softmax, one row a thread: reads S, writes u over it.  The base is set by a row's
-//                first visible stage and moves only when a stage's sum passes 2^15 (f16 ends at
-//                2^16), then to the maximum, if that is more than 2^8 above; O is rescaled in
+//                first visible stage and moves only when a stage's sum passes kSumLimit (f16 ends at
+//                2^16), then by the maximum, if that is more than 2^9 above; O is rescaled in
 //                tensor memory by all rows of a warp together.  (The maximum in every stage instead
 //                cost 6 us of 52.)
 // Before, they stage their rows of q by coalesced asynchronous copies and normalise them in place (rows
@@ -64,8 +65,16 @@ constexpr int kThreads = 512;
 constexpr int kTmemCols = 512;             // per tile: two 64-column score buffers, then O
 constexpr uint32_t kTmemTile = 256;
 constexpr uint32_t kTmemS = 0, kTmemO = 128;
-constexpr float kSumLimit = 32768.f;      // a stage sum of u past this takes the maximum path
-constexpr float kRebase = 8.f;            // log2 units a maximum must exceed the base by to move it
+constexpr float kSumLimit = 61440.f;      // a stage sum of u past this takes the maximum path
+// Log2 units a maximum must exceed the base by to move it: 64 keys under it sum to less than 2^(6 + 9), so a row whose
+// sum is past the limit moves.
+constexpr float kRebase = 9.f;
+static_assert(kKeys * 512 < kSumLimit, "a row past the limit moves its base");
+// A maximum is alone if no other block of the stage comes within 2^-kAlone of it.  The units that the base
+// lies below a maximum are lost above it, and where K's scales differ from block to block (by 2^0.7 in
+// the standard deviation), 7 for every row took 5% of the stages to the maximum path, and 8 x 256 over
+// 768 39.5 us; with 2 beside others it is 0.5%, as with none.
+constexpr float kAlone = 6.f, kFlatHeadroom = 2.f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D>
@@ -80,7 +89,7 @@ struct Pre8 {
     static constexpr int kOffV = kOffK + kKStages * kStage;
     static constexpr int kOffRaw = kOffV + kVStages * kStage;
     static constexpr int kOffBars = kOffRaw + kCvtWarps * kAhead * 2 * kUnit;
-    static constexpr int kOffInv = kOffBars + 512;     // [2][128] 1 / l, then whether every wait ended
+    static constexpr int kOffInv = kOffBars + 512;     // [2][128] 2^-7 / l, then whether every wait ended
     static constexpr int kSmem = kOffInv + 2 * kRows * 4 + 16;
     static constexpr int kLoads = kBlockSize * D / 512;  // 16-byte pieces of a block a lane takes
 };
@@ -257,15 +266,19 @@ struct Converter {
 };
 
 // The scales of a block as the softmax takes them, from its word of exponents (K in the low byte):
-// the factor qf 2^kK on s, kV, and 2^-kV.
+// the factor qf 2^kK on s, kV, and 2^(-kV - 7).
 __device__ __forceinline__ float k_factor(int e, float qf) { return qf * __int_as_float((e & 255) << 23); }
 __device__ __forceinline__ float v_exponent(int e) { return static_cast<float>((e >> 8) - kExpBias); }
-__device__ __forceinline__ float v_unscale(int e) { return __int_as_float((2 * kExpBias - (e >> 8)) << 23); }
+__device__ __forceinline__ float v_unscale(int e) {
+    return __int_as_float((2 * kExpBias - kHeadroom - (e >> 8)) << 23);
+}
 
-// Largest s f + kV of the stage's visible keys c <= lim (all of them with kAll).
+// Largest s f + kV of the stage's visible keys c <= lim (all of them with kAll); second: that of the other blocks.
 template <bool kAll>
-__device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf) {
+__device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf,
+                                           float& second) {
     float best = -INFINITY;
+    second = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
         float m0 = -INFINITY, m1 = -INFINITY;
@@ -280,14 +293,16 @@ __device__ __forceinline__ float stage_max(const uint32_t (&s)[2][32], int lim, 
             m0 = fmax3(m0, x[0], x[1]);
             m1 = fmax3(m1, x[2], x[3]);
         }
-        const float m = fmaxf(m0, m1);
-        best = fmaxf(best, m == -INFINITY ? m : fmaf(m, k_factor(ew[i], qf), v_exponent(ew[i])));
+        float m = fmaxf(m0, m1);
+        m = m == -INFINITY ? m : fmaf(m, k_factor(ew[i], qf), v_exponent(ew[i]));
+        second = fmaxf(second, fminf(best, m));
+        best = fmaxf(best, m);
     }
     return best;
 }
 
-// u of the stage against base -nbase, as f16 pairs into the 32 columns at `dst`; returns their plain
-// sum, and lsum gets the sum of u 2^-kV.
+// u of the stage, 2^(s f + kV + nbase), as f16 pairs into the 32 columns at `dst`; returns their plain
+// sum, and lsum gets the sum of u 2^(-kV - 7).
 template <bool kAll>
 __device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf,
                                          float nbase, uint32_t dst, float& lsum) {
@@ -322,7 +337,7 @@ __device__ __forceinline__ float stage_u(const uint32_t (&s)[2][32], int lim, co
     return all;
 }
 
-// The stage's sum of 2^(s f - base), the normaliser's terms, each by an exponential of its own (far_scale),
+// The stage's sum of 2^(s f + nbase), the normaliser's terms, each by an exponential of its own (far_scale),
 // in two steps, so that it ends with fp32's subnormals.
 __device__ __forceinline__ float stage_terms(const uint32_t (&s)[2][32], int lim, const int (&ew)[kParts], float qf,
                                              float nbase) {
@@ -612,8 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             if (!full) full = __any_sync(0xffffffffu, !(weigh() <= limit));
             if (full) {
                 tmem_wait_st();  // a first attempt's u: the second goes over it
-                const float mx = unmasked ? stage_max<true>(s, lim, ew, qf) : stage_max<false>(s, lim, ew, qf);
-                const float top = fmaxf(base, mx);
+                float second;
+                const float top = unmasked ? stage_max<true>(s, lim, ew, qf, second)
+                                           : stage_max<false>(s, lim, ew, qf, second);
+                const float target = top - (top - second > kAlone ? (float)kHeadroom : kFlatHeadroom);
                 const bool move = top > base + kRebase;  // always at a row's first visible key
                 const bool rescale = move && base != -INFINITY;
                 if (__any_sync(0xffffffffu, rescale)) {
@@ -622,14 +639,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
                     if (j > 0) ok = mbar_wait_warp(&bars->o_done[t], (j - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    scale_o<D>(tm + kTmemO, rescale ? fast_exp2(base - top) : 1.f);
+                    scale_o<D>(tm + kTmemO, rescale ? fast_exp2(base - target) : 1.f);
                     // in two steps: l, whose terms carry 2^-kV, may count where the factor is zero
-                    const float half = rescale ? fast_exp2(0.5f * (base - top)) : 1.f;
+                    const float half = rescale ? fast_exp2(0.5f * (base - target)) : 1.f;
                     l = l * half * half;
                 }
-                if (move) base = top;
+                if (move) base = target;
                 weigh();
-                if (limit < 0.f) lsum = stage_terms(s, lim, ew, qf, base == -INFINITY ? 0.f : -base);
+                if (limit < 0.f) lsum = stage_terms(s, lim, ew, qf, base == -INFINITY ? 0.f : -base - kHeadroom);
             }
             l += lsum;
             tmem_wait_st();
@@ -638,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(&bars->p_full[t][j & 1]);
         }
         if (ok && myst > 0) ok = mbar_wait_warp(&bars->o_final[t], 0);
-        row_inv[t * kRows + r] = l > 0.f ? 1.f / l : 0.f;
+        row_inv[t * kRows + r] = l > 0.f ? 1.f / (1 << kHeadroom) / l : 0.f;
         if (!ok && lane == 0) {
             *all_ok = 0;
             atomicOr(a.status, kDevTimeout);
