@@ -173,7 +173,7 @@ int pa_decode(const pa_pool *pool, const void *q, const int32_t *block_tables, i
  * taken exactly as stored; q enters the tensor core as f16 after each row is brought to a
  * maximum in [2^14, 2^15) by a power of two (exact for elements above 2^-29 of the row's
  * maximum), the softmax weights as f16, each with its block's V scale, under a running
- * maximum of their products; sums are fp32.
+ * maximum of their products; sums are fp32.  A NaN among the scores a head sees makes its result NaN.
  */
 int pa_decode8(const pa_pool8 *pool, const void *q, const int32_t *block_tables, int32_t max_blocks,
                const int32_t *seq_lens, int32_t batch, int32_t num_heads, float scale, void *out,

@@ -625,7 +625,9 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
             for (int j = 0; j < 2; ++j) {
                 const int col = nt * 8 + 2 * tig + j;
                 if (gid == 0) {
-                    pm[col] = m[nt][j];
+                    // a column with no score but NaN (l = NaN) has found no maximum, but must not pass for one
+                    // without keys, which the merge leaves out
+                    pm[col] = m[nt][j] == -INFINITY && l[nt][j] != 0.f ? 0.f : m[nt][j];
                     pm[16 + col] = l[nt][j];
                 }
 #pragma unroll

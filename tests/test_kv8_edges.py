@@ -130,3 +130,76 @@ def test_prefill_with_a_sink(where, chunk, d, code):
     c = sink_case(92, 4096, d, where, chunk, code)
     sink_check(c, pa.pa_prefill_chunked8(c.pool, c.q, c.cu, c.tables, c.lens, c.scale, c.max_chunk))
     clean()
+
+
+# ----------------------------------------------------------------------------- NaN among the scores
+@gpu
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_nan_in_a_query_row(d, many):
+    """A NaN in q makes the result of that (sequence, head) NaN, adds nothing to the weights, and concerns no other."""
+    lens = [40, 700, 17, 3, 0] * (30 if many else 1)
+    c = Case(101, lens, 16, 4, d)
+    ref, spread, want, mag = c.reference()
+    q = c.q.clone()
+    bad = [(0, 0, 5), (1, 7, d - 1), (2, 15, 0), (3, 4, 9)]
+    for b, h, i in bad:
+        q[b, h, i] = float("nan")
+    w = torch.zeros(len(lens), 4, c.tables.shape[1], device="cuda")
+    out8 = pa.pa_decode8(c.pool, q, c.tables, c.lens, c.scale)
+    out = pa.pa_decode8_weights(c.pool, q, c.tables, c.lens, c.scale, w)
+    k, v = R.dequant(c.k, c.exps[..., 0]), R.dequant(c.v, c.exps[..., 1])
+    w16 = torch.zeros_like(w)
+    out16 = pa.pa_decode_weights(pa.PaPool(k.to(torch.bfloat16), v.to(torch.bfloat16)), q, c.tables, c.lens, c.scale, w16)
+    for o in (out8, out, out16):
+        for b, h, _ in bad:
+            assert torch.isnan(o[b, h]).all()
+            o[b, h] = ref[b, h].to(o.dtype)
+        check(o, ref, spread, 700, mag)
+    heads = torch.full((len(lens), 4), 4.0, device="cuda")
+    for b, h, _ in bad:
+        heads[b, h // 4] -= 1
+    heads[[b for b, n in enumerate(lens) if n == 0]] = 0
+    for got in (w, w16):
+        assert torch.allclose(got.sum(2), heads, rtol=2.0 ** -11)
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("n", [17, 33, 700 * 16 + 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_nan_in_a_key_that_is_alone_in_its_block(d, n):
+    """The last block holds one key, whose K has a NaN: every head of its kv head sees it, whichever warp and
+    split the block falls to.  Its weights get the decay and nothing else."""
+    c = Case(102, [n, 50], 8, 2, d)
+    ref, spread, want, mag = c.reference()
+    c.k[c.tables_h[0][n // 16], 1, 0, 3] = NAN_CODE
+    w0 = torch.rand(2, 2, c.tables.shape[1], device="cuda")
+    w = w0.clone()
+    out8 = pa.pa_decode8(c.pool, c.q, c.tables, c.lens, c.scale)
+    out = pa.pa_decode8_weights(c.pool, c.q, c.tables, c.lens, c.scale, w, 0.5)
+    for o in (out8, out):
+        assert torch.isnan(o[0, 4:]).all()
+        o[0, 4:] = ref[0, 4:].to(o.dtype)
+        check(o, ref, spread, n, mag)
+    nb = (n + 15) // 16
+    assert torch.equal(w[0, 1, :nb], w0[0, 1, :nb] * 0.5) and torch.isfinite(w).all()
+    assert torch.allclose(w[0, 0, :nb].double(), w0[0, 0, :nb].double() * 0.5 + want[0][0], rtol=2.0 ** -11)
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_prefill_nan_in_a_query_row(d):
+    c = Case(103, [100, 3, 700], 8, 2, d, [4, 1, 3])
+    ref, spread, _, mag = c.reference()
+    q = c.q.clone()
+    bad = [(0, 1), (2, 7), (4, 0), (7, 5)]
+    for r, h in bad:
+        q[r, h, 11] = float("nan")
+    out = pa.pa_prefill_chunked8(c.pool, q, c.cu, c.tables, c.lens, c.scale, c.max_chunk)
+    for r, h in bad:
+        assert torch.isnan(out[r, h]).all()
+        out[r, h] = ref[r, h].to(out.dtype)
+    check(out, ref, spread, 700, mag)
+    clean()
