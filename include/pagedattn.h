@@ -299,6 +299,7 @@ int pa_prefill_chunked(const pa_pool *pool, const void *q, const int32_t *cu_q_l
 /*
  * pa_prefill_chunked8 -- pa_prefill_chunked over an 8-bit pool: same arguments and
  * errors, arithmetic as pa_decode8.  Chunks of at most 16 / group queries run on the decode kernel.
+ * A NaN in V concerns the queries that see its key, and its column, alone.
  */
 int pa_prefill_chunked8(const pa_pool8 *pool, const void *q, const int32_t *cu_q_lens, const int32_t *block_tables,
                         int32_t max_blocks, const int32_t *seq_lens, int32_t batch, int32_t num_heads,

@@ -179,6 +179,7 @@ template <int BITS, int D, int NT, bool MQ, bool WEIGHTS, int WIDE>
 __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE))
     decode_lanes_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ LanesArgs a) {
+    static_assert(!MQ || BITS == 8, "codes of 8 bits");
     using Sh = Lanes<BITS, D>;
     constexpr int kWarps = warps_of(BITS, D, NT, WIDE), kThreads = kWarps * 32;
     constexpr int kCtas = ctas_of(WIDE);
@@ -541,14 +542,52 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
                 }
             }
         }
-        if (kbase + kBlockSize > L) {
+        if (MQ ? !whole : kbase + kBlockSize > L) {
             // rows past the sequence's end: whatever they hold (NaN times u = 0 is NaN)
+            uint32_t some = 0u;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (kbase + (vrow ^ (r & 1 ? kNext : 0)) + (r >> 1) * 8 >= L) {
+            for (int r = 0; r < 4; ++r) {
+                const int key = kbase + (vrow ^ (r & 1 ? kNext : 0)) + (r >> 1) * 8;
+                if (key >= L) {
 #pragma unroll
                     for (int w = 0; w < kVWords; ++w) vw[r][w] = 0u;
                 }
+                if (MQ && key > all_see) {
+#pragma unroll
+                    for (int w = 0; w < kVWords; ++w) {
+                        some |= nan_bits(vw[r][w]);
+                        vw[r][w] &= ~nan_codes(vw[r][w]);
+                    }
+                }
+            }
+            if (MQ && __any_sync(0xffffffffu, (some & 0x80808080u) != 0u)) {
+                // keys that only some columns see: a NaN stays out of the product too, where it would reach
+                // every column, and goes straight into the sums of those that see it
+                const uint32_t plane = st_at + (a.k_second ? 0 : Sh::kPlane);
+#pragma unroll 1
+                for (int row = max(0, all_see + 1 - kbase); row < min(kBlockSize, L - kbase); ++row) {
+                    uint32_t x[4];
+                    if constexpr (kRowB == 64) {
+                        const uint2 p = lds8(plane + row * 64 + (((gid >> 1) ^ (row >> 1 & 3)) << 4) + (gid & 1) * 8);
+                        x[0] = p.x, x[1] = p.y;
+                    } else {
+                        const uint4 p = lds16(plane + row * 128 + ((gid ^ (row & 7)) << 4));
+                        x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w;
+                    }
+#pragma unroll
+                    for (int w = 0; w < kSteps / 2; ++w) {
+                        const uint32_t nan = nan_codes(x[w]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (kbase + row <= colpos[nt][j] && nan >> (8 * i) & 1u)
+                                        ot[nt][2 * w + (i >> 1)][j + 2 * (i & 1)] = __int_as_float(0x7fffffff);
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int w = 0; w < kVWords; ++w) {

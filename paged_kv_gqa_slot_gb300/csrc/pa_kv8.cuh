@@ -82,6 +82,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
         : "r"(w));
 }
 
+// Bit 7 of every byte says whether that code of the word is a NaN (0x7f and 0xff); the other bits are arbitrary.
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+// 0xff in the bytes that are, 0 in the others.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (nan_bits(w) >> 7 & 0x01010101u) * 0xffu; }
+
 // Four values rounded to nearest even e4m3, lowest byte first (magnitudes past 448 saturate, NaN
 // stays NaN).
 __device__ __forceinline__ uint32_t to_e4m3x4(float x0, float x1, float x2, float x3) {

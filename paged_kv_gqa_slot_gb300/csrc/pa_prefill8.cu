@@ -48,6 +48,7 @@
 // 118); one call site of the two softmax attempts (121 us against 108).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_internal.h"
 #include "pa_kv8.cuh"
@@ -89,8 +90,9 @@ struct Pre8 {
     static constexpr int kOffV = kOffK + kKStages * kStage;
     static constexpr int kOffRaw = kOffV + kVStages * kStage;
     static constexpr int kOffBars = kOffRaw + kCvtWarps * kAhead * 2 * kUnit;
-    static constexpr int kOffInv = kOffBars + 512;     // [2][128] 2^-7 / l, then whether every wait ended
-    static constexpr int kSmem = kOffInv + 2 * kRows * 4 + 16;
+    static constexpr int kOffInv = kOffBars + 512;     // [2][128] 2^-7 / l, then whether every wait ended, and whether kOffNan names a key
+    static constexpr int kOffNan = kOffInv + 2 * kRows * 4 + 16;  // [D] first key with a NaN in V's column d (see Converter)
+    static constexpr int kSmem = kOffNan + D * 4;
     static constexpr int kLoads = kBlockSize * D / 512;  // 16-byte pieces of a block a lane takes
 };
 static_assert(Pre8<128>::kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -159,6 +161,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // Converter warp w: of K (the first half of the warps) or V, every kSide-th pair of blocks, whose codes
 // come into the warp's own raw slots by a bulk copy each, kAhead pairs ahead.
+// A NaN of V in a key that only some rows see stays out of the product, where it would reach all of them (NaN
+// times u = 0 is NaN): the key goes on record for its column, and the epilogue sets the column in the rows that see it.
 template <int D>
 struct Converter {
     using P = Pre8<D>;
@@ -168,13 +172,14 @@ struct Converter {
     const Pre8Args& a;
     const int32_t* bt;
     const uint8_t* pool;  // of this warp's side, at its kv head
-    int L, nst, nblk, w, lane, first;
+    int L, nst, nblk, w, lane, all_see, first;  // all_see: the last key that every row sees
     bool is_v;
     int next_id;  // lanes 0 and 1: of the pair to be fetched next
 
     __device__ __forceinline__ Converter(uint8_t* smem_, Bars8* bars_, const Pre8Args& a_, const int32_t* bt_, int kvh,
-                                         int L_, int nst_, int nblk_, int w_, int lane_)
-        : smem(smem_), bars(bars_), a(a_), bt(bt_), L(L_), nst(nst_), nblk(nblk_), w(w_), lane(lane_) {
+                                         int L_, int nst_, int nblk_, int w_, int lane_, int all_see_)
+        : smem(smem_), bars(bars_), a(a_), bt(bt_), L(L_), nst(nst_), nblk(nblk_), w(w_), lane(lane_),
+          all_see(all_see_) {
         is_v = w >= kSide;
         first = is_v ? w - kSide : w;
         pool = (is_v ? a.v : a.k) + (size_t)kvh * P::kUnit;
@@ -199,6 +204,31 @@ struct Converter {
             if (blk + 2 * kSide < nblk) next_id = __ldg(bt + blk + 2 * kSide);
         }
     }
+    // The n-th pair's codes in its raw slot: NaNs of keys that only some rows see become zeros and go on record.
+    // (Every lane reads and writes the pieces that it then widens.)
+    __device__ __forceinline__ void scrub(int n, int pair) {
+        const auto at = [&](int i) { return reinterpret_cast<uint32_t*>(smem + P::kOffRaw + (w * kAhead + n % kAhead) * (2 * P::kUnit) + lane * 16 + i * 512); };
+        uint32_t some = 0u;
+#pragma unroll
+        for (int i = 0; i < 2 * P::kLoads; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at(i));
+            some |= nan_bits(v.x) | nan_bits(v.y) | nan_bits(v.z) | nan_bits(v.w);
+        }
+        if (!(some & 0x80808080u)) return;
+        int* first_nan = reinterpret_cast<int*>(smem + P::kOffNan);
+#pragma unroll 1
+        for (int i = 0; i < 2 * P::kLoads * 4; ++i) {
+            const int piece = (i >> 2) * 32 + lane, key = pair * 2 * kBlockSize + piece / (D / 16);
+            const int d = piece % (D / 16) * 16 + (i & 3) * 4;
+            uint32_t* word = at(i >> 2) + (i & 3);
+            const uint32_t nan = nan_codes(*word);
+            if (!nan || key <= all_see || key >= L) continue;
+            *word &= ~nan;
+            for (int j = 0; j < 4; ++j)
+                if (nan >> (8 * j) & 1u) atomicMin(first_nan + d + j, key);
+            *(reinterpret_cast<int*>(smem + P::kOffInv) + 2 * kRows + 1) = 1;
+        }
+    }
     __device__ __forceinline__ void start() {
         if (lane < kAhead) mbar_init(&bars->raw_full[w][lane], 1);
         fence_mbar_init();
@@ -215,12 +245,13 @@ struct Converter {
         // rows from here on are zeros: past the blocks the CTA needs, and V past the sequence's end (u is 0
         // there, but 0 times NaN is NaN)
         const int end = is_v ? min(L, nblk * kBlockSize) : nblk * kBlockSize;
-        for (int pair = first; pair < nst * kPairs; pair += kSide, ++n) {
+        const auto one = [&](int pair, auto masked) {
             const int stage = pair / kPairs, slot = stage % kKStages;
             uint4 codes[2 * P::kLoads];
             if (2 * pair < nblk) {
                 ok = mbar_wait_warp(&bars->raw_full[w][n % kAhead], (n / kAhead) & 1);
-                if (!ok) break;
+                if (!ok) return;
+                if constexpr (decltype(masked)::value) scrub(n, pair);
             }
 #pragma unroll
             for (int i = 0; i < 2 * P::kLoads; ++i)
@@ -234,7 +265,7 @@ struct Converter {
                     if (pair * 2 * kBlockSize + (i * 32 + lane) / (D / 16) >= end) codes[i] = make_uint4(0u, 0u, 0u, 0u);
             }
             if (stage >= kKStages) ok = mbar_wait_warp(&empty[slot], ((stage / kKStages) & 1) ^ 1);
-            if (!ok) break;
+            if (!ok) return;
             uint8_t* dst = slots + slot * P::kStage + pair % kPairs * (2 * kBlockSize * 128);
 #pragma unroll
             for (int i = 0; i < 2 * P::kLoads; ++i) {
@@ -255,7 +286,14 @@ struct Converter {
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
             issue(n + kAhead);  // over the codes, which every lane has read
-        }
+            ++n;
+        };
+        // pairs of keys that every row sees, then the others (in one loop with a branch the scrubbing made every
+        // pair slower: 8 x 256 over 768 38.7 us against 38.4)
+        const int clear = is_v ? min((all_see + 1) / (2 * kBlockSize), nst * kPairs) : nst * kPairs;
+        int pair = first;
+        for (; pair < clear && ok; pair += kSide) one(pair, std::false_type{});
+        for (; pair < nst * kPairs && ok; pair += kSide) one(pair, std::true_type{});
         if (!ok) {
             // a wait ran out: the copies in flight must still land before their memory is used again
             for (int i = n; i < n + kAhead; ++i)
@@ -372,6 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     Bars8* bars = reinterpret_cast<Bars8*>(smem + P::kOffBars);
     float* row_inv = reinterpret_cast<float*>(smem + P::kOffInv);
     int* all_ok = reinterpret_cast<int*>(row_inv + 2 * kRows);
+    int* some_nan = all_ok + 1;
+    int* first_nan = reinterpret_cast<int*>(smem + P::kOffNan);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     // blockIdx.x = (rank * batch + b) * num_kv_heads + kvh: rank 0 is every chunk's last CTA
     const int rb = a.by_heads.div((int)blockIdx.x), kvh = a.by_heads.mod((int)blockIdx.x, rb);
@@ -401,8 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
         }
         mbar_init(&bars->drain, kMmaWarps);
         *all_ok = 1;
+        *some_nan = 0;
         fence_mbar_init();
     }
+    if (warp >= kCvtWarp && threadIdx.x - kCvtWarp * 32 < D) first_nan[threadIdx.x - kCvtWarp * 32] = 0x7fffffff;
     if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, kTmemCols);
         tmem_relinquish();
@@ -450,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
     constexpr int kLanes = D / 8, kPerLoad = 32 / kLanes;  // lanes of a row of q, rows of one load
     const int t_tile = (warp >> 2) & 1, w_row = (warp & 3) * 32;
     int first_id = -1;
-    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane};
+    Converter<D> cvt{smem, bars, a, bt, kvh, L, nst, nblk, warp - kCvtWarp, lane,
+                     L - C + a.by_group.div(row0)};
     if (warp < kSoftmaxWarps) {
         if (lane < nblk) first_id = __ldg(bt + lane);
         const int c = lane % kLanes, r0 = w_row + lane / kLanes, n = live_of(t_tile);
@@ -676,6 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill8_kernel(const __grid_cons
             for (int c = 0; c < D / 2; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(tm + c0 + c, o);
+                if (*some_nan) {
+                    const int pos = L - C + a.by_group.div(row0 + t * kRows + r);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (first_nan[c0 + c + e] <= pos) o[e] = 0x7fffffffu;
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     const auto w = [&](int i) {

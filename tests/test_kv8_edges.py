@@ -203,3 +203,49 @@ def test_short_prefill_nan_in_a_query_row(d):
         out[r, h] = ref[r, h].to(out.dtype)
     check(out, ref, spread, 700, mag)
     clean()
+
+
+# ----------------------------------------------------------------------------- NaN in the V of a later key
+@gpu
+@pytest.mark.parametrize("cached,chunks,hq,hkv", [
+    ([100, 0], [40, 300], 8, 2), ([16, 770], [17, 129], 32, 8), ([5, 60], [200, 31], 6, 2), ([0, 31], [130, 64], 2, 2),
+    ([700, 0] * 4, [130, 257] * 4, 64, 8),          # two tiles a CTA
+    ([100, 0, 31], [4, 4, 2], 16, 4), ([29, 1000], [8, 5], 4, 2),  # the short form
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_nan_in_later_values_stays_with_those_that_see_it(d, cached, chunks, hq, hkv):
+    """V's NaN at a position reaches exactly the queries at or past it, in its column."""
+    lens = [a + b for a, b in zip(cached, chunks)]
+    c = Case(111, lens, hq, hkv, d, chunks)
+    ref, spread, _, mag = c.reference()
+    rng = np.random.RandomState(7)
+    g = hq // hkv
+    nan = torch.zeros(c.q.shape, dtype=torch.bool, device="cuda")
+    for b, (n, m) in enumerate(zip(lens, chunks)):
+        for i in range(3):
+            pos = n - 1 - int(rng.randint(0, m)) if i else n - 1
+            h, col = int(rng.randint(hkv)), slice(None) if i == 1 else slice(int(rng.randint(d)), None, 37)
+            codes = c.v[c.tables_h[b][pos // 16], h, pos % 16]
+            codes[col] = NAN_CODE if i else 0xff
+            nan[c.cu_h[b] + pos - (n - m):c.cu_h[b + 1], h * g:(h + 1) * g, col] = True
+    out = pa.pa_prefill_chunked8(c.pool, c.q, c.cu, c.tables, c.lens, c.scale, c.max_chunk)
+    assert torch.equal(torch.isnan(out), nan)
+    out[nan] = ref[nan].to(out.dtype)
+    check(out, ref, spread, max(lens), mag)
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("chunks", [[40, 300], [4, 2]])
+def test_prefill_nan_in_cached_values_reaches_every_query(d, chunks):
+    c = Case(112, [360, 500], 8, 2, d, chunks)
+    ref, spread, _, mag = c.reference()
+    for pos in (0, 100, 200 - 1):
+        c.v[c.tables_h[1][pos // 16], 1, pos % 16, 5] = NAN_CODE
+    out = pa.pa_prefill_chunked8(c.pool, c.q, c.cu, c.tables, c.lens, c.scale, c.max_chunk)
+    rows = slice(c.cu_h[1], c.cu_h[2])
+    assert torch.isnan(out[rows, 4:, 5]).all()
+    out[rows, 4:, 5] = ref[rows, 4:, 5].to(out.dtype)
+    check(out, ref, spread, 500, mag)
+    clean()
