@@ -90,7 +90,7 @@ typedef struct {
  * head): half the time of a decode, and twice the blocks of a memory budget
  * (pa_kv_block_bytes with dtype_bytes = 1).  The caller owns the three tensors and zeroes
  * them, or at least writes a block's offset 0 before its other rows; exponents outside the range
- * (a zeroed pool's) are read as its nearer end.
+ * (a zeroed pool's) are taken as its nearer end, by every call.
  */
 typedef struct {
     void *k_cache;        /* [num_blocks, num_kv_heads, 16, head_dim] e4m3, 16-byte aligned */

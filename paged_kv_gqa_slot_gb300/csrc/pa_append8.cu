@@ -128,7 +128,7 @@ __device__ __forceinline__ void append_unit(const Append8Args& a, int t0, int he
             x[i] = make_uint4(0u, 0u, 0u, 0u);
             if (src >= 0) x[i] = __ldg(a.rows[is_v] + ((size_t)src * a.num_kv_heads + kvh) * kLanes + c);
         }
-        const int k_old = static_cast<int>(*exp_at) - kExpBias;
+        const int k_old = valid_exp(*exp_at) - kExpBias;  // as the reading kernels take it
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
             mag = max_mag2(max_mag2(max_mag2(max_mag2(mag, x[i].x), x[i].y), x[i].z), x[i].w);

@@ -25,13 +25,10 @@ __device__ __forceinline__ float exp2_int(int e) {
     return __int_as_float((min(max(e, -126), 127) + 127) << 23);
 }
 
-// A block's word of exponents (K in the low byte), each brought into the range the format has: a
-// tile that was never written may hold anything, zeros first of all.
-__device__ __forceinline__ int valid_exps(int word) {
-    const int k = min(max(word & 255, kExpMin + kExpBias), kExpMax + kExpBias);
-    const int v = min(max(word >> 8 & 255, kExpMin + kExpBias), kExpMax + kExpBias);
-    return k | v << 8;
-}
+// An exponent byte brought into the range the format has: a tile that was never written may hold
+// anything, zeros first of all.  And a block's word of them (K in the low byte).
+__device__ __forceinline__ int valid_exp(int byte) { return min(max(byte, kExpMin + kExpBias), kExpMax + kExpBias); }
+__device__ __forceinline__ int valid_exps(int word) { return valid_exp(word & 255) | valid_exp(word >> 8 & 255) << 8; }
 
 // The kernels' softmax weighs V by u = 2^(x + kV - base) (but for a constant factor) and sums the normaliser's 2^(x - base) as u 2^-kV.
 // u ends at 2^-126 and the normaliser holds 2^-kB of the block that set the base, so that is right as

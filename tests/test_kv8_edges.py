@@ -249,3 +249,28 @@ def test_prefill_nan_in_cached_values_reaches_every_query(d, chunks):
     out[rows, 4:, 5] = ref[rows, 4:, 5].to(out.dtype)
     check(out, ref, spread, 500, mag)
     clean()
+
+
+# ----------------------------------------------------------------------------- exponent bytes outside the range
+@gpu
+@pytest.mark.parametrize("byte,size", [(255, 2.0 ** 120), (247, 2.0 ** 121), (0, 2.0 ** -92), (20, 2.0 ** -95), (0, 0.0)])
+def test_append_takes_an_exponent_as_it_is_read(byte, size):
+    """Rows behind offset 0 of a block whose exponent byte is outside 27 .. 246: the append goes by the
+    nearer end, as the reading calls do, for the codes that stay and for the new ones."""
+    hkv, d = 2, 64
+    k, v, exps = make_pool(121, 3, hkv, d)
+    exps[:] = byte
+    pool = pa.PaPool8(k, v, exps)
+    kh, vh = k.cpu().numpy(), v.cpu().numpy()
+    eh = np.clip(exps.cpu().numpy(), 27, 246)
+    gen = torch.Generator().manual_seed(5)
+    new = [(torch.randn(3, hkv, d, generator=gen) * size).to(torch.bfloat16) for _ in range(2)]
+    slots = [5, 6, 16 + 9]
+    pa.pa_kv_append8(pool, new[0].cuda(), new[1].cuda(), torch.tensor(slots, device="cuda"))
+    for i, codes in enumerate((kh, vh)):
+        R.append(codes, eh[:, :, i], new[i].double().numpy(), slots)
+    got = exps.cpu().numpy()
+    assert np.array_equal(got[:2], eh[:2]) and (got[2] == byte).all()
+    for g, w in ((k, kh), (v, vh)):
+        assert np.array_equal(R.VALUES[g.cpu().numpy()], R.VALUES[w], equal_nan=True)
+    clean()
