@@ -12,14 +12,14 @@
 // else it reads them again for the copy), finds the e-th smallest key by four 8-bit radix passes,
 // ranks ties and survivors with two block scans, and gathers through the resulting source list.  The
 // weights of a sequence share a few exponents, so the lanes of a warp that hold the same digit
-// count together before they add to a bin.  W_j is the sum in 64 bits rounded once, so it does not
-// depend on the order of the heads; it is formed from fp32 sums and their exact errors (fp64
-// arithmetic, of which an SM does two operations a cycle, took half the kernel's time).  Rows in
+// count together before they add to a bin.  W_j is the sum in 64 bits rounded once; it is formed
+// from fp32 sums and their exact errors (fp64 arithmetic, of which an SM does two operations a cycle,
+// took half the kernel's time), and in fp64 only where these leave the rounding open.  Rows in
 // shared memory are read whole before any output is written; the others are gathered in
 // ascending tiles, each read before it is written, from sources at or past it: outputs may be
 // their inputs.
 //
-// Measured on GB300, 8 kv heads: 64 sequences of 72 blocks 5.3 us, 16 of 2048 13.9 us, nearly all of it the
+// Measured on GB300, 8 kv heads: 64 sequences of 72 blocks 5.3 us, 16 of 2048 14.2 us, nearly all of it the
 // latency of the radix passes' barriers and the scans (the bytes would take 0.1 and 0.4 us).
 #include <algorithm>
 
@@ -39,20 +39,35 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// W_j of one entry: the sum over heads of col[h * width], rounded once.  s + err is the sum to
-// 48 bits: every addition's error is exact and added up on its own.
+__device__ __noinline__ float sum64(const float* col, int heads, int width) {
+    double d = 0.0;
+    for (int h = 0; h < heads; ++h) d += (double)col[(size_t)h * width];
+    return (float)d;
+}
+
+// W_j of one entry: the sum over heads of col[h * width] in fp64, rounded once.  s + err is the sum but for the
+// roundings of err itself: every addition's error, at most 2^-24 of (1 + 2^-10) s, is exact and added up on its own.
+//  * All numbers are multiples of q, the step of fp32 at the smallest weight `least`, and so are s and err.
+//    While err stays below 2^24 q >= least, it is exact, and so is fp64's sum: with least >= heads 2^-23 s, s + err
+//    rounds to W_j.
+//  * Otherwise err is off by at most heads^2 2^-48 (1 + 2^-9) s, and fp64's sum by at most heads 2^-53 s: where both
+//    ends of that range round to the same number, it is W_j.
+//  * The rest, negative weights, infinities and NaN are summed in fp64.
+// (Without the first rule every table had entries on their way to fp64, as sums that lie in the middle of two
+// numbers are common, and 16 x 2048 took 15.3 us.)
 struct WeightSum {
-    float s = 0.f, err = 0.f;
-    __device__ __forceinline__ void add(float w) {
+    float s = 0.f, err = 0.f, least = INFINITY;
+    __device__ __forceinline__ void add(float w, bool in) {  // w = 0 unless `in`
         const float t = s + w, z = t - s;
         err += (s - (t - z)) + (w - z);
         s = t;
+        least = fminf(least, in ? w : INFINITY);
     }
     __device__ __forceinline__ float value(const float* col, int heads, int width) const {
-        if (fabsf(s) < INFINITY) return s + err;
-        double d = 0.0;  // infinities, NaN, sums past the fp32 range
-        for (int h = 0; h < heads; ++h) d += (double)col[(size_t)h * width];
-        return (float)d;
+        const float n = static_cast<float>(heads);
+        if (s < INFINITY && least >= s * (n * 0x1p-23f)) return s + err;
+        const float off = s * (n * n * 0x1p-47f), lo = s + (err - off), hi = s + (err + off);
+        return s < INFINITY && least >= 0.f && lo == hi ? lo : sum64(col, heads, width);
     }
 };
 
@@ -98,7 +113,7 @@ __global__ void __launch_bounds__(T) evict_kernel(const __grid_constant__ EvictA
             for (int h = 0; h < 8; ++h) v[h] = h0 + h < heads ? weights[(size_t)(h0 + h) * width + j] : 0.f;
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
-                w.add(v[h]);
+                w.add(v[h], h0 + h < heads);
                 if (resident && h0 + h < heads) rows[(h0 + h) * width + j] = v[h];
             }
         }

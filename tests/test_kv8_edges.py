@@ -274,3 +274,42 @@ def test_append_takes_an_exponent_as_it_is_read(byte, size):
     for g, w in ((k, kh), (v, vh)):
         assert np.array_equal(R.VALUES[g.cpu().numpy()], R.VALUES[w], equal_nan=True)
     clean()
+
+
+# ----------------------------------------------------------------------------- sums of the eviction
+@gpu
+@pytest.mark.parametrize("width", [12, 600, 30000])
+def test_evict_sums_at_a_rounding_border(width):
+    """W is the fp64 sum rounded once: 1 + 2^-24 + 2^-49 lies just above the middle of two fp32 numbers and
+    counts as the upper one, 1 + 2^-24 as the lower; sums whose terms cancel keep fp64's remainder."""
+    w = np.full((1, 3, width), 9.0, np.float32)
+    w[0, :, 3] = 1.0, 2.0 ** -24, 2.0 ** -49       # 1 + 2^-23
+    w[0, :, 5] = 1.0, 0.0, 0.0                     # 1: the lowest of these
+    w[0, :, 6] = 1.0, 2.0 ** -24, 0.0              # 1 again (to even)
+    w[0, :, 7] = 2.0 ** -24, 1.0, -(2.0 ** -49)    # 1 again (below the middle)
+    w[0, :, 8] = 2.0 ** 40, 2.0 ** -20, -(2.0 ** 40)  # 0 in fp64, 2^-20 in exact arithmetic
+    w[0, :, 9] = 2.0 ** 40, 2.0 ** -10, -(2.0 ** 40)  # 2^-10
+    tables = np.arange(width, dtype=np.int32)[None]
+    order = [8, 9, 5, 6, 7, 3]
+    for e in range(1, 7):
+        t, _, _, evicted, num = pa.pa_kv_evict(*(torch.tensor(x, device="cuda") for x in (tables, np.array([width * 16], np.int32), w)),
+                                               width - e, 0, 1)
+        assert num.tolist() == [e] and evicted[0, :e].tolist() == sorted(order[:e]), e
+    clean()
+
+
+@gpu
+def test_evict_many_heads_of_mixed_signs():
+    rng = np.random.RandomState(8)
+    b, h, width = 3, 70, 300
+    w = (rng.randn(b, h, width) * np.exp2(rng.uniform(-30, 30, size=(b, h, width)))).astype(np.float32)
+    lens = [width * 16, width * 16 - 5, 2000]
+    tables = rng.permutation(b * width).reshape(b, width).astype(np.int32)
+    total = np.zeros((b, width))
+    for i in range(h):
+        total = total + w[:, i].astype(np.float64)
+    one = total.astype(np.float32)[:, None]        # the same ranking from sums that need no rounding
+    got = pa.pa_kv_evict(*(torch.tensor(x, device="cuda") for x in (tables, np.array(lens, np.int32), w)), 100, 2, 3)
+    want = R.evict(tables.tolist(), lens, one.tolist(), 100, 2, 3)
+    assert got[0].tolist() == want[0] and got[3].tolist() == want[3]
+    clean()
