@@ -476,12 +476,12 @@ def _decode_weights(what, pool, device, q, block_tables, seq_lens, scale, weight
     width = _width(block_tables, seq_lens, B)
     if weights.shape != (B, pool.num_kv_heads, width):
         raise ValueError(f"weights: need shape {(B, pool.num_kv_heads, width)}, got {tuple(weights.shape)}")
-    if B == 0 or width == 0:
+    if B == 0:
         return out
     need = B * pool.num_kv_heads * width * (16 if Hq // pool.num_kv_heads > 8 else 8)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.float32, device=weights.device) if stream is None else \
-            _like(weights.expand(need // weights.numel(), *weights.shape), stream)
+            _like(weights.expand(need // max(weights.numel(), 1), *weights.shape), stream)
     elif workspace.numel() < need:
         raise ValueError(f"workspace: need {need} floats, got {workspace.numel()}")
     _call(what, device, stream, pool.ref, _arg(q, _BF16, "q", device),

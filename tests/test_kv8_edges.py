@@ -313,3 +313,21 @@ def test_evict_many_heads_of_mixed_signs():
     want = R.evict(tables.tolist(), lens, one.tolist(), 100, 2, 3)
     assert got[0].tolist() == want[0] and got[3].tolist() == want[3]
     clean()
+
+
+# ----------------------------------------------------------------------------- tables of no width
+@gpu
+def test_decode_with_weights_over_tables_of_no_width_is_refused():
+    """As the decode without weights: there is no row to read, and no result to give."""
+    c = Case(131, [40, 50], 8, 2, 128)
+    none = c.tables[:, :0].contiguous()
+    w = torch.zeros(2, 2, 0, device="cuda")
+    bf16 = pa.PaPool(torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(pa.PagedAttnError):
+        pa.pa_decode8(c.pool, c.q, none, c.lens, c.scale)
+    for call, pool in ((pa.pa_decode8_weights, c.pool), (pa.pa_decode_weights, bf16)):
+        with pytest.raises(pa.PagedAttnError):
+            call(pool, c.q, none, c.lens, c.scale, w)
+        with pytest.raises(pa.PagedAttnError):
+            call(pool, c.q, none, c.lens, c.scale, w, stream=torch.cuda.current_stream())
+        assert call(pool, c.q[:0], none[:0], c.lens[:0], c.scale, w[:0]).shape == (0, 8, 128)
