@@ -504,9 +504,24 @@ __global__ void __launch_bounds__(warps_of(BITS, D, NT, WIDE) * 32, ctas_of(WIDE
                 float t = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 4);
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
+                float from = odd ? m[nt][1] : m[nt][0];
+                if (far) {
+                    // terms under m may be subnormal though they count: under the block's own maximum instead
+                    float own[2], top[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        top[j] = fmaxf(st[nt][j], st[nt][2 + j]);
+                        for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+                        const float base = top[j] == -INFINITY ? 0.f : top[j];
+                        own[j] = fast_exp2(st[nt][j] - base) + fast_exp2(st[nt][2 + j] - base);
+                        for (int o = 4; o < 32; o <<= 1) own[j] += __shfl_xor_sync(0xffffffffu, own[j], o);
+                    }
+                    t = odd ? own[1] : own[0];
+                    from = odd ? top[1] : top[0];
+                }
                 if (gid < 2)
                     a.ws[(((size_t)b * a.num_kv_heads + kvh) * a.max_blocks + entry_at(k)) * (8 * NT) + nt * 8 +
-                         2 * tig + gid] = fast_log2(t) + (odd ? m[nt][1] : m[nt][0]);
+                         2 * tig + gid] = fast_log2(t) + from;
             }
             // rows (tokens) x columns (heads) -> transposed: the B operand of the V product
             if constexpr (BITS == 8) {

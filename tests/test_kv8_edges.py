@@ -331,3 +331,29 @@ def test_decode_with_weights_over_tables_of_no_width_is_refused():
         with pytest.raises(pa.PagedAttnError):
             call(pool, c.q, none, c.lens, c.scale, w, stream=torch.cuda.current_stream())
         assert call(pool, c.q[:0], none[:0], c.lens[:0], c.scale, w[:0]).shape == (0, 8, 128)
+
+
+# ----------------------------------------------------------------------------- weights under large V scales
+@gpu
+@pytest.mark.parametrize("lens", [[300, 1000], [300, 250] * 30])  # a cluster a sequence; one CTA, five blocks a warp
+@pytest.mark.parametrize("byte", [27, 127 - 7, 127 + 100, 246])
+def test_weights_do_not_depend_on_the_scale_of_v(byte, lens):
+    """Blocks of very different weight, V at any scale: the weights follow K alone."""
+    for d in (64, 128):
+        c = Case(141, lens, 16, 8, d, scale=1.2, spread=0.0)
+        c.exps[..., 1] = byte
+        if byte == 246:  # 448 * 2^119 is the end of the range; keep the sums inside it
+            c.v[:] = torch.where(c.v & 0x7f == NAN_CODE, c.v, c.v & 0x9f)
+        ref, spread, want, mag = c.reference()
+        w = torch.zeros(len(lens), 8, c.tables.shape[1], device="cuda")
+        out = pa.pa_decode8_weights(c.pool, c.q, c.tables, c.lens, c.scale, w)
+        check(out, ref, spread, max(lens), mag)
+        least = 1.0
+        rel = 2 * mag * 2.0 ** -19 + 2.0 ** -13
+        for b, n in enumerate(lens):
+            nb = (n + 15) // 16
+            big = want[b] > 2.0 ** -60
+            least = min(least, float(want[b][big].min()))
+            assert bool(((w[b, :, :nb].double() - want[b]).abs()[big] <= rel * want[b][big]).all())
+        assert least < 2.0 ** -16
+        clean()
