@@ -371,7 +371,8 @@ int pa_splitkv_num_partitions(int32_t batch, int32_t num_kv_heads, int32_t max_b
  * prefix does not cover.
  *
  * Bytes of one block (K and V of every layer): num_layers * 2 * num_kv_heads * block_size
- * * head_dim * dtype_bytes.  Qwen3-32B (64 layers, 8 kv heads, d 128, bf16, 16-token blocks)
+ * * head_dim * dtype_bytes, and for the 8-bit pool (dtype_bytes 1) 2 more per layer and kv head,
+ * its exponents.  Qwen3-32B (64 layers, 8 kv heads, d 128, bf16, 16-token blocks)
  * gives 4 MiB, so 5360 blocks are 22.48 GB (20.94 GiB).  0 on a non-positive argument.
  */
 int64_t pa_kv_block_bytes(int32_t num_layers, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

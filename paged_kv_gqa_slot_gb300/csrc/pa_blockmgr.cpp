@@ -179,7 +179,9 @@ extern "C" {
 int64_t pa_kv_block_bytes(int32_t num_layers, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                           int32_t dtype_bytes) {
     if (num_layers <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || dtype_bytes <= 0) return 0;
-    return (int64_t)num_layers * 2 * num_kv_heads * block_size * head_dim * dtype_bytes;
+    // the 8-bit pool (dtype_bytes 1) also holds an exponent byte for K and one for V per kv head
+    const int64_t exps = dtype_bytes == 1 ? 2 : 0;
+    return (int64_t)num_layers * num_kv_heads * ((int64_t)2 * block_size * head_dim * dtype_bytes + exps);
 }
 
 int32_t pa_kv_budget_blocks(int64_t budget_bytes, int32_t num_layers, int32_t num_kv_heads, int32_t head_dim,
