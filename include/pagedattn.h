@@ -63,7 +63,8 @@ enum pa_status {
     PA_ERR_OUT_OF_RANGE = -4, /* pa_device_status: a block id / slot / length outside the pool was skipped */
     PA_ERR_TIMEOUT = -5,      /* pa_device_status: a pipeline wait ran out (a bug, never expected) */
     PA_ERR_TOO_LARGE = -6,    /* pa_decode_splitkv_noalloc: the request does not fit its static scratch */
-    PA_ERR_REJECTED = -7      /* pa_bm_admit: the request's whole lifetime does not fit the pool */
+    PA_ERR_REJECTED = -7,     /* pa_bm_admit: the request's whole lifetime does not fit the pool */
+    PA_ERR_NO_MEMORY = -8     /* pa_bm_*: no host memory; nothing has changed */
 };
 
 /* Device status bits reported by pa_device_status. */

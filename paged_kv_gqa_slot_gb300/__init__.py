@@ -50,6 +50,7 @@ PA_ERR_CUDA = -3
 PA_ERR_OUT_OF_RANGE = -4
 PA_ERR_TIMEOUT = -5
 PA_ERR_TOO_LARGE = -6
+PA_ERR_NO_MEMORY = -8
 PA_DEV_OUT_OF_RANGE = 1
 PA_DEV_TIMEOUT = 2
 
@@ -587,7 +588,7 @@ class BlockManager:
         self.block_size = block_size
         self._h = library().pa_bm_create(num_blocks, block_size, 1 if prefix_cache else 0)
         if not self._h:
-            raise PagedAttnError("pa_bm_create failed")
+            raise PagedAttnError("pa_bm_create", PA_ERR_INVALID_ARG if num_blocks <= 0 or block_size <= 0 else PA_ERR_NO_MEMORY)
 
     def close(self):
         if self._h:

@@ -20,6 +20,10 @@
 // are copied into the request's own block (copy on write: a cached block is never written),
 // so only the tokens after them are computed.  The source block is pinned (one reference) for
 // the request's lifetime, so no other request can take it and overwrite it before the copy.
+//
+// No memory: every call allocates what it needs before it changes anything (a cached block's place in the
+// release order is a list node that it keeps, moved by splicing), and returns PA_ERR_NO_MEMORY; no exception
+// leaves the C interface.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -52,7 +56,7 @@ struct Block {
     uint64_t hash = 0;
     uint64_t parent = 0;                 // hash of the block before it (0 for a first block), when cached
     std::vector<int32_t> tokens;         // the block's token ids, when cached
-    std::list<int32_t>::iterator lru;    // position in the evictable list (refs == 0 && cached)
+    std::list<int32_t>::iterator lru;    // when cached: its node, in `evictable` (refs == 0) or in `held`
 };
 
 struct Request {
@@ -64,6 +68,16 @@ struct Request {
     int32_t pinned = -1;                 // copy-on-write source block held for the request, or -1
 };
 
+// f(), or PA_ERR_NO_MEMORY where it found none.
+template <class F>
+int guarded(F f) {
+    try {
+        return f();
+    } catch (...) {  // std::bad_alloc: nothing else is thrown
+        return PA_ERR_NO_MEMORY;
+    }
+}
+
 }  // namespace
 
 struct pa_blockmgr {
@@ -72,6 +86,7 @@ struct pa_blockmgr {
     std::vector<Block> blocks;
     std::vector<int32_t> free_list;      // never used or released uncached; popped from the back
     std::list<int32_t> evictable;        // cached with no user; front = released longest ago
+    std::list<int32_t> held;             // nodes of the cached blocks that have a user
     std::unordered_multimap<uint64_t, int32_t> by_hash;
     std::unordered_multimap<uint64_t, int32_t> by_parent;  // cached blocks by their parent's hash
     std::unordered_map<int64_t, Request> requests;
@@ -139,12 +154,33 @@ struct pa_blockmgr {
     void drop_ref(int32_t id) {
         Block& b = blocks[id];
         if (--b.refs > 0) return;
-        if (b.cached) {
-            evictable.push_back(id);
-            b.lru = std::prev(evictable.end());
-        } else {
-            free_list.push_back(id);
+        if (b.cached)
+            evictable.splice(evictable.end(), held, b.lru);
+        else
+            free_list.push_back(id);  // (room for every block from the start)
+    }
+
+    // A block with a user enters the prefix cache, or nothing changes (no memory).
+    void cache(int32_t id, uint64_t hash, uint64_t parent, const int32_t* toks) {
+        Block& b = blocks[id];
+        b.tokens.assign(toks, toks + block_size);
+        held.push_back(id);
+        try {
+            auto at = by_hash.emplace(hash, id);
+            try {
+                by_parent.emplace(parent, id);
+            } catch (...) {
+                by_hash.erase(at);
+                throw;
+            }
+        } catch (...) {
+            held.pop_back();
+            throw;
         }
+        b.lru = std::prev(held.end());
+        b.cached = true;
+        b.hash = hash;
+        b.parent = parent;
     }
 
     void register_full_blocks(Request& r, int32_t computed) {
@@ -158,16 +194,10 @@ struct pa_blockmgr {
             const uint64_t h = chain(parent, toks);
             Block& b = blocks[id];
             if (!b.cached) {
-                if (lookup(h, toks) < 0) {  // another request may already hold this content
-                    b.cached = true;
-                    b.hash = h;
-                    b.parent = parent;
-                    b.tokens.assign(toks, toks + block_size);
-                    by_hash.emplace(h, id);
-                    by_parent.emplace(parent, id);
-                } else {
+                if (lookup(h, toks) < 0)  // another request may already hold this content
+                    cache(id, h, parent, toks);
+                else
                     b.hash = h;  // the chain continues through an uncached duplicate
-                }
             }
             r.registered = i + 1;
         }
@@ -198,8 +228,13 @@ pa_blockmgr* pa_bm_create(int32_t num_blocks, int32_t block_size, int32_t enable
     if (!m) return nullptr;
     m->block_size = block_size;
     m->prefix_cache = enable_prefix_cache != 0;
-    m->blocks.resize(num_blocks);
-    m->free_list.reserve(num_blocks);
+    try {
+        m->blocks.resize(num_blocks);
+        m->free_list.reserve(num_blocks);
+    } catch (...) {
+        delete m;
+        return nullptr;
+    }
     for (int32_t i = num_blocks - 1; i >= 0; --i) m->free_list.push_back(i);  // hand out 0, 1, 2, ... first
     return m;
 }
@@ -259,10 +294,12 @@ int admit(pa_blockmgr* m, int64_t request_id, const int32_t* tokens, int32_t n_t
     if (need_new > available) return PA_ERR_REJECTED;
     Request r;
     r.tokens.assign(tokens, tokens + n_tokens);
+    r.blocks.reserve(need_total);
     r.capacity = (int32_t)lifetime;
+    Request& entry = m->requests[request_id];  // the last allocation: from here on nothing fails
     auto hold = [&](int32_t id) {
         Block& b = m->blocks[id];
-        if (b.refs++ == 0) m->evictable.erase(b.lru);
+        if (b.refs++ == 0) m->held.splice(m->held.end(), m->evictable, b.lru);
     };
     for (int32_t id : hits) {
         hold(id);
@@ -289,7 +326,7 @@ int admit(pa_blockmgr* m, int64_t request_id, const int32_t* tokens, int32_t n_t
         }
         *n_copy = rows;
     }
-    m->requests.emplace(request_id, std::move(r));
+    entry = std::move(r);
     return PA_OK;
 }
 
@@ -299,15 +336,19 @@ extern "C" {
 
 int pa_bm_admit(pa_blockmgr* m, int64_t request_id, const int32_t* tokens, int32_t n_tokens, int32_t max_new_tokens,
                 int32_t* block_table, int32_t table_cap, int32_t* n_blocks, int32_t* n_cached_tokens) {
-    return admit(m, request_id, tokens, n_tokens, max_new_tokens, block_table, table_cap, n_blocks, n_cached_tokens,
-                 false, nullptr, nullptr, nullptr);
+    return guarded([&] {
+        return admit(m, request_id, tokens, n_tokens, max_new_tokens, block_table, table_cap, n_blocks, n_cached_tokens,
+                     false, nullptr, nullptr, nullptr);
+    });
 }
 
 int pa_bm_admit_cow(pa_blockmgr* m, int64_t request_id, const int32_t* tokens, int32_t n_tokens,
                     int32_t max_new_tokens, int32_t* block_table, int32_t table_cap, int32_t* n_blocks,
                     int32_t* n_cached_tokens, int64_t* copy_src, int64_t* copy_dst, int32_t* n_copy) {
-    return admit(m, request_id, tokens, n_tokens, max_new_tokens, block_table, table_cap, n_blocks, n_cached_tokens,
-                 true, copy_src, copy_dst, n_copy);
+    return guarded([&] {
+        return admit(m, request_id, tokens, n_tokens, max_new_tokens, block_table, table_cap, n_blocks, n_cached_tokens,
+                     true, copy_src, copy_dst, n_copy);
+    });
 }
 
 int pa_bm_commit(pa_blockmgr* m, int64_t request_id, const int32_t* new_tokens, int32_t n_new, int32_t computed) {
@@ -318,9 +359,15 @@ int pa_bm_commit(pa_blockmgr* m, int64_t request_id, const int32_t* new_tokens, 
     Request& r = it->second;
     const int64_t len = (int64_t)r.tokens.size() + n_new;
     if (len > r.capacity || computed < 0 || computed > len) return PA_ERR_INVALID_ARG;
-    r.tokens.insert(r.tokens.end(), new_tokens, new_tokens + n_new);
-    m->register_full_blocks(r, computed);
-    return PA_OK;
+    return guarded([&] {
+        r.tokens.insert(r.tokens.end(), new_tokens, new_tokens + n_new);
+        // blocks for whose cache entries there is no memory now enter at a later commit
+        guarded([&] {
+            m->register_full_blocks(r, computed);
+            return PA_OK;
+        });
+        return PA_OK;
+    });
 }
 
 int pa_bm_evict(pa_blockmgr* m, int64_t request_id, const int32_t* block_ids, int32_t n) {
@@ -331,32 +378,34 @@ int pa_bm_evict(pa_blockmgr* m, int64_t request_id, const int32_t* block_ids, in
     if (n == 0) return PA_OK;
     Request& r = it->second;
     const int32_t bs = m->block_size;
-    // the ids in the order of the request's table; only blocks whose every token is there may leave
-    const int32_t full = (int32_t)r.tokens.size() / bs;
-    std::vector<char> leaves(r.blocks.size(), 0);
-    int32_t at = 0;
-    for (int32_t i = 0; i < full && at < n; ++i)
-        if (r.blocks[i] == block_ids[at]) {
-            leaves[i] = 1;
-            ++at;
+    return guarded([&] {
+        // the ids in the order of the request's table; only blocks whose every token is there may leave
+        const int32_t full = (int32_t)r.tokens.size() / bs;
+        std::vector<char> leaves(r.blocks.size(), 0);
+        int32_t at = 0;
+        for (int32_t i = 0; i < full && at < n; ++i)
+            if (r.blocks[i] == block_ids[at]) {
+                leaves[i] = 1;
+                ++at;
+            }
+        if (at < n) return PA_ERR_INVALID_ARG;  // not the request's, not full, out of order, or twice
+        std::vector<int32_t> blocks, tokens;
+        blocks.reserve(r.blocks.size() - n);
+        tokens.reserve(r.tokens.size() - (size_t)n * bs);
+        for (size_t i = 0; i < r.blocks.size(); ++i) {
+            if (leaves[i]) continue;
+            blocks.push_back(r.blocks[i]);
+            const size_t t0 = std::min(r.tokens.size(), i * bs), t1 = std::min(r.tokens.size(), (i + 1) * bs);
+            tokens.insert(tokens.end(), r.tokens.begin() + t0, r.tokens.begin() + t1);
         }
-    if (at < n) return PA_ERR_INVALID_ARG;  // not the request's, not full, out of order, or twice
-    std::vector<int32_t> blocks, tokens;
-    blocks.reserve(r.blocks.size() - n);
-    tokens.reserve(r.tokens.size() - (size_t)n * bs);
-    for (size_t i = 0; i < r.blocks.size(); ++i) {
-        if (leaves[i]) continue;
-        blocks.push_back(r.blocks[i]);
-        const size_t t0 = std::min(r.tokens.size(), i * bs), t1 = std::min(r.tokens.size(), (i + 1) * bs);
-        tokens.insert(tokens.end(), r.tokens.begin() + t0, r.tokens.begin() + t1);
-    }
-    for (size_t i = r.blocks.size(); i-- > 0;)  // later blocks first, as at a release
-        if (leaves[i]) m->drop_ref(r.blocks[i]);
-    r.blocks.swap(blocks);
-    r.tokens.swap(tokens);
-    r.capacity -= n * bs;
-    r.evicted = true;
-    return PA_OK;
+        for (size_t i = r.blocks.size(); i-- > 0;)  // later blocks first, as at a release
+            if (leaves[i]) m->drop_ref(r.blocks[i]);
+        r.blocks.swap(blocks);
+        r.tokens.swap(tokens);
+        r.capacity -= n * bs;
+        r.evicted = true;
+        return PA_OK;
+    });
 }
 
 int pa_bm_release(pa_blockmgr* m, int64_t request_id) {

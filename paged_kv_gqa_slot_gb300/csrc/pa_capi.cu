@@ -100,7 +100,10 @@ bool pool_map(CUtensorMap* out, void* base, long long rows, int d, int kind) {
     if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lk(g_mu);
     if (cache.size() > 256) cache.clear();
-    cache[key] = m;
+    try {
+        cache[key] = m;
+    } catch (...) {  // no memory: encoded again by the next call
+    }
     *out = m;
     return true;
 }
@@ -184,7 +187,10 @@ bool rows_map(CUtensorMap* out, const void* base, long long tokens, int heads, i
     if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lk(g_mu);
     if (cache.size() > 256) cache.clear();
-    cache[key] = m;
+    try {
+        cache[key] = m;
+    } catch (...) {  // no memory: encoded again by the next call
+    }
     *out = m;
     return true;
 }
@@ -629,6 +635,7 @@ const char* pa_status_str(int status) {
         case PA_ERR_TIMEOUT: return "PA_ERR_TIMEOUT";
         case PA_ERR_TOO_LARGE: return "PA_ERR_TOO_LARGE";
         case PA_ERR_REJECTED: return "PA_ERR_REJECTED";
+        case PA_ERR_NO_MEMORY: return "PA_ERR_NO_MEMORY";
         default: return "PA_ERR_UNKNOWN";
     }
 }
