@@ -34,10 +34,11 @@
 // the sums into weights, adds the group's heads in order and updates its own entry: no
 // atomics, no second launch.
 //
-// Measured on GB300, 32 q / 8 kv heads of d 128, 8-bit: 64 x ~1088 tokens 25.7 us (83% of the copy bandwidth;
+// Measured on GB300, 32 q / 8 kv heads of d 128, 8-bit: 64 x ~1088 tokens 25.6 us (84% of the copy bandwidth;
 // 23.1 with the copies alone), 64 x ~8192 with 64 q heads 164 us (98%), 4 queries of each of 64 x ~1088
-// 30.6 us, 1 x 1152 6.1 us; bf16 with weights 64 x ~1088 45 us (95%).  Long batches are bound by
-// memory, short ones by the chain table, block, merge and by the ends of their one wave.
+// 31.5 us, 1 x 1152 6.1 us; with weights 64 x ~1088 28.1 us, bf16 45 us (95%).  Long batches are bound by
+// memory, short ones by the chain table, block, merge and by the ends of their one wave.  Splits follow the
+// tables' width, not the lengths: 64 x ~1088 in tables of 576 blocks and more runs in two splits, 30.4 us.
 #include <algorithm>
 #include <atomic>
 

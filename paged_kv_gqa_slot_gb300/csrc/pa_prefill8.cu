@@ -36,16 +36,19 @@
 // loaded by the threads that own them took 4000 cycles more).  At the end all warps normalise O, stage
 // the rows in the free Q buffer and store them coalesced.
 //
-// Measured on GB300 (32 q / 8 kv heads, d 128), the bf16 pool's kernel on the same values in brackets:
-// 8 x 256 over 768 cached tokens 37 us (59), over 3840 105 (195), 1 x 256 over 768 15.7 (26.9),
-// 8 x 1024 over 1024 173 (304): 0.72 us a stage of two tiles, 1400 cycles, of which the matrix
+// Measured on GB300 (32 q / 8 kv heads, d 128), the bf16 pool's kernel on the same dequantised values in
+// brackets: 8 x 256 over 768 cached tokens 38.3 us (34.5), over 3840 110 (111), 1 x 256 over 768 16.4
+// (14.9), 8 x 1024 over 1024 178 (167): 0.75 us a stage of two tiles, 1450 cycles, of which the matrix
 // pipe needs 1280 (Q K^T reads Q and K from shared memory for 768, u V runs for 512), and about
 // 8 us a CTA outside its stages: loads that wait for one another (lengths, table, codes) and q 4.5,
-// output 2.5.
+// output 2.5.  So a chunk over a short prefix is slower than from a bf16 pool, by up to an eighth, and one over a
+// long prefix as fast.  At d 64 8 x 256 over 768 takes 30.4 us (125), over 3840 95.5 (513).
+// Of these, keeping far scales exact cost 0.5 us of the 38.3, keeping later keys' NaNs apart 0.7.
 // Tried and not kept: Q in tensor memory, which would bring the pipe to 1024 cycles but leaves room for
 // one score buffer a tile, so that its softmax and its instructions take turns; stages of 128 keys with one
-// buffer; two threads a row; codes loaded into registers a pair ahead (115 us for 8 x 256 + 3840 became
-// 118); one call site of the two softmax attempts (121 us against 108).
+// buffer; two threads a row (these three and one tile a CTA were measured at 51 to 75 us, before uniform warp
+// indices, paired conversion and coalesced loads of q); codes loaded into registers a pair ahead (115 us for
+// 8 x 256 + 3840 became 118); one call site of the two softmax attempts (121 us against 108).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
