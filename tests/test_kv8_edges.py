@@ -92,8 +92,8 @@ def sink_case(seed, n, d, where, chunk, code):
 
 
 def sink_check(c, out):
-    """The bounds of test_kv8.tolerance, but with the flush counted where f16 has it.  A row's base lies at
-    least 7 log2 units below its largest contribution, so a weight's u = p 2^7 / p_max or more, its rounding to f16
+    """The bounds of test_kv8.tolerance, but with the flush counted where f16 has it.  The dominant
+    key stands alone, so a row's base lies at least 7 log2 units below its contribution, and a weight's u = p 2^7 / p_max or more, its rounding to f16
     is at most 2^-11 of it or, below 2^-14, half of f16's smallest step, 2^-25: in p at most 2^-32 a key, and the
     keys' |V| average at most V_mean."""
     ref, spread, _, mag = c.reference()
