@@ -307,6 +307,110 @@ int pa_prefill_chunked8(const pa_pool8 *pool, const void *q, const int32_t *cu_q
                         int32_t max_chunk, float scale, void *out, pa_stream_t stream);
 
 /*
+ * pa_prefill_packed -- causal attention over whole prompts, packed one after another, before any
+ * of their tokens is cached: row t of sequence b (rows cu_lens[b] .. cu_lens[b+1]) attends to the
+ * rows cu_lens[b] .. t of its own sequence, query head h to kv head h / (num_heads / num_kv_heads).
+ * K and V are read where the projection left them; pa_kv_append brings them into a pool, before
+ * or after.  ("Qwen3-4B / 8B / 32B", "Warm Prefix-Cache TTFT": the cold prompts that table begins
+ * with.)
+ *   q              num_tokens rows of [num_heads, head_dim] bf16, 16-byte aligned, q_stride elements
+ *                  apart; k, v: rows of [num_kv_heads, head_dim], k_stride and v_stride apart (views
+ *                  of one fused projection, say).  A stride is a multiple of 8, at least its row and
+ *                  below 2^39
+ *   cu_lens        [batch + 1] int32, non-decreasing, within [0, num_tokens]
+ *   max_len        an upper bound of the sequences' lengths (sizes the grid).  Rows past it are
+ *                  reported (PA_DEV_OUT_OF_RANGE) and not written
+ *   out            [num_tokens, num_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside
+ *                  every sequence stay as they are.  It overlaps none of the inputs
+ * A sequence whose rows are not within [0, num_tokens] is skipped and sets PA_DEV_OUT_OF_RANGE.  A
+ * NaN or an infinity in K or V concerns the rows that see its key alone, in V its column alone.
+ * head_dim 64 or 128, any group size, batch <= 65535; arithmetic as pa_prefill_chunked.
+ */
+int pa_prefill_packed(const void *q, const void *k, const void *v, const int32_t *cu_lens, int32_t batch,
+                      int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t max_len, float scale, void *out,
+                      pa_stream_t stream);
+
+/*
+ * pa_kv_grow -- a step's new tokens enter the sequences, without the host: blocks from a free list on
+ * the GPU, and from the token counts everything that the step's other calls take.  Sequence b
+ * holds seq_lens[b] tokens and asks for new_lens[b] more, which need
+ *   need[b] = ceil((seq_lens[b] + new_lens[b]) / 16) - ceil(seq_lens[b] / 16)  blocks.
+ * In the order of b, a sequence gets its tokens, all or none, when
+ *   need[b] == 0 or need[0] + .. + need[b] <= *num_free,  and  new_lens[0] + .. + new_lens[b] <= max_tokens
+ * (a request that does not fit holds its place: those behind it that need blocks wait too).  Then
+ *   block_tables   [batch, max_blocks], in place: entries ceil(seq_lens[b] / 16) .. take the blocks, from
+ *                  the end of the free list, free_blocks[*num_free - 1] first; all others stay
+ *   seq_lens_out   [batch] the lengths, with the tokens given;  num_free_out [1] the blocks left
+ *   cu_lens        [batch + 1] int32 first row of every sequence's new tokens; cu_lens[batch] the rows
+ *   slot_mapping   [max_tokens] int64 cache slot of every row (pa_kv_append), -1 past the last
+ *   positions      [max_tokens] int32 place of the row's token in its sequence, 0 past the last
+ *   token_seqs     [max_tokens] int32 sequence of the row, -1 past the last
+ * seq_lens_out may be seq_lens, num_free_out may be num_free; otherwise no two arrays overlap.  A
+ * sequence with a negative length or count, or with more tokens than max_blocks * 16, gets none, asks
+ * for none and sets PA_DEV_OUT_OF_RANGE; so does *num_free outside [0, capacity], which is clamped.
+ *   free_blocks    [capacity] int32 block ids, the first *num_free of them free.  They are handed on
+ *                  as they are: the calls that read the tables check them.  batch <= 65535
+ */
+int pa_kv_grow(int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens, const int32_t *new_lens,
+               int32_t batch, const int32_t *free_blocks, int32_t capacity, const int32_t *num_free,
+               int32_t max_tokens, int32_t *seq_lens_out, int32_t *num_free_out, int32_t *cu_lens,
+               int64_t *slot_mapping, int32_t *positions, int32_t *token_seqs, pa_stream_t stream);
+
+/*
+ * pa_kv_free -- blocks go back to the free list of pa_kv_grow: the entries ids[r][0 .. counts[r]) that are
+ * not negative, row after row in their order, to free_blocks[*num_free], [*num_free + 1], ...; then
+ *   num_free_out   [1] the blocks free now (may be num_free)
+ * ids is a block table (counts: the blocks of the sequences that have finished, 0 for the others) or
+ * the `evicted` of pa_kv_evict (counts: its num_evicted).  A block that other sequences still use is the
+ * caller's to keep out.
+ *   ids            [rows, width] int32, width below 2^22 (else PA_ERR_UNSUPPORTED);  counts [rows]
+ *                  int32, outside [0, width] clamped and reported
+ * Blocks past the list's capacity are dropped; they, and *num_free outside [0, capacity] (clamped), set
+ * PA_DEV_OUT_OF_RANGE.  No two arrays overlap but num_free_out and num_free.
+ */
+int pa_kv_free(const int32_t *ids, const int32_t *counts, int32_t rows, int32_t width, int32_t *free_blocks,
+               int32_t capacity, const int32_t *num_free, int32_t *num_free_out, pa_stream_t stream);
+
+/*
+ * pa_linear_decode, pa_linear_prefill -- linear attention with a decay for each head, as the layers
+ * between the full-attention ones of a hybrid stack compute it ("Qwen3.5": 3 of every 4 layers, with a
+ * per-request recurrent state).  With a = exp(log_decay[h]) of kv head h, over a sequence's tokens t,
+ *   S_t = a S_{t-1} + k_t v_t^T  (head_dim x head_dim),   o_t = scale q_t^T S_t,
+ * query head i reading the state of kv head i / (num_heads / num_kv_heads).  The state lives in
+ *   state          [num_slots, num_kv_heads, head_dim (of k), head_dim (of v)] fp32, 16-byte aligned,
+ * sequence b's in slot state_slots[b]; the call reads it and leaves the new one there.  A sequence
+ * whose tokens are all this call's (seq_lens[b] equals its row count) begins with S = 0, whatever the
+ * slot holds.
+ *   log_decay      [num_kv_heads] fp32, taken into [-1e4, 0]
+ *   state_slots    [batch] int32; a negative slot is padding: zero rows, no state.  One past num_slots
+ *                  likewise, and sets PA_DEV_OUT_OF_RANGE.  The same slot twice is a caller error
+ *   seq_lens       [batch] int32, tokens of the sequence including this call's
+ *   q, k, v        rows of [heads, head_dim] bf16, q_stride, k_stride, v_stride elements apart, as
+ *                  pa_prefill_packed's;  out contiguous bf16, overlapping nothing
+ * pa_linear_decode: row b is sequence b's newest token; seq_lens[b] <= 0 is padding (zero row, no state).
+ * pa_linear_prefill: rows cu_q_lens[b] .. cu_q_lens[b+1] are its newest tokens, any number; none leaves the
+ * state as it is.  Rows outside every sequence stay as they are; rows past max_chunk, a sequence with
+ * fewer tokens than rows and one whose rows are not within [0, num_tokens] as in pa_prefill_packed.
+ * Both keep S in fp32 throughout; the prefill's products take q, k and v as they are, the scores and S
+ * (where q reads it) as bf16, and k's weighted rows (where S gathers them) as two bf16 parts.  A NaN or an
+ * infinity in a row of v concerns its column from that row on, which may turn NaN as a whole.
+ *   workspace      pa_linear_workspace_bytes(...) bytes, 16-byte aligned (may be NULL where that is 0),
+ *                  not shared by calls that may run at the same time; nothing in it outlives the call
+ * head_dim 64 or 128, any group size, batch <= 65535.
+ */
+int pa_linear_decode(float *state, int32_t num_slots, const int32_t *state_slots, const void *q, const void *k,
+                     const void *v, const float *log_decay, const int32_t *seq_lens, int32_t batch,
+                     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, float scale, void *out, pa_stream_t stream);
+size_t pa_linear_workspace_bytes(int32_t batch, int32_t num_kv_heads, int32_t head_dim, int32_t max_chunk);
+int pa_linear_prefill(float *state, int32_t num_slots, const int32_t *state_slots, const void *q, const void *k,
+                      const void *v, const float *log_decay, const int32_t *cu_q_lens, const int32_t *seq_lens,
+                      int32_t batch, int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t max_chunk, float scale,
+                      void *workspace, void *out, pa_stream_t stream);
+
+/*
  * pa_device_status -- synchronise `stream`, then read the device status word of the
  * current device into *flags (PA_DEV_* bits, 0 = clean), clearing it when `clear` != 0.
  * Returns PA_OK, PA_ERR_OUT_OF_RANGE or PA_ERR_TIMEOUT according to the bits (timeout

@@ -11,7 +11,10 @@ pa_decode8, pa_prefill_chunked8; pa_decode_weights / pa_decode8_weights and pa_k
 eviction by accumulated attention weight.  Tensors must be CUDA,
 contiguous, and of the dtypes the header states (bf16 data, int32 tables,
 int64 slot mapping, fp32 split-KV workspace).  Calls are asynchronous on the
-given stream (default: torch's current stream).
+given stream (default: torch's current stream).  For a hybrid stack's step: pa_prefill_packed
+(cold prompts, rows strided as a fused projection leaves them), pa_kv_grow and pa_kv_free (tables,
+lengths and slots built on the GPU from a free list) and pa_linear_decode / pa_linear_prefill
+(linear attention with a decay for each head).
 """
 from __future__ import annotations
 
@@ -27,7 +30,8 @@ __all__ = ["PaPool", "PaPool8", "pa_kv_append8", "pa_decode8", "pa_prefill_chunk
            "pa_combine", "pa_prefill_chunked",
            "pa_device_status", "pa_selftest_wait_timeout", "pa_splitkv_workspace_bytes", "pa_decode_num_splits", "pa_splitkv_num_partitions",
            "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes", "PagedAttnError",
-           "BlockManager", "pa_kv_block_bytes", "pa_kv_budget_blocks",
+           "pa_prefill_packed", "pa_kv_grow", "pa_kv_free", "pa_linear_decode", "pa_linear_prefill",
+           "pa_linear_workspace_bytes", "BlockManager", "pa_kv_block_bytes", "pa_kv_budget_blocks",
            "library", "library_path", "BLOCK_SIZE", "EXPORTED_SYMBOLS"]
 
 BLOCK_SIZE = 16
@@ -38,7 +42,8 @@ EXPORTED_SYMBOLS = ("pa_kv_append8", "pa_decode8", "pa_prefill_chunked8", "pa_de
                     "pa_decode_splitkv", "pa_combine",
                     "pa_prefill_chunked", "pa_device_status", "pa_decode_num_splits", "pa_splitkv_num_partitions",
                     "pa_status_str", "pa_version", "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes",
-                    "pa_selftest_wait_timeout",
+                    "pa_selftest_wait_timeout", "pa_prefill_packed", "pa_kv_grow", "pa_kv_free", "pa_linear_decode",
+                    "pa_linear_prefill", "pa_linear_workspace_bytes",
                     "pa_kv_block_bytes", "pa_kv_budget_blocks", "pa_bm_create", "pa_bm_destroy", "pa_bm_admit", "pa_bm_admit_cow",
                     "pa_bm_commit", "pa_bm_release", "pa_bm_slots", "pa_bm_stats")
 
@@ -89,6 +94,7 @@ def library() -> ctypes.CDLL:
                            "(or __graft_entry__.build()) first -- there is no fallback path")
     lib = ctypes.CDLL(str(_LIB_PATH))
     P, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    I64 = ctypes.c_int64
     pool = ctypes.POINTER(_PaPoolC)
     pool8 = ctypes.POINTER(_PaPool8C)
     weights_args = [P, P, I32, P, I32, I32, F32, F32, P, P, P, P]
@@ -101,6 +107,13 @@ def library() -> ctypes.CDLL:
         "pa_weights_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "pa_kv_evict": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
         "pa_bm_evict": (ctypes.c_int, [P, ctypes.c_int64, P, I32]),
+        "pa_prefill_packed": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, I32, I64, I64, I64, I32, F32, P, P]),
+        "pa_kv_grow": (ctypes.c_int, [P, I32, P, P, I32, P, I32, P, I32, P, P, P, P, P, P, P]),
+        "pa_kv_free": (ctypes.c_int, [P, P, I32, I32, P, I32, P, P, P]),
+        "pa_linear_decode": (ctypes.c_int, [P, I32, P, P, P, P, P, P, I32, I32, I32, I32, I64, I64, I64, F32, P, P]),
+        "pa_linear_prefill": (ctypes.c_int, [P, I32, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I64, I64, I64, I32,
+                                             F32, P, P, P]),
+        "pa_linear_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "pa_kv_append": (ctypes.c_int, [pool, P, P, P, I32, P]),
         "pa_kv_copy": (ctypes.c_int, [pool, P, P, I32, P]),
         "pa_decode": (ctypes.c_int, [pool, P, P, I32, P, I32, I32, F32, P, P]),
@@ -536,6 +549,154 @@ def pa_kv_evict(block_tables: torch.Tensor, seq_lens: torch.Tensor, weights: tor
           int(keep_blocks), int(sink_blocks), int(recent_blocks), new_tables.data_ptr(), new_lens.data_ptr(),
           new_weights.data_ptr(), evicted.data_ptr(), num.data_ptr())
     return new_tables, new_lens, new_weights, evicted, num
+
+
+# ----------------------------------------------------------------------------- a hybrid stack's step
+def _strided(t: torch.Tensor, heads: int, dim: int, name: str, device: int) -> Tuple[int, int]:
+    """Address and row stride of bf16 rows [heads, dim] on the call's device: each row contiguous, the
+    rows any multiple of 8 elements apart (a view of a fused projection)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: need [rows, {heads}, {dim}], got {tuple(shape)}")
+    if t.dtype is not _BF16 or not t.is_cuda:
+        raise ValueError(f"{name}: need a CUDA {_BF16} tensor, got {t.dtype} on {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors are on cuda:{device}")
+    row, head, one = t.stride()
+    if shape[0] <= 1:
+        row = heads * dim
+    if one != 1 or (head != dim and heads > 1) or row < heads * dim or row % 8:
+        raise ValueError(f"{name}: need rows of {heads} x {dim} contiguous elements, a multiple of 8 apart, got strides "
+                         f"{t.stride()}")
+    return t.data_ptr(), row
+
+
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A result tensor on `like`'s device, allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=like.device) if raw else torch.cuda.default_stream(like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _packed(q, k, v, out, stream):
+    """Check the rows of a packed call; (device, rows, heads, kv heads, dim, addresses, strides, out)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q / k: need [rows, heads, head_dim], got {tuple(q.shape)} / {tuple(k.shape)}")
+    rows, heads, dim = q.shape
+    kvh, d = k.shape[1], q.get_device()
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError(f"q, k, v: need equal row counts, got {rows}, {k.shape[0]}, {v.shape[0]}")
+    qp, qs = _strided(q, heads, dim, "q", d)
+    kp, ks = _strided(k, kvh, dim, "k", d)
+    vp, vs = _strided(v, kvh, dim, "v", d)
+    if out is None:
+        out = _new(q, (rows, heads, dim), _BF16, stream)
+    elif out.shape != q.shape:
+        raise ValueError(f"out: need shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    return d, rows, heads, kvh, dim, (qp, kp, vp), (qs, ks, vs), out
+
+
+def pa_prefill_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_lens: torch.Tensor, scale: float,
+                      max_len: int, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: rows cu_lens[b] .. cu_lens[b+1] of q [rows, num_heads, head_dim],
+    k and v [rows, num_kv_heads, head_dim] are sequence b.  Rows may be strided views."""
+    d, rows, heads, kvh, dim, p, s, out = _packed(q, k, v, out, stream)
+    _call("pa_prefill_packed", d, stream, *p, _arg(cu_lens, _I32, "cu_lens", d), cu_lens.numel() - 1, rows, heads, kvh,
+          dim, *s, int(max_len), float(scale), _arg(out, _BF16, "out", d))
+    return out
+
+
+def pa_kv_grow(block_tables: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor,
+               num_free: torch.Tensor, max_tokens: int, in_place: bool = False, stream=None):
+    """Give every sequence its new_lens tokens while the free list and max_tokens last.  block_tables is
+    updated in place, and seq_lens and num_free [1] with in_place.  Returns (block_tables, seq_lens, num_free,
+    cu_lens, slot_mapping, positions, token_seqs)."""
+    if block_tables.dim() != 2:
+        raise ValueError(f"block_tables: need [batch, max_blocks], got {tuple(block_tables.shape)}")
+    B, width = block_tables.shape
+    if seq_lens.shape != (B,) or new_lens.shape != (B,) or num_free.numel() != 1:
+        raise ValueError(f"seq_lens / new_lens / num_free: need shapes {(B,)} / {(B,)} / (1,), got "
+                         f"{tuple(seq_lens.shape)} / {tuple(new_lens.shape)} / {tuple(num_free.shape)}")
+    d, rows = block_tables.get_device(), int(max_tokens)
+    if rows < 0:
+        raise ValueError(f"max_tokens: need 0 or more, got {rows}")
+    lens = seq_lens if in_place else _new(seq_lens, (B,), _I32, stream)
+    left = num_free if in_place else _new(num_free, num_free.shape, _I32, stream)
+    cu = _new(block_tables, (B + 1,), _I32, stream)
+    slots = _new(block_tables, (rows,), _I64, stream)
+    more = _new(block_tables, (2, rows), _I32, stream)
+    positions, token_seqs = more[0], more[1]
+    _call("pa_kv_grow", d, stream, _arg(block_tables, _I32, "block_tables", d), width, _arg(seq_lens, _I32, "seq_lens", d),
+          _arg(new_lens, _I32, "new_lens", d), B, _arg(free_blocks, _I32, "free_blocks", d), free_blocks.numel(),
+          _arg(num_free, _I32, "num_free", d), rows, lens.data_ptr(), left.data_ptr(), cu.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), token_seqs.data_ptr())
+    return block_tables, lens, left, cu, slots, positions, token_seqs
+
+
+def pa_kv_free(ids: torch.Tensor, counts: torch.Tensor, free_blocks: torch.Tensor, num_free: torch.Tensor,
+               in_place: bool = False, stream=None) -> torch.Tensor:
+    """Push the blocks ids[r, :counts[r]] (negative entries do not count) onto the free list, which is updated
+    in place; returns num_free [1] after that (num_free itself with in_place)."""
+    if ids.dim() != 2 or counts.shape != (ids.shape[0],) or num_free.numel() != 1:
+        raise ValueError(f"ids / counts / num_free: need [rows, width] / [rows] / [1], got {tuple(ids.shape)} / "
+                         f"{tuple(counts.shape)} / {tuple(num_free.shape)}")
+    d = free_blocks.get_device()
+    left = num_free if in_place else _new(num_free, num_free.shape, _I32, stream)
+    _call("pa_kv_free", d, stream, _arg(ids, _I32, "ids", d), _arg(counts, _I32, "counts", d), ids.shape[0],
+          ids.shape[1], _arg(free_blocks, _I32, "free_blocks", d), free_blocks.numel(),
+          _arg(num_free, _I32, "num_free", d), left.data_ptr())
+    return left
+
+
+def _linear_state(state, kvh, dim, state_slots, log_decay, seq_lens, batch, device):
+    """Check the state pool and the arrays beside it; their addresses."""
+    if state.dim() != 4 or tuple(state.shape[1:]) != (kvh, dim, dim):
+        raise ValueError(f"state: need [num_slots, {kvh}, {dim}, {dim}], got {tuple(state.shape)}")
+    if state_slots.shape != (batch,) or seq_lens.shape != (batch,) or log_decay.shape != (kvh,):
+        raise ValueError(f"state_slots / seq_lens / log_decay: need shapes {(batch,)} / {(batch,)} / {(kvh,)}, got "
+                         f"{tuple(state_slots.shape)} / {tuple(seq_lens.shape)} / {tuple(log_decay.shape)}")
+    return (_arg(state, _F32, "state", device), _arg(state_slots, _I32, "state_slots", device),
+            _arg(log_decay, _F32, "log_decay", device), _arg(seq_lens, _I32, "seq_lens", device))
+
+
+def pa_linear_decode(state: torch.Tensor, state_slots: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                     v: torch.Tensor, log_decay: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token a sequence of linear attention: state [num_slots, num_kv_heads, d, d] fp32, updated in place at
+    state_slots [batch]; q [batch, num_heads, d], k and v [batch, num_kv_heads, d], which may be strided views."""
+    d, rows, heads, kvh, dim, p, s, out = _packed(q, k, v, out, stream)
+    st, slots, decay, lens = _linear_state(state, kvh, dim, state_slots, log_decay, seq_lens, rows, d)
+    _call("pa_linear_decode", d, stream, st, state.shape[0], slots, *p, decay, lens, rows, heads, kvh, dim, *s,
+          float(scale), _arg(out, _BF16, "out", d))
+    return out
+
+
+def pa_linear_workspace_bytes(batch: int, num_kv_heads: int, head_dim: int, max_chunk: int) -> int:
+    return int(library().pa_linear_workspace_bytes(batch, num_kv_heads, head_dim, max_chunk))
+
+
+def pa_linear_prefill(state: torch.Tensor, state_slots: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                      v: torch.Tensor, log_decay: torch.Tensor, cu_q_lens: torch.Tensor, seq_lens: torch.Tensor,
+                      scale: float, max_chunk: int, workspace: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A chunk of tokens a sequence of linear attention: rows cu_q_lens[b] .. cu_q_lens[b+1] are sequence b's newest
+    tokens, and its state goes on from slot state_slots[b] (from zero when seq_lens[b] counts no others)."""
+    d, rows, heads, kvh, dim, p, s, out = _packed(q, k, v, out, stream)
+    B = cu_q_lens.numel() - 1
+    st, slots, decay, lens = _linear_state(state, kvh, dim, state_slots, log_decay, seq_lens, B, d)
+    need = pa_linear_workspace_bytes(B, kvh, dim, int(max_chunk))
+    if workspace is None:
+        workspace = _new(q, ((need + 3) // 4,), _F32, stream)
+    elif workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace: need {need} bytes, got {workspace.numel() * workspace.element_size()}")
+    _call("pa_linear_prefill", d, stream, st, state.shape[0], slots, *p, decay, _arg(cu_q_lens, _I32, "cu_q_lens", d),
+          lens, B, rows, heads, kvh, dim, *s, int(max_chunk), float(scale),
+          _arg(workspace, workspace.dtype, "workspace", d) or None, _arg(out, _BF16, "out", d))
+    return out
 
 
 def pa_device_status(clear: bool = True, stream=None) -> int:

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <atomic>
 #include <cstdlib>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <mutex>
 #include <stdint.h>
@@ -89,6 +90,55 @@ struct EvictArgs {
     int max_blocks, num_kv_heads, keep, sink, recent;
 };
 
+// Rows of a packed call (pa_prefill_packed, pa_linear_*): q, k, v with row strides in elements.
+struct PackedArgs {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* out;
+    const int32_t* cu_lens;  // [B+1] (null: one row a sequence)
+    unsigned* status;
+    long long q_stride, k_stride, v_stride;
+    int batch, num_tokens, num_heads, num_kv_heads, head_dim, max_len;
+    float scale;
+};
+
+// What a linear-attention call has besides its rows.
+struct LinearArgs {
+    PackedArgs rows;
+    float* state;               // [num_slots, Hkv, D, D]
+    const int32_t* state_slots; // [B]
+    const float* log_decay;     // [Hkv]
+    const int32_t* seq_lens;    // [B]
+    int num_slots;
+};
+
+// Arguments of pa_kv_grow and of pa_kv_free.
+struct GrowArgs {
+    int32_t* tables;
+    const int32_t* seq_lens;
+    const int32_t* new_lens;
+    const int32_t* free_blocks;
+    const int32_t* num_free;
+    int32_t* seq_lens_out;
+    int32_t* num_free_out;
+    int32_t* cu_lens;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* token_seqs;
+    unsigned* status;
+    int max_blocks, batch, capacity, max_tokens;
+};
+struct FreeArgs {
+    const int32_t* ids;
+    const int32_t* counts;
+    int32_t* free_blocks;
+    const int32_t* num_free;
+    int32_t* num_free_out;
+    unsigned* status;
+    int rows, width, capacity;
+};
+
 const DeviceInfo& device_info();
 // 3-D TMA map (d, head, token) over a [tokens, heads, d] bf16 tensor (d = 128), 128-byte
 // swizzled, box (64, box_heads, box_tokens); false if it cannot be encoded.
@@ -164,6 +214,13 @@ cudaError_t launch_decode8(const Pool8View& pool, const AttnArgs& a, cudaStream_
 cudaError_t launch_decode8_mq(const Pool8View& pool, const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill8(const Pool8View& pool, const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream);
+cudaError_t launch_grow(const GrowArgs& a, cudaStream_t stream);
+cudaError_t launch_free(const FreeArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_packed(const PackedArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream);
+size_t linear_workspace(int batch, int num_kv_heads, int head_dim, int max_chunk);
+constexpr int kFreeMaxWidth = (1 << 22) - 1;  // row length of pa_kv_free: 512 rows count below 2^31
 constexpr int kEvictMaxBlocks = 49152;  // table width of an eviction: a word of shared memory each
 cudaError_t launch_combine(const float* ws_o, const float* ws_lse, int batch, int num_heads, int head_dim,
                            int num_partitions, void* out, cudaStream_t stream);
