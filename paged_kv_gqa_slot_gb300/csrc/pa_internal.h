@@ -223,6 +223,8 @@ cudaError_t launch_free(const FreeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_packed(const PackedArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream);
+// chunks of 128 tokens on the tensor cores
+cudaError_t launch_linear_prefill_tc(const LinearArgs& a, cudaStream_t stream);
 size_t linear_workspace(int batch, int num_kv_heads, int head_dim, int max_chunk);
 constexpr int kFreeMaxWidth = (1 << 22) - 1;  // row length of pa_kv_free: 512 rows count below 2^31
 constexpr int kEvictMaxBlocks = 49152;  // table width of an eviction: a word of shared memory each

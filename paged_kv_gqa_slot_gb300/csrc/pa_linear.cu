@@ -16,6 +16,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMinLogDecay = -1e4f;
+constexpr int kFewTokens = 4;  // chunks up to this long go token by token
 
 // log2 of a head's decay; a NaN is taken as the lower end
 __device__ __forceinline__ float log2_decay(float log_decay) {
@@ -176,6 +177,7 @@ cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream) {
 size_t linear_workspace(int, int, int, int) { return 0; }
 
 cudaError_t launch_linear_prefill(const LinearArgs& a, void*, cudaStream_t stream) {
+    if (a.rows.max_len > kFewTokens) return launch_linear_prefill_tc(a, stream);
     const dim3 grid(a.rows.num_kv_heads, a.rows.batch);
     return a.rows.head_dim == 64 ? launch(linear_step_kernel<64>, grid, 64, a, stream)
                                  : launch(linear_step_kernel<128>, grid, 128, a, stream);

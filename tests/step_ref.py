@@ -57,8 +57,13 @@ def packed_bound(ref, size):
     return 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * (size + ref.abs()) + 1e-30
 
 
-def linear(state, slots, q, k, v, log_decay, cu, lens, scale, most=None):
-    """(o, its terms' size, new state, its terms' size), fp64; rows outside every sequence are NaN."""
+CHUNK = 128  # tokens that a prefill takes at a time: q reads the state that its chunk begins with
+
+
+def linear(state, slots, q, k, v, log_decay, cu, lens, scale):
+    """(o, its terms' size, new state, its terms' size), fp64; rows outside every sequence are NaN.
+    A term of o is a score of its chunk times v, or an element of q times one of the state that the chunk
+    begins with; a term of the state k times v, or what it was, with their decays."""
     kvh, d = k.shape[1], q.shape[2]
     group = q.shape[1] // kvh
     out = torch.full(q.shape, math.nan, dtype=torch.float64, device=q.device)
@@ -85,7 +90,13 @@ def linear(state, slots, q, k, v, log_decay, cu, lens, scale, most=None):
             for hq in range(h * group, (h + 1) * group):
                 z = q[c0:c1, hq].double()
                 out[c0:c1, hq] = ((z @ x.T * far) @ y + lead * (z @ old)) * scale
-                size[c0:c1, hq] = ((z @ x.T * far).abs() @ y.abs() + lead * (z.abs() @ old.abs())) * abs(scale)
+                near = far * (i[:, None] // CHUNK == i // CHUNK)
+                size[c0:c1, hq] = ((z @ x.T * near).abs() @ y.abs()) * abs(scale)
+                begin = old
+                for p in range(0, n, CHUNK):
+                    e = min(p + CHUNK, n)
+                    size[c0 + p:c0 + e, hq] += lead[:e - p] * (z[p:e].abs() @ begin.abs()) * abs(scale)
+                    begin = torch.exp(a * (e - p)) * begin + (x[p:e] * rest[n - (e - p):]).T @ y[p:e]
             new[slots[b], h] = torch.exp(a * n) * old + (x * rest).T @ y
             new_size[slots[b], h] = torch.exp(a * n) * old.abs() + (x.abs() * rest).T @ y.abs()
     return out, size, new, new_size
@@ -93,10 +104,11 @@ def linear(state, slots, q, k, v, log_decay, cu, lens, scale, most=None):
 
 def linear_bounds(ref, size, new_size, n, one_token=False):
     """Outputs: half a bf16 step of the result; the scores, and S where q reads it, as bf16 (2^-8 of every term)
-    unless the call is for one token; fp32 sums (each of n + 2 d additions up to 2^-22 of the terms' size).
+    unless the call is for one token; the error that S itself has (below 2^-16 of sum a^.. |k| |v|, taken as 2^-12
+    of the terms), and fp32 sums (each of n + 2 d additions up to 2^-22 of the terms' size).
     State: k's weighted rows as two bf16 parts, 2^-16 of every term, and the sums."""
     sums = (n + 256) * 2.0 ** -22
-    out = 2.0 ** -8 * ref.abs() + ((0 if one_token else 2.0 ** -8) + sums) * size + 1e-30
+    out = 2.0 ** -8 * ref.abs() + ((0 if one_token else 2.0 ** -8 + 2.0 ** -12) + sums) * size + 1e-30
     return out, ((0 if one_token else 2.0 ** -16) + sums) * new_size + 1e-30
 
 

@@ -288,27 +288,25 @@ def test_chunks_and_single_tokens_in_turn_are_one_sequence(d):
     """A prompt in chunks of any size, then token by token, against the whole at once."""
     n, heads, kvh = 700, 4, 2
     whole = Case(33, [n], heads, kvh, d, fresh=(0,))
-    ref, size, new, new_size = whole.reference()
-    bound, new_bound = R.linear_bounds(ref, size, new_size, n)
-    # a state that leaves a call is rounded as its terms are: one more 2^-16 of them a call
-    calls = 0
+    ref, _, new, new_size = whole.reference()
+    _, new_bound = R.linear_bounds(ref, ref, new_size, n)
+    carried = whole.state.double()  # the state between the calls, in 64 bits
     at = 0
-    for step in (1, 130, 64, 3, 1, 300, 128, 17):
+    for step in (1, 130, 64, 3, 1, 300, 128, 17) + (1,) * 56:
         rows = slice(at, at + step)
-        cu = torch.tensor([0, step], device="cuda").int()
         lens = torch.tensor([at + step], device="cuda").int()
-        out = pa.pa_linear_prefill(whole.state, whole.slots, whole.q[rows], whole.k[rows], whole.v[rows], whole.log_decay,
-                                   cu, lens, whole.scale, step)
-        within(out, ref[rows], bound[rows], f"chunk at {at}")
+        part = [x[rows] for x in (whole.q, whole.k, whole.v)]
+        if step == 1 and at > 0:
+            out = pa.pa_linear_decode(whole.state, whole.slots, *part, whole.log_decay, lens, whole.scale)
+        else:
+            cu = torch.tensor([0, step], device="cuda").int()
+            out = pa.pa_linear_prefill(whole.state, whole.slots, *part, whole.log_decay, cu, lens, whole.scale, step)
+        mine, size, carried, _ = R.linear(carried, whole.slots.tolist(), *part, whole.log_decay, [0, step], [at + step], whole.scale)
+        bound, _ = R.linear_bounds(mine, size, size, n)
+        within(out, mine, bound, f"{step} at {at}")
+        within(mine, ref[rows], 1e-12 * (size + 1), "the reference's parts")
         at += step
-        calls += 1
-    while at < n:
-        rows = slice(at, at + 1)
-        lens = torch.tensor([at + 1], device="cuda").int()
-        out = pa.pa_linear_decode(whole.state, whole.slots, whole.q[rows], whole.k[rows], whole.v[rows], whole.log_decay,
-                                  lens, whole.scale)
-        within(out, ref[rows], bound[rows], f"token at {at}")
-        at += 1
+    assert at == n
     within(whole.state, new, new_bound, "state")
     clean()
 
