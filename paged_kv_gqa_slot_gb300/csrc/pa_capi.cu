@@ -233,17 +233,18 @@ bool plane_maps(PlaneMaps* out, const void* k, const void* v, long long rows, in
     return plane_map(&out->k, k, rows, row_bytes, 0) && plane_map(&out->v, v, rows, row_bytes, 0);
 }
 
-// 3-D map (d, head, row) over bf16 rows `stride` elements apart, 128-byte swizzled, box (64 columns,
-// box_heads heads, box_rows rows).  Encoded by every call, as plane_map: nothing is kept by an address.
+// 4-D map (64 columns, head, row, column half) over bf16 rows `stride` elements apart, 128-byte swizzled, box
+// (64, box_heads, box_rows, box_halves): a whole tile in one copy, half by half, or one half.  Encoded by every
+// call, as plane_map: nothing is kept by an address.
 bool strided_map(CUtensorMap* out, const void* base, long long rows, int heads, int d, long long stride,
-                 int box_heads, int box_rows) {
+                 int box_heads, int box_rows, int box_halves) {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint64_t dims[4] = {64, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)(d / 64)};
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, (cuuint32_t)box_halves};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

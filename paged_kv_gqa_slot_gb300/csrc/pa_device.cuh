@@ -122,6 +122,16 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// 4-D tiled load of a tile of packed rows (strided_map): heads from `head`, rows from `row`, column halves from `half`.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int head, int row, int half,
+                                              uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(row), "r"(half), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // 3-D tiled store from this CTA's shared memory (bulk-group completion: commit, then wait).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -160,6 +170,14 @@ __device__ __forceinline__ uint64_t l2_evict_last_policy() {
 // TMA with 128-byte swizzling: rows of 128 B, chunk index XOR (row mod 8).
 __device__ __forceinline__ uint32_t swz128(int row, int chunk) {
     return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+// Nonzero if one of the eight bf16 values is a NaN or an infinity: all exponent bits set, which a carry out of
+// them shows (0x0080 added to the masked exponent 0x7f80 gives 0x8000).
+__device__ __forceinline__ uint32_t not_finite(const uint4& x) {
+    const uint32_t a = (x.x & 0x7f807f80u) + 0x00800080u, b = (x.y & 0x7f807f80u) + 0x00800080u;
+    const uint32_t c = (x.z & 0x7f807f80u) + 0x00800080u, d = (x.w & 0x7f807f80u) + 0x00800080u;
+    return (a | b | c | d) & 0x80008000u;
 }
 
 // ---------------------------------------------------------------- warp MMA (bf16 -> fp32)

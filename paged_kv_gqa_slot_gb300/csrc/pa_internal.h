@@ -152,10 +152,10 @@ struct PlaneMaps {
     int paired, k_second;
 };
 bool plane_maps(PlaneMaps* out, const void* k, const void* v, long long rows, int row_bytes);
-// 3-D TMA map (d, head, row) over bf16 rows `stride` elements apart, 128-byte swizzled, box (64, box_heads,
-// box_rows); false if it cannot be encoded.
+// 4-D TMA map (64 columns, head, row, column half) over bf16 rows `stride` elements apart, 128-byte swizzled, box
+// (64, box_heads, box_rows, box_halves); false if it cannot be encoded.
 bool strided_map(CUtensorMap* out, const void* base, long long rows, int heads, int d, long long stride,
-                 int box_heads, int box_rows);
+                 int box_heads, int box_rows, int box_halves);
 unsigned* device_status_ptr();
 
 // One-time set-up of a kernel (function attributes, occupancy queries) on each device:

@@ -21,7 +21,8 @@
 // that row on the column is NaN, and so is the state's.
 //
 // One CTA a (sequence, kv head), one an SM.  Warps: 0-3 P and the outputs (one row a thread), 4-7 the
-// state (one row a thread), 8-11 K~ and the look at V, 12 MMA issue and tensor memory, 13 TMA loads.
+// state (one row a thread), 8-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and V, 14 of Q (one thread
+// issues a copy in about half a microsecond), 15 the look at V.
 #include <algorithm>
 #include <climits>
 
@@ -32,8 +33,8 @@ namespace pa {
 namespace {
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 448;
-constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kQLoadWarp = 14, kCleanWarp = 15;
 constexpr int kHalf = kChunk * 128;  // [128 rows][64 columns] bf16
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMinLogDecay = -1e4f;
@@ -42,11 +43,11 @@ template <int D>
 struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kOffQ = 0;                    // two tiles
-    static constexpr int kOffK = kOffQ + 2 * kTile;    // two; a tile becomes the high parts of K~ in place
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kTile;        // two tiles; each becomes the high parts of K~ in place
     static constexpr int kOffLo = kOffK + 2 * kTile;   // the low parts
-    static constexpr int kOffV = kOffLo + kTile;
-    static constexpr int kOffS = kOffV + kTile;        // the state, bf16, D rows
+    static constexpr int kOffV = kOffLo + kTile;       // two tiles
+    static constexpr int kOffS = kOffV + 2 * kTile;    // the state, bf16, D rows
     static constexpr int kOffBars = kOffS + D * 128 * kHalves;
     static constexpr int kOffBad = kOffBars + 256;     // [D] first token of a column with a value that is not finite
     static constexpr int kSmem = kOffBad + D * 4;
@@ -57,7 +58,7 @@ struct Layout {
 static_assert(Layout<128>::kSmem <= 227 * 1024, "shared memory");
 
 struct Bars {
-    uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full, v_empty, v_clean;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
     uint64_t s_full, p_full, o_full, o_empty;  // scores, P, outputs ready; outputs read
     uint64_t k_raw;                            // Q K^T of the chunk is done: K may become K~
     uint64_t kt_full, st_full, u_full;         // K~ ready; the state ready for the chunk; K~^T V done
@@ -79,6 +80,21 @@ __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1,
         "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Sixteen values as bf16, in one 32-byte store (a whole sector a thread) where the address allows it.
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, bool wide) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+    if (!wide) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 template <int D>
@@ -125,12 +141,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->k_empty[s], 1);
-            mbar_init(&bars->q_full[s], 1);
-            mbar_init(&bars->q_empty[s], 1);
+            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->v_empty[s], 1);
+            mbar_init(&bars->v_clean[s], 32);
         }
-        mbar_init(&bars->v_full, 1);
-        mbar_init(&bars->v_empty, 1);
-        mbar_init(&bars->v_clean, 128);
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->s_full, 1);
         mbar_init(&bars->p_full, 128);
         mbar_init(&bars->o_full, 1);
@@ -154,69 +170,69 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const uint32_t tmem = bars->tmem_base;
     bool ok = true;
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- TMA loads, in the order of use
-        if (lane == 0) {
-            prefetch_tensormap(&tm_q);
+    if (warp == kLoadWarp || warp == kQLoadWarp) {
+        // ---------------------------------------------------------------- TMA loads
+        if (lane == 0 && warp == kLoadWarp) {
+            auto load = [&](int off, const CUtensorMap* map, int c, uint64_t* full) {
+                mbar_arrive_expect_tx(full, L::kTile);
+                tma_load_rows(smem + off + (c & 1) * L::kTile, map, kvh, c0 + c * kChunk, 0, full);
+            };
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
-            auto load = [&](int off, const CUtensorMap* map, int head, int c, uint64_t* full) {
-                mbar_arrive_expect_tx(full, L::kTile);
-                for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(smem + off + h * kHalf, map, 64 * h, head, c0 + c * kChunk, full);
-            };
-            int ks = 0, vs = 0, qs = 0;  // copies issued
-            for (int c = 0; c < chunks && ok; ++c) {
+            int ks = 0, vs = 0;  // copies issued
+            for (int c = 0; c < chunks; ++c) {
                 if (c >= 2) ok = mbar_wait(&bars->k_empty[c & 1], ((c >> 1) & 1) ^ 1);
                 if (!ok) break;
-                load(L::kOffK + (c & 1) * L::kTile, &tm_k, kvh, c, &bars->k_full[c & 1]);
+                load(L::kOffK, &tm_k, c, &bars->k_full[c & 1]);
                 ++ks;
-                for (int h = 0; h < g && ok; ++h) {
-                    const int i = c * g + h;
-                    if (i >= 2) ok = mbar_wait(&bars->q_empty[i & 1], ((i >> 1) & 1) ^ 1);
-                    if (!ok) break;
-                    load(L::kOffQ + (i & 1) * L::kTile, &tm_q, kvh * g + h, c, &bars->q_full[i & 1]);
-                    ++qs;
-                    if (h == 0) {
-                        if (c >= 1) ok = mbar_wait(&bars->v_empty, (c & 1) ^ 1);
-                        if (!ok) break;
-                        load(L::kOffV, &tm_v, kvh, c, &bars->v_full);
-                        ++vs;
-                    }
-                }
+                if (c >= 2) ok = mbar_wait(&bars->v_empty[c & 1], ((c >> 1) & 1) ^ 1);
+                if (!ok) break;
+                load(L::kOffV, &tm_v, c, &bars->v_full[c & 1]);
+                ++vs;
             }
             // before the CTA may leave: every copy issued here has landed
             for (int i = max(0, ks - 2); i < ks; ++i)
                 if (!mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1)) ok = false;
-            for (int i = max(0, qs - 2); i < qs; ++i)
-                if (!mbar_wait(&bars->q_full[i & 1], (i >> 1) & 1)) ok = false;
-            if (vs && !mbar_wait(&bars->v_full, (vs - 1) & 1)) ok = false;
+            for (int i = max(0, vs - 2); i < vs; ++i)
+                if (!mbar_wait(&bars->v_full[i & 1], (i >> 1) & 1)) ok = false;
+        } else if (lane == 0) {
+            prefetch_tensormap(&tm_q);
+            int qs = 0;
+            for (int c = 0; c < chunks && ok; ++c) {
+                for (int h = 0; h < g; ++h) {
+                    if (qs > 0) ok = mbar_wait(&bars->q_empty, (qs & 1) ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars->q_full, L::kTile);
+                    tma_load_rows(smem + L::kOffQ, &tm_q, kvh * g + h, c0 + c * kChunk, 0, &bars->q_full);
+                    ++qs;
+                }
+            }
+            if (qs && !mbar_wait(&bars->q_full, (qs - 1) & 1)) ok = false;
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
         constexpr uint32_t idesc_s = tc_idesc_bf16(kChunk, kChunk, false);
         constexpr uint32_t idesc_o = tc_idesc_bf16(kChunk, D, true);
         constexpr uint32_t idesc_u = tc_idesc_bf16(kChunk, D, true) | (1u << 15);  // A MN-major too
-        const uint64_t qd0 = smem_desc_sw128(smem_u32(smem + L::kOffQ), 0, 1024);
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + L::kOffQ), 0, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), 0, 1024);
-        const uint64_t vd = smem_desc_sw128(smem_u32(smem + L::kOffV), kHalf, 1024);
+        const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kOffV), kHalf, 1024);
         const uint64_t sd = smem_desc_sw128(smem_u32(smem + L::kOffS), D * 128, 1024);
         // K~^T as A: at d = 64 its rows 64 .. 127 are whatever lies behind the tile, in lanes that nobody reads
         const uint64_t hd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), kHalf, 1024);
         const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
         for (int c = 0; c < chunks && ok; ++c) {
-            const uint64_t kslot = (uint64_t)(((c & 1) * L::kTile) >> 4);
+            const uint64_t kslot = (uint64_t)(((c & 1) * L::kTile) >> 4), vd = vd0 + kslot;
             ok = mbar_wait_warp(&bars->k_full[c & 1], (c >> 1) & 1);
             for (int h = 0; h < g && ok; ++h) {
                 const int i = c * g + h;
-                const uint64_t qslot = (uint64_t)(((i & 1) * L::kTile) >> 4);
-                ok = mbar_wait_warp(&bars->q_full[i & 1], (i >> 1) & 1);
+                ok = mbar_wait_warp(&bars->q_full, i & 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                    tc_mma_ew(tmem + L::kColP, qd0 + qslot + off, kd0 + kslot + off, idesc_s, kk > 0 ? 1u : 0u);
+                    tc_mma_ew(tmem + L::kColP, qd + off, kd0 + kslot + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 tc_commit_ew(&bars->s_full);
                 if (h == g - 1) tc_commit_ew(&bars->k_raw);
@@ -227,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_ew(tmem + L::kColO2, qd0 + qslot + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                    tc_mma_ew(tmem + L::kColO2, qd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
                               sd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
-                tc_commit_ew(&bars->q_empty[i & 1]);
-                if (h == 0) ok = mbar_wait_warp(&bars->v_clean, c & 1);
+                tc_commit_ew(&bars->q_empty);
+                if (h == 0) ok = mbar_wait_warp(&bars->v_clean[c & 1], (c >> 1) & 1);
                 if (ok) ok = mbar_wait_warp(&bars->p_full, i & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -251,68 +267,72 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             }
             tc_commit_ew(&bars->u_full);
             tc_commit_ew(&bars->k_empty[c & 1]);
-            tc_commit_ew(&bars->v_empty);
+            tc_commit_ew(&bars->v_empty[c & 1]);
         }
         // every MMA this warp issued has finished before the tensor memory is released
         tc_commit_ew(&bars->drain);
         if (!mbar_wait_warp(&bars->drain, 0)) ok = false;
-    } else if (warp >= 8) {
-        // ---------------------------------------------------------------- V looked over, K weighted: row r of the chunk
+    } else if (warp >= kCleanWarp) {
+        // ---------------------------------------------------------------- V looked over
         for (int c = 0; c < chunks && ok; ++c) {
             const int n = min(kChunk, len - c * kChunk);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full, c & 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[c & 1], (c >> 1) & 1));
             if (!ok) break;
-            uint8_t* vt = smem + L::kOffV + r * 128;
-            bool dirty = false;
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) {
-                uint4* at = reinterpret_cast<uint4*>(vt + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4));
-                const uint4 x = *at;
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                bool found = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    found |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-                if (found) {
+            uint8_t* tile = smem + L::kOffV + (c & 1) * L::kTile;
+            // a pass that only reads (its loads run ahead), and only where something was found the repair
+            uint32_t seen = 0;
+#pragma unroll 16
+            for (int i = lane; i < L::kTile / 16; i += 32) seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
+            if (seen) {
+                for (int i = lane; i < L::kTile / 16; i += 32) {
+                    uint4* at = reinterpret_cast<uint4*>(tile + 16 * i);
+                    if (!not_finite(*at)) continue;
+                    const int half = i / (kHalf / 16), row = i / 8 % kChunk, col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t v = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-                        if ((v & 0x7f80u) != 0x7f80u) continue;
-                        if (r < n) {
-                            atomicMin(&bad[i * 8 + e], c * kChunk + r);
+                        uint16_t* x = reinterpret_cast<uint16_t*>(at) + e;
+                        if ((*x & 0x7f80u) != 0x7f80u) continue;
+                        if (row < n) {
+                            atomicMin(&bad[col + e], c * kChunk + row);
                             bars->any_bad = 1;
                         }
-                        w[e / 2] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                        *x = 0;
                     }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                    dirty = true;
                 }
+                fence_proxy_async_smem();
             }
-            if (dirty) fence_proxy_async_smem();
-            mbar_arrive(&bars->v_clean);
+            mbar_arrive(&bars->v_clean[c & 1]);
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- K weighted: row r of the chunk
+        for (int c = 0; c < chunks && ok; ++c) {
+            const int n = min(kChunk, len - c * kChunk);
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, c & 1));
             if (!ok) break;
             // k_raw also means that the products with the low parts of the chunk before are done
-            const float w = fast_exp2((float)(n - 1 - r) * la);
+            const float w = r < n ? fast_exp2((float)(n - 1 - r) * la) : 0.f;
             uint8_t* hi = smem + L::kOffK + (c & 1) * L::kTile + r * 128;
             uint8_t* lo = smem + L::kOffLo + r * 128;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const int off = (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4);
-                uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-                if (r < n) {  // rows past the sequence's end are not its own: zero
-                    x = *reinterpret_cast<const uint4*>(hi + off);
-                    uint32_t in[4] = {x.x, x.y, x.z, x.w}, h2[4], l2[4];
+#pragma unroll
+            for (int hh = 0; hh < L::kHalves; ++hh) {
+                uint4 in[8];  // the loads of a half in flight together
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    in[i] = *reinterpret_cast<const uint4*>(hi + hh * kHalf + ((i ^ (r & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int off = hh * kHalf + ((i ^ (r & 7)) << 4);
+                    uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, lw[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float f0 = bf16_lo(in[e]) * w, f1 = bf16_hi(in[e]) * w;
-                        h2[e] = pack_bf16x2(f0, f1);
-                        l2[e] = pack_bf16x2(f0 - bf16_lo(h2[e]), f1 - bf16_hi(h2[e]));
+                        // rows past the sequence's end are not its own: zero
+                        float f0 = r < n ? bf16_lo(x[e]) : 0.f, f1 = r < n ? bf16_hi(x[e]) : 0.f;
+                        mul_x2(f0, f1, f0, f1, w, w);
+                        x[e] = pack_bf16x2(f0, f1);
+                        lw[e] = pack_bf16x2(f0 - bf16_lo(x[e]), f1 - bf16_hi(x[e]));
                     }
-                    x = make_uint4(h2[0], h2[1], h2[2], h2[3]);
-                    y = make_uint4(l2[0], l2[1], l2[2], l2[3]);
+                    *reinterpret_cast<uint4*>(hi + off) = make_uint4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<uint4*>(lo + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
                 }
-                *reinterpret_cast<uint4*>(hi + off) = x;
-                *reinterpret_cast<uint4*>(lo + off) = y;
             }
             fence_proxy_async_smem();
             mbar_arrive(&bars->kt_full);
@@ -387,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     } else {
         // ---------------------------------------------------------------- P and the outputs: row r of the chunk
         const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const float lead = fast_exp2((float)(r + 1) * la) * a.scale;
+        const float lead = fast_exp2((float)(r + 1) * la) * a.scale, row = (float)r;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         for (int i = 0; i < chunks * g && ok; ++i) {
             const int c = i / g, h = i - c * g;
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, i & 1));
@@ -403,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     // P goes over the first half of the scores: column x / 2 has been read
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float d0 = (float)(r - x - e), d1 = (float)(r - x - e - 1);  // rows between j and i
+                        const float d0 = row - (float)(x + e), d1 = row - (float)(x + e + 1);  // rows between j and i
                         float y0, y1;
                         mul_x2(y0, y1, d0, d1, la, la);
                         mul_x2(y0, y1, fast_exp2(y0), fast_exp2(y1), __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
@@ -441,10 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                         if (t >= bad[x + e]) o[e] = __uint_as_float(0x7fffffffu);
                 if (t < len) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(dst + x + e) =
-                            make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                       pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                    for (int e = 0; e < 32; e += 16) store16(dst + x + e, o + e, wide);
                 }
             }
             tc_fence_before();
@@ -473,9 +491,9 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
     t.group = p.num_heads / p.num_kv_heads;
     t.scale = p.scale;
     CUtensorMap q, k, v;
-    if (!strided_map(&q, p.q, p.num_tokens, p.num_heads, D, p.q_stride, 1, kChunk) ||
-        !strided_map(&k, p.k, p.num_tokens, p.num_kv_heads, D, p.k_stride, 1, kChunk) ||
-        !strided_map(&v, p.v, p.num_tokens, p.num_kv_heads, D, p.v_stride, 1, kChunk))
+    if (!strided_map(&q, p.q, p.num_tokens, p.num_heads, D, p.q_stride, 1, kChunk, Layout<D>::kHalves) ||
+        !strided_map(&k, p.k, p.num_tokens, p.num_kv_heads, D, p.k_stride, 1, kChunk, Layout<D>::kHalves) ||
+        !strided_map(&v, p.v, p.num_tokens, p.num_kv_heads, D, p.v_stride, 1, kChunk, Layout<D>::kHalves))
         return cudaErrorInvalidValue;
     const long long ctas = (long long)p.batch * p.num_kv_heads;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -335,14 +335,14 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
             auto load_q = [&](int t) {
                 mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
+                // a copy a half: those of a box with fewer than 128 rows would lie closer than kHalf
                 for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, 64 * h, head0, c0 + tok0 + t * a.tpt,
-                                &bars->q_full[t]);
+                    tma_load_rows(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, head0, c0 + tok0 + t * a.tpt, h,
+                                  &bars->q_full[t]);
             };
             auto load = [&](int off, const CUtensorMap* map, int j, uint64_t* full) {
                 mbar_arrive_expect_tx(full, L::kTile);
-                for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_3d(smem + off + h * kHalf, map, 64 * h, kvh, c0 + j * kKeys, full);
+                tma_load_rows(smem + off, map, kvh, c0 + j * kKeys, 0, full);
             };
             prefetch_tensormap(&tm_q);
             prefetch_tensormap(&tm_k);
@@ -448,30 +448,26 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
                 continue;
             }
             uint8_t* tile = smem + L::kOffV + vs * L::kTile;
-            bool dirty = false;
+            // a pass that only reads (its loads run ahead), and only where something was found the repair
+            uint32_t seen = 0;
 #pragma unroll 8
-            for (int i = i0; i < L::kTile / 16; i += 64) {
-                uint4 x = *reinterpret_cast<const uint4*>(tile + 16 * i);
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                bool found = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    found |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-                if (found) {
-                    const int half = i / (kHalf / 16), row = i / 8 % kRows, chunk = (i & 7) ^ (row & 7);
+            for (int i = i0; i < L::kTile / 16; i += 64) seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
+            if (seen) {
+                for (int i = i0; i < L::kTile / 16; i += 64) {
+                    uint4* at = reinterpret_cast<uint4*>(tile + 16 * i);
+                    if (!not_finite(*at)) continue;
+                    const int half = i / (kHalf / 16), row = i / 8 % kRows, col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t v = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-                        if ((v & 0x7f80u) != 0x7f80u) continue;
-                        const int what = (v & 0x7fu) ? 0 : (v & 0x8000u) ? 2 : 1;
-                        atomicMin(&bad[what * D + half * 64 + chunk * 8 + e], j * kKeys + row);
-                        w[e / 2] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+                        uint16_t* x = reinterpret_cast<uint16_t*>(at) + e;
+                        if ((*x & 0x7f80u) != 0x7f80u) continue;
+                        const int what = (*x & 0x7fu) ? 0 : (*x & 0x8000u) ? 2 : 1;
+                        atomicMin(&bad[what * D + col + e], j * kKeys + row);
+                        *x = 0;
                     }
-                    *reinterpret_cast<uint4*>(tile + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    bars->any_bad = 1;
-                    dirty = true;
                 }
+                bars->any_bad = 1;
+                fence_proxy_async_smem();
             }
-            if (dirty) fence_proxy_async_smem();
             mbar_arrive(&bars->v_clean[vs]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
@@ -549,6 +545,7 @@ int tile_heads(int group) {
 
 template <int D>
 cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
+    using L = Layout<D>;
     static OncePerDevice configured;
     const cudaError_t e = configured.run([] {
         return cudaFuncSetAttribute(packed_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
@@ -563,10 +560,10 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
     t.scale_log2 = a.scale * kLog2e;
     t.split_all = std::fabs(a.scale) * std::sqrt((float)D) > kSplitScale;
     CUtensorMap q, k, v, out;
-    if (!strided_map(&q, a.q, a.num_tokens, a.num_heads, D, a.q_stride, t.th, t.tpt) ||
-        !strided_map(&k, a.k, a.num_tokens, a.num_kv_heads, D, a.k_stride, 1, kKeys) ||
-        !strided_map(&v, a.v, a.num_tokens, a.num_kv_heads, D, a.v_stride, 1, kKeys) ||
-        !strided_map(&out, a.out, a.num_tokens, a.num_heads, D, (long long)a.num_heads * D, t.th, t.tpt))
+    if (!strided_map(&q, a.q, a.num_tokens, a.num_heads, D, a.q_stride, t.th, t.tpt, 1) ||
+        !strided_map(&k, a.k, a.num_tokens, a.num_kv_heads, D, a.k_stride, 1, kKeys, L::kHalves) ||
+        !strided_map(&v, a.v, a.num_tokens, a.num_kv_heads, D, a.v_stride, 1, kKeys, L::kHalves) ||
+        !strided_map(&out, a.out, a.num_tokens, a.num_heads, D, (long long)a.num_heads * D, t.th, t.tpt, 1))
         return cudaErrorInvalidValue;
     const long long ctas = (long long)t.pairs * a.batch * t.subs;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
