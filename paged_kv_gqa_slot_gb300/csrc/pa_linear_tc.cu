@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             uint8_t* tile = smem + L::kOffV + (c & 1) * L::kTile;
             // a pass that only reads (its loads run ahead), and only where something was found the repair
             uint32_t seen = 0;
-#pragma unroll 16
+#pragma unroll 8
             for (int i = lane; i < L::kTile / 16; i += 32) seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
             if (seen) {
                 for (int i = lane; i < L::kTile / 16; i += 32) {
@@ -312,15 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             const float w = r < n ? fast_exp2((float)(n - 1 - r) * la) : 0.f;
             uint8_t* hi = smem + L::kOffK + (c & 1) * L::kTile + r * 128;
             uint8_t* lo = smem + L::kOffLo + r * 128;
+#pragma unroll 1
+            for (int i0 = 0; i0 < D / 8; i0 += 4) {
+                uint4 in[4];  // four loads in flight together
+                const int base = (i0 >> 3) * kHalf;
 #pragma unroll
-            for (int hh = 0; hh < L::kHalves; ++hh) {
-                uint4 in[8];  // the loads of a half in flight together
+                for (int i = 0; i < 4; ++i)
+                    in[i] = *reinterpret_cast<const uint4*>(hi + base + ((((i0 & 7) + i) ^ (r & 7)) << 4));
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    in[i] = *reinterpret_cast<const uint4*>(hi + hh * kHalf + ((i ^ (r & 7)) << 4));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int off = hh * kHalf + ((i ^ (r & 7)) << 4);
+                for (int i = 0; i < 4; ++i) {
+                    const int off = base + ((((i0 & 7) + i) ^ (r & 7)) << 4);
                     uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, lw[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (c > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, (c - 1) & 1));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t u[32];
                 if (c > 0) {
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         if (ok) {
             tc_fence_after();
             const bool any_bad = bars->any_bad != 0;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t u[32];
                 tmem_ld32(tm_u + x, u);
@@ -414,17 +415,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, i & 1));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
+            // (loops over column blocks are not unrolled: the roles run at the same time, and their code has to
+            // fit the instruction cache together; unrolled, a chunk took 8500 cycles instead of NNNN)
+#pragma unroll 1
             for (int x = 0; x < kChunk; x += 32) {
                 // (a warp's rows are r & ~31 .. + 31: to the right of the diagonal there are zeros)
                 uint32_t w[16];
                 if (x <= (r | 31)) {
+                    const float base = row - (float)x;
                     uint32_t s[32];
                     tmem_ld32(tm + L::kColP + x, s);
                     // P goes over the first half of the scores: column x / 2 has been read
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float d0 = row - (float)(x + e), d1 = row - (float)(x + e + 1);  // rows between j and i
+                        const float d0 = base - (float)e, d1 = base - (float)(e + 1);  // rows between j and i
                         float y0, y1;
                         mul_x2(y0, y1, d0, d1, la, la);
                         mul_x2(y0, y1, fast_exp2(y0), fast_exp2(y1), __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             const int t = c * kChunk + r;
             const bool any_bad = bars->any_bad != 0;
             __nv_bfloat16* dst = p.out + ((size_t)(c0 + t) * p.num_heads + (size_t)kvh * g + h) * D;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t o1[32], o2[32];
                 tmem_ld32_async(tm + L::kColO1 + x, o1);
