@@ -128,7 +128,7 @@ int pa_linear_decode(float* state, int32_t num_slots, const int32_t* state_slots
     if (rc) return rc;
     LinearArgs a = {rows_of(q, k, v, batch, batch, num_heads, num_kv_heads, head_dim, q_stride, k_stride, v_stride,
                             scale, out),
-                    state, state_slots, log_decay, seq_lens, num_slots};
+                    state, state_slots, log_decay, seq_lens, num_slots, 1};
     a.rows.max_len = 1;
     a.rows.status = device_status_ptr();
     if (!a.rows.status) return PA_ERR_CUDA;
@@ -155,7 +155,7 @@ int pa_linear_prefill(float* state, int32_t num_slots, const int32_t* state_slot
     if (!array_ok(cu_q_lens, 4)) return PA_ERR_INVALID_ARG;
     LinearArgs a = {rows_of(q, k, v, batch, num_tokens, num_heads, num_kv_heads, head_dim, q_stride, k_stride,
                             v_stride, scale, out),
-                    state, state_slots, log_decay, seq_lens, num_slots};
+                    state, state_slots, log_decay, seq_lens, num_slots, max_chunk};
     a.rows.cu_lens = cu_q_lens;
     a.rows.max_len = max_chunk < num_tokens ? max_chunk : num_tokens;
     if (linear_workspace(batch, num_kv_heads, head_dim, max_chunk) > 0 && !array_ok(workspace, 16))

@@ -111,6 +111,7 @@ struct LinearArgs {
     const float* log_decay;     // [Hkv]
     const int32_t* seq_lens;    // [B]
     int num_slots;
+    int max_chunk;              // prefill: as given (rows.max_len is no longer than the rows there are)
 };
 
 // Arguments of pa_kv_grow and of pa_kv_free.
@@ -224,7 +225,9 @@ cudaError_t launch_prefill_packed(const PackedArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream);
 // chunks of 128 tokens on the tensor cores
-cudaError_t launch_linear_prefill_tc(const LinearArgs& a, cudaStream_t stream);
+cudaError_t launch_linear_prefill_tc(const LinearArgs& a, void* workspace, cudaStream_t stream);
+// segments that it cuts a sequence of up to max_chunk tokens into (at most; their states fill the workspace)
+int linear_segments(int batch, int num_kv_heads, int max_chunk);
 size_t linear_workspace(int batch, int num_kv_heads, int head_dim, int max_chunk);
 constexpr int kFreeMaxWidth = (1 << 22) - 1;  // row length of pa_kv_free: 512 rows count below 2^31
 constexpr int kEvictMaxBlocks = 49152;  // table width of an eviction: a word of shared memory each

@@ -174,10 +174,14 @@ cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream) {
     return a.rows.head_dim == 64 ? decode<64>(a, stream) : decode<128>(a, stream);
 }
 
-size_t linear_workspace(int, int, int, int) { return 0; }
+size_t linear_workspace(int batch, int num_kv_heads, int head_dim, int max_chunk) {
+    if (max_chunk <= kFewTokens) return 0;
+    return (size_t)(linear_segments(batch, num_kv_heads, max_chunk) - 1) * batch * num_kv_heads * head_dim * head_dim *
+           sizeof(float);
+}
 
-cudaError_t launch_linear_prefill(const LinearArgs& a, void*, cudaStream_t stream) {
-    if (a.rows.max_len > kFewTokens) return launch_linear_prefill_tc(a, stream);
+cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream) {
+    if (a.max_chunk > kFewTokens) return launch_linear_prefill_tc(a, workspace, stream);
     const dim3 grid(a.rows.num_kv_heads, a.rows.batch);
     return a.rows.head_dim == 64 ? launch(linear_step_kernel<64>, grid, 64, a, stream)
                                  : launch(linear_step_kernel<128>, grid, 128, a, stream);

@@ -8,8 +8,9 @@
 // that is four products on the tensor core: Q K^T, P V (P the weighted, masked scores), Q S and K~^T V
 // (K~ the weighted keys).  The powers enter as 2^{(i-j) log2 a} <= 1, so nothing overflows however
 // strong the decay.  A token moves (2 heads + 2 kv heads) d 2 bytes; per SM and 128 tokens of one head that is
-// 128 KB, about 5900 cycles of HBM time at d = 128, against about 2600 of tensor core: HBM bounds
-// it, as long as the chain of one chunk (Q K^T, K~, K~^T V, S) stays below.
+// 128 KB, about 5900 cycles of HBM time at d = 128, against 2600 of tensor core and 4400 of shared-memory
+// bandwidth (the operands of four products, the copies, K~ and S): HBM bounds it, as long as the chain of
+// one chunk (Q K^T, K~, K~^T V, S) stays below.
 //
 // S stays in tensor memory in fp32 (lane: row of k, column: column of v).  Each chunk it is read once,
 // written to shared memory as bf16 (the operand of Q S: one rounding, as the scores have) and back,
@@ -20,9 +21,18 @@
 // arrives, what is not finite becomes 0, and the first token it was seen at is noted per column; from
 // that row on the column is NaN, and so is the state's.
 //
-// One CTA a (sequence, kv head), one an SM.  Warps: 0-3 P and the outputs (one row a thread), 4-7 the
-// state (one row a thread), 8-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and V, 14 of Q (one thread
-// issues a copy in about half a microsecond), 15 the look at V.
+// Few sequences leave most SMs idle, so a long one is cut into segments: first every segment but the last
+// gathers what its own tokens add to the state (K~^T V alone, weighted to the segment's end), then one pass
+// over the states turns these into what each segment begins with, and then all segments run at once.  It
+// costs a second read of K and V.
+//
+// An item is one (segment, sequence, kv head).  A CTA, one an SM, takes item after item: near the end of
+// one it asks for a block of the grid that has not started (clusterlaunchcontrol), so that the
+// copies of the next item run under the end of this one.  Warps: 0-3 P and the outputs (one row a
+// thread), 4-7 the state (one row a thread), 8-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and
+// V, 14 of Q (one thread issues a copy in about half a microsecond), 15 the look at V, 16 the items.
+// The loops over column blocks are not unrolled and rare paths are short: the roles run at the same time, and
+// their code has to fit the instruction cache together (152 states x 1024 tokens took 52 us unrolled, 36 so).
 #include <algorithm>
 #include <climits>
 
@@ -33,46 +43,81 @@ namespace pa {
 namespace {
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12, kLoadWarp = 13, kQLoadWarp = 14, kCleanWarp = 15;
+constexpr int kThreads = 544;
+constexpr int kMmaWarp = 12, kLoadWarp = 13, kQLoadWarp = 14, kCleanWarp = 15, kItemWarp = 16;
 constexpr int kHalf = kChunk * 128;  // [128 rows][64 columns] bf16
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMinLogDecay = -1e4f;
+
+// One item: what its roles need.  chunks < 0: there is none, the CTA is done; 0: padding, zero rows.
+struct Item {
+    const float* begin;  // the state it begins with (null: zero)
+    float* end;          // where its last state goes (null: nowhere)
+    int row, len, chunks, kvh;
+    float la;            // log2 of the decay
+    int any_bad;         // a value of V was not finite
+};
 
 template <int D>
 struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kOffQ = 0;
+    static constexpr int kOffQ = 0;                    // (gather: a second tile of low parts)
     static constexpr int kOffK = kOffQ + kTile;        // two tiles; each becomes the high parts of K~ in place
     static constexpr int kOffLo = kOffK + 2 * kTile;   // the low parts
     static constexpr int kOffV = kOffLo + kTile;       // two tiles
     static constexpr int kOffS = kOffV + 2 * kTile;    // the state, bf16, D rows
     static constexpr int kOffBars = kOffS + D * 128 * kHalves;
-    static constexpr int kOffBad = kOffBars + 256;     // [D] first token of a column with a value that is not finite
-    static constexpr int kSmem = kOffBad + D * 4;
+    static constexpr int kOffItem = kOffBars + 384;    // two items
+    static constexpr int kOffTab = kOffItem + 128;     // [2][32] a^31 .. a^0
+    static constexpr int kOffBad = kOffTab + 256;      // [2][D] first token of a column with a value that is not finite
+    static constexpr int kSmem = kOffBad + 2 * D * 4;
     // tensor memory: scores and P, P V, Q S, the state
     static constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = kColO1 + D, kColU = kColO2 + D;
     static constexpr int kTmemCols = 512;
 };
 static_assert(Layout<128>::kSmem <= 227 * 1024, "shared memory");
+static_assert(sizeof(Item) <= 64, "item");
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
     uint64_t s_full, p_full, o_full, o_empty;  // scores, P, outputs ready; outputs read
     uint64_t k_raw;                            // Q K^T of the chunk is done: K may become K~
     uint64_t kt_full, st_full, u_full;         // K~ ready; the state ready for the chunk; K~^T V done
-    uint64_t drain;
+    uint64_t item_full[2], item_empty[2], soon, next, drain;
+    uint4 reply;                               // of clusterlaunchcontrol
     uint32_t tmem_base;
-    int any_bad;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 384, "barrier block");
 
 struct TcArgs {
     LinearArgs l;
-    int group;
+    float* segments;   // [batch][segs - 1][kv heads][D][D]: what a segment adds, then what the next begins with
+    int group, segs, seg_chunks;
     float scale;
 };
+
+// Sequence b's rows; len 0: nothing to do.
+struct Rows {
+    int row, len, slot;
+    bool fresh, bad;
+};
+__device__ __forceinline__ Rows rows_of(const LinearArgs& l, int b) {
+    const PackedArgs& p = l.rows;
+    const int c0 = p.cu_lens[b], c1 = p.cu_lens[b + 1], total = l.seq_lens[b];
+    Rows r;
+    r.slot = l.state_slots[b];
+    r.row = c0;
+    r.bad = c0 < 0 || c1 < c0 || c1 > p.num_tokens || total < c1 - c0;
+    r.len = r.bad ? 0 : min(c1 - c0, p.max_len);
+    r.fresh = total == c1 - c0;
+    r.bad |= r.len > 0 && (c1 - c0 > p.max_len || r.slot >= l.num_slots);
+    return r;
+}
+// log2 of a head's decay (a NaN is taken as the lower end)
+__device__ __forceinline__ float log2_decay(float log_decay) {
+    return fminf(fmaxf(log_decay, kMinLogDecay), 0.f) * kLog2e;
+}
 
 // d = (a0 * b0, a1 * b1), each rounded to nearest even
 __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
@@ -81,6 +126,8 @@ __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1,
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Sixteen values as bf16, in one 32-byte store (a whole sector a thread) where the address allows it.
 __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, bool wide) {
@@ -97,7 +144,54 @@ __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, bool
                  : "memory");
 }
 
-template <int D>
+// The items as one warp sees them, in order; next() waits for one and done() gives it back.
+struct Items {
+    Bars* bars;
+    uint8_t* slots;
+    int n = 0;
+    __device__ __forceinline__ Item* next(bool& ok) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[n & 1], (n >> 1) & 1));
+        Item* it = reinterpret_cast<Item*>(slots + (n & 1) * 64);
+        return ok && it->chunks >= 0 ? it : nullptr;
+    }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[n & 1]);
+        ++n;
+    }
+};
+
+// Take over a block of the grid that has not started; false: there is none left (it is not asked again then).
+__device__ __forceinline__ bool take_block(Bars* bars, uint32_t& phase, unsigned& id, bool& ok) {
+    if ((threadIdx.x & 31) == 0) {
+        fence_proxy_async_smem();  // the reply before has been read
+        mbar_arrive_expect_tx(&bars->next, 16);
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                         smem_u32(&bars->reply)),
+                     "r"(smem_u32(&bars->next))
+                     : "memory");
+    }
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, mbar_wait(&bars->next, phase));
+    phase ^= 1;
+    if (!ok) return false;
+    uint32_t got, x, y, z;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
+        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
+        : "r"(smem_u32(&bars->reply))
+        : "memory");
+    __syncwarp();
+    id = x;
+    return got != 0;
+}
+
+// kGather: only what the tokens of a segment add to the state (K~^T V), into a.segments.
+template <int D, bool kGather>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                              const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v,
@@ -105,45 +199,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBars);
-    int* bad = reinterpret_cast<int*>(smem + L::kOffBad);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const PackedArgs& p = a.l.rows;
-    const int kvh = (int)(blockIdx.x % (unsigned)p.num_kv_heads), b = (int)(blockIdx.x / (unsigned)p.num_kv_heads);
-    pdl_wait();
+    const int g = a.group;
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
         if (threadIdx.x == 0) atomicOr(p.status, kDevOutOfRange);
         return;
     }
-    const bool report = kvh == 0 && threadIdx.x == 0;
-    const int c0 = p.cu_lens[b], c1 = p.cu_lens[b + 1], total = a.l.seq_lens[b], slot = a.l.state_slots[b];
-    if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || total < c1 - c0) {
-        if (report) atomicOr(p.status, kDevOutOfRange);
-        return;
-    }
-    const int len = min(c1 - c0, p.max_len);
-    if (report && (c1 - c0 > p.max_len || (len > 0 && slot >= a.l.num_slots))) atomicOr(p.status, kDevOutOfRange);
-    if (len == 0) return;
-    const int g = a.group;
-    if (slot < 0 || slot >= a.l.num_slots) {  // padding: zero rows
-        const int per = g * D / 8;
-        for (long long i = threadIdx.x; i < (long long)len * per; i += kThreads)
-            *reinterpret_cast<uint4*>(p.out + ((size_t)(c0 + i / per) * p.num_heads + (size_t)kvh * g) * D + i % per * 8) =
-                make_uint4(0u, 0u, 0u, 0u);
-        return;
-    }
-    float* state = a.l.state + ((size_t)slot * p.num_kv_heads + kvh) * D * D;
-    const bool fresh = total == c1 - c0;
-    const int chunks = (len + kChunk - 1) / kChunk;
-    // log2 of the decay (a NaN is taken as the lower end)
-    const float la = fminf(fmaxf(a.l.log_decay[kvh], kMinLogDecay), 0.f) * kLog2e;
-
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kItemWarp * 32) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->k_empty[s], 1);
             mbar_init(&bars->v_full[s], 1);
             mbar_init(&bars->v_empty[s], 1);
             mbar_init(&bars->v_clean[s], 32);
+            mbar_init(&bars->item_full[s], 32);
+            mbar_init(&bars->item_empty[s], kItemWarp);  // every other warp
         }
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
@@ -155,11 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         mbar_init(&bars->kt_full, 128);
         mbar_init(&bars->st_full, 128);
         mbar_init(&bars->u_full, 1);
+        mbar_init(&bars->soon, 1);
+        mbar_init(&bars->next, 1);
         mbar_init(&bars->drain, 1);
-        bars->any_bad = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x < D) bad[threadIdx.x] = INT_MAX;
     if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, L::kTmemCols);
         tmem_relinquish();
@@ -168,47 +239,116 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
+    pdl_wait();
     bool ok = true;
+    Items items{bars, smem + L::kOffItem};
 
-    if (warp == kLoadWarp || warp == kQLoadWarp) {
-        // ---------------------------------------------------------------- TMA loads
-        if (lane == 0 && warp == kLoadWarp) {
-            auto load = [&](int off, const CUtensorMap* map, int c, uint64_t* full) {
-                mbar_arrive_expect_tx(full, L::kTile);
-                tma_load_rows(smem + off + (c & 1) * L::kTile, map, kvh, c0 + c * kChunk, 0, full);
-            };
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-            int ks = 0, vs = 0;  // copies issued
-            for (int c = 0; c < chunks; ++c) {
-                if (c >= 2) ok = mbar_wait(&bars->k_empty[c & 1], ((c >> 1) & 1) ^ 1);
-                if (!ok) break;
-                load(L::kOffK, &tm_k, c, &bars->k_full[c & 1]);
-                ++ks;
-                if (c >= 2) ok = mbar_wait(&bars->v_empty[c & 1], ((c >> 1) & 1) ^ 1);
-                if (!ok) break;
-                load(L::kOffV, &tm_v, c, &bars->v_full[c & 1]);
-                ++vs;
+    if (warp == kItemWarp) {
+        // ---------------------------------------------------------------- the items
+        // id = (segment * batch + b) * kv heads + kv head
+        unsigned id = blockIdx.x;
+        uint32_t phase = 0;
+        for (int n = 0; ok; ++n) {
+            bool there = true;
+            if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->soon, (n - 1) & 1));
+                if (ok && n > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
+                if (ok) there = take_block(bars, phase, id, ok);
             }
-            // before the CTA may leave: every copy issued here has landed
-            for (int i = max(0, ks - 2); i < ks; ++i)
-                if (!mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1)) ok = false;
-            for (int i = max(0, vs - 2); i < vs; ++i)
-                if (!mbar_wait(&bars->v_full[i & 1], (i >> 1) & 1)) ok = false;
-        } else if (lane == 0) {
-            prefetch_tensormap(&tm_q);
-            int qs = 0;
-            for (int c = 0; c < chunks && ok; ++c) {
-                for (int h = 0; h < g; ++h) {
-                    if (qs > 0) ok = mbar_wait(&bars->q_empty, (qs & 1) ^ 1);
+            Item it = {nullptr, nullptr, 0, 0, -1, 0, 0.f, 0};
+            while (ok && there) {
+                const int kvh = (int)(id % (unsigned)p.num_kv_heads), sb = (int)(id / (unsigned)p.num_kv_heads);
+                const int b = sb % p.batch, seg = sb / p.batch;
+                const Rows w = rows_of(a.l, b);
+                if (!kGather && w.bad && kvh == 0 && seg == 0 && lane == 0) atomicOr(p.status, kDevOutOfRange);
+                const int all = (w.len + kChunk - 1) / kChunk, first = seg * a.seg_chunks;
+                const bool pad = w.slot < 0 || w.slot >= a.l.num_slots;
+                const int chunks = min(a.seg_chunks, all - first);
+                const bool last = first + chunks >= all;
+                if (chunks > 0 && !(kGather && (last || pad))) {
+                    const size_t dd = (size_t)D * D;
+                    it.row = w.row + first * kChunk;
+                    it.len = min(w.len - first * kChunk, chunks * kChunk);
+                    it.chunks = pad ? 0 : chunks;
+                    it.kvh = kvh;
+                    it.la = log2_decay(a.l.log_decay[kvh]);
+                    if (!pad) {
+                        float* state = a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * dd;
+                        // what the segment adds, or what the one behind it begins with
+                        float* own = a.segments + (((size_t)b * (a.segs - 1) + seg) * p.num_kv_heads + kvh) * dd;
+                        if (kGather) {
+                            it.end = own;
+                        } else {
+                            it.begin = seg > 0 ? own - (size_t)p.num_kv_heads * dd : w.fresh ? nullptr : state;
+                            it.end = last ? state : nullptr;
+                            if (it.begin)
+                                for (int i = lane * 128; i < D * D * 4; i += 32 * 128)
+                                    prefetch_l2(reinterpret_cast<const char*>(it.begin) + i);
+                        }
+                    }
+                    break;
+                }
+                there = take_block(bars, phase, id, ok);
+            }
+            if (!ok) break;
+            if (lane == 0) *reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64) = it;
+            if (!kGather && there) {
+                reinterpret_cast<float*>(smem + L::kOffTab)[(n & 1) * 32 + lane] = fast_exp2((float)(31 - lane) * it.la);
+                for (int i = lane; i < D; i += 32) reinterpret_cast<int*>(smem + L::kOffBad)[(n & 1) * D + i] = INT_MAX;
+            }
+            __syncwarp();
+            mbar_arrive(&bars->item_full[n & 1]);
+            if (!there) break;
+        }
+    } else if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- TMA loads of K and V
+        int kc = 0, vc = 0;  // copies issued
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            if (lane == 0) {
+                const int row = it->row, kvh = it->kvh, chunks = it->chunks;
+                for (int c = 0; c < chunks && ok; ++c) {
+                    if (kc >= 2) ok = mbar_wait(&bars->k_empty[kc & 1], ((kc >> 1) & 1) ^ 1);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&bars->q_full, L::kTile);
-                    tma_load_rows(smem + L::kOffQ, &tm_q, kvh * g + h, c0 + c * kChunk, 0, &bars->q_full);
-                    ++qs;
+                    mbar_arrive_expect_tx(&bars->k_full[kc & 1], L::kTile);
+                    tma_load_rows(smem + L::kOffK + (kc & 1) * L::kTile, &tm_k, kvh, row + c * kChunk, 0,
+                                  &bars->k_full[kc & 1]);
+                    ++kc;
+                    if (vc >= 2) ok = mbar_wait(&bars->v_empty[vc & 1], ((vc >> 1) & 1) ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars->v_full[vc & 1], L::kTile);
+                    tma_load_rows(smem + L::kOffV + (vc & 1) * L::kTile, &tm_v, kvh, row + c * kChunk, 0,
+                                  &bars->v_full[vc & 1]);
+                    ++vc;
+                }
+                mbar_arrive(&bars->soon);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {  // before the CTA may leave: every copy issued here has landed
+            for (int i = max(0, kc - 2); i < kc; ++i)
+                if (!mbar_wait(&bars->k_full[i & 1], (i >> 1) & 1)) ok = false;
+            for (int i = max(0, vc - 2); i < vc; ++i)
+                if (!mbar_wait(&bars->v_full[i & 1], (i >> 1) & 1)) ok = false;
+        }
+    } else if (warp == kQLoadWarp) {
+        // ---------------------------------------------------------------- TMA loads of Q
+        int qc = 0;
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            if (!kGather && lane == 0) {
+                const int row = it->row, kvh = it->kvh, chunks = it->chunks;
+                for (int c = 0; c < chunks && ok; ++c) {
+                    for (int h = 0; h < g; ++h) {
+                        if (qc > 0) ok = mbar_wait(&bars->q_empty, (qc & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bars->q_full, L::kTile);
+                        tma_load_rows(smem + L::kOffQ, &tm_q, kvh * g + h, row + c * kChunk, 0, &bars->q_full);
+                        ++qc;
+                    }
                 }
             }
-            if (qs && !mbar_wait(&bars->q_full, (qs - 1) & 1)) ok = false;
+            __syncwarp();
         }
+        if (lane == 0 && qc && !mbar_wait(&bars->q_full, (qc - 1) & 1)) ok = false;
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
         constexpr uint32_t idesc_s = tc_idesc_bf16(kChunk, kChunk, false);
@@ -220,258 +360,337 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint64_t sd = smem_desc_sw128(smem_u32(smem + L::kOffS), D * 128, 1024);
         // K~^T as A: at d = 64 its rows 64 .. 127 are whatever lies behind the tile, in lanes that nobody reads
         const uint64_t hd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), kHalf, 1024);
-        const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
-        for (int c = 0; c < chunks && ok; ++c) {
-            const uint64_t kslot = (uint64_t)(((c & 1) * L::kTile) >> 4), vd = vd0 + kslot;
-            ok = mbar_wait_warp(&bars->k_full[c & 1], (c >> 1) & 1);
-            for (int h = 0; h < g && ok; ++h) {
-                const int i = c * g + h;
-                ok = mbar_wait_warp(&bars->q_full, i & 1);
-                if (!ok) break;
-                tc_fence_after();
+        const uint64_t ld0 = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
+        const uint64_t ld1 = kGather ? smem_desc_sw128(smem_u32(smem + L::kOffQ), kHalf, 1024) : ld0;
+        int cc = 0, ii = 0;  // chunks and chunks' heads so far
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            const int chunks = it->chunks;
+            for (int c = 0; c < chunks && ok; ++c, ++cc) {
+                const uint64_t slot = (uint64_t)(((cc & 1) * L::kTile) >> 4), vd = vd0 + slot;
+                if (!kGather) {
+                    ok = mbar_wait_warp(&bars->k_full[cc & 1], (cc >> 1) & 1);
+                    for (int h = 0; h < g && ok; ++h, ++ii) {
+                        ok = mbar_wait_warp(&bars->q_full, ii & 1);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                    tc_mma_ew(tmem + L::kColP, qd + off, kd0 + kslot + off, idesc_s, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                            tc_mma_ew(tmem + L::kColP, qd + off, kd0 + slot + off, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit_ew(&bars->s_full);
+                        if (h == g - 1) tc_commit_ew(&bars->k_raw);
+                        // Q S, once the state is in shared memory and the outputs before are read
+                        if (h == 0) ok = mbar_wait_warp(&bars->st_full, cc & 1);
+                        if (ok && ii > 0) ok = mbar_wait_warp(&bars->o_empty, (ii - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma_ew(tmem + L::kColO2, qd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                                      sd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
+                        tc_commit_ew(&bars->q_empty);
+                        if (h == 0) ok = mbar_wait_warp(&bars->v_clean[cc & 1], (cc >> 1) & 1);
+                        if (ok) ok = mbar_wait_warp(&bars->p_full, ii & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kChunk / 16; ++kk)
+                            tc_mma_ts_ew(tmem + L::kColO1, tmem + L::kColP + kk * 8,
+                                         vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
+                        tc_commit_ew(&bars->o_full);
+                    }
+                } else {
+                    if (c == 0) ok = mbar_wait_warp(&bars->st_full, items.n & 1);  // the item before has been read
+                    if (ok) ok = mbar_wait_warp(&bars->v_full[cc & 1], (cc >> 1) & 1);
                 }
-                tc_commit_ew(&bars->s_full);
-                if (h == g - 1) tc_commit_ew(&bars->k_raw);
-                // Q S, once the state is in shared memory and the outputs before are read
-                if (h == 0) ok = mbar_wait_warp(&bars->st_full, c & 1);
-                if (ok && i > 0) ok = mbar_wait_warp(&bars->o_empty, (i - 1) & 1);
+                if (ok) ok = mbar_wait_warp(&bars->kt_full, cc & 1);
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t lo = (cc & 1) ? ld1 : ld0;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_ew(tmem + L::kColO2, qd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
-                              sd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
-                tc_commit_ew(&bars->q_empty);
-                if (h == 0) ok = mbar_wait_warp(&bars->v_clean[c & 1], (c >> 1) & 1);
-                if (ok) ok = mbar_wait_warp(&bars->p_full, i & 1);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kChunk / 16; ++kk)
-                    tc_mma_ts_ew(tmem + L::kColO1, tmem + L::kColP + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                                 idesc_o, kk > 0 ? 1u : 0u);
-                tc_commit_ew(&bars->o_full);
+                for (int kk = 0; kk < kChunk / 16; ++kk) {
+                    const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
+                    tc_mma_ew(tmem + L::kColU, hd0 + slot + off, vd + off, idesc_u, !kGather || c > 0 || kk > 0 ? 1u : 0u);
+                    tc_mma_ew(tmem + L::kColU, lo + off, vd + off, idesc_u, 1u);
+                }
+                if (!kGather || c + 1 == chunks) tc_commit_ew(&bars->u_full);
+                tc_commit_ew(&bars->k_empty[cc & 1]);
+                tc_commit_ew(&bars->v_empty[cc & 1]);
             }
-            if (ok) ok = mbar_wait_warp(&bars->kt_full, c & 1);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kChunk / 16; ++kk) {
-                const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
-                tc_mma_ew(tmem + L::kColU, hd0 + kslot + off, vd + off, idesc_u, 1u);
-                tc_mma_ew(tmem + L::kColU, ld + off, vd + off, idesc_u, 1u);
-            }
-            tc_commit_ew(&bars->u_full);
-            tc_commit_ew(&bars->k_empty[c & 1]);
-            tc_commit_ew(&bars->v_empty[c & 1]);
         }
         // every MMA this warp issued has finished before the tensor memory is released
         tc_commit_ew(&bars->drain);
         if (!mbar_wait_warp(&bars->drain, 0)) ok = false;
-    } else if (warp >= kCleanWarp) {
+    } else if (warp == kCleanWarp) {
         // ---------------------------------------------------------------- V looked over
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int n = min(kChunk, len - c * kChunk);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[c & 1], (c >> 1) & 1));
-            if (!ok) break;
-            uint8_t* tile = smem + L::kOffV + (c & 1) * L::kTile;
-            // a pass that only reads (its loads run ahead), and only where something was found the repair
-            uint32_t seen = 0;
+        // (a segment that is gathered has no row of others, and its NaN belong into what it adds)
+        int cc = 0;
+        for (Item* it; (it = items.next(ok)); items.done()) {
+            const int chunks = kGather ? 0 : it->chunks, len = it->len;
+            int* bad = reinterpret_cast<int*>(smem + L::kOffBad) + (items.n & 1) * D;
+            for (int c = 0; c < chunks && ok; ++c, ++cc) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[cc & 1], (cc >> 1) & 1));
+                if (!ok) break;
+                uint8_t* tile = smem + L::kOffV + (cc & 1) * L::kTile;
+                // a pass that only reads (its loads run ahead), and only where something was found the repair
+                uint32_t seen = 0;
 #pragma unroll 8
-            for (int i = lane; i < L::kTile / 16; i += 32) seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
-            if (seen) {
-                for (int i = lane; i < L::kTile / 16; i += 32) {
-                    uint4* at = reinterpret_cast<uint4*>(tile + 16 * i);
-                    if (!not_finite(*at)) continue;
-                    const int half = i / (kHalf / 16), row = i / 8 % kChunk, col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
-                    for (int e = 0; e < 8; ++e) {
-                        uint16_t* x = reinterpret_cast<uint16_t*>(at) + e;
-                        if ((*x & 0x7f80u) != 0x7f80u) continue;
-                        if (row < n) {
-                            atomicMin(&bad[col + e], c * kChunk + row);
-                            bars->any_bad = 1;
+                for (int i = lane; i < L::kTile / 16; i += 32)
+                    seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
+                if (seen) {
+#pragma unroll 1
+                    for (int i = lane; i < L::kTile / 16; i += 32) {
+                        const int half = i / (kHalf / 16), row = i / 8 % kChunk;
+                        const int col = half * 64 + ((i & 7) ^ (row & 7)) * 8, t = c * kChunk + row;
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
+                            uint16_t* x = reinterpret_cast<uint16_t*>(tile + 16 * i) + e;
+                            if ((*x & 0x7f80u) != 0x7f80u) continue;
+                            if (t < len) {
+                                atomicMin(&bad[col + e], t);
+                                it->any_bad = 1;
+                            }
+                            *x = 0;
                         }
-                        *x = 0;
                     }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
+                mbar_arrive(&bars->v_clean[cc & 1]);
             }
-            mbar_arrive(&bars->v_clean[c & 1]);
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- K weighted: row r of the chunk
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int n = min(kChunk, len - c * kChunk);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, c & 1));
-            if (!ok) break;
-            // k_raw also means that the products with the low parts of the chunk before are done
-            const float w = r < n ? fast_exp2((float)(n - 1 - r) * la) : 0.f;
-            uint8_t* hi = smem + L::kOffK + (c & 1) * L::kTile + r * 128;
-            uint8_t* lo = smem + L::kOffLo + r * 128;
-#pragma unroll 1
-            for (int i0 = 0; i0 < D / 8; i0 += 4) {
-                uint4 in[4];  // four loads in flight together
-                const int base = (i0 >> 3) * kHalf;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    in[i] = *reinterpret_cast<const uint4*>(hi + base + ((((i0 & 7) + i) ^ (r & 7)) << 4));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int off = base + ((((i0 & 7) + i) ^ (r & 7)) << 4);
-                    uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, lw[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // rows past the sequence's end are not its own: zero
-                        float f0 = r < n ? bf16_lo(x[e]) : 0.f, f1 = r < n ? bf16_hi(x[e]) : 0.f;
-                        mul_x2(f0, f1, f0, f1, w, w);
-                        x[e] = pack_bf16x2(f0, f1);
-                        lw[e] = pack_bf16x2(f0 - bf16_lo(x[e]), f1 - bf16_hi(x[e]));
-                    }
-                    *reinterpret_cast<uint4*>(hi + off) = make_uint4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<uint4*>(lo + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        int cc = 0;
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            const int chunks = it->chunks, len = it->len;
+            const float la = it->la;
+            for (int c = 0; c < chunks && ok; ++c, ++cc) {
+                const int n = min(kChunk, len - c * kChunk);
+                if (!kGather) {  // (it also means that the products with the low parts of the chunk before are done)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, cc & 1));
+                } else {
+                    // (the tile was free to be loaded: the products of the chunk two before are done with the low parts)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
                 }
+                if (!ok) break;
+                // weighted to the end of the chunk, or of the segment
+                const int left = kGather ? len - c * kChunk : n;
+                const float w = r < n ? fast_exp2((float)(left - 1 - r) * la) : 0.f;
+                uint8_t* hi = smem + L::kOffK + (cc & 1) * L::kTile + r * 128;
+                uint8_t* lo = smem + (kGather && (cc & 1) ? L::kOffQ : L::kOffLo) + r * 128;
+#pragma unroll 1
+                for (int i0 = 0; i0 < D / 8; i0 += 4) {
+                    uint4 in[4];  // four loads in flight together
+                    const int base = (i0 >> 3) * kHalf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        in[i] = r < n ? *reinterpret_cast<const uint4*>(hi + base + ((((i0 & 7) + i) ^ (r & 7)) << 4))
+                                      : make_uint4(0u, 0u, 0u, 0u);  // rows past the sequence's end are not its own
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int off = base + ((((i0 & 7) + i) ^ (r & 7)) << 4);
+                        uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, lw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float f0, f1;
+                            mul_x2(f0, f1, bf16_lo(x[e]), bf16_hi(x[e]), w, w);
+                            x[e] = pack_bf16x2(f0, f1);
+                            lw[e] = pack_bf16x2(f0 - bf16_lo(x[e]), f1 - bf16_hi(x[e]));
+                        }
+                        *reinterpret_cast<uint4*>(hi + off) = make_uint4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<uint4*>(lo + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->kt_full);
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->kt_full);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- the state: row r of S
         const uint32_t tm_u = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::kColU;
         const bool mine = r < D;
         uint8_t* ss = smem + L::kOffS + r * 128;
-        for (int c = 0; c < chunks && ok; ++c) {
-            const int n = min(kChunk, len - c * kChunk);
-            const float f = fast_exp2((float)n * la);
-            if (c > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, (c - 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                uint32_t u[32];
-                if (c > 0) {
-                    tmem_ld32(tm_u + x, u);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const uint4 v = mine && !fresh ? *reinterpret_cast<const uint4*>(state + (size_t)r * D + x + e)
-                                                       : make_uint4(0u, 0u, 0u, 0u);
-                        u[e] = v.x;
-                        u[e + 1] = v.y;
-                        u[e + 2] = v.z;
-                        u[e + 3] = v.w;
-                    }
-                }
-                if (mine) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = pack_bf16x2(__uint_as_float(u[e + 2 * q]), __uint_as_float(u[e + 2 * q + 1]));
-                        const int chunk = (x + e) >> 3;
-                        *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-                tmem_st32_nowait(tm_u + x, u);
+        int uc = 0;  // completed K~^T V that this role has waited for
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            const int chunks = it->chunks, len = it->len;
+            const float la = it->la;
+            if (kGather) {
+                tc_fence_before();
+                mbar_arrive(&bars->st_full);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->st_full);
-        }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, (chunks - 1) & 1));
-        if (ok) {
+            for (int c = 0; c < (kGather ? 0 : chunks); ++c) {
+                const float f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
+                const float* from = it->begin;
+                if (c > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
+                    ++uc;
+                }
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t u[32];
+                    if (c > 0) {
+                        tmem_ld32(tm_u + x, u);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const uint4 v = mine && from ? *reinterpret_cast<const uint4*>(from + (size_t)r * D + x + e)
+                                                         : make_uint4(0u, 0u, 0u, 0u);
+                            u[e] = v.x;
+                            u[e + 1] = v.y;
+                            u[e + 2] = v.z;
+                            u[e + 3] = v.w;
+                        }
+                    }
+                    if (mine) {  // as bf16 for Q S, and back times a^n
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                w[q] = pack_bf16x2(__uint_as_float(u[e + 2 * q]), __uint_as_float(u[e + 2 * q + 1]));
+                            const int chunk = (x + e) >> 3;
+                            *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+                    tmem_st32_nowait(tm_u + x, u);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->st_full);
+            }
+            if (chunks == 0) continue;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
+            ++uc;
+            float* to = it->end;
+            if (!ok || !to) continue;
             tc_fence_after();
-            const bool any_bad = bars->any_bad != 0;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t u[32];
                 tmem_ld32(tm_u + x, u);
-                if (any_bad)
-                    for (int e = 0; e < 32; ++e)
-                        if (bad[x + e] < len) u[e] = 0x7fffffffu;
                 if (mine) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(state + (size_t)r * D + x + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                        *reinterpret_cast<uint4*>(to + (size_t)r * D + x + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
                 }
+            }
+            if (!kGather && it->any_bad && mine) {
+                const int* bad = reinterpret_cast<const int*>(smem + L::kOffBad) + (items.n & 1) * D;
+#pragma unroll 1
+                for (int x = 0; x < D; ++x)
+                    if (bad[x] < len) to[(size_t)r * D + x] = __uint_as_float(0x7fffffffu);
             }
         }
         tc_fence_before();
     } else {
         // ---------------------------------------------------------------- P and the outputs: row r of the chunk
         const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const float lead = fast_exp2((float)(r + 1) * la) * a.scale, row = (float)r;
+        const float row = (float)r;
         const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-        for (int i = 0; i < chunks * g && ok; ++i) {
-            const int c = i / g, h = i - c * g;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, i & 1));
-            if (!ok) break;
-            tc_fence_after();
-            // (loops over column blocks are not unrolled: the roles run at the same time, and their code has to
-            // fit the instruction cache together; unrolled, a chunk took 8500 cycles instead of NNNN)
+        int ii = 0;
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            if (kGather) continue;
+            const int chunks = it->chunks, len = it->len;
+            const float la = it->la;
+            __nv_bfloat16* out = p.out + ((size_t)it->row * p.num_heads + (size_t)it->kvh * g) * D;
+            if (chunks == 0) {  // padding: zero rows
+                const int per = g * D / 8;
 #pragma unroll 1
-            for (int x = 0; x < kChunk; x += 32) {
-                // (a warp's rows are r & ~31 .. + 31: to the right of the diagonal there are zeros)
-                uint32_t w[16];
-                if (x <= (r | 31)) {
-                    const float base = row - (float)x;
-                    uint32_t s[32];
-                    tmem_ld32(tm + L::kColP + x, s);
-                    // P goes over the first half of the scores: column x / 2 has been read
+                for (long long i = r; i < (long long)len * per; i += 128)
+                    *reinterpret_cast<uint4*>(out + (size_t)(i / per) * p.num_heads * D + i % per * 8) = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const float lead = fast_exp2((row + 1.f) * la) * a.scale;
+            const float* tab = reinterpret_cast<const float*>(smem + L::kOffTab) + (items.n & 1) * 32;
+            const int* bad = reinterpret_cast<const int*>(smem + L::kOffBad) + (items.n & 1) * D;
+            int c = 0, h = 0;
+            for (; c < chunks; ++ii) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, ii & 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < kChunk; x += 32) {
+                    // P goes over the first half of the scores: columns x / 2 .. x / 2 + 15 have been read
+                    uint32_t w[16];
+                    if (x < 32 * warp) {  // below the diagonal: a^{i-j} = a^{i-x-31} a^{31-(j-x)}
+                        const float f = fast_exp2((row - (float)(x + 31)) * la) * a.scale;
+                        uint32_t s[32];
+                        tmem_ld32(tm + L::kColP + x, s);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float d0 = base - (float)e, d1 = base - (float)(e + 1);  // rows between j and i
-                        float y0, y1;
-                        mul_x2(y0, y1, d0, d1, la, la);
-                        mul_x2(y0, y1, fast_exp2(y0), fast_exp2(y1), __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                        w[e / 2] = pack_bf16x2(d0 >= 0.f ? y0 : 0.f, d1 >= 0.f ? y1 : 0.f);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 t = *reinterpret_cast<const float4*>(tab + e);
+                            float y0, y1, y2, y3;
+                            mul_x2(y0, y1, t.x, t.y, f, f);
+                            mul_x2(y2, y3, t.z, t.w, f, f);
+                            mul_x2(y0, y1, y0, y1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                            mul_x2(y2, y3, y2, y3, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                            w[e / 2] = pack_bf16x2(y0, y1);
+                            w[e / 2 + 1] = pack_bf16x2(y2, y3);
+                        }
+                    } else if (x == 32 * warp) {  // on it: the powers one by one, as a^{-31} may overflow
+                        const float base = row - (float)x;
+                        uint32_t s[32];
+                        tmem_ld32(tm + L::kColP + x, s);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float d0 = base - (float)e, d1 = base - (float)(e + 1);  // rows between j and i
+                            float y0, y1;
+                            mul_x2(y0, y1, d0, d1, la, la);
+                            mul_x2(y0, y1, fast_exp2(y0), fast_exp2(y1), a.scale, a.scale);
+                            mul_x2(y0, y1, y0, y1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                            w[e / 2] = pack_bf16x2(d0 >= 0.f ? y0 : 0.f, d1 >= 0.f ? y1 : 0.f);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = 0u;
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = 0u;
+                    tmem_st8_nowait(tm + L::kColP + x / 2, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                    tmem_st8_nowait(tm + L::kColP + x / 2 + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
                 }
-                tmem_st8_nowait(tm + L::kColP + x / 2, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-                tmem_st8_nowait(tm + L::kColP + x / 2 + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars->p_full);
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full, i & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const int t = c * kChunk + r;
-            const bool any_bad = bars->any_bad != 0;
-            __nv_bfloat16* dst = p.out + ((size_t)(c0 + t) * p.num_heads + (size_t)kvh * g + h) * D;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars->p_full);
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full, ii & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int t = c * kChunk + r;
+                __nv_bfloat16* dst = out + ((size_t)t * p.num_heads + h) * D;
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o1[32], o2[32];
-                tmem_ld32_async(tm + L::kColO1 + x, o1);
-                tmem_ld32_async(tm + L::kColO2 + x, o2);
-                tmem_wait_ld(o1);
-                tmem_wait_ld(o2);
-                float o[32];
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o1[32], o2[32];
+                    tmem_ld32_async(tm + L::kColO1 + x, o1);
+                    tmem_ld32_async(tm + L::kColO2 + x, o2);
+                    tmem_wait_ld(o1);
+                    tmem_wait_ld(o2);
+                    float o[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    o[e] = fmaf(__uint_as_float(o2[e]), lead, __uint_as_float(o1[e]) * a.scale);
-                if (any_bad)
-                    for (int e = 0; e < 32; ++e)
-                        if (t >= bad[x + e]) o[e] = __uint_as_float(0x7fffffffu);
-                if (t < len) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 16) store16(dst + x + e, o + e, wide);
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(o2[e]), lead, __uint_as_float(o1[e]));
+                    if (t < len) {
+                        store16(dst + x, o, wide);
+                        store16(dst + x + 16, o + 16, wide);
+                    }
+                }
+                tc_fence_before();
+                if (it->any_bad && t < len) {
+#pragma unroll 1
+                    for (int x = 0; x < D; ++x)
+                        if (t >= bad[x]) dst[x] = __ushort_as_bfloat16(0x7fff);
+                }
+                mbar_arrive(&bars->o_empty);
+                if (++h == g) {
+                    h = 0;
+                    ++c;
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&bars->o_empty);
         }
+        tc_fence_before();
     }
     if (!ok && lane == 0) atomicOr(p.status, kDevTimeout);
     __syncthreads();
@@ -482,11 +701,69 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
 }
 
+// What each segment adds becomes what the next begins with: S <- a^(segment) S + what it adds, from the
+// state the sequence has.  Four elements a thread; the segments of a sequence one after another.
 template <int D>
-cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) linear_carry_kernel(const TcArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const PackedArgs& p = a.l.rows;
+    const int b = blockIdx.y, kvh = blockIdx.x / (D * D / 1024), at = blockIdx.x % (D * D / 1024) * 256 + threadIdx.x;
+    const Rows w = rows_of(a.l, b);
+    const int all = (w.len + kChunk - 1) / kChunk, n = (all + a.seg_chunks - 1) / a.seg_chunks - 1;
+    if (n <= 0 || w.slot < 0 || w.slot >= a.l.num_slots) return;
+    const float f = fast_exp2((float)(a.seg_chunks * kChunk) * log2_decay(a.l.log_decay[kvh]));
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!w.fresh) s = reinterpret_cast<const float4*>(a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * D * D)[at];
+    float4* seg = reinterpret_cast<float4*>(a.segments + ((size_t)b * (a.segs - 1) * p.num_kv_heads + kvh) * D * D) + at;
+    const size_t step = (size_t)p.num_kv_heads * D * D / 4;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        float4 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < n) x[i] = seg[(size_t)(i0 + i) * step];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i0 + i >= n) break;
+            s.x = fmaf(s.x, f, x[i].x);
+            s.y = fmaf(s.y, f, x[i].y);
+            s.z = fmaf(s.z, f, x[i].z);
+            s.w = fmaf(s.w, f, x[i].w);
+            seg[(size_t)(i0 + i) * step] = s;
+        }
+    }
+}
+
+// Segments a sequence: as many as make the waves of items end soonest, counting an item's start, its state
+// and what gathering costs as three chunks; one when the sequences and heads fill the GPU by themselves.
+int segments_of(int batch, int num_kv_heads, int max_chunk) {
+    const int sms = device_info().num_sms;
+    const long long pairs = (long long)batch * num_kv_heads;
+    const int chunks = (max_chunk - 1) / kChunk + 1;
+    if (pairs >= sms || chunks < 8) return 1;
+    int best = 1;
+    long long least = LLONG_MAX;
+    for (int n = 1; n <= 64 && n <= chunks / 2; ++n) {
+        const long long waves = (pairs * n + sms - 1) / sms;
+        const long long per = (chunks + n - 1) / n;
+        const long long cost = waves * (n == 1 ? 2 * per : 3 * per + 6);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
+}
+
+template <int D>
+cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     static OncePerDevice configured;
     const cudaError_t e = configured.run([] {
-        return cudaFuncSetAttribute(linear_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+        cudaError_t r = cudaSuccess;
+        for (const void* fn : {(const void*)linear_kernel<D, false>, (const void*)linear_kernel<D, true>})
+            if (r == cudaSuccess) r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+        return r;
     });
     if (e != cudaSuccess) return e;
     const PackedArgs& p = a.rows;
@@ -494,28 +771,46 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
     t.l = a;
     t.group = p.num_heads / p.num_kv_heads;
     t.scale = p.scale;
+    t.segments = static_cast<float*>(workspace);
+    const int chunks = (a.max_chunk - 1) / kChunk + 1;
+    const int segs = segments_of(p.batch, p.num_kv_heads, a.max_chunk);
+    t.seg_chunks = (chunks + segs - 1) / segs;
+    t.segs = (chunks + t.seg_chunks - 1) / t.seg_chunks;
     CUtensorMap q, k, v;
     if (!strided_map(&q, p.q, p.num_tokens, p.num_heads, D, p.q_stride, 1, kChunk, Layout<D>::kHalves) ||
         !strided_map(&k, p.k, p.num_tokens, p.num_kv_heads, D, p.k_stride, 1, kChunk, Layout<D>::kHalves) ||
         !strided_map(&v, p.v, p.num_tokens, p.num_kv_heads, D, p.v_stride, 1, kChunk, Layout<D>::kHalves))
         return cudaErrorInvalidValue;
-    const long long ctas = (long long)p.batch * p.num_kv_heads;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long pairs = (long long)p.batch * p.num_kv_heads;
+    if (pairs * t.segs > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Layout<D>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<D>, q, k, v, t);
+    if (t.segs > 1) {
+        cfg.gridDim = dim3((unsigned)(pairs * (t.segs - 1)));
+        cudaError_t r = cudaLaunchKernelEx(&cfg, linear_kernel<D, true>, q, k, v, t);
+        if (r != cudaSuccess) return r;
+        cudaLaunchConfig_t carry = cfg;
+        carry.gridDim = dim3(p.num_kv_heads * (D * D / 1024), p.batch);
+        carry.blockDim = dim3(256);
+        carry.dynamicSmemBytes = 0;
+        r = cudaLaunchKernelEx(&carry, linear_carry_kernel<D>, t);
+        if (r != cudaSuccess) return r;
+    }
+    cfg.gridDim = dim3((unsigned)(pairs * t.segs));
+    return cudaLaunchKernelEx(&cfg, linear_kernel<D, false>, q, k, v, t);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_prefill_tc(const LinearArgs& a, cudaStream_t stream) {
-    return a.rows.head_dim == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+int linear_segments(int batch, int num_kv_heads, int max_chunk) { return segments_of(batch, num_kv_heads, max_chunk); }
+
+cudaError_t launch_linear_prefill_tc(const LinearArgs& a, void* workspace, cudaStream_t stream) {
+    return a.rows.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
 }
 
 }  // namespace pa
