@@ -303,6 +303,48 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// Eight words (sixteen bf16) to global memory, in one 32-byte store, a whole sector, where the address allows it.
+__device__ __forceinline__ void store_32(void* dst, const uint32_t* w, bool wide) {
+    if (!wide) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// A warp takes over a block of the grid that has not started (clusterlaunchcontrol): its x coordinate in `id`.
+// False: there is none left, and it may not be asked again; or the wait ran out (ok false).  `reply` and `next`
+// (an mbarrier of count 1, its phase in `phase`) are shared memory of this use alone.
+__device__ __forceinline__ bool take_block(uint4* reply, uint64_t* next, uint32_t& phase, unsigned& id, bool& ok) {
+    if ((threadIdx.x & 31) == 0) {
+        fence_proxy_async_smem();  // the reply before has been read
+        mbar_arrive_expect_tx(next, 16);
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                         smem_u32(reply)),
+                     "r"(smem_u32(next))
+                     : "memory");
+    }
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, mbar_wait(next, phase));
+    phase ^= 1;
+    if (!ok) return false;
+    uint32_t got, x, y, z;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
+        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
+        : "r"(smem_u32(reply))
+        : "memory");
+    __syncwarp();
+    if (got) id = x;
+    return got != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05 (5th-gen tensor cores, TMEM)
 // TMEM addresses: bits 31..16 lane, bits 15..0 column (32-bit cells).
 

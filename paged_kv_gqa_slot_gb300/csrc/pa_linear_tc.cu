@@ -129,19 +129,12 @@ __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1,
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Sixteen values as bf16, in one 32-byte store (a whole sector a thread) where the address allows it.
+// Sixteen values as bf16.
 __device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, bool wide) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-    if (!wide) {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        return;
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+    store_32(dst, w, wide);
 }
 
 // The items as one warp sees them, in order; next() waits for one and done() gives it back.
@@ -161,34 +154,6 @@ struct Items {
         ++n;
     }
 };
-
-// Take over a block of the grid that has not started; false: there is none left (it is not asked again then).
-__device__ __forceinline__ bool take_block(Bars* bars, uint32_t& phase, unsigned& id, bool& ok) {
-    if ((threadIdx.x & 31) == 0) {
-        fence_proxy_async_smem();  // the reply before has been read
-        mbar_arrive_expect_tx(&bars->next, 16);
-        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                         smem_u32(&bars->reply)),
-                     "r"(smem_u32(&bars->next))
-                     : "memory");
-    }
-    __syncwarp();
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars->next, phase));
-    phase ^= 1;
-    if (!ok) return false;
-    uint32_t got, x, y, z;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%4];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
-        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
-        : "r"(smem_u32(&bars->reply))
-        : "memory");
-    __syncwarp();
-    id = x;
-    return got != 0;
-}
 
 // kGather: only what the tokens of a segment add to the state (K~^T V), into a.segments.
 template <int D, bool kGather>
@@ -253,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars->soon, (n - 1) & 1));
                 if (ok && n > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
-                if (ok) there = take_block(bars, phase, id, ok);
+                if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
             }
             Item it = {nullptr, nullptr, 0, 0, -1, 0, 0.f, 0};
             while (ok && there) {
@@ -288,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     }
                     break;
                 }
-                there = take_block(bars, phase, id, ok);
+                there = take_block(&bars->reply, &bars->next, phase, id, ok);
             }
             if (!ok) break;
             if (lane == 0) *reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64) = it;

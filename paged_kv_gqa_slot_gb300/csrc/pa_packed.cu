@@ -4,8 +4,9 @@
 //   o_i = sum_{j <= i} softmax_j(scale <q_i, k_j>) v_j   within each sequence
 //
 // A query tile is 128 rows of (token, head) pairs: th heads of one kv head's group, 128 / th tokens, so
-// the heads of a group share every K and V tile and the tile of a short prompt is well filled.  A
-// CTA, one an SM, holds two neighbouring tiles and walks the keys in stages of 128:
+// the heads of a group share every K and V tile and the tile of a short prompt is well filled.  An
+// item is two neighbouring tiles of one sequence and head group; a CTA, one an SM, walks its keys in stages
+// of 128:
 //   S_t = Q_t K^T     tcgen05.mma M = N = 128, both operands from shared memory, S_t in tensor memory
 //   softmax           one thread a row: P_t (bf16) over the first half of S_t
 //   O_t += P_t V      tcgen05.mma M = 128, N = d, P_t from tensor memory
@@ -14,6 +15,10 @@
 // d = 128 (two products of 128 x 128 x 128), which bounds the kernel at long prompts.  N = 128
 // matters: with both operands in shared memory, 64-key products are bound by its bandwidth.
 //
+// A CTA takes item after item: once the copies of one are on their way it asks for a block of the grid that has
+// not started (clusterlaunchcontrol), and the next item's Q, K and V arrive and its first scores are
+// computed under the end of the one before.  Items go sequence by sequence, each sequence's longest first.
+//
 // Base of the softmax: a stage is taken against the row's current base; only a row's first stage, or
 // one whose sum passes 2^16, takes the maximum, and O is rescaled where the maximum grew by more than
 // 2^8.  P is rounded to bf16 and the normaliser sums the rounded values, so their rounding moves
@@ -21,10 +26,11 @@
 // 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
 //
 // Masked keys have P = 0, and 0 times a NaN or an infinity in V is NaN.  So in the stages that hold a
-// key masked for some row, two warps look V over before its product: what is not finite is replaced
+// key masked for some row, a warp looks V over before its product: what is not finite is replaced
 // by 0, and the first token it was seen at noted per column; rows at or behind it get it back.
 //
-// Warps: 0-3 and 4-7 softmax of tiles 0 and 1, 8 MMA issue and tensor memory, 9 TMA loads, 10-11 V.
+// Warps: 0-3 and 4-7 softmax and outputs of tiles 0 and 1, 8 MMA issue and tensor memory, 9 TMA loads, 10
+// the look at V, 11 the items.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -37,7 +43,7 @@ namespace {
 
 constexpr int kRows = 128;              // rows of a query tile (MMA M)
 constexpr int kKeys = 128;              // keys a stage (MMA N of Q K^T)
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10, kItemWarp = 11;
 constexpr int kThreads = 384;
 constexpr int kHalf = kRows * 128;      // [128 rows][64 columns] bf16
 constexpr float kRescaleThreshold = 8.f;
@@ -55,39 +61,39 @@ struct Layout {
     static constexpr int kOffK = 2 * kTile;
     static constexpr int kOffV = kOffK + kKSlots * kTile;
     static constexpr int kOffBars = kOffV + kVSlots * kTile;
-    static constexpr int kOffBad = kOffBars + 256;     // [3][D] first token of a NaN, +inf, -inf in a column of V
+    static constexpr int kOffItem = kOffBars + 384;    // two items
+    static constexpr int kOffBad = kOffItem + 128;     // [3][D] first token of a NaN, +inf, -inf in a column of V
     static constexpr int kSmem = kOffBad + 3 * D * 4;
     static constexpr int kColsO = 2 * kKeys;           // tensor memory: S_0, S_1, O_0, O_1
     static constexpr int kTmemCols = 512;
 };
 static_assert(Layout<128>::kSmem <= 227 * 1024, "shared memory");
 
+// One item: two tiles of sequence rows [row, row + len), the first of them at token tok0.
+struct Item {
+    int row, len, tok0, head0, kvh;
+    int none;     // there is none: the CTA is done
+    int any_bad;  // a value of V in a stage with masked keys was not finite
+};
+static_assert(sizeof(Item) <= 64, "item");
+
 template <int D>
 struct Bars {
-    uint64_t q_full[2], k_full[Layout<D>::kKSlots], k_empty[Layout<D>::kKSlots], v_full[Layout<D>::kVSlots],
-        v_empty[Layout<D>::kVSlots], v_clean[Layout<D>::kVSlots], s_full[2], p_full[2], o_final[2], drain;
+    uint64_t q_full[2], q_empty[2], k_full[Layout<D>::kKSlots], k_empty[Layout<D>::kKSlots], v_full[Layout<D>::kVSlots],
+        v_empty[Layout<D>::kVSlots], v_clean[Layout<D>::kVSlots], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t item_full[2], item_empty[2], soon, next, drain;
+    uint4 reply;  // of clusterlaunchcontrol
     uint32_t tmem_base;
-    int any_bad;
 };
-static_assert(sizeof(Bars<64>) <= 256 && sizeof(Bars<128>) <= 256, "barrier block");
+static_assert(sizeof(Bars<64>) <= 384 && sizeof(Bars<128>) <= 384, "barrier block");
 
 struct TcArgs {
     PackedArgs p;
     int th, tpt;       // heads and tokens of a tile
     int subs;          // tiles' head groups: num_heads / th
-    int pairs;         // tile pairs the grid holds a sequence
     int split_all;
     float scale_log2;  // scale * log2(e), signed
 };
-
-__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 
 // (a0, a1) += the two bf16 values of a packed word, each widened exactly.
 __device__ __forceinline__ void add_bf16x2(float& a0, float& a1, uint32_t w) {
@@ -97,19 +103,14 @@ __device__ __forceinline__ void add_bf16x2(float& a0, float& a1, uint32_t w) {
         : "r"(w));
 }
 
-// The extreme visible score of a stage's quarter (32 keys, `lim` the last visible of them): the
-// largest, or with kNeg (a negative scale) minus the smallest.
-template <bool kAll, bool kNeg>
-__device__ __forceinline__ float quarter_max(const uint32_t (&s)[32], int lim) {
+// The largest visible sgn * score of a quarter of a stage (32 keys, `lim` the last visible of them).
+__device__ __forceinline__ float quarter_max(const uint32_t (&s)[32], int lim, float sgn) {
     float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
     for (int c = 0; c < 32; c += 4) {
         float a[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            a[e] = kNeg ? -__uint_as_float(s[c + e]) : __uint_as_float(s[c + e]);
-            if (!kAll) a[e] = c + e > lim ? -INFINITY : a[e];
-        }
+        for (int e = 0; e < 4; ++e) a[e] = c + e > lim ? -INFINITY : __uint_as_float(s[c + e]) * sgn;
         m0 = fmax3(m0, a[0], a[1]);
         m1 = fmax3(m1, a[2], a[3]);
     }
@@ -121,41 +122,29 @@ __device__ __forceinline__ float quarter_max(const uint32_t (&s)[32], int lim) {
 template <bool kAll, bool kSplit>
 __device__ __forceinline__ void quarter_p(const uint32_t (&s)[32], int lim, float sl, float nbase, uint32_t dst,
                                           float (&ls)[4]) {
-    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-        float x0, x1;
-        fma_x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl, sl, nbase, nbase);
-        if (!kAll) {
-            x0 = c > lim ? -INFINITY : x0;  // 2^-inf = 0
-            x1 = c + 1 > lim ? -INFINITY : x1;
-        }
-        w[c / 2] = pack_bf16x2(fast_exp2(x0), fast_exp2(x1));
-    }
+    for (int c0 = 0; c0 < 32; c0 += 16) {
+        uint32_t w[8], lo[8];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        add_bf16x2(ls[0], ls[1], w[i]);
-        add_bf16x2(ls[2], ls[3], w[i + 1]);
-    }
-    tmem_st16_nowait(dst, w);
-    if (kSplit) {
-        uint32_t lo[16];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
+        for (int i = 0; i < 8; ++i) {
+            const int c = c0 + 2 * i;
             float x0, x1;
             fma_x2(x0, x1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl, sl, nbase, nbase);
             if (!kAll) {
-                x0 = c > lim ? -INFINITY : x0;
+                x0 = c > lim ? -INFINITY : x0;  // 2^-inf = 0
                 x1 = c + 1 > lim ? -INFINITY : x1;
             }
-            lo[c / 2] = pack_bf16x2(fast_exp2(x0) - bf16_lo(w[c / 2]), fast_exp2(x1) - bf16_hi(w[c / 2]));
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            w[i] = pack_bf16x2(x0, x1);
+            add_bf16x2(ls[0], ls[1], w[i]);
+            if (kSplit) {
+                lo[i] = pack_bf16x2(x0 - bf16_lo(w[i]), x1 - bf16_hi(w[i]));
+                add_bf16x2(ls[2], ls[3], lo[i]);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            add_bf16x2(ls[0], ls[1], lo[i]);
-            add_bf16x2(ls[2], ls[3], lo[i + 1]);
-        }
-        tmem_st16_nowait(dst + 64, lo);
+        tmem_st8_nowait(dst + c0 / 2, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+        if (kSplit) tmem_st8_nowait(dst + 64 + c0 / 2, lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
     }
 }
 
@@ -168,16 +157,6 @@ __device__ __forceinline__ float stage_p(const uint32_t (&s0)[32], const uint32_
     quarter_p<kAll, kSplit>(s2, lim - 64, sl, nbase, dst + 32, ls);
     quarter_p<kAll, kSplit>(s3, lim - 96, sl, nbase, dst + 48, ls);
     return (ls[0] + ls[1]) + (ls[2] + ls[3]);
-}
-
-template <bool kNeg>
-__device__ __forceinline__ float stage_max(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const uint32_t (&s2)[32],
-                                           const uint32_t (&s3)[32], int lim, bool unmasked) {
-    if (unmasked)
-        return fmaxf(fmaxf(quarter_max<true, kNeg>(s0, lim), quarter_max<true, kNeg>(s1, lim)),
-                     fmaxf(quarter_max<true, kNeg>(s2, lim), quarter_max<true, kNeg>(s3, lim)));
-    return fmaxf(fmaxf(quarter_max<false, kNeg>(s0, lim), quarter_max<false, kNeg>(s1, lim - 32)),
-                 fmaxf(quarter_max<false, kNeg>(s2, lim - 64), quarter_max<false, kNeg>(s3, lim - 96)));
 }
 
 // O (the row's D fp32 columns of tensor memory at `taddr`) *= f.
@@ -194,14 +173,16 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float f) {
     tmem_wait_st();
 }
 
-// The softmax of one tile's rows, stage by stage; `pos` the row's own key.  Returns false when a
-// wait ran out.  tcgen05.ld / st are warp-collective, so every branch that leads to one is the warp's.
+// The softmax of one tile's rows, stage by stage (the first is number `sc` of the tile's); `pos` the row's own
+// key.  Returns false when a wait ran out.  tcgen05.ld / st are warp-collective, so every branch that leads to one
+// is the warp's.
 template <int D, bool kSplit>
-__device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int n, int pos, float sl, uint32_t tm_s,
+__device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n, int pos, float sl, uint32_t tm_s,
                                              uint32_t tm_o, float& l_out) {
     float m_used = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
-        if (__any_sync(0xffffffffu, !mbar_wait(&bars->s_full[t], j & 1))) return false;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j, ++sc) {
+        if (__any_sync(0xffffffffu, !mbar_wait(&bars->s_full[t], sc & 1))) return false;
         tc_fence_after();
         const int lim = pos - j * kKeys;
         const bool unmasked = __all_sync(0xffffffffu, lim >= kKeys - 1);
@@ -214,31 +195,33 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int n, int po
         tmem_wait_ld(s1);
         tmem_wait_ld(s2);
         tmem_wait_ld(s3);
-        float sum = 0.f;
-        bool full = __any_sync(0xffffffffu, m_used == -INFINITY && lim >= 0);
-        auto p = [&] {
-            const float nbase = m_used == -INFINITY ? 0.f : -m_used;
-            return unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s)
-                            : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s);
-        };
-        if (!full) {
-            sum = p();
-            full = __any_sync(0xffffffffu, !(sum <= kSpecSumLimit));
-        }
-        if (full) {
-            const float mx = sl < 0.f ? stage_max<true>(s0, s1, s2, s3, lim, unmasked)
-                                      : stage_max<false>(s0, s1, s2, s3, lim, unmasked);
-            const float mxs = mx == -INFINITY ? -INFINITY : mx * fabsf(sl);  // log2 units
-            const float m_new = fmaxf(m_used, mxs);
-            const bool rebase = m_new > m_used + kRescaleThreshold;  // always for the first visible key
-            // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
-            if (__any_sync(0xffffffffu, rebase && m_used != -INFINITY))
-                scale_o<D>(tm_o, rebase && m_used != -INFINITY ? fast_exp2(m_used - m_new) : 1.f);
-            if (rebase) {
-                l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - m_new);
-                m_used = m_new;
+        float sum;
+        // against the base there is, unless a row has none yet; once more with a new one if a sum says so
+        bool rebased = false, full = __any_sync(0xffffffffu, m_used == -INFINITY && lim >= 0);
+#pragma unroll 1
+        for (;;) {
+            if (full) {
+                const float sgn = sl < 0.f ? -1.f : 1.f;
+                const float mx = fmaxf(fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn)),
+                                       fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn)));
+                const float mxs = mx == -INFINITY ? -INFINITY : mx * fabsf(sl);  // log2 units
+                const float m_new = fmaxf(m_used, mxs);
+                const bool rebase = m_new > m_used + kRescaleThreshold;  // always for the first visible key
+                // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
+                if (__any_sync(0xffffffffu, rebase && m_used != -INFINITY))
+                    scale_o<D>(tm_o, rebase && m_used != -INFINITY ? fast_exp2(m_used - m_new) : 1.f);
+                if (rebase) {
+                    l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - m_new);
+                    m_used = m_new;
+                }
+                rebased = true;
             }
-            sum = p();
+            const float nbase = m_used == -INFINITY ? 0.f : -m_used;
+            sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s)
+                           : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s);
+            if (rebased) break;
+            full = __any_sync(0xffffffffu, !(sum <= kSpecSumLimit));
+            if (!full) break;
         }
         l += sum;
         tmem_wait_st();
@@ -249,76 +232,78 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int n, int po
     return true;
 }
 
-// The two-part form as a function of its own: its code stays out of the usual tile's way.
+// Tokens and key stages of an item's tiles.
+struct Tiles {
+    int ntok[2], n[2], nst, first_masked;
+    __device__ __forceinline__ Tiles(const Item* it, int tpt) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            ntok[t] = max(0, min(tpt, it->len - it->tok0 - t * tpt));
+            n[t] = ntok[t] > 0 ? (it->tok0 + t * tpt + ntok[t] + kKeys - 1) / kKeys : 0;
+        }
+        nst = max(n[0], n[1]);
+        first_masked = (it->tok0 + 1) / kKeys;  // stages before it are visible to every row
+    }
+};
+
+// The items as one warp sees them, in order; next() waits for one and done() gives it back.
 template <int D>
-__device__ __noinline__ bool softmax_rows_split(Bars<D>* bars, int t, int n, int pos, float sl, uint32_t tm_s,
-                                                uint32_t tm_o, float* l_out) {
-    return softmax_rows<D, true>(bars, t, n, pos, sl, tm_s, tm_o, *l_out);
-}
+struct Items {
+    Bars<D>* bars;
+    uint8_t* slots;
+    int n = 0;
+    __device__ __forceinline__ Item* next(bool& ok) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_full[n & 1], (n >> 1) & 1));
+        Item* it = reinterpret_cast<Item*>(slots + (n & 1) * 64);
+        return ok && !it->none ? it : nullptr;
+    }
+    __device__ __forceinline__ void done() {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[n & 1]);
+        ++n;
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                              const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v,
-                                                             const __grid_constant__ CUtensorMap tm_out,
                                                              const __grid_constant__ TcArgs a) {
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars<D>* bars = reinterpret_cast<Bars<D>*>(smem + L::kOffBars);
     int* bad = reinterpret_cast<int*>(smem + L::kOffBad);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // blockIdx.x = (rank * batch + b) * subs + sub: rank 0 holds every sequence's last (longest) pair
-    const int sub = (int)(blockIdx.x % (unsigned)a.subs);
-    const int rb = (int)(blockIdx.x / (unsigned)a.subs);
-    const int b = rb % a.p.batch, rank = rb / a.p.batch;
-    const int head0 = sub * a.th, kvh = head0 / (a.p.num_heads / a.p.num_kv_heads);
-    pdl_wait();
-    const bool report = rank == 0 && sub == 0 && threadIdx.x == 0;
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
         if (threadIdx.x == 0) atomicOr(a.p.status, kDevOutOfRange);
         return;
     }
-    const int c0 = a.p.cu_lens[b], c1 = a.p.cu_lens[b + 1];
-    if (c0 < 0 || c1 < c0 || c1 > a.p.num_tokens) {
-        if (report) atomicOr(a.p.status, kDevOutOfRange);
-        return;
-    }
-    if (c1 - c0 > a.p.max_len && report) atomicOr(a.p.status, kDevOutOfRange);
-    const int len = min(c1 - c0, a.p.max_len);
-    const int pairs = (len + 2 * a.tpt - 1) / (2 * a.tpt);
-    if (rank >= pairs) return;
-    const int tok0 = (pairs - 1 - rank) * 2 * a.tpt;  // first token of tile 0
-    int ntok[2], n[2];                                // tokens and stages of the two tiles
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        ntok[t] = max(0, min(a.tpt, len - tok0 - t * a.tpt));
-        n[t] = ntok[t] > 0 ? (tok0 + t * a.tpt + ntok[t] + kKeys - 1) / kKeys : 0;
-    }
-    const int nst = max(n[0], n[1]);
-    const int first_masked = (tok0 + 1) / kKeys;      // stages before it are visible to every row
-
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kItemWarp * 32) {
         for (int s = 0; s < L::kKSlots; ++s) {
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->k_empty[s], 1);
         }
         for (int s = 0; s < L::kVSlots; ++s) {
             mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->v_empty[s], 3);  // the products' commit, and the two warps that look V over
-            mbar_init(&bars->v_clean[s], 64);
+            mbar_init(&bars->v_empty[s], 2);  // the products' commit, and the warp that looks V over
+            mbar_init(&bars->v_clean[s], 32);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
+            mbar_init(&bars->q_empty[t], 1);
             mbar_init(&bars->s_full[t], 1);
             mbar_init(&bars->p_full[t], 128);
-            mbar_init(&bars->o_final[t], 1);
+            mbar_init(&bars->o_full[t], 1);
+            mbar_init(&bars->o_empty[t], 128);
+            mbar_init(&bars->item_full[t], 1);
+            mbar_init(&bars->item_empty[t], kItemWarp);  // every other warp
         }
+        mbar_init(&bars->soon, 1);
+        mbar_init(&bars->next, 1);
         mbar_init(&bars->drain, 1);
-        bars->any_bad = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x >= kCleanWarp * 32)
-        for (int i = threadIdx.x - kCleanWarp * 32; i < 3 * D; i += 64) bad[i] = INT_MAX;
     if (warp == kMmaWarp) {
         tmem_alloc(&bars->tmem_base, L::kTmemCols);
         tmem_relinquish();
@@ -327,48 +312,122 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
+    pdl_wait();
+    bool ok = true;
+    Items<D> items{bars, smem + L::kOffItem};
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- TMA loads, in the order of use
-        if (lane == 0) {
-            bool ok = true;
-            const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
-            auto load_q = [&](int t) {
-                mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
-                // a copy a half: those of a box with fewer than 128 rows would lie closer than kHalf
-                for (int h = 0; h < L::kHalves; ++h)
-                    tma_load_rows(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, head0, c0 + tok0 + t * a.tpt, h,
-                                  &bars->q_full[t]);
-            };
-            auto load = [&](int off, const CUtensorMap* map, int j, uint64_t* full) {
-                mbar_arrive_expect_tx(full, L::kTile);
-                tma_load_rows(smem + off, map, kvh, c0 + j * kKeys, 0, full);
-            };
-            prefetch_tensormap(&tm_q);
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-            if (n[0] > 0) load_q(0);
-            int k_issued = 0, v_issued = 0;
-            for (int j = 0; j < nst && ok; ++j) {
-                const int ks = j % L::kKSlots, vs = j % L::kVSlots;
-                if (j >= L::kKSlots) ok = mbar_wait(&bars->k_empty[ks], ((j / L::kKSlots) & 1) ^ 1);
-                if (!ok) break;
-                load(L::kOffK + ks * L::kTile, &tm_k, j, &bars->k_full[ks]);
-                ++k_issued;
-                if (j == 0 && n[1] > 0) load_q(1);
-                if (j >= L::kVSlots) ok = mbar_wait(&bars->v_empty[vs], ((j / L::kVSlots) & 1) ^ 1);
-                if (!ok) break;
-                load(L::kOffV + vs * L::kTile, &tm_v, j, &bars->v_full[vs]);
-                ++v_issued;
+    // registers: 256 softmax threads of 200 and 128 others of 96 are fewer than the 384 x 168 of the launch
+    if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp == kItemWarp) {
+        // ---------------------------------------------------------------- the items
+        // id = pair * subs + sub, the pairs of the sequences counted one after another; ids only rise, so the
+        // walk over the sequences (32 at a time, one a lane) goes on where it was
+        unsigned id = blockIdx.x;
+        uint32_t phase = 0;
+        int b0 = 0;
+        unsigned before = 0;  // pairs of the sequences before b0
+        auto look = [&](int b, int& row, int& len) {  // sequence b's rows and pairs
+            row = len = 0;
+            if (b >= a.p.batch) return 0u;
+            const int c0 = a.p.cu_lens[b], c1 = a.p.cu_lens[b + 1];
+            const bool off = c0 < 0 || c1 < c0 || c1 > a.p.num_tokens;
+            if (off || c1 - c0 > a.p.max_len) atomicOr(a.p.status, kDevOutOfRange);
+            row = c0;
+            len = off ? 0 : min(c1 - c0, a.p.max_len);
+            return (unsigned)((len + 2 * a.tpt - 1) / (2 * a.tpt));
+        };
+        auto sums = [&](unsigned x) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned up = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += up;
             }
-            // before the CTA may leave: every copy issued here has landed
-            for (int t = 0; t < 2; ++t)
-                if (n[t] > 0 && (t == 0 || k_issued > 0) && !mbar_wait(&bars->q_full[t], 0)) ok = false;
-            for (int j = max(0, k_issued - L::kKSlots); j < k_issued; ++j)
+            return x;
+        };
+        int row, len;
+        unsigned mine = look(lane, row, len), upto = sums(mine);
+        for (int n = 0; ok; ++n) {
+            bool there = true;
+            if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->soon, (n - 1) & 1));
+                if (ok && n > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
+                if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
+            }
+            if (!ok) break;
+            const unsigned pair = id / (unsigned)a.subs, sub = id % (unsigned)a.subs;
+            while (there && pair >= before + __shfl_sync(0xffffffffu, upto, 31)) {
+                before += __shfl_sync(0xffffffffu, upto, 31);
+                b0 += 32;
+                there = b0 < a.p.batch;  // past the last pair: there are no others
+                if (there) {
+                    mine = look(b0 + lane, row, len);
+                    upto = sums(mine);
+                }
+            }
+            Item* it = reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64);
+            if (there && pair >= before + upto - mine && pair < before + upto) {  // the sequence's own lane
+                it->row = row;
+                it->len = len;
+                // the longest pair of a sequence first
+                it->tok0 = (int)(before + upto - 1 - pair) * 2 * a.tpt;
+                it->head0 = (int)sub * a.th;
+                it->kvh = it->head0 / (a.p.num_heads / a.p.num_kv_heads);
+                it->none = 0;
+                it->any_bad = 0;
+            }
+            if (!there && lane == 0) it->none = 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->item_full[n & 1]);
+            if (!there) break;
+        }
+        // (sequences behind the last pair that anybody took are looked at for their offsets, too)
+        if (blockIdx.x == 0)
+            for (; b0 < a.p.batch; b0 += 32) look(b0 + lane, row, len);
+    } else if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- TMA loads, in the order of use
+        const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
+        int kc = 0, vc = 0, q0 = 0, q1 = 0;  // copies issued
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            if (lane == 0) {
+                const Tiles w(it, a.tpt);
+                const int base = it->row, tok0 = it->tok0, head0 = it->head0, kvh = it->kvh;
+                auto load_q = [&](int t, int& qc) {
+                    if (qc > 0 && ok) ok = mbar_wait(&bars->q_empty[t], (qc & 1) ^ 1);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
+                    // a copy a half: those of a box with fewer than 128 rows would lie closer than kHalf
+                    for (int h = 0; h < L::kHalves; ++h)
+                        tma_load_rows(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, head0, base + tok0 + t * a.tpt, h,
+                                      &bars->q_full[t]);
+                    ++qc;
+                };
+                load_q(0, q0);
+                for (int j = 0; j < w.nst && ok; ++j) {
+                    const int ks = kc % L::kKSlots, vs = vc % L::kVSlots;
+                    if (kc >= L::kKSlots) ok = mbar_wait(&bars->k_empty[ks], ((kc / L::kKSlots) & 1) ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars->k_full[ks], L::kTile);
+                    tma_load_rows(smem + L::kOffK + ks * L::kTile, &tm_k, kvh, base + j * kKeys, 0, &bars->k_full[ks]);
+                    ++kc;
+                    if (j == 0 && w.n[1] > 0) load_q(1, q1);
+                    if (ok && vc >= L::kVSlots) ok = mbar_wait(&bars->v_empty[vs], ((vc / L::kVSlots) & 1) ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars->v_full[vs], L::kTile);
+                    tma_load_rows(smem + L::kOffV + vs * L::kTile, &tm_v, kvh, base + j * kKeys, 0, &bars->v_full[vs]);
+                    ++vc;
+                }
+                mbar_arrive(&bars->soon);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) {  // before the CTA may leave: every copy issued here has landed
+            if (q0 && !mbar_wait(&bars->q_full[0], (q0 - 1) & 1)) ok = false;
+            if (q1 && !mbar_wait(&bars->q_full[1], (q1 - 1) & 1)) ok = false;
+            for (int j = max(0, kc - L::kKSlots); j < kc; ++j)
                 if (!mbar_wait(&bars->k_full[j % L::kKSlots], (j / L::kKSlots) & 1)) ok = false;
-            for (int j = max(0, v_issued - L::kVSlots); j < v_issued; ++j)
+            for (int j = max(0, vc - L::kVSlots); j < vc; ++j)
                 if (!mbar_wait(&bars->v_full[j % L::kVSlots], (j / L::kVSlots) & 1)) ok = false;
-            if (!ok) atomicOr(a.p.status, kDevTimeout);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
@@ -377,155 +436,193 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
         const uint64_t qd0 = smem_desc_sw128(smem_u32(smem + L::kOffQ), 0, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), 0, 1024);
         const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kOffV), kHalf, 1024);
-        const bool split[2] = {a.split_all || tok0 + 1 <= kFewKeys, a.split_all || tok0 + a.tpt + 1 <= kFewKeys};
-        auto issue_qk = [&](int t, int j) {
-            const uint64_t qd = qd0 + (uint64_t)((t * L::kTile) >> 4);
-            const uint64_t kd = kd0 + (uint64_t)(((j % L::kKSlots) * L::kTile) >> 4);
+        int kc = 0, vc = 0;                    // stages so far
+        int sc[2] = {0, 0}, ic[2] = {0, 0};    // the tiles' own stages and items so far
+        uint32_t cleaned = 0;                  // parity of each slot's looks so far
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            const Tiles w(it, a.tpt);
+            const bool split[2] = {a.split_all || it->tok0 + 1 <= kFewKeys, a.split_all || it->tok0 + a.tpt + 1 <= kFewKeys};
+            auto issue_qk = [&](int t, int j) {  // stage j of the item, in K slot (kc + j) % slots
+                const uint64_t qd = qd0 + (uint64_t)((t * L::kTile) >> 4);
+                const uint64_t kd = kd0 + (uint64_t)((((kc + j) % L::kKSlots) * L::kTile) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                tc_mma_ew(tmem + t * kKeys, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
-            tc_commit_ew(&bars->s_full[t]);
-        };
-        auto issue_pv = [&](int t, int j) {
-            const uint64_t vd = vd0 + (uint64_t)(((j % L::kVSlots) * L::kTile) >> 4);
-            const uint32_t to = tmem + L::kColsO + t * D, tp = tmem + t * kKeys;
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc_mma_ts_ew(to, tp + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (split[t]) {  // the low parts of P, against the same V
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                    tc_mma_ew(tmem + t * kKeys, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                tc_commit_ew(&bars->s_full[t]);
+                if (j + 1 == w.n[t]) tc_commit_ew(&bars->q_empty[t]);
+            };
+            auto issue_pv = [&](int t, int j) {
+                const uint64_t vd = vd0 + (uint64_t)((((vc + j) % L::kVSlots) * L::kTile) >> 4);
+                const uint32_t to = tmem + L::kColsO + t * D, tp = tmem + t * kKeys;
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc_mma_ts_ew(to, tp + 64 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, 1u);
-            }
-            if (j + 1 == n[t]) tc_commit_ew(&bars->o_final[t]);
-        };
-        bool ok = mbar_wait_warp(&bars->k_full[0], 0);
+                    tc_mma_ts_ew(to, tp + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                if (split[t]) {  // the low parts of P, against the same V
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (n[t] == 0 || !ok) continue;
-            ok = mbar_wait_warp(&bars->q_full[t], 0);
-            if (!ok) continue;
-            tc_fence_after();
-            issue_qk(t, 0);
-        }
-        if (ok) tc_commit_ew(&bars->k_empty[0]);
-        for (int j = 0; j < nst && ok; ++j) {
-            // V(j) and K(j+1) are normally long in place, so they are waited for before P
-            const int vs = j % L::kVSlots;
-            ok = j < first_masked ? mbar_wait_warp(&bars->v_full[vs], (j / L::kVSlots) & 1)
-                                  : mbar_wait_warp(&bars->v_clean[vs], ((j - first_masked) / L::kVSlots) & 1);
-            if (ok && j + 1 < nst) ok = mbar_wait_warp(&bars->k_full[(j + 1) % L::kKSlots], ((j + 1) / L::kKSlots) & 1);
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        tc_mma_ts_ew(to, tp + 64 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, 1u);
+                }
+                if (j + 1 == w.n[t]) tc_commit_ew(&bars->o_full[t]);
+            };
+            ok = mbar_wait_warp(&bars->k_full[kc % L::kKSlots], (kc / L::kKSlots) & 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (j >= n[t] || !ok) continue;
-                ok = mbar_wait_warp(&bars->p_full[t], j & 1);
+                if (w.n[t] == 0 || !ok) continue;
+                ok = mbar_wait_warp(&bars->q_full[t], ic[t] & 1);
                 if (!ok) continue;
                 tc_fence_after();
-                issue_pv(t, j);
-                if (j + 1 < n[t]) issue_qk(t, j + 1);  // S_t takes the place of P_t, after its product in issue order
+                issue_qk(t, 0);
             }
-            if (!ok) break;
-            tc_commit_ew(&bars->v_empty[vs]);
-            if (j + 1 < nst) tc_commit_ew(&bars->k_empty[(j + 1) % L::kKSlots]);
+            if (ok) tc_commit_ew(&bars->k_empty[kc % L::kKSlots]);
+#pragma unroll 1
+            for (int j = 0; j < w.nst && ok; ++j) {
+                // V(j) and K(j+1) are normally long in place, so they are waited for before P
+                const int vs = (vc + j) % L::kVSlots, ks = (kc + j + 1) % L::kKSlots;
+                if (j < w.first_masked) {
+                    ok = mbar_wait_warp(&bars->v_full[vs], ((vc + j) / L::kVSlots) & 1);
+                } else {
+                    ok = mbar_wait_warp(&bars->v_clean[vs], (cleaned >> vs) & 1);
+                    cleaned ^= 1u << vs;
+                }
+                if (ok && j + 1 < w.nst) ok = mbar_wait_warp(&bars->k_full[ks], ((kc + j + 1) / L::kKSlots) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= w.n[t] || !ok) continue;
+                    ok = mbar_wait_warp(&bars->p_full[t], (sc[t] + j) & 1);
+                    // the outputs of the tile's item before have been read
+                    if (ok && j == 0 && ic[t] > 0) ok = mbar_wait_warp(&bars->o_empty[t], (ic[t] - 1) & 1);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_pv(t, j);
+                    if (j + 1 < w.n[t]) issue_qk(t, j + 1);  // S_t takes the place of P_t, after its product in issue order
+                }
+                if (!ok) break;
+                tc_commit_ew(&bars->v_empty[vs]);
+                if (j + 1 < w.nst) tc_commit_ew(&bars->k_empty[ks]);
+            }
+            kc += w.nst;
+            vc += w.nst;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sc[t] += w.n[t];
+                ic[t] += w.n[t] > 0;
+            }
         }
         // every MMA this warp issued has finished before the tensor memory is released
         tc_commit_ew(&bars->drain);
         if (!mbar_wait_warp(&bars->drain, 0)) ok = false;
-        if (!ok && lane == 0) atomicOr(a.p.status, kDevTimeout);
-    } else if (warp >= kCleanWarp) {
+    } else if (warp == kCleanWarp) {
         // ---------------------------------------------------------------- V of the stages with masked keys
-        const int i0 = threadIdx.x - kCleanWarp * 32;
-        bool ok = true;
-        // every stage is followed, so that a barrier's phases cannot pass these warps by
-        for (int j = 0; j < nst && ok; ++j) {
-            const int vs = j % L::kVSlots;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (j / L::kVSlots) & 1));
-            if (!ok) break;
-            if (j < first_masked) {
-                if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
-                continue;
-            }
-            uint8_t* tile = smem + L::kOffV + vs * L::kTile;
-            // a pass that only reads (its loads run ahead), and only where something was found the repair
-            uint32_t seen = 0;
+        int vc = 0;
+        for (Item* it; (it = items.next(ok)); items.done()) {
+            const Tiles w(it, a.tpt);
+            // every stage is followed, so that a barrier's phases cannot pass this warp by
+            for (int j = 0; j < w.nst && ok; ++j, ++vc) {
+                const int vs = vc % L::kVSlots;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (vc / L::kVSlots) & 1));
+                if (!ok) break;
+                if (j >= w.first_masked) {
+                    uint8_t* tile = smem + L::kOffV + vs * L::kTile;
+                    // a pass that only reads (its loads run ahead), and only where something was found the repair
+                    uint32_t seen = 0;
 #pragma unroll 8
-            for (int i = i0; i < L::kTile / 16; i += 64) seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
-            if (seen) {
-                for (int i = i0; i < L::kTile / 16; i += 64) {
-                    uint4* at = reinterpret_cast<uint4*>(tile + 16 * i);
-                    if (!not_finite(*at)) continue;
-                    const int half = i / (kHalf / 16), row = i / 8 % kRows, col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
-                    for (int e = 0; e < 8; ++e) {
-                        uint16_t* x = reinterpret_cast<uint16_t*>(at) + e;
-                        if ((*x & 0x7f80u) != 0x7f80u) continue;
-                        const int what = (*x & 0x7fu) ? 0 : (*x & 0x8000u) ? 2 : 1;
-                        atomicMin(&bad[what * D + col + e], j * kKeys + row);
-                        *x = 0;
+                    for (int i = lane; i < L::kTile / 16; i += 32)
+                        seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
+                    if (__any_sync(0xffffffffu, seen != 0)) {
+                        if (!it->any_bad) {  // the notes of the item before have been read
+                            if (items.n > 0)
+                                ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[(items.n - 1) & 1],
+                                                                       ((items.n - 1) >> 1) & 1));
+                            if (!ok) break;
+                            for (int i = lane; i < 3 * D; i += 32) bad[i] = INT_MAX;
+                            __syncwarp();
+                            if (lane == 0) it->any_bad = 1;
+                            __syncwarp();
+                        }
+#pragma unroll 1
+                        for (int i = lane; i < L::kTile / 16; i += 32) {
+                            const int half = i / (kHalf / 16), row = i / 8 % kRows;
+                            const int col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
+#pragma unroll 1
+                            for (int e = 0; e < 8; ++e) {
+                                uint16_t* x = reinterpret_cast<uint16_t*>(tile + 16 * i) + e;
+                                if ((*x & 0x7f80u) != 0x7f80u) continue;
+                                const int what = (*x & 0x7fu) ? 0 : (*x & 0x8000u) ? 2 : 1;
+                                atomicMin(&bad[what * D + col + e], j * kKeys + row);
+                                *x = 0;
+                            }
+                        }
+                        fence_proxy_async_smem();
                     }
+                    mbar_arrive(&bars->v_clean[vs]);
                 }
-                bars->any_bad = 1;
-                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
             }
-            mbar_arrive(&bars->v_clean[vs]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
         }
-        if (!ok && lane == 0) atomicOr(a.p.status, kDevTimeout);
+    }
     } else {
-        // ---------------------------------------------------------------- softmax and epilogue, one row a thread
+        // ---------------------------------------------------------------- softmax and outputs, one row a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = warp >> 2, r = threadIdx.x & 127;
-        const int first = tok0 + t * a.tpt;                    // the tile's first token
         const int qi = r / a.th, hh = r - qi * a.th;
-        const bool valid = qi < ntok[t];
-        const int pos = valid ? first + qi : -1;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tm_s = tmem + lanes + t * kKeys, tm_o = tmem + lanes + L::kColsO + t * D;
-        if (n[t] > 0) {
+        const bool wide = (reinterpret_cast<uintptr_t>(a.p.out) & 31u) == 0;
+        int sc = 0, ic = 0;  // the tile's stages and items so far
+        for (const Item* it; (it = items.next(ok)); items.done()) {
+            const int first = it->tok0 + t * a.tpt;  // the tile's first token
+            const int ntok = max(0, min(a.tpt, it->len - first));
+            if (ntok == 0) continue;
+            const int n = (first + ntok + kKeys - 1) / kKeys;
+            const bool valid = qi < ntok;
+            const int pos = valid ? first + qi : -1;
             float l = 0.f;
-            const bool two = a.split_all || first + 1 <= kFewKeys;
-            bool ok = two ? softmax_rows_split<D>(bars, t, n[t], pos, a.scale_log2, tm_s, tm_o, &l)
-                          : softmax_rows<D, false>(bars, t, n[t], pos, a.scale_log2, tm_s, tm_o, l);
-            if (ok) ok = !__any_sync(0xffffffffu, !mbar_wait(&bars->o_final[t], 0));
-            if (!ok) {
-                if (lane == 0) atomicOr(a.p.status, kDevTimeout);
-            } else {
-                tc_fence_after();
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const bool any_bad = bars->any_bad != 0;
-                uint8_t* qs = smem + L::kOffQ + t * L::kTile;
-                __nv_bfloat16* dst = a.p.out + ((size_t)(c0 + first + qi) * a.p.num_heads + head0 + hh) * D;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tm_o + c, o);
-                    if (any_bad) {
-                        for (int e = 0; e < 32; ++e) {
-                            float x = __uint_as_float(o[e]);
-                            if (pos >= bad[D + c + e]) x += INFINITY;
-                            if (pos >= bad[2 * D + c + e]) x -= INFINITY;
-                            if (pos >= bad[c + e]) x = NAN;
-                            o[e] = __float_as_uint(x);
-                        }
-                    }
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 v;
-                            v.x = pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            v.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            v.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            v.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c + e) = v;
-                        }
-                    }
+            if (a.split_all || first + 1 <= kFewKeys)
+                ok = softmax_rows<D, true>(bars, t, sc, n, pos, a.scale_log2, tm_s, tm_o, l);
+            else
+                ok = softmax_rows<D, false>(bars, t, sc, n, pos, a.scale_log2, tm_s, tm_o, l);
+            sc += n;
+            if (ok) ok = !__any_sync(0xffffffffu, !mbar_wait(&bars->o_full[t], ic & 1));
+            ++ic;
+            if (!ok) continue;
+            tc_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const bool any_bad = it->any_bad != 0;
+            __nv_bfloat16* dst = a.p.out + ((size_t)(it->row + first + qi) * a.p.num_heads + it->head0 + hh) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tm_o + c, o);
+                if (c + 32 == D) {
+                    tc_fence_before();
+                    mbar_arrive(&bars->o_empty[t]);
                 }
-                (void)qs;
+                if (valid) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    store_32(dst + c, v, wide);
+                    store_32(dst + c + 16, v + 8, wide);
+                }
+            }
+            if (any_bad && valid) {
+#pragma unroll 1
+                for (int c = 0; c < D; ++c) {
+                    float x = __bfloat162float(dst[c]);
+                    if (pos >= bad[D + c]) x += INFINITY;
+                    if (pos >= bad[2 * D + c]) x -= INFINITY;
+                    if (pos >= bad[c]) x = NAN;
+                    if (!isfinite(x)) dst[c] = __float2bfloat16_rn(x);
+                }
             }
         }
         tc_fence_before();
     }
+    if (!ok && lane == 0) atomicOr(a.p.status, kDevTimeout);
     __syncthreads();
     pdl_trigger();
     if (warp == kMmaWarp) {
@@ -556,16 +653,17 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
     t.th = tile_heads(a.num_heads / a.num_kv_heads);
     t.tpt = kRows / t.th;
     t.subs = a.num_heads / t.th;
-    t.pairs = (a.max_len + 2 * t.tpt - 1) / (2 * t.tpt);
     t.scale_log2 = a.scale * kLog2e;
     t.split_all = std::fabs(a.scale) * std::sqrt((float)D) > kSplitScale;
-    CUtensorMap q, k, v, out;
+    CUtensorMap q, k, v;
     if (!strided_map(&q, a.q, a.num_tokens, a.num_heads, D, a.q_stride, t.th, t.tpt, 1) ||
         !strided_map(&k, a.k, a.num_tokens, a.num_kv_heads, D, a.k_stride, 1, kKeys, L::kHalves) ||
-        !strided_map(&v, a.v, a.num_tokens, a.num_kv_heads, D, a.v_stride, 1, kKeys, L::kHalves) ||
-        !strided_map(&out, a.out, a.num_tokens, a.num_heads, D, (long long)a.num_heads * D, t.th, t.tpt, 1))
+        !strided_map(&v, a.v, a.num_tokens, a.num_kv_heads, D, a.v_stride, 1, kKeys, L::kHalves))
         return cudaErrorInvalidValue;
-    const long long ctas = (long long)t.pairs * a.batch * t.subs;
+    // an upper bound of the pairs that sequences of num_tokens rows in all, and of max_len each, can have
+    const long long two = 2 * t.tpt;
+    const long long pairs = std::min((a.num_tokens + a.batch * (two - 1)) / two, a.batch * ((a.max_len + two - 1) / two));
+    const long long ctas = std::max(1LL, pairs) * t.subs;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -575,7 +673,7 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, packed_kernel<D>, q, k, v, out, t);
+    return cudaLaunchKernelEx(&cfg, packed_kernel<D>, q, k, v, t);
 }
 
 }  // namespace
