@@ -62,7 +62,7 @@ template <int D>
 struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kOffQ = 0;                    // (gather: a second tile of low parts)
+    static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kTile;        // two tiles; each becomes the high parts of K~ in place
     static constexpr int kOffLo = kOffK + 2 * kTile;   // the low parts
     static constexpr int kOffV = kOffLo + kTile;       // two tiles
@@ -82,7 +82,7 @@ static_assert(sizeof(Item) <= 64, "item");
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
     uint64_t s_full, p_full, o_full, o_empty;  // scores, P, outputs ready; outputs read
-    uint64_t k_raw;                            // Q K^T of the chunk is done: K may become K~
+    uint64_t k_raw;                            // Q K^T of the chunk is done, K may become K~ (gather: K~^T V of the chunk is done)
     uint64_t kt_full, st_full, u_full;         // K~ ready; the state ready for the chunk; K~^T V done
     uint64_t item_full[2], item_empty[2], soon, next, drain;
     uint4 reply;                               // of clusterlaunchcontrol
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x & 127;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, r = threadIdx.x & 127;
     const PackedArgs& p = a.l.rows;
     const int g = a.group;
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
@@ -325,11 +325,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint64_t sd = smem_desc_sw128(smem_u32(smem + L::kOffS), D * 128, 1024);
         // K~^T as A: at d = 64 its rows 64 .. 127 are whatever lies behind the tile, in lanes that nobody reads
         const uint64_t hd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), kHalf, 1024);
-        const uint64_t ld0 = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
-        const uint64_t ld1 = kGather ? smem_desc_sw128(smem_u32(smem + L::kOffQ), kHalf, 1024) : ld0;
+        const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
         int cc = 0, ii = 0;  // chunks and chunks' heads so far
         for (const Item* it; (it = items.next(ok)); items.done()) {
-            const int chunks = it->chunks;
+            const int chunks = __shfl_sync(0xffffffffu, it->chunks, 0);  // (uniform, and with it all that is counted here)
             for (int c = 0; c < chunks && ok; ++c, ++cc) {
                 const uint64_t slot = (uint64_t)(((cc & 1) * L::kTile) >> 4), vd = vd0 + slot;
                 if (!kGather) {
@@ -372,14 +371,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (ok) ok = mbar_wait_warp(&bars->kt_full, cc & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t lo = (cc & 1) ? ld1 : ld0;
 #pragma unroll
                 for (int kk = 0; kk < kChunk / 16; ++kk) {
                     const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
                     tc_mma_ew(tmem + L::kColU, hd0 + slot + off, vd + off, idesc_u, !kGather || c > 0 || kk > 0 ? 1u : 0u);
-                    tc_mma_ew(tmem + L::kColU, lo + off, vd + off, idesc_u, 1u);
+                    tc_mma_ew(tmem + L::kColU, ld + off, vd + off, idesc_u, 1u);
                 }
                 if (!kGather || c + 1 == chunks) tc_commit_ew(&bars->u_full);
+                if (kGather) tc_commit_ew(&bars->k_raw);
                 tc_commit_ew(&bars->k_empty[cc & 1]);
                 tc_commit_ew(&bars->v_empty[cc & 1]);
             }
@@ -435,15 +434,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (!kGather) {  // (it also means that the products with the low parts of the chunk before are done)
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, cc & 1));
                 } else {
-                    // (the tile was free to be loaded: the products of the chunk two before are done with the low parts)
+                    // Not while the products of the chunk before run: with K~ written beside them (and two tiles of low parts)
+                    // about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of its operands in place
+                    // and its commits outstanding until the waits ran out; in turn it has not been seen.
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
+                    if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
                 }
                 if (!ok) break;
                 // weighted to the end of the chunk, or of the segment
                 const int left = kGather ? len - c * kChunk : n;
                 const float w = r < n ? fast_exp2((float)(left - 1 - r) * la) : 0.f;
                 uint8_t* hi = smem + L::kOffK + (cc & 1) * L::kTile + r * 128;
-                uint8_t* lo = smem + (kGather && (cc & 1) ? L::kOffQ : L::kOffLo) + r * 128;
+                uint8_t* lo = smem + L::kOffLo + r * 128;
 #pragma unroll 1
                 for (int i0 = 0; i0 < D / 8; i0 += 4) {
                     uint4 in[4];  // four loads in flight together

@@ -148,6 +148,17 @@ __device__ __forceinline__ void quarter_p(const uint32_t (&s)[32], int lim, floa
     }
 }
 
+// A quarter seen whole, its P as 16 words (quarter_p<true, false> without its stores).
+__device__ __forceinline__ void quarter_w(const uint32_t (&s)[32], float sl, float nbase, uint32_t* w, float (&ls)[4]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x0, x1;
+        fma_x2(x0, x1, __uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]), sl, sl, nbase, nbase);
+        w[i] = pack_bf16x2(fast_exp2(x0), fast_exp2(x1));
+        add_bf16x2(ls[(i & 1) * 2], ls[(i & 1) * 2 + 1], w[i]);
+    }
+}
+
 template <bool kAll, bool kSplit>
 __device__ __forceinline__ float stage_p(const uint32_t (&s0)[32], const uint32_t (&s1)[32], const uint32_t (&s2)[32],
                                          const uint32_t (&s3)[32], int lim, float sl, float nbase, uint32_t dst) {
@@ -187,19 +198,42 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
         const int lim = pos - j * kKeys;
         const bool unmasked = __all_sync(0xffffffffu, lim >= kKeys - 1);
         uint32_t s0[32], s1[32], s2[32], s3[32];
-        tmem_ld32_async(tm_s, s0);
-        tmem_ld32_async(tm_s + 32, s1);
-        tmem_ld32_async(tm_s + 64, s2);
-        tmem_ld32_async(tm_s + 96, s3);
-        tmem_wait_ld(s0);
-        tmem_wait_ld(s1);
-        tmem_wait_ld(s2);
-        tmem_wait_ld(s3);
         float sum;
+        const bool usual = !kSplit && unmasked && j > 0;
+        if (usual) {
+            const float nb = -m_used;
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t w[32];
+            tmem_ld32(tm_s, s0);
+            tmem_ld32_async(tm_s + 32, s1);
+            quarter_w(s0, sl, nb, w, ls);
+            tmem_wait_ld(s1);
+            tmem_ld32_async(tm_s + 64, s2);
+            quarter_w(s1, sl, nb, w + 16, ls);
+            tmem_st32_nowait(tm_s, w);
+            tmem_wait_ld(s2);
+            tmem_ld32_async(tm_s + 96, s3);
+            quarter_w(s2, sl, nb, w, ls);
+            tmem_wait_ld(s3);
+            quarter_w(s3, sl, nb, w + 16, ls);
+            tmem_st32_nowait(tm_s + 32, w);
+            sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        } else {
+            tmem_ld32_async(tm_s, s0);
+            tmem_ld32_async(tm_s + 32, s1);
+            tmem_ld32_async(tm_s + 64, s2);
+            tmem_ld32_async(tm_s + 96, s3);
+            tmem_wait_ld(s0);
+            tmem_wait_ld(s1);
+            tmem_wait_ld(s2);
+            tmem_wait_ld(s3);
+            sum = INFINITY;
+        }
         // against the base there is, unless a row has none yet; once more with a new one if a sum says so
-        bool rebased = false, full = __any_sync(0xffffffffu, m_used == -INFINITY && lim >= 0);
+        bool rebased = false, full = !usual && __any_sync(0xffffffffu, m_used == -INFINITY && lim >= 0);
+        if (usual) full = __any_sync(0xffffffffu, !(sum <= kSpecSumLimit));
 #pragma unroll 1
-        for (;;) {
+        while (!usual || full) {
             if (full) {
                 const float sgn = sl < 0.f ? -1.f : 1.f;
                 const float mx = fmaxf(fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn)),
@@ -235,14 +269,16 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
 // Tokens and key stages of an item's tiles.
 struct Tiles {
     int ntok[2], n[2], nst, first_masked;
+    // (through shuffles, so that the compiler knows them, and all that follows from them, to be the warp's)
     __device__ __forceinline__ Tiles(const Item* it, int tpt) {
+        const int len = __shfl_sync(0xffffffffu, it->len, 0), tok0 = __shfl_sync(0xffffffffu, it->tok0, 0);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            ntok[t] = max(0, min(tpt, it->len - it->tok0 - t * tpt));
-            n[t] = ntok[t] > 0 ? (it->tok0 + t * tpt + ntok[t] + kKeys - 1) / kKeys : 0;
+            ntok[t] = max(0, min(tpt, len - tok0 - t * tpt));
+            n[t] = ntok[t] > 0 ? (tok0 + t * tpt + ntok[t] + kKeys - 1) / kKeys : 0;
         }
         nst = max(n[0], n[1]);
-        first_masked = (it->tok0 + 1) / kKeys;  // stages before it are visible to every row
+        first_masked = (tok0 + 1) / kKeys;  // stages before it are visible to every row
     }
 };
 
@@ -274,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars<D>* bars = reinterpret_cast<Bars<D>*>(smem + L::kOffBars);
     int* bad = reinterpret_cast<int*>(smem + L::kOffBad);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {  // the swizzled layouts need the declared alignment
         if (threadIdx.x == 0) atomicOr(a.p.status, kDevOutOfRange);
         return;
@@ -389,8 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
         const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
         int kc = 0, vc = 0, q0 = 0, q1 = 0;  // copies issued
         for (const Item* it; (it = items.next(ok)); items.done()) {
+            const Tiles w(it, a.tpt);
             if (lane == 0) {
-                const Tiles w(it, a.tpt);
                 const int base = it->row, tok0 = it->tok0, head0 = it->head0, kvh = it->kvh;
                 auto load_q = [&](int t, int& qc) {
                     if (qc > 0 && ok) ok = mbar_wait(&bars->q_empty[t], (qc & 1) ^ 1);
@@ -441,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
         uint32_t cleaned = 0;                  // parity of each slot's looks so far
         for (const Item* it; (it = items.next(ok)); items.done()) {
             const Tiles w(it, a.tpt);
-            const bool split[2] = {a.split_all || it->tok0 + 1 <= kFewKeys, a.split_all || it->tok0 + a.tpt + 1 <= kFewKeys};
+            const int tok0 = __shfl_sync(0xffffffffu, it->tok0, 0);
+            const bool split[2] = {a.split_all || tok0 + 1 <= kFewKeys, a.split_all || tok0 + a.tpt + 1 <= kFewKeys};
             auto issue_qk = [&](int t, int j) {  // stage j of the item, in K slot (kc + j) % slots
                 const uint64_t qd = qd0 + (uint64_t)((t * L::kTile) >> 4);
                 const uint64_t kd = kd0 + (uint64_t)((((kc + j) % L::kKSlots) * L::kTile) >> 4);
