@@ -19,9 +19,9 @@
 // not started (clusterlaunchcontrol), and the next item's Q, K and V arrive and its first scores are
 // computed under the end of the one before.  Items go sequence by sequence, each sequence's longest first.
 //
-// Base of the softmax: a stage is taken against the row's current base; only a row's first stage, or
-// one whose sum passes 2^16, takes the maximum, and O is rescaled where the maximum grew by more than
-// 2^8.  P is rounded to bf16 and the normaliser sums the rounded values, so their rounding moves
+// Base of the softmax: a stage is taken against the row's current base, 0 to begin with (P, O and the sums have
+// the range of fp32).  Only a stage whose sum passes 2^16, or a first one whose sum is below 2^-40, takes the
+// maximum; the base moves there, and O is rescaled where the maximum grew by more than 2^8.  P is rounded to bf16 and the normaliser sums the rounded values, so their rounding moves
 // weight between keys but not its total.  Where few keys can dominate (a tile with a row of at most
 // 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
 //
@@ -47,7 +47,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10, kItemWarp = 11;
 constexpr int kThreads = 384;
 constexpr int kHalf = kRows * 128;      // [128 rows][64 columns] bf16
 constexpr float kRescaleThreshold = 8.f;
-constexpr float kSpecSumLimit = 65536.f;
+constexpr float kSumMost = 65536.f, kFirstSumLeast = 0x1p-40f;  // a stage's sum outside takes the maximum
 constexpr float kSplitScale = 2.f;      // |scale| sqrt(d) past this: P in two parts
 constexpr int kFewKeys = 128;           // a tile with a row of at most this many keys: the same
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -190,7 +190,7 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float f) {
 template <int D, bool kSplit>
 __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n, int pos, float sl, uint32_t tm_s,
                                              uint32_t tm_o, float& l_out) {
-    float m_used = -INFINITY, l = 0.f;
+    float base = 0.f, l = 0.f;  // P = 2^(score - base)
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++sc) {
         if (__any_sync(0xffffffffu, !mbar_wait(&bars->s_full[t], sc & 1))) return false;
@@ -199,23 +199,23 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
         const bool unmasked = __all_sync(0xffffffffu, lim >= kKeys - 1);
         uint32_t s0[32], s1[32], s2[32], s3[32];
         float sum;
-        const bool usual = !kSplit && unmasked && j > 0;
-        if (usual) {
-            const float nb = -m_used;
+        if (D == 128 && !kSplit && unmasked) {
+            // the usual stage, quarter by quarter, each loaded while the one before is worked on (1 x 16384: 703 us
+            // against 773; at d = 64, where the softmax bounds both tiles, 135 against 131)
             float ls[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t w[32];
             tmem_ld32(tm_s, s0);
             tmem_ld32_async(tm_s + 32, s1);
-            quarter_w(s0, sl, nb, w, ls);
+            quarter_w(s0, sl, -base, w, ls);
             tmem_wait_ld(s1);
             tmem_ld32_async(tm_s + 64, s2);
-            quarter_w(s1, sl, nb, w + 16, ls);
+            quarter_w(s1, sl, -base, w + 16, ls);
             tmem_st32_nowait(tm_s, w);
             tmem_wait_ld(s2);
             tmem_ld32_async(tm_s + 96, s3);
-            quarter_w(s2, sl, nb, w, ls);
+            quarter_w(s2, sl, -base, w, ls);
             tmem_wait_ld(s3);
-            quarter_w(s3, sl, nb, w + 16, ls);
+            quarter_w(s3, sl, -base, w + 16, ls);
             tmem_st32_nowait(tm_s + 32, w);
             sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
         } else {
@@ -227,35 +227,27 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
             tmem_wait_ld(s1);
             tmem_wait_ld(s2);
             tmem_wait_ld(s3);
-            sum = INFINITY;
+            sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
+                           : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
         }
-        // against the base there is, unless a row has none yet; once more with a new one if a sum says so
-        bool rebased = false, full = !usual && __any_sync(0xffffffffu, m_used == -INFINITY && lim >= 0);
-        if (usual) full = __any_sync(0xffffffffu, !(sum <= kSpecSumLimit));
-#pragma unroll 1
-        while (!usual || full) {
-            if (full) {
-                const float sgn = sl < 0.f ? -1.f : 1.f;
-                const float mx = fmaxf(fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn)),
-                                       fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn)));
-                const float mxs = mx == -INFINITY ? -INFINITY : mx * fabsf(sl);  // log2 units
-                const float m_new = fmaxf(m_used, mxs);
-                const bool rebase = m_new > m_used + kRescaleThreshold;  // always for the first visible key
-                // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
-                if (__any_sync(0xffffffffu, rebase && m_used != -INFINITY))
-                    scale_o<D>(tm_o, rebase && m_used != -INFINITY ? fast_exp2(m_used - m_new) : 1.f);
-                if (rebase) {
-                    l *= m_used == -INFINITY ? 0.f : fast_exp2(m_used - m_new);
-                    m_used = m_new;
-                }
-                rebased = true;
+        // a sum past 2^16, or a first one below 2^-40: once more against a new base
+        if (__any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && pos >= 0 && sum < kFirstSumLeast))) {
+            const float sgn = sl < 0.f ? -1.f : 1.f;
+            const float mx = fabsf(sl) * fmaxf(fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn)),
+                                               fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn)));
+            // (a maximum that is no number leaves the base: the row's result is none either)
+            float f = 1.f;
+            if (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY) {
+                f = fast_exp2(base - mx);
+                base = mx;
             }
-            const float nbase = m_used == -INFINITY ? 0.f : -m_used;
-            sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s)
-                           : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, nbase, tm_s);
-            if (rebased) break;
-            full = __any_sync(0xffffffffu, !(sum <= kSpecSumLimit));
-            if (!full) break;
+            // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
+            if (j > 0) {
+                if (__any_sync(0xffffffffu, f != 1.f)) scale_o<D>(tm_o, f);
+                l *= f;
+            }
+            sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
+                           : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
         }
         l += sum;
         tmem_wait_st();
@@ -629,23 +621,40 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool any_bad = it->any_bad != 0;
             __nv_bfloat16* dst = a.p.out + ((size_t)(it->row + first + qi) * a.p.num_heads + it->head0 + hh) * D;
+            // Two neighbouring lanes store 64 bytes of one row together, then of the other's: half the lines a store touches.
+            const bool odd = lane & 1;
+            const unsigned long long at = valid ? reinterpret_cast<unsigned long long>(dst) : 0;
+            auto row_of = [&](int from) {
+                const unsigned long long row = __shfl_sync(0xffffffffu, at, from);
+                return row ? reinterpret_cast<__nv_bfloat16*>(row) + (odd ? 16 : 0) : nullptr;
+            };
+            __nv_bfloat16* even_row = row_of(lane & ~1);
+            __nv_bfloat16* odd_row = row_of(lane | 1);
+            uint32_t o[32];
+            tmem_ld32(tm_o, o);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tm_o + c, o);
-                if (c + 32 == D) {
+                uint32_t v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                if (c + 32 < D) tmem_ld32_async(tm_o + c + 32, o);  // on their way while these are stored
+                uint32_t first[8], second[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[8 + e], 1);
+                    first[e] = odd ? got : v[e];
+                    second[e] = odd ? v[8 + e] : got;
+                }
+                if (even_row) store_32(even_row + c, first, wide);
+                if (odd_row) store_32(odd_row + c, second, wide);
+                if (c + 32 < D) tmem_wait_ld(o);
+                if (c + 64 == D) {
                     tc_fence_before();
                     mbar_arrive(&bars->o_empty[t]);
                 }
-                if (valid) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    store_32(dst + c, v, wide);
-                    store_32(dst + c + 16, v + 8, wide);
-                }
             }
+            __syncwarp();
             if (any_bad && valid) {
 #pragma unroll 1
                 for (int c = 0; c < D; ++c) {
