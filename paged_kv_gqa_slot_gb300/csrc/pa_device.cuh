@@ -69,19 +69,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return done != 0;
 }
 
-// Whether the phase with the given parity is complete, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // Wait for the phase with the given parity to complete; false after `limit` SM cycles.
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, long long limit) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -135,16 +122,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// 4-D tiled load of a tile of packed rows (strided_map): heads from `head`, rows from `row`, column halves from `half`.
-__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int head, int row, int half,
-                                              uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(row), "r"(half), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // 3-D tiled store from this CTA's shared memory (bulk-group completion: commit, then wait).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -183,14 +160,6 @@ __device__ __forceinline__ uint64_t l2_evict_last_policy() {
 // TMA with 128-byte swizzling: rows of 128 B, chunk index XOR (row mod 8).
 __device__ __forceinline__ uint32_t swz128(int row, int chunk) {
     return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
-}
-
-// Nonzero if one of the eight bf16 values is a NaN or an infinity: all exponent bits set, which a carry out of
-// them shows (0x0080 added to the masked exponent 0x7f80 gives 0x8000).
-__device__ __forceinline__ uint32_t not_finite(const uint4& x) {
-    const uint32_t a = (x.x & 0x7f807f80u) + 0x00800080u, b = (x.y & 0x7f807f80u) + 0x00800080u;
-    const uint32_t c = (x.z & 0x7f807f80u) + 0x00800080u, d = (x.w & 0x7f807f80u) + 0x00800080u;
-    return (a | b | c | d) & 0x80008000u;
 }
 
 // ---------------------------------------------------------------- warp MMA (bf16 -> fp32)
@@ -314,48 +283,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// Eight words (sixteen bf16) to global memory, in one 32-byte store, a whole sector, where the address allows it.
-__device__ __forceinline__ void store_32(void* dst, const uint32_t* w, bool wide) {
-    if (!wide) {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        return;
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-// A warp takes over a block of the grid that has not started (clusterlaunchcontrol): its x coordinate in `id`.
-// False: there is none left, and it may not be asked again; or the wait ran out (ok false).  `reply` and `next`
-// (an mbarrier of count 1, its phase in `phase`) are shared memory of this use alone.
-__device__ __forceinline__ bool take_block(uint4* reply, uint64_t* next, uint32_t& phase, unsigned& id, bool& ok) {
-    if ((threadIdx.x & 31) == 0) {
-        fence_proxy_async_smem();  // the reply before has been read
-        mbar_arrive_expect_tx(next, 16);
-        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                         smem_u32(reply)),
-                     "r"(smem_u32(next))
-                     : "memory");
-    }
-    __syncwarp();
-    ok = __all_sync(0xffffffffu, mbar_wait(next, phase));
-    phase ^= 1;
-    if (!ok) return false;
-    uint32_t got, x, y, z;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%4];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
-        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
-        : "r"(smem_u32(reply))
-        : "memory");
-    __syncwarp();
-    if (got) id = x;
-    return got != 0;
 }
 
 // ---------------------------------------------------------------- tcgen05 (5th-gen tensor cores, TMEM)

@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const LinearArgs a) 
     const bool live = st && len > 0;
     __nv_bfloat16* out = a.rows.out + ((size_t)b * a.rows.num_heads + (size_t)kvh * g) * D;
     if (!live) {
-        for (int i = tid; i < g * CW; i += 256) out[(size_t)(i / CW) * D + (blockIdx.x % (D / CW)) * CW + i % CW] = __float2bfloat16_rn(0.f);
+        for (int i = tid; i < g * CW; i += 256)
+            out[(size_t)(i / CW) * D + (blockIdx.x % (D / CW)) * CW + i % CW] = __float2bfloat16_rn(0.f);
         return;
     }
     float4 s[N];
@@ -176,8 +177,8 @@ cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream) {
 
 size_t linear_workspace(int batch, int num_kv_heads, int head_dim, int max_chunk) {
     if (max_chunk <= kFewTokens) return 0;
-    return (size_t)(linear_segments(batch, num_kv_heads, max_chunk) - 1) * batch * num_kv_heads * head_dim * head_dim *
-           sizeof(float);
+    const int segments = linear_segments(batch, num_kv_heads, max_chunk);
+    return segments == 1 ? 0 : (size_t)segments * batch * num_kv_heads * head_dim * head_dim * sizeof(float);
 }
 
 cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream) {

@@ -32,11 +32,11 @@
 // thread), 4-7 the state (one row a thread), 8-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and
 // V, 14 of Q (one thread issues a copy in about half a microsecond), 15 the look at V, 16 the items.
 // The loops over column blocks are not unrolled and rare paths are short: the roles run at the same time, and
-// their code has to fit the instruction cache together (152 states x 1024 tokens took 52 us unrolled, 36 so).
+// their code has to fit the instruction cache together (152 states x 1024 tokens took 52 us unrolled, 36 rolled up).
 #include <algorithm>
 #include <climits>
 
-#include "pa_device.cuh"
+#include "pa_step.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -82,7 +82,7 @@ static_assert(sizeof(Item) <= 64, "item");
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
     uint64_t s_full, p_full, o_full, o_empty;  // scores, P, outputs ready; outputs read
-    uint64_t k_raw;                            // Q K^T of the chunk is done, K may become K~ (gather: K~^T V of the chunk is done)
+    uint64_t k_raw;                            // Q K^T of the chunk is done, K may become K~ (gather: K~^T V is done)
     uint64_t kt_full, st_full, u_full;         // K~ ready; the state ready for the chunk; K~^T V done
     uint64_t item_full[2], item_empty[2], soon, next, drain;
     uint4 reply;                               // of clusterlaunchcontrol
@@ -92,7 +92,7 @@ static_assert(sizeof(Bars) <= 384, "barrier block");
 
 struct TcArgs {
     LinearArgs l;
-    float* segments;   // [batch][segs - 1][kv heads][D][D]: what a segment adds, then what the next begins with
+    float* segments;   // [batch][segs][kv heads][D][D]: what the segment before adds, then what this one begins with
     int group, segs, seg_chunks;
     float scale;
 };
@@ -128,14 +128,6 @@ __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1,
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-// Sixteen values as bf16.
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, bool wide) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-    store_32(dst, w, wide);
-}
 
 // The items as one warp sees them, in order; next() waits for one and done() gives it back.
 struct Items {
@@ -239,12 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     it.la = log2_decay(a.l.log_decay[kvh]);
                     if (!pad) {
                         float* state = a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * dd;
-                        // what the segment adds, or what the one behind it begins with
-                        float* own = a.segments + (((size_t)b * (a.segs - 1) + seg) * p.num_kv_heads + kvh) * dd;
+                        // (the first of several segments begins with a copy: the last may end before it starts)
+                        float* own = a.segments + (((size_t)b * a.segs + seg) * p.num_kv_heads + kvh) * dd;
                         if (kGather) {
-                            it.end = own;
+                            it.end = own + (size_t)p.num_kv_heads * dd;  // for the next one
                         } else {
-                            it.begin = seg > 0 ? own - (size_t)p.num_kv_heads * dd : w.fresh ? nullptr : state;
+                            it.begin = seg == 0 && w.fresh ? nullptr : seg == 0 && last ? state : own;
                             it.end = last ? state : nullptr;
                             if (it.begin)
                                 for (int i = lane * 128; i < D * D * 4; i += 32 * 128)
@@ -258,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (!ok) break;
             if (lane == 0) *reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64) = it;
             if (!kGather && there) {
-                reinterpret_cast<float*>(smem + L::kOffTab)[(n & 1) * 32 + lane] = fast_exp2((float)(31 - lane) * it.la);
+                reinterpret_cast<float*>(smem + L::kOffTab)[(n & 1) * 32 + lane] =
+                    fast_exp2((float)(31 - lane) * it.la);
                 for (int i = lane; i < D; i += 32) reinterpret_cast<int*>(smem + L::kOffBad)[(n & 1) * D + i] = INT_MAX;
             }
             __syncwarp();
@@ -328,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
         int cc = 0, ii = 0;  // chunks and chunks' heads so far
         for (const Item* it; (it = items.next(ok)); items.done()) {
-            const int chunks = __shfl_sync(0xffffffffu, it->chunks, 0);  // (uniform, and with it all that is counted here)
+            // (uniform, and with it all that is counted here)
+            const int chunks = __shfl_sync(0xffffffffu, it->chunks, 0);
             for (int c = 0; c < chunks && ok; ++c, ++cc) {
                 const uint64_t slot = (uint64_t)(((cc & 1) * L::kTile) >> 4), vd = vd0 + slot;
                 if (!kGather) {
@@ -374,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
                 for (int kk = 0; kk < kChunk / 16; ++kk) {
                     const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
-                    tc_mma_ew(tmem + L::kColU, hd0 + slot + off, vd + off, idesc_u, !kGather || c > 0 || kk > 0 ? 1u : 0u);
+                    tc_mma_ew(tmem + L::kColU, hd0 + slot + off, vd + off, idesc_u,
+                              !kGather || c > 0 || kk > 0 ? 1u : 0u);
                     tc_mma_ew(tmem + L::kColU, ld + off, vd + off, idesc_u, 1u);
                 }
                 if (!kGather || c + 1 == chunks) tc_commit_ew(&bars->u_full);
@@ -434,9 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (!kGather) {  // (it also means that the products with the low parts of the chunk before are done)
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, cc & 1));
                 } else {
-                    // Not while the products of the chunk before run: with K~ written beside them (and two tiles of low parts)
-                    // about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of its operands in place
-                    // and its commits outstanding until the waits ran out; in turn it has not been seen.
+                    // Not while the products of the chunk before run: with K~ written beside them (and two tiles of
+                    // low parts) about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of its
+                    // operands in place and its commits outstanding until the waits ran out; in turn it has not been
+                    // seen (2 10^6 calls), and is faster too (1 x 20000 tokens 191 us against 225).
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
                     if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
                 }
@@ -495,23 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 }
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < D; x += 32) {
-                    uint32_t u[32];
-                    if (c > 0) {
-                        tmem_ld32(tm_u + x, u);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const uint4 v = mine && from ? *reinterpret_cast<const uint4*>(from + (size_t)r * D + x + e)
-                                                         : make_uint4(0u, 0u, 0u, 0u);
-                            u[e] = v.x;
-                            u[e + 1] = v.y;
-                            u[e + 2] = v.z;
-                            u[e + 3] = v.w;
-                        }
-                    }
-                    if (mine) {  // as bf16 for Q S, and back times a^n
+                auto take = [&](uint32_t (&u)[32], int x) {  // as bf16 for Q S, and back times a^n
+                    if (mine) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint32_t w[4];
@@ -526,6 +507,34 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
                     tmem_st32_nowait(tm_u + x, u);
+                };
+                if (c > 0) {
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t u[32];
+                        tmem_ld32(tm_u + x, u);
+                        take(u, x);
+                    }
+                } else {
+                    const bool there = mine && from;
+                    const float* row = from + (size_t)r * D;
+                    const bool wide = (reinterpret_cast<uintptr_t>(from) & 31u) == 0;
+                    auto load = [&](uint32_t (&u)[32], int x) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (there)
+                                load_32(row + x + e, u + e, wide);
+                            else
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) u[e + i] = 0u;
+                        }
+                    };
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t u[32];
+                        load(u, x);
+                        take(u, x);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -538,14 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             float* to = it->end;
             if (!ok || !to) continue;
             tc_fence_after();
+            const bool wide = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t u[32];
                 tmem_ld32(tm_u + x, u);
                 if (mine) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(to + (size_t)r * D + x + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                    for (int e = 0; e < 32; e += 8) store_32(to + (size_t)r * D + x + e, u + e, wide);
                 }
             }
             if (!kGather && it->any_bad && mine) {
@@ -571,7 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 const int per = g * D / 8;
 #pragma unroll 1
                 for (long long i = r; i < (long long)len * per; i += 128)
-                    *reinterpret_cast<uint4*>(out + (size_t)(i / per) * p.num_heads * D + i % per * 8) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(out + (size_t)(i / per) * p.num_heads * D + i % per * 8) =
+                        make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
             const float lead = fast_exp2((row + 1.f) * la) * a.scale;
@@ -629,21 +639,33 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 tc_fence_after();
                 const int t = c * kChunk + r;
                 __nv_bfloat16* dst = out + ((size_t)t * p.num_heads + h) * D;
+                // two neighbouring lanes store 64 bytes of one row together, then of the other's; with this and the
+                // state's 32-byte accesses 152 states x 1 chunk take 10.1 us against 11.3, x 8 34.1 against 36.0
+                const bool odd = lane & 1;
+                const bool even_row = (t & ~1) < len, odd_row = (t | 1) < len;
+                __nv_bfloat16* first = out + ((size_t)(t & ~1) * p.num_heads + h) * D + (odd ? 16 : 0);
+                const size_t step = (size_t)p.num_heads * D;
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
-                    uint32_t o1[32], o2[32];
+                    uint32_t o1[32], o2[32], v[16], w0[8], w1[8];
                     tmem_ld32_async(tm + L::kColO1 + x, o1);
                     tmem_ld32_async(tm + L::kColO2 + x, o2);
                     tmem_wait_ld(o1);
                     tmem_wait_ld(o2);
-                    float o[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(o2[e]), lead, __uint_as_float(o1[e]));
-                    if (t < len) {
-                        store16(dst + x, o, wide);
-                        store16(dst + x + 16, o + 16, wide);
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = pack_bf16x2(fmaf(__uint_as_float(o2[2 * e]), lead, __uint_as_float(o1[2 * e])),
+                                           fmaf(__uint_as_float(o2[2 * e + 1]), lead, __uint_as_float(o1[2 * e + 1])));
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[8 + e], 1);
+                        w0[e] = odd ? got : v[e];
+                        w1[e] = odd ? v[8 + e] : got;
                     }
+                    if (even_row) store_32(first + x, w0, wide);
+                    if (odd_row) store_32(first + step + x, w1, wide);
                 }
+                __syncwarp();
                 tc_fence_before();
                 if (it->any_bad && t < len) {
 #pragma unroll 1
@@ -682,8 +704,10 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const TcArgs a) {
     const float f = fast_exp2((float)(a.seg_chunks * kChunk) * log2_decay(a.l.log_decay[kvh]));
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!w.fresh) s = reinterpret_cast<const float4*>(a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * D * D)[at];
-    float4* seg = reinterpret_cast<float4*>(a.segments + ((size_t)b * (a.segs - 1) * p.num_kv_heads + kvh) * D * D) + at;
+    float4* seg = reinterpret_cast<float4*>(a.segments + ((size_t)b * a.segs * p.num_kv_heads + kvh) * D * D) + at;
     const size_t step = (size_t)p.num_kv_heads * D * D / 4;
+    if (!w.fresh) seg[0] = s;
+    seg += step;
     constexpr int kAhead = 4;
     for (int i0 = 0; i0 < n; i0 += kAhead) {
         float4 x[kAhead];
@@ -729,7 +753,8 @@ cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     const cudaError_t e = configured.run([] {
         cudaError_t r = cudaSuccess;
         for (const void* fn : {(const void*)linear_kernel<D, false>, (const void*)linear_kernel<D, true>})
-            if (r == cudaSuccess) r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+            if (r == cudaSuccess)
+                r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
         return r;
     });
     if (e != cudaSuccess) return e;
@@ -739,7 +764,8 @@ cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     t.group = p.num_heads / p.num_kv_heads;
     t.scale = p.scale;
     t.segments = static_cast<float*>(workspace);
-    const int chunks = (a.max_chunk - 1) / kChunk + 1;
+    // as many segments as the workspace was sized for, or fewer: no sequence is longer than the rows there are
+    const int chunks = (std::min(a.max_chunk, p.num_tokens) - 1) / kChunk + 1;
     const int segs = segments_of(p.batch, p.num_kv_heads, a.max_chunk);
     t.seg_chunks = (chunks + segs - 1) / segs;
     t.segs = (chunks + t.seg_chunks - 1) / t.seg_chunks;

@@ -17,13 +17,15 @@
 //
 // A CTA takes item after item: once the copies of one are on their way it asks for a block of the grid that has
 // not started (clusterlaunchcontrol), and the next item's Q, K and V arrive and its first scores are
-// computed under the end of the one before.  Items go sequence by sequence, each sequence's longest first.
+// computed under the end of the one before.  Items go sequence by sequence, each sequence's longest first (longest
+// first altogether was no faster: 7 prompts at d = 64 94 us against 92, 48 prompts 219 against 224).
 //
 // Base of the softmax: a stage is taken against the row's current base, 0 to begin with (P, O and the sums have
 // the range of fp32).  Only a stage whose sum passes 2^16, or a first one whose sum is below 2^-40, takes the
-// maximum; the base moves there, and O is rescaled where the maximum grew by more than 2^8.  P is rounded to bf16 and the normaliser sums the rounded values, so their rounding moves
-// weight between keys but not its total.  Where few keys can dominate (a tile with a row of at most
-// 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
+// maximum; the base moves there, and O is rescaled where the maximum grew by more than 2^8.  P is rounded to bf16
+// and the normaliser sums the rounded values, so their rounding moves weight between keys but not its total.  Where
+// few keys can dominate (a tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts,
+// in the two halves of S_t.
 //
 // Masked keys have P = 0, and 0 times a NaN or an infinity in V is NaN.  So in the stages that hold a
 // key masked for some row, a warp looks V over before its product: what is not finite is replaced
@@ -35,7 +37,7 @@
 #include <climits>
 #include <cmath>
 
-#include "pa_device.cuh"
+#include "pa_step.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -346,252 +348,261 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
 
     // registers: 256 softmax threads of 200 and 128 others of 96 are fewer than the 384 x 168 of the launch
     if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (warp == kItemWarp) {
-        // ---------------------------------------------------------------- the items
-        // id = pair * subs + sub, the pairs of the sequences counted one after another; ids only rise, so the
-        // walk over the sequences (32 at a time, one a lane) goes on where it was
-        unsigned id = blockIdx.x;
-        uint32_t phase = 0;
-        int b0 = 0;
-        unsigned before = 0;  // pairs of the sequences before b0
-        auto look = [&](int b, int& row, int& len) {  // sequence b's rows and pairs
-            row = len = 0;
-            if (b >= a.p.batch) return 0u;
-            const int c0 = a.p.cu_lens[b], c1 = a.p.cu_lens[b + 1];
-            const bool off = c0 < 0 || c1 < c0 || c1 > a.p.num_tokens;
-            if (off || c1 - c0 > a.p.max_len) atomicOr(a.p.status, kDevOutOfRange);
-            row = c0;
-            len = off ? 0 : min(c1 - c0, a.p.max_len);
-            return (unsigned)((len + 2 * a.tpt - 1) / (2 * a.tpt));
-        };
-        auto sums = [&](unsigned x) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned up = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += up;
-            }
-            return x;
-        };
-        int row, len;
-        unsigned mine = look(lane, row, len), upto = sums(mine);
-        for (int n = 0; ok; ++n) {
-            bool there = true;
-            if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->soon, (n - 1) & 1));
-                if (ok && n > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
-                if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
-            }
-            if (!ok) break;
-            const unsigned pair = id / (unsigned)a.subs, sub = id % (unsigned)a.subs;
-            while (there && pair >= before + __shfl_sync(0xffffffffu, upto, 31)) {
-                before += __shfl_sync(0xffffffffu, upto, 31);
-                b0 += 32;
-                there = b0 < a.p.batch;  // past the last pair: there are no others
-                if (there) {
-                    mine = look(b0 + lane, row, len);
-                    upto = sums(mine);
-                }
-            }
-            Item* it = reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64);
-            if (there && pair >= before + upto - mine && pair < before + upto) {  // the sequence's own lane
-                it->row = row;
-                it->len = len;
-                // the longest pair of a sequence first
-                it->tok0 = (int)(before + upto - 1 - pair) * 2 * a.tpt;
-                it->head0 = (int)sub * a.th;
-                it->kvh = it->head0 / (a.p.num_heads / a.p.num_kv_heads);
-                it->none = 0;
-                it->any_bad = 0;
-            }
-            if (!there && lane == 0) it->none = 1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->item_full[n & 1]);
-            if (!there) break;
-        }
-        // (sequences behind the last pair that anybody took are looked at for their offsets, too)
-        if (blockIdx.x == 0)
-            for (; b0 < a.p.batch; b0 += 32) look(b0 + lane, row, len);
-    } else if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- TMA loads, in the order of use
-        const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
-        int kc = 0, vc = 0, q0 = 0, q1 = 0;  // copies issued
-        for (const Item* it; (it = items.next(ok)); items.done()) {
-            const Tiles w(it, a.tpt);
-            if (lane == 0) {
-                const int base = it->row, tok0 = it->tok0, head0 = it->head0, kvh = it->kvh;
-                auto load_q = [&](int t, int& qc) {
-                    if (qc > 0 && ok) ok = mbar_wait(&bars->q_empty[t], (qc & 1) ^ 1);
-                    if (!ok) return;
-                    mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
-                    // a copy a half: those of a box with fewer than 128 rows would lie closer than kHalf
-                    for (int h = 0; h < L::kHalves; ++h)
-                        tma_load_rows(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, head0, base + tok0 + t * a.tpt, h,
-                                      &bars->q_full[t]);
-                    ++qc;
-                };
-                load_q(0, q0);
-                for (int j = 0; j < w.nst && ok; ++j) {
-                    const int ks = kc % L::kKSlots, vs = vc % L::kVSlots;
-                    if (kc >= L::kKSlots) ok = mbar_wait(&bars->k_empty[ks], ((kc / L::kKSlots) & 1) ^ 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bars->k_full[ks], L::kTile);
-                    tma_load_rows(smem + L::kOffK + ks * L::kTile, &tm_k, kvh, base + j * kKeys, 0, &bars->k_full[ks]);
-                    ++kc;
-                    if (j == 0 && w.n[1] > 0) load_q(1, q1);
-                    if (ok && vc >= L::kVSlots) ok = mbar_wait(&bars->v_empty[vs], ((vc / L::kVSlots) & 1) ^ 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bars->v_full[vs], L::kTile);
-                    tma_load_rows(smem + L::kOffV + vs * L::kTile, &tm_v, kvh, base + j * kKeys, 0, &bars->v_full[vs]);
-                    ++vc;
-                }
-                mbar_arrive(&bars->soon);
-            }
-            __syncwarp();
-        }
-        if (lane == 0) {  // before the CTA may leave: every copy issued here has landed
-            if (q0 && !mbar_wait(&bars->q_full[0], (q0 - 1) & 1)) ok = false;
-            if (q1 && !mbar_wait(&bars->q_full[1], (q1 - 1) & 1)) ok = false;
-            for (int j = max(0, kc - L::kKSlots); j < kc; ++j)
-                if (!mbar_wait(&bars->k_full[j % L::kKSlots], (j / L::kKSlots) & 1)) ok = false;
-            for (int j = max(0, vc - L::kVSlots); j < vc; ++j)
-                if (!mbar_wait(&bars->v_full[j % L::kVSlots], (j / L::kVSlots) & 1)) ok = false;
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- MMA issue
-        constexpr uint32_t idesc_s = tc_idesc_bf16(kRows, kKeys, false);
-        constexpr uint32_t idesc_o = tc_idesc_bf16(kRows, D, true);
-        const uint64_t qd0 = smem_desc_sw128(smem_u32(smem + L::kOffQ), 0, 1024);
-        const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), 0, 1024);
-        const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kOffV), kHalf, 1024);
-        int kc = 0, vc = 0;                    // stages so far
-        int sc[2] = {0, 0}, ic[2] = {0, 0};    // the tiles' own stages and items so far
-        uint32_t cleaned = 0;                  // parity of each slot's looks so far
-        for (const Item* it; (it = items.next(ok)); items.done()) {
-            const Tiles w(it, a.tpt);
-            const int tok0 = __shfl_sync(0xffffffffu, it->tok0, 0);
-            const bool split[2] = {a.split_all || tok0 + 1 <= kFewKeys, a.split_all || tok0 + a.tpt + 1 <= kFewKeys};
-            auto issue_qk = [&](int t, int j) {  // stage j of the item, in K slot (kc + j) % slots
-                const uint64_t qd = qd0 + (uint64_t)((t * L::kTile) >> 4);
-                const uint64_t kd = kd0 + (uint64_t)((((kc + j) % L::kKSlots) * L::kTile) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                    tc_mma_ew(tmem + t * kKeys, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-                }
-                tc_commit_ew(&bars->s_full[t]);
-                if (j + 1 == w.n[t]) tc_commit_ew(&bars->q_empty[t]);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == kItemWarp) {
+            // ---------------------------------------------------------------- the items
+            // id = pair * subs + sub, the pairs of the sequences counted one after another; ids only rise, so the
+            // walk over the sequences (32 at a time, one a lane) goes on where it was
+            unsigned id = blockIdx.x;
+            uint32_t phase = 0;
+            int b0 = 0;
+            unsigned before = 0;  // pairs of the sequences before b0
+            bool reports = id == 0;
+            auto look = [&](int b, int& row, int& len) {  // sequence b's rows and pairs
+                row = len = 0;
+                if (b >= a.p.batch) return 0u;
+                const int c0 = a.p.cu_lens[b], c1 = a.p.cu_lens[b + 1];
+                const bool off = c0 < 0 || c1 < c0 || c1 > a.p.num_tokens;
+                if (off || c1 - c0 > a.p.max_len) atomicOr(a.p.status, kDevOutOfRange);
+                row = c0;
+                len = off ? 0 : min(c1 - c0, a.p.max_len);
+                return (unsigned)((len + 2 * a.tpt - 1) / (2 * a.tpt));
             };
-            auto issue_pv = [&](int t, int j) {
-                const uint64_t vd = vd0 + (uint64_t)((((vc + j) % L::kVSlots) * L::kTile) >> 4);
-                const uint32_t to = tmem + L::kColsO + t * D, tp = tmem + t * kKeys;
+            auto sums = [&](unsigned x) {
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc_mma_ts_ew(to, tp + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-                if (split[t]) {  // the low parts of P, against the same V
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc_mma_ts_ew(to, tp + 64 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, 1u);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned up = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += up;
                 }
-                if (j + 1 == w.n[t]) tc_commit_ew(&bars->o_full[t]);
+                return x;
             };
-            ok = mbar_wait_warp(&bars->k_full[kc % L::kKSlots], (kc / L::kKSlots) & 1);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (w.n[t] == 0 || !ok) continue;
-                ok = mbar_wait_warp(&bars->q_full[t], ic[t] & 1);
-                if (!ok) continue;
-                tc_fence_after();
-                issue_qk(t, 0);
-            }
-            if (ok) tc_commit_ew(&bars->k_empty[kc % L::kKSlots]);
-#pragma unroll 1
-            for (int j = 0; j < w.nst && ok; ++j) {
-                // V(j) and K(j+1) are normally long in place, so they are waited for before P
-                const int vs = (vc + j) % L::kVSlots, ks = (kc + j + 1) % L::kKSlots;
-                if (j < w.first_masked) {
-                    ok = mbar_wait_warp(&bars->v_full[vs], ((vc + j) / L::kVSlots) & 1);
-                } else {
-                    ok = mbar_wait_warp(&bars->v_clean[vs], (cleaned >> vs) & 1);
-                    cleaned ^= 1u << vs;
-                }
-                if (ok && j + 1 < w.nst) ok = mbar_wait_warp(&bars->k_full[ks], ((kc + j + 1) / L::kKSlots) & 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (j >= w.n[t] || !ok) continue;
-                    ok = mbar_wait_warp(&bars->p_full[t], (sc[t] + j) & 1);
-                    // the outputs of the tile's item before have been read
-                    if (ok && j == 0 && ic[t] > 0) ok = mbar_wait_warp(&bars->o_empty[t], (ic[t] - 1) & 1);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    issue_pv(t, j);
-                    if (j + 1 < w.n[t]) issue_qk(t, j + 1);  // S_t takes the place of P_t, after its product in issue order
+            int row, len;
+            unsigned mine = look(lane, row, len), upto = sums(mine);
+            for (int n = 0; ok; ++n) {
+                bool there = true;
+                if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->soon, (n - 1) & 1));
+                    if (ok && n > 1)
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
+                    if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
                 }
                 if (!ok) break;
-                tc_commit_ew(&bars->v_empty[vs]);
-                if (j + 1 < w.nst) tc_commit_ew(&bars->k_empty[ks]);
-            }
-            kc += w.nst;
-            vc += w.nst;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sc[t] += w.n[t];
-                ic[t] += w.n[t] > 0;
-            }
-        }
-        // every MMA this warp issued has finished before the tensor memory is released
-        tc_commit_ew(&bars->drain);
-        if (!mbar_wait_warp(&bars->drain, 0)) ok = false;
-    } else if (warp == kCleanWarp) {
-        // ---------------------------------------------------------------- V of the stages with masked keys
-        int vc = 0;
-        for (Item* it; (it = items.next(ok)); items.done()) {
-            const Tiles w(it, a.tpt);
-            // every stage is followed, so that a barrier's phases cannot pass this warp by
-            for (int j = 0; j < w.nst && ok; ++j, ++vc) {
-                const int vs = vc % L::kVSlots;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (vc / L::kVSlots) & 1));
-                if (!ok) break;
-                if (j >= w.first_masked) {
-                    uint8_t* tile = smem + L::kOffV + vs * L::kTile;
-                    // a pass that only reads (its loads run ahead), and only where something was found the repair
-                    uint32_t seen = 0;
-#pragma unroll 8
-                    for (int i = lane; i < L::kTile / 16; i += 32)
-                        seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
-                    if (__any_sync(0xffffffffu, seen != 0)) {
-                        if (!it->any_bad) {  // the notes of the item before have been read
-                            if (items.n > 0)
-                                ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[(items.n - 1) & 1],
-                                                                       ((items.n - 1) >> 1) & 1));
-                            if (!ok) break;
-                            for (int i = lane; i < 3 * D; i += 32) bad[i] = INT_MAX;
-                            __syncwarp();
-                            if (lane == 0) it->any_bad = 1;
-                            __syncwarp();
-                        }
-#pragma unroll 1
-                        for (int i = lane; i < L::kTile / 16; i += 32) {
-                            const int half = i / (kHalf / 16), row = i / 8 % kRows;
-                            const int col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
-#pragma unroll 1
-                            for (int e = 0; e < 8; ++e) {
-                                uint16_t* x = reinterpret_cast<uint16_t*>(tile + 16 * i) + e;
-                                if ((*x & 0x7f80u) != 0x7f80u) continue;
-                                const int what = (*x & 0x7fu) ? 0 : (*x & 0x8000u) ? 2 : 1;
-                                atomicMin(&bad[what * D + col + e], j * kKeys + row);
-                                *x = 0;
-                            }
-                        }
-                        fence_proxy_async_smem();
+                reports |= there && id == 0;
+                const unsigned pair = id / (unsigned)a.subs, sub = id % (unsigned)a.subs;
+                while (there && pair >= before + __shfl_sync(0xffffffffu, upto, 31)) {
+                    before += __shfl_sync(0xffffffffu, upto, 31);
+                    b0 += 32;
+                    there = b0 < a.p.batch;  // past the last pair: there are no others
+                    if (there) {
+                        mine = look(b0 + lane, row, len);
+                        upto = sums(mine);
                     }
-                    mbar_arrive(&bars->v_clean[vs]);
+                }
+                Item* it = reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64);
+                if (there && pair >= before + upto - mine && pair < before + upto) {  // the sequence's own lane
+                    it->row = row;
+                    it->len = len;
+                    // the longest pair of a sequence first
+                    it->tok0 = (int)(before + upto - 1 - pair) * 2 * a.tpt;
+                    it->head0 = (int)sub * a.th;
+                    it->kvh = it->head0 / (a.p.num_heads / a.p.num_kv_heads);
+                    it->none = 0;
+                    it->any_bad = 0;
+                }
+                if (!there && lane == 0) it->none = 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->item_full[n & 1]);
+                if (!there) break;
+            }
+            // (sequences behind the last pair that anybody took are looked at for their offsets, too)
+            if (reports)
+                for (; b0 < a.p.batch; b0 += 32) look(b0 + lane, row, len);
+        } else if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- TMA loads, in the order of use
+            const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
+            int kc = 0, vc = 0, q0 = 0, q1 = 0;  // copies issued
+            for (const Item* it; (it = items.next(ok)); items.done()) {
+                const Tiles w(it, a.tpt);
+                if (lane == 0) {
+                    const int base = it->row, tok0 = it->tok0, head0 = it->head0, kvh = it->kvh;
+                    auto load_q = [&](int t, int& qc) {
+                        if (qc > 0 && ok) ok = mbar_wait(&bars->q_empty[t], (qc & 1) ^ 1);
+                        if (!ok) return;
+                        mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
+                        // a copy a half: those of a box with fewer than 128 rows would lie closer than kHalf
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tma_load_rows(smem + L::kOffQ + t * L::kTile + h * kHalf, &tm_q, head0,
+                                          base + tok0 + t * a.tpt, h,
+                                          &bars->q_full[t]);
+                        ++qc;
+                    };
+                    load_q(0, q0);
+                    for (int j = 0; j < w.nst && ok; ++j) {
+                        const int ks = kc % L::kKSlots, vs = vc % L::kVSlots;
+                        if (kc >= L::kKSlots) ok = mbar_wait(&bars->k_empty[ks], ((kc / L::kKSlots) & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bars->k_full[ks], L::kTile);
+                        tma_load_rows(smem + L::kOffK + ks * L::kTile, &tm_k, kvh, base + j * kKeys, 0,
+                                      &bars->k_full[ks]);
+                        ++kc;
+                        if (j == 0 && w.n[1] > 0) load_q(1, q1);
+                        if (ok && vc >= L::kVSlots) ok = mbar_wait(&bars->v_empty[vs], ((vc / L::kVSlots) & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bars->v_full[vs], L::kTile);
+                        tma_load_rows(smem + L::kOffV + vs * L::kTile, &tm_v, kvh, base + j * kKeys, 0,
+                                      &bars->v_full[vs]);
+                        ++vc;
+                    }
+                    mbar_arrive(&bars->soon);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
+            }
+            if (lane == 0) {  // before the CTA may leave: every copy issued here has landed
+                if (q0 && !mbar_wait(&bars->q_full[0], (q0 - 1) & 1)) ok = false;
+                if (q1 && !mbar_wait(&bars->q_full[1], (q1 - 1) & 1)) ok = false;
+                for (int j = max(0, kc - L::kKSlots); j < kc; ++j)
+                    if (!mbar_wait(&bars->k_full[j % L::kKSlots], (j / L::kKSlots) & 1)) ok = false;
+                for (int j = max(0, vc - L::kVSlots); j < vc; ++j)
+                    if (!mbar_wait(&bars->v_full[j % L::kVSlots], (j / L::kVSlots) & 1)) ok = false;
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- MMA issue
+            constexpr uint32_t idesc_s = tc_idesc_bf16(kRows, kKeys, false);
+            constexpr uint32_t idesc_o = tc_idesc_bf16(kRows, D, true);
+            const uint64_t qd0 = smem_desc_sw128(smem_u32(smem + L::kOffQ), 0, 1024);
+            const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), 0, 1024);
+            const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kOffV), kHalf, 1024);
+            int kc = 0, vc = 0;                    // stages so far
+            int sc[2] = {0, 0}, ic[2] = {0, 0};    // the tiles' own stages and items so far
+            uint32_t cleaned = 0;                  // parity of each slot's looks so far
+            for (const Item* it; (it = items.next(ok)); items.done()) {
+                const Tiles w(it, a.tpt);
+                const int tok0 = __shfl_sync(0xffffffffu, it->tok0, 0);
+                const bool split[2] = {a.split_all || tok0 + 1 <= kFewKeys,
+                                       a.split_all || tok0 + a.tpt + 1 <= kFewKeys};
+                auto issue_qk = [&](int t, int j) {  // stage j of the item, in K slot (kc + j) % slots
+                    const uint64_t qd = qd0 + (uint64_t)((t * L::kTile) >> 4);
+                    const uint64_t kd = kd0 + (uint64_t)((((kc + j) % L::kKSlots) * L::kTile) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                        tc_mma_ew(tmem + t * kKeys, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit_ew(&bars->s_full[t]);
+                    if (j + 1 == w.n[t]) tc_commit_ew(&bars->q_empty[t]);
+                };
+                auto issue_pv = [&](int t, int j) {
+                    const uint64_t vd = vd0 + (uint64_t)((((vc + j) % L::kVSlots) * L::kTile) >> 4);
+                    const uint32_t to = tmem + L::kColsO + t * D, tp = tmem + t * kKeys;
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        tc_mma_ts_ew(to, tp + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o,
+                                     (j > 0 || kk > 0) ? 1u : 0u);
+                    if (split[t]) {  // the low parts of P, against the same V
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            tc_mma_ts_ew(to, tp + 64 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, 1u);
+                    }
+                    if (j + 1 == w.n[t]) tc_commit_ew(&bars->o_full[t]);
+                };
+                ok = mbar_wait_warp(&bars->k_full[kc % L::kKSlots], (kc / L::kKSlots) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (w.n[t] == 0 || !ok) continue;
+                    ok = mbar_wait_warp(&bars->q_full[t], ic[t] & 1);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    issue_qk(t, 0);
+                }
+                if (ok) tc_commit_ew(&bars->k_empty[kc % L::kKSlots]);
+#pragma unroll 1
+                for (int j = 0; j < w.nst && ok; ++j) {
+                    // V(j) and K(j+1) are normally long in place, so they are waited for before P
+                    const int vs = (vc + j) % L::kVSlots, ks = (kc + j + 1) % L::kKSlots;
+                    if (j < w.first_masked) {
+                        ok = mbar_wait_warp(&bars->v_full[vs], ((vc + j) / L::kVSlots) & 1);
+                    } else {
+                        ok = mbar_wait_warp(&bars->v_clean[vs], (cleaned >> vs) & 1);
+                        cleaned ^= 1u << vs;
+                    }
+                    if (ok && j + 1 < w.nst) ok = mbar_wait_warp(&bars->k_full[ks], ((kc + j + 1) / L::kKSlots) & 1);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (j >= w.n[t] || !ok) continue;
+                        ok = mbar_wait_warp(&bars->p_full[t], (sc[t] + j) & 1);
+                        // the outputs of the tile's item before have been read
+                        if (ok && j == 0 && ic[t] > 0) ok = mbar_wait_warp(&bars->o_empty[t], (ic[t] - 1) & 1);
+                        if (!ok) continue;
+                        tc_fence_after();
+                        issue_pv(t, j);
+                        // S_t takes the place of P_t, after its product in issue order
+                        if (j + 1 < w.n[t]) issue_qk(t, j + 1);
+                    }
+                    if (!ok) break;
+                    tc_commit_ew(&bars->v_empty[vs]);
+                    if (j + 1 < w.nst) tc_commit_ew(&bars->k_empty[ks]);
+                }
+                kc += w.nst;
+                vc += w.nst;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    sc[t] += w.n[t];
+                    ic[t] += w.n[t] > 0;
+                }
+            }
+            // every MMA this warp issued has finished before the tensor memory is released
+            tc_commit_ew(&bars->drain);
+            if (!mbar_wait_warp(&bars->drain, 0)) ok = false;
+        } else if (warp == kCleanWarp) {
+            // ---------------------------------------------------------------- V of the stages with masked keys
+            int vc = 0;
+            for (Item* it; (it = items.next(ok)); items.done()) {
+                const Tiles w(it, a.tpt);
+                // every stage is followed, so that a barrier's phases cannot pass this warp by
+                for (int j = 0; j < w.nst && ok; ++j, ++vc) {
+                    const int vs = vc % L::kVSlots;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (vc / L::kVSlots) & 1));
+                    if (!ok) break;
+                    if (j >= w.first_masked) {
+                        uint8_t* tile = smem + L::kOffV + vs * L::kTile;
+                        // a pass that only reads (its loads run ahead), and only where something was found the repair
+                        uint32_t seen = 0;
+#pragma unroll 8
+                        for (int i = lane; i < L::kTile / 16; i += 32)
+                            seen |= not_finite(*reinterpret_cast<const uint4*>(tile + 16 * i));
+                        if (__any_sync(0xffffffffu, seen != 0)) {
+                            if (!it->any_bad) {  // the notes of the item before have been read
+                                if (items.n > 0)
+                                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[(items.n - 1) & 1],
+                                                                           ((items.n - 1) >> 1) & 1));
+                                if (!ok) break;
+                                for (int i = lane; i < 3 * D; i += 32) bad[i] = INT_MAX;
+                                __syncwarp();
+                                if (lane == 0) it->any_bad = 1;
+                                __syncwarp();
+                            }
+#pragma unroll 1
+                            for (int i = lane; i < L::kTile / 16; i += 32) {
+                                const int half = i / (kHalf / 16), row = i / 8 % kRows;
+                                const int col = half * 64 + ((i & 7) ^ (row & 7)) * 8;
+#pragma unroll 1
+                                for (int e = 0; e < 8; ++e) {
+                                    uint16_t* x = reinterpret_cast<uint16_t*>(tile + 16 * i) + e;
+                                    if ((*x & 0x7f80u) != 0x7f80u) continue;
+                                    const int what = (*x & 0x7fu) ? 0 : (*x & 0x8000u) ? 2 : 1;
+                                    atomicMin(&bad[what * D + col + e], j * kKeys + row);
+                                    *x = 0;
+                                }
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        mbar_arrive(&bars->v_clean[vs]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
+                }
             }
         }
-    }
     } else {
         // ---------------------------------------------------------------- softmax and outputs, one row a thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -621,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool any_bad = it->any_bad != 0;
             __nv_bfloat16* dst = a.p.out + ((size_t)(it->row + first + qi) * a.p.num_heads + it->head0 + hh) * D;
-            // Two neighbouring lanes store 64 bytes of one row together, then of the other's: half the lines a store touches.
+            // Two neighbouring lanes store 64 bytes of one row together, then of the other's: half the lines a
+            // store touches.
             const bool odd = lane & 1;
             const unsigned long long at = valid ? reinterpret_cast<unsigned long long>(dst) : 0;
             auto row_of = [&](int from) {
@@ -708,7 +720,8 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     // an upper bound of the pairs that sequences of num_tokens rows in all, and of max_len each, can have
     const long long two = 2 * t.tpt;
-    const long long pairs = std::min((a.num_tokens + a.batch * (two - 1)) / two, a.batch * ((a.max_len + two - 1) / two));
+    const long long pairs =
+        std::min((a.num_tokens + a.batch * (two - 1)) / two, a.batch * ((a.max_len + two - 1) / two));
     const long long ctas = std::max(1LL, pairs) * t.subs;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
