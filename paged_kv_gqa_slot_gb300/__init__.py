@@ -368,11 +368,16 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
     """A result tensor of t's shape, type and device, allocated for the stream that writes it."""
     if stream is None:
         return torch.empty_like(t)
+    with _on(stream, t.device):
+        return torch.empty_like(t)
+
+
+def _on(stream, device):
+    """The given stream (an object or a raw handle) as the current one, for allocations."""
     if not isinstance(stream, torch.cuda.Stream):
         raw = int(stream)
-        stream = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _width(block_tables: torch.Tensor, seq_lens: torch.Tensor, batch: int) -> int:
@@ -558,9 +563,9 @@ def _strided(t: torch.Tensor, heads: int, dim: int, name: str, device: int) -> T
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name}: need [rows, {heads}, {dim}], got {tuple(shape)}")
-    if t.dtype is not _BF16 or not t.is_cuda:
-        raise ValueError(f"{name}: need a CUDA {_BF16} tensor, got {t.dtype} on {t.device}")
-    if t.get_device() != device:
+    if t.dtype is not _BF16 or t.get_device() != device or device < 0:
+        if t.dtype is not _BF16 or not t.is_cuda:
+            raise ValueError(f"{name}: need a CUDA {_BF16} tensor, got {t.dtype} on {t.device}")
         raise ValueError(f"{name}: on cuda:{t.get_device()}, the call's other tensors are on cuda:{device}")
     row, head, one = t.stride()
     if shape[0] <= 1:
@@ -575,28 +580,26 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     """A result tensor on `like`'s device, allocated for the stream that writes it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        raw = int(stream)
-        stream = torch.cuda.ExternalStream(raw, device=like.device) if raw else torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
+    with _on(stream, like.device):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _packed(q, k, v, out, stream):
     """Check the rows of a packed call; (device, rows, heads, kv heads, dim, addresses, strides, out)."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError(f"q / k: need [rows, heads, head_dim], got {tuple(q.shape)} / {tuple(k.shape)}")
-    rows, heads, dim = q.shape
-    kvh, d = k.shape[1], q.get_device()
-    if k.shape[0] != rows or v.shape[0] != rows:
-        raise ValueError(f"q, k, v: need equal row counts, got {rows}, {k.shape[0]}, {v.shape[0]}")
+    shape, kshape = q.shape, k.shape
+    if len(shape) != 3 or len(kshape) != 3:
+        raise ValueError(f"q / k: need [rows, heads, head_dim], got {tuple(shape)} / {tuple(kshape)}")
+    rows, heads, dim = shape
+    kvh, d = kshape[1], q.get_device()
+    if kshape[0] != rows or v.shape[0] != rows:
+        raise ValueError(f"q, k, v: need equal row counts, got {rows}, {kshape[0]}, {v.shape[0]}")
     qp, qs = _strided(q, heads, dim, "q", d)
     kp, ks = _strided(k, kvh, dim, "k", d)
     vp, vs = _strided(v, kvh, dim, "v", d)
     if out is None:
-        out = _new(q, (rows, heads, dim), _BF16, stream)
-    elif out.shape != q.shape:
-        raise ValueError(f"out: need shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        out = _new(q, shape, _BF16, stream)
+    elif out.shape != shape:
+        raise ValueError(f"out: need shape {tuple(shape)}, got {tuple(out.shape)}")
     return d, rows, heads, kvh, dim, (qp, kp, vp), (qs, ks, vs), out
 
 
@@ -624,12 +627,12 @@ def pa_kv_grow(block_tables: torch.Tensor, seq_lens: torch.Tensor, new_lens: tor
     d, rows = block_tables.get_device(), int(max_tokens)
     if rows < 0:
         raise ValueError(f"max_tokens: need 0 or more, got {rows}")
-    lens = seq_lens if in_place else _new(seq_lens, (B,), _I32, stream)
-    left = num_free if in_place else _new(num_free, num_free.shape, _I32, stream)
+    lens = seq_lens if in_place else _like(seq_lens, stream)
+    left = num_free if in_place else _like(num_free, stream)
     cu = _new(block_tables, (B + 1,), _I32, stream)
     slots = _new(block_tables, (rows,), _I64, stream)
-    more = _new(block_tables, (2, rows), _I32, stream)
-    positions, token_seqs = more[0], more[1]
+    positions = _new(block_tables, (rows,), _I32, stream)
+    token_seqs = _new(block_tables, (rows,), _I32, stream)
     _call("pa_kv_grow", d, stream, _arg(block_tables, _I32, "block_tables", d), width, _arg(seq_lens, _I32, "seq_lens", d),
           _arg(new_lens, _I32, "new_lens", d), B, _arg(free_blocks, _I32, "free_blocks", d), free_blocks.numel(),
           _arg(num_free, _I32, "num_free", d), rows, lens.data_ptr(), left.data_ptr(), cu.data_ptr(),
@@ -645,7 +648,7 @@ def pa_kv_free(ids: torch.Tensor, counts: torch.Tensor, free_blocks: torch.Tenso
         raise ValueError(f"ids / counts / num_free: need [rows, width] / [rows] / [1], got {tuple(ids.shape)} / "
                          f"{tuple(counts.shape)} / {tuple(num_free.shape)}")
     d = free_blocks.get_device()
-    left = num_free if in_place else _new(num_free, num_free.shape, _I32, stream)
+    left = num_free if in_place else _like(num_free, stream)
     _call("pa_kv_free", d, stream, _arg(ids, _I32, "ids", d), _arg(counts, _I32, "counts", d), ids.shape[0],
           ids.shape[1], _arg(free_blocks, _I32, "free_blocks", d), free_blocks.numel(),
           _arg(num_free, _I32, "num_free", d), left.data_ptr())
@@ -654,7 +657,8 @@ def pa_kv_free(ids: torch.Tensor, counts: torch.Tensor, free_blocks: torch.Tenso
 
 def _linear_state(state, kvh, dim, state_slots, log_decay, seq_lens, batch, device):
     """Check the state pool and the arrays beside it; their addresses."""
-    if state.dim() != 4 or tuple(state.shape[1:]) != (kvh, dim, dim):
+    shape = state.shape
+    if len(shape) != 4 or shape[1] != kvh or shape[2] != dim or shape[3] != dim:
         raise ValueError(f"state: need [num_slots, {kvh}, {dim}, {dim}], got {tuple(state.shape)}")
     if state_slots.shape != (batch,) or seq_lens.shape != (batch,) or log_decay.shape != (kvh,):
         raise ValueError(f"state_slots / seq_lens / log_decay: need shapes {(batch,)} / {(batch,)} / {(kvh,)}, got "
@@ -688,7 +692,11 @@ def pa_linear_prefill(state: torch.Tensor, state_slots: torch.Tensor, q: torch.T
     d, rows, heads, kvh, dim, p, s, out = _packed(q, k, v, out, stream)
     B = cu_q_lens.numel() - 1
     st, slots, decay, lens = _linear_state(state, kvh, dim, state_slots, log_decay, seq_lens, B, d)
-    need = pa_linear_workspace_bytes(B, kvh, dim, int(max_chunk))
+    if _current_device() == d:
+        need = pa_linear_workspace_bytes(B, kvh, dim, int(max_chunk))
+    else:  # (a device of more SMs cuts sequences into more segments)
+        with torch.cuda.device(d):
+            need = pa_linear_workspace_bytes(B, kvh, dim, int(max_chunk))
     if workspace is None:
         workspace = _new(q, ((need + 3) // 4,), _F32, stream)
     elif workspace.numel() * workspace.element_size() < need:

@@ -14,8 +14,8 @@
 //
 // S stays in tensor memory in fp32 (lane: row of k, column: column of v).  Each chunk it is read once,
 // written to shared memory as bf16 (the operand of Q S: one rounding, as the scores have) and back,
-// multiplied by a^n, for K~^T V to add to.  K~ enters as two bf16 parts (2^-16 of every term), since what
-// it adds stays in the state.
+// multiplied by a^n, for K~^T V to add to.  K~ enters as three bf16 parts, all 24 bits, since what it
+// adds stays in the state (two parts: 2^-16 of every term).
 //
 // Masked rows of P are zero, and 0 times a NaN or an infinity in V is NaN: V is looked over when it
 // arrives, what is not finite becomes 0, and the first token it was seen at is noted per column; from
@@ -58,32 +58,39 @@ struct Item {
     int any_bad;         // a value of V was not finite
 };
 
-template <int D>
+template <int D, bool kGather>
 struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + kTile;        // two tiles; each becomes the high parts of K~ in place
-    static constexpr int kOffLo = kOffK + 2 * kTile;   // the low parts
-    static constexpr int kOffV = kOffLo + kTile;       // two tiles
-    static constexpr int kOffS = kOffV + 2 * kTile;    // the state, bf16, D rows
-    static constexpr int kOffBars = kOffS + D * 128 * kHalves;
+    // K~ is written and multiplied in pieces, as shared memory has no room for all of its middle and low parts beside
+    // the rest (it has where only they are needed).
+    static constexpr int kPieces = kGather ? 1 : 2;
+    static constexpr int kRows = kChunk / kPieces;
+    static constexpr int kPart = kRows * 128;              // [rows of a piece][64 columns] of the middle or low parts
+    static constexpr int kOffK = 0;                        // two tiles; each becomes the high parts of K~ in place
+    static constexpr int kOffMid = kOffK + 2 * kTile;
+    static constexpr int kOffLow = kOffMid + kHalves * kPart;
+    static constexpr int kOffV = kOffLow + kHalves * kPart;  // two tiles
+    static constexpr int kOffQ = kOffV + 2 * kTile;
+    static constexpr int kOffS = kOffQ + (kGather ? 0 : kTile);  // the state, bf16, D rows
+    static constexpr int kOffBars = kOffS + (kGather ? 0 : D * 128 * kHalves);
     static constexpr int kOffItem = kOffBars + 384;    // two items
     static constexpr int kOffTab = kOffItem + 128;     // [2][32] a^31 .. a^0
     static constexpr int kOffBad = kOffTab + 256;      // [2][D] first token of a column with a value that is not finite
     static constexpr int kSmem = kOffBad + 2 * D * 4;
-    // tensor memory: scores and P, P V, Q S, the state
-    static constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = kColO1 + D, kColU = kColO2 + D;
+    // tensor memory: scores and P; the outputs; K~^T V (gather: of the high parts, and of the others); the state
+    static constexpr uint32_t kColP = 0, kColO = 128, kColU = kColO + D, kColU2 = kColU + D, kColS = kColU2;
     static constexpr int kTmemCols = 512;
 };
-static_assert(Layout<128>::kSmem <= 227 * 1024, "shared memory");
+static_assert(Layout<128, false>::kSmem <= 227 * 1024, "shared memory");
 static_assert(sizeof(Item) <= 64, "item");
 
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
-    uint64_t s_full, p_full, o_full, o_empty;  // scores, P, outputs ready; outputs read
-    uint64_t k_raw;                            // Q K^T of the chunk is done, K may become K~ (gather: K~^T V is done)
-    uint64_t kt_full, st_full, u_full;         // K~ ready; the state ready for the chunk; K~^T V done
+    uint64_t s_full, qs_full, p_full, o_full, o_empty;  // scores, Q S, P with Q S weighted, outputs ready; outputs read
+    uint64_t k_raw, piece;                     // K may become K~: Q K^T of the chunk is done (gather: K~^T V of the
+                                               // chunk before); K~^T V of its first piece is done
+    uint64_t kt_full, st_full, u_full;         // a piece of K~ ready; the state ready for the chunk; K~^T V done
     uint64_t item_full[2], item_empty[2], soon, next, drain;
     uint4 reply;                               // of clusterlaunchcontrol
     uint32_t tmem_base;
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                                                              const __grid_constant__ CUtensorMap tm_k,
                                                              const __grid_constant__ CUtensorMap tm_v,
                                                              const __grid_constant__ TcArgs a) {
-    using L = Layout<D>;
+    using L = Layout<D, kGather>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBars);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, r = threadIdx.x & 127;
@@ -176,10 +183,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->qs_full, 1);
         mbar_init(&bars->p_full, 128);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_empty, 128);
         mbar_init(&bars->k_raw, 1);
+        mbar_init(&bars->piece, 1);
         mbar_init(&bars->kt_full, 128);
         mbar_init(&bars->st_full, 128);
         mbar_init(&bars->u_full, 1);
@@ -318,8 +327,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint64_t sd = smem_desc_sw128(smem_u32(smem + L::kOffS), D * 128, 1024);
         // K~^T as A: at d = 64 its rows 64 .. 127 are whatever lies behind the tile, in lanes that nobody reads
         const uint64_t hd0 = smem_desc_sw128(smem_u32(smem + L::kOffK), kHalf, 1024);
-        const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLo), kHalf, 1024);
+        const uint64_t md = smem_desc_sw128(smem_u32(smem + L::kOffMid), L::kPart, 1024);
+        const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLow), L::kPart, 1024);
         int cc = 0, ii = 0;  // chunks and chunks' heads so far
+        // K~^T V over a piece of K~, V from where its chunk's tiles begin; `first`: from zero.  The small parts come
+        // first, or into sums of their own: the tensor core cuts every sum off to 24 bits.
+        auto issue_u = [&](int piece, uint64_t hd, uint64_t vd, bool first) {
+            const uint32_t small = tmem + (kGather ? L::kColU2 : L::kColU);
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+#pragma unroll
+                for (int kk = 0; kk < L::kRows / 16; ++kk) {
+                    const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4), all = off + (uint64_t)((piece * L::kPart) >> 4);
+                    tc_mma_ew(part == 2 ? tmem + L::kColU : small, part == 0 ? ld + off : part == 1 ? md + off : hd + all,
+                              vd + all, idesc_u, first && kk == 0 && (part == 0 || (kGather && part == 2)) ? 0u : 1u);
+                }
+            }
+        };
         for (const Item* it; (it = items.next(ok)); items.done()) {
             // (uniform, and with it all that is counted here)
             const int chunks = __shfl_sync(0xffffffffu, it->chunks, 0);
@@ -338,40 +362,42 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                         }
                         tc_commit_ew(&bars->s_full);
                         if (h == g - 1) tc_commit_ew(&bars->k_raw);
-                        // Q S, once the state is in shared memory and the outputs before are read
+                        // Q S, once the state is in shared memory (K~^T V before has been read) and the outputs before are
                         if (h == 0) ok = mbar_wait_warp(&bars->st_full, cc & 1);
                         if (ok && ii > 0) ok = mbar_wait_warp(&bars->o_empty, (ii - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            tc_mma_ew(tmem + L::kColO2, qd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                            tc_mma_ew(tmem + L::kColO, qd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
                                       sd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
+                        tc_commit_ew(&bars->qs_full);
                         tc_commit_ew(&bars->q_empty);
                         if (h == 0) ok = mbar_wait_warp(&bars->v_clean[cc & 1], (cc >> 1) & 1);
+                        if (h == g - 1) {  // the first piece of K~, and the second is written under P V
+                            if (ok) ok = mbar_wait_warp(&bars->kt_full, 0);
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_u(0, hd0 + slot, vd, true);
+                            tc_commit_ew(&bars->piece);
+                        }
                         if (ok) ok = mbar_wait_warp(&bars->p_full, ii & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < kChunk / 16; ++kk)
-                            tc_mma_ts_ew(tmem + L::kColO1, tmem + L::kColP + kk * 8,
-                                         vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, kk > 0 ? 1u : 0u);
+                            tc_mma_ts_ew(tmem + L::kColO, tmem + L::kColP + kk * 8,
+                                         vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_o, 1u);
                         tc_commit_ew(&bars->o_full);
                     }
                 } else {
                     if (c == 0) ok = mbar_wait_warp(&bars->st_full, items.n & 1);  // the item before has been read
                     if (ok) ok = mbar_wait_warp(&bars->v_full[cc & 1], (cc >> 1) & 1);
                 }
-                if (ok) ok = mbar_wait_warp(&bars->kt_full, cc & 1);
+                if (ok) ok = mbar_wait_warp(&bars->kt_full, kGather ? cc & 1 : 1);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kChunk / 16; ++kk) {
-                    const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
-                    tc_mma_ew(tmem + L::kColU, hd0 + slot + off, vd + off, idesc_u,
-                              !kGather || c > 0 || kk > 0 ? 1u : 0u);
-                    tc_mma_ew(tmem + L::kColU, ld + off, vd + off, idesc_u, 1u);
-                }
+                issue_u(L::kPieces - 1, hd0 + slot, vd, kGather && c == 0);
                 if (!kGather || c + 1 == chunks) tc_commit_ew(&bars->u_full);
                 if (kGather) tc_commit_ew(&bars->k_raw);
                 tc_commit_ew(&bars->k_empty[cc & 1]);
@@ -426,64 +452,87 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             const float la = it->la;
             for (int c = 0; c < chunks && ok; ++c, ++cc) {
                 const int n = min(kChunk, len - c * kChunk);
-                if (!kGather) {  // (it also means that the products with the low parts of the chunk before are done)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, cc & 1));
-                } else {
-                    // Not while the products of the chunk before run: with K~ written beside them (and two tiles of
-                    // low parts) about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of its
-                    // operands in place and its commits outstanding until the waits ran out; in turn it has not been
-                    // seen (2 10^6 calls), and is faster too (1 x 20000 tokens 191 us against 225).
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
-                    if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
-                }
-                if (!ok) break;
                 // weighted to the end of the chunk, or of the segment
                 const int left = kGather ? len - c * kChunk : n;
-                const float w = r < n ? fast_exp2((float)(left - 1 - r) * la) : 0.f;
-                uint8_t* hi = smem + L::kOffK + (cc & 1) * L::kTile + r * 128;
-                uint8_t* lo = smem + L::kOffLo + r * 128;
+                // a thread: a row of the piece, and of its 16-byte parts all or one half
+                constexpr int kParts = D / 8 / L::kPieces;
+                const int pr = r & (L::kRows - 1), first = r / L::kRows * kParts;
 #pragma unroll 1
-                for (int i0 = 0; i0 < D / 8; i0 += 4) {
-                    uint4 in[4];  // four loads in flight together
-                    const int base = (i0 >> 3) * kHalf;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        in[i] = r < n ? *reinterpret_cast<const uint4*>(hi + base + ((((i0 & 7) + i) ^ (r & 7)) << 4))
-                                      : make_uint4(0u, 0u, 0u, 0u);  // rows past the sequence's end are not its own
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int off = base + ((((i0 & 7) + i) ^ (r & 7)) << 4);
-                        uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, lw[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float f0, f1;
-                            mul_x2(f0, f1, bf16_lo(x[e]), bf16_hi(x[e]), w, w);
-                            x[e] = pack_bf16x2(f0, f1);
-                            lw[e] = pack_bf16x2(f0 - bf16_lo(x[e]), f1 - bf16_hi(x[e]));
-                        }
-                        *reinterpret_cast<uint4*>(hi + off) = make_uint4(x[0], x[1], x[2], x[3]);
-                        *reinterpret_cast<uint4*>(lo + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                for (int piece = 0; piece < L::kPieces && ok; ++piece) {
+                    if (kGather) {
+                        // Not while the products of the chunk before run: with K~ written beside them (and two tiles of
+                        // low parts) about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of
+                        // its operands in place and its commits outstanding until the waits ran out; in turn it has not
+                        // been seen (5 10^6 calls), and is faster too.
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
+                        if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
+                    } else {  // (the first: it also means that the products of the chunk before are done)
+                        ok = __all_sync(0xffffffffu, mbar_wait(piece ? &bars->piece : &bars->k_raw, cc & 1));
                     }
+                    if (!ok) break;
+                    const int row = piece * L::kRows + pr;
+                    const float w = row < n ? fast_exp2((float)(left - 1 - row) * la) : 0.f;
+                    uint8_t* hi = smem + L::kOffK + (cc & 1) * L::kTile + row * 128;
+                    uint8_t* mid = smem + L::kOffMid + pr * 128;
+                    uint8_t* low = smem + L::kOffLow + pr * 128;
+#pragma unroll 1
+                    for (int i0 = first; i0 < first + kParts; i0 += 4) {
+                        uint4 in[4];  // four loads in flight together
+                        const int half = i0 >> 3;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            in[i] = row < n ? *reinterpret_cast<const uint4*>(
+                                                  hi + half * kHalf + ((((i0 & 7) + i) ^ (row & 7)) << 4))
+                                            : make_uint4(0u, 0u, 0u, 0u);  // rows past the sequence's end are not its own
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = (((i0 & 7) + i) ^ (row & 7)) << 4;
+                            uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, m[4], l[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {  // (the differences are exact)
+                                float f0, f1;
+                                mul_x2(f0, f1, bf16_lo(x[e]), bf16_hi(x[e]), w, w);
+                                x[e] = pack_bf16x2(f0, f1);
+                                f0 -= bf16_lo(x[e]);
+                                f1 -= bf16_hi(x[e]);
+                                m[e] = pack_bf16x2(f0, f1);
+                                l[e] = pack_bf16x2(f0 - bf16_lo(m[e]), f1 - bf16_hi(m[e]));
+                            }
+                            *reinterpret_cast<uint4*>(hi + half * kHalf + at) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4*>(mid + half * L::kPart + at) = make_uint4(m[0], m[1], m[2], m[3]);
+                            *reinterpret_cast<uint4*>(low + half * L::kPart + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars->kt_full);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars->kt_full);
             }
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- the state: row r of S
-        const uint32_t tm_u = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::kColU;
+        const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const bool mine = r < D;
         uint8_t* ss = smem + L::kOffS + r * 128;
         int uc = 0;  // completed K~^T V that this role has waited for
+        // S <- f S + K~^T V, columns x .. x + 31 (gather: the sums of the high parts and of the others)
+        auto step = [&](uint32_t (&s)[32], int x, float f) {
+            uint32_t u[32];
+            tmem_ld32_async(tm + L::kColS + x, s);
+            tmem_ld32_async(tm + L::kColU + x, u);
+            tmem_wait_ld(s);
+            tmem_wait_ld(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), f, __uint_as_float(u[e])));
+        };
         for (const Item* it; (it = items.next(ok)); items.done()) {
             const int chunks = it->chunks, len = it->len;
             const float la = it->la;
+            float f = 1.f;  // the decay over the chunk before
             if (kGather) {
                 tc_fence_before();
                 mbar_arrive(&bars->st_full);
             }
             for (int c = 0; c < (kGather ? 0 : chunks); ++c) {
-                const float f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
                 const float* from = it->begin;
                 if (c > 0) {
                     ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
@@ -491,51 +540,46 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 }
                 if (!ok) break;
                 tc_fence_after();
-                auto take = [&](uint32_t (&u)[32], int x) {  // as bf16 for Q S, and back times a^n
-                    if (mine) {
+                auto take = [&](uint32_t (&s)[32], int x) {  // kept, and as bf16 for Q S
+                    tmem_st32_nowait(tm + L::kColS + x, s);
+                    if (!mine) return;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                w[q] = pack_bf16x2(__uint_as_float(u[e + 2 * q]), __uint_as_float(u[e + 2 * q + 1]));
-                            const int chunk = (x + e) >> 3;
-                            *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = pack_bf16x2(__uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
+                        const int chunk = (x + e) >> 3;
+                        *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-                    tmem_st32_nowait(tm_u + x, u);
                 };
                 if (c > 0) {
 #pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
-                        uint32_t u[32];
-                        tmem_ld32(tm_u + x, u);
-                        take(u, x);
+                        uint32_t s[32];
+                        step(s, x, f);
+                        take(s, x);
                     }
                 } else {
                     const bool there = mine && from;
                     const float* row = from + (size_t)r * D;
                     const bool wide = (reinterpret_cast<uintptr_t>(from) & 31u) == 0;
-                    auto load = [&](uint32_t (&u)[32], int x) {
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t s[32];
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             if (there)
-                                load_32(row + x + e, u + e, wide);
+                                load_32(row + x + e, s + e, wide);
                             else
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) u[e + i] = 0u;
+                                for (int i = 0; i < 8; ++i) s[e + i] = 0u;
                         }
-                    };
-#pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t u[32];
-                        load(u, x);
-                        take(u, x);
+                        take(s, x);
                     }
                 }
+                f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
                 tmem_wait_st();
                 tc_fence_before();
                 fence_proxy_async_smem();
@@ -550,11 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             const bool wide = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
-                uint32_t u[32];
-                tmem_ld32(tm_u + x, u);
+                uint32_t s[32];
+                step(s, x, f);
                 if (mine) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) store_32(to + (size_t)r * D + x + e, u + e, wide);
+                    for (int e = 0; e < 32; e += 8) store_32(to + (size_t)r * D + x + e, s + e, wide);
                 }
             }
             if (!kGather && it->any_bad && mine) {
@@ -631,6 +675,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     tmem_st8_nowait(tm + L::kColP + x / 2, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
                     tmem_st8_nowait(tm + L::kColP + x / 2 + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
                 }
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->qs_full, ii & 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {  // Q S weighted, for P V to add to
+                    uint32_t o[32];
+                    tmem_ld32(tm + L::kColO + x, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * lead);
+                    tmem_st32_nowait(tm + L::kColO + x, o);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars->p_full);
@@ -647,15 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 const size_t step = (size_t)p.num_heads * D;
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
-                    uint32_t o1[32], o2[32], v[16], w0[8], w1[8];
-                    tmem_ld32_async(tm + L::kColO1 + x, o1);
-                    tmem_ld32_async(tm + L::kColO2 + x, o2);
-                    tmem_wait_ld(o1);
-                    tmem_wait_ld(o2);
+                    uint32_t o[32], v[16], w0[8], w1[8];
+                    tmem_ld32(tm + L::kColO + x, o);
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        v[e] = pack_bf16x2(fmaf(__uint_as_float(o2[2 * e]), lead, __uint_as_float(o1[2 * e])),
-                                           fmaf(__uint_as_float(o2[2 * e + 1]), lead, __uint_as_float(o1[2 * e + 1])));
+                        v[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[8 + e], 1);
@@ -751,10 +802,11 @@ template <int D>
 cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     static OncePerDevice configured;
     const cudaError_t e = configured.run([] {
-        cudaError_t r = cudaSuccess;
-        for (const void* fn : {(const void*)linear_kernel<D, false>, (const void*)linear_kernel<D, true>})
-            if (r == cudaSuccess)
-                r = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kSmem);
+        cudaError_t r = cudaFuncSetAttribute((const void*)linear_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Layout<D, false>::kSmem);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute((const void*)linear_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Layout<D, true>::kSmem);
         return r;
     });
     if (e != cudaSuccess) return e;
@@ -770,21 +822,21 @@ cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     t.seg_chunks = (chunks + segs - 1) / segs;
     t.segs = (chunks + t.seg_chunks - 1) / t.seg_chunks;
     CUtensorMap q, k, v;
-    if (!strided_map(&q, p.q, p.num_tokens, p.num_heads, D, p.q_stride, 1, kChunk, Layout<D>::kHalves) ||
-        !strided_map(&k, p.k, p.num_tokens, p.num_kv_heads, D, p.k_stride, 1, kChunk, Layout<D>::kHalves) ||
-        !strided_map(&v, p.v, p.num_tokens, p.num_kv_heads, D, p.v_stride, 1, kChunk, Layout<D>::kHalves))
+    if (!strided_map(&q, p.q, p.num_tokens, p.num_heads, D, p.q_stride, 1, kChunk, D / 64) ||
+        !strided_map(&k, p.k, p.num_tokens, p.num_kv_heads, D, p.k_stride, 1, kChunk, D / 64) ||
+        !strided_map(&v, p.v, p.num_tokens, p.num_kv_heads, D, p.v_stride, 1, kChunk, D / 64))
         return cudaErrorInvalidValue;
     const long long pairs = (long long)p.batch * p.num_kv_heads;
     if (pairs * t.segs > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<D>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (t.segs > 1) {
         cfg.gridDim = dim3((unsigned)(pairs * (t.segs - 1)));
+        cfg.dynamicSmemBytes = Layout<D, true>::kSmem;
         cudaError_t r = cudaLaunchKernelEx(&cfg, linear_kernel<D, true>, q, k, v, t);
         if (r != cudaSuccess) return r;
         cudaLaunchConfig_t carry = cfg;
@@ -795,6 +847,7 @@ cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
         if (r != cudaSuccess) return r;
     }
     cfg.gridDim = dim3((unsigned)(pairs * t.segs));
+    cfg.dynamicSmemBytes = Layout<D, false>::kSmem;
     return cudaLaunchKernelEx(&cfg, linear_kernel<D, false>, q, k, v, t);
 }
 

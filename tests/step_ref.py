@@ -106,7 +106,8 @@ def linear_bounds(ref, size, new_size, n, one_token=False):
     """Outputs: half a bf16 step of the result; the scores, and S where q reads it, as bf16 (2^-8 of every term)
     unless the call is for one token; the error that S itself has (below 2^-16 of sum a^.. |k| |v|, taken as 2^-12
     of the terms), and fp32 sums (each of n + 2 d additions up to 2^-22 of the terms' size).
-    State: k's weighted rows as two bf16 parts, 2^-16 of every term, and the sums."""
+    State: the decays' exponents, products of two fp32 numbers and up to 126 where the term does not vanish, 2^-16 of
+    every term, and the sums."""
     sums = (n + 256) * 2.0 ** -22
     out = 2.0 ** -8 * ref.abs() + ((0 if one_token else 2.0 ** -8 + 2.0 ** -12) + sums) * size + 1e-30
     return out, ((0 if one_token else 2.0 ** -16) + sums) * new_size + 1e-30

@@ -53,6 +53,20 @@ def test_segments_end_in_any_order():
 
 
 @gpu
+@pytest.mark.parametrize("lens,d", [([640, 1], 128), ([3000], 128), ([640, 70], 64), ([2600], 64)])
+def test_the_state_keeps_32_bits(lens, d):
+    """Its error's size against its own: the parts of k's weighted rows 2^-24, the exponents (up to 6 where a term
+    counts) 2^-21, the sums, 8 a chunk of up to 24 chunks, 2^-24 each and of either sign, 2^-20.2: below 2^-19.5
+    together, where two bf16 parts would leave 2^-18 of the terms' size."""
+    c = Case(48, lens, 2, 2, d, decay=-0.012)
+    _, _, new, _ = c.reference()
+    c.prefill()
+    off, size = (c.state.double() - new)[c.slots.long()], new[c.slots.long()]
+    assert float(off.square().mean().sqrt()) <= 2.0 ** -19.5 * float(size.square().mean().sqrt())
+    clean()
+
+
+@gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_arrays_aligned_to_16_bytes_and_no_more(d):
     def moved(x, by):
