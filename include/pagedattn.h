@@ -393,8 +393,9 @@ int pa_kv_free(const int32_t *ids, const int32_t *counts, int32_t rows, int32_t 
  * state as it is.  Rows outside every sequence stay as they are; rows past max_chunk, a sequence with
  * fewer tokens than rows and one whose rows are not within [0, num_tokens] as in pa_prefill_packed.
  * Both keep S in fp32 throughout; the prefill's products take q, k and v as they are, the scores and S
- * (where q reads it) as bf16, and k's weighted rows (where S gathers them) as two bf16 parts.  A NaN or an
- * infinity in a row of v concerns its column from that row on, which may turn NaN as a whole.
+ * (where q reads it) as bf16, and k's weighted rows (where S gathers them) in full, as three bf16
+ * parts.  A NaN or an infinity in a row of v concerns its column from that row on, which may turn NaN
+ * as a whole.
  *   workspace      pa_linear_workspace_bytes(...) bytes, 16-byte aligned (may be NULL where that is 0),
  *                  not shared by calls that may run at the same time; nothing in it outlives the call
  * head_dim 64 or 128, any group size, batch <= 65535.

@@ -7,15 +7,23 @@
 //   S'  = a^n S + sum_j (a^{n-1-j} k_j) v_j^T
 // that is four products on the tensor core: Q K^T, P V (P the weighted, masked scores), Q S and K~^T V
 // (K~ the weighted keys).  The powers enter as 2^{(i-j) log2 a} <= 1, so nothing overflows however
-// strong the decay.  A token moves (2 heads + 2 kv heads) d 2 bytes; per SM and 128 tokens of one head that is
-// 128 KB, about 5900 cycles of HBM time at d = 128, against 2600 of tensor core and 4400 of shared-memory
-// bandwidth (the operands of four products, the copies, K~ and S): HBM bounds it, as long as the chain of
-// one chunk (Q K^T, K~, K~^T V, S) stays below.
+// strong the decay.
 //
-// S stays in tensor memory in fp32 (lane: row of k, column: column of v).  Each chunk it is read once,
-// written to shared memory as bf16 (the operand of Q S: one rounding, as the scores have) and back,
-// multiplied by a^n, for K~^T V to add to.  K~ enters as three bf16 parts, all 24 bits, since what it
-// adds stays in the state (two parts: 2^-16 of every term).
+// Rounding.  P and S enter their products as bf16, one rounding of every term, as the outputs are bf16.  What is
+// added to S stays there, so K~ enters as three bf16 parts, all 24 bits of it; and since the tensor core cuts its
+// sums off instead of rounding them, K~^T V is summed from zero, the small parts first, and added to a^n S by the
+// threads in fp32.  The state is then within 2.5e-7 of 64 bits (two parts 2.4e-6; three, added to S by the tensor
+// core, 1.0e-6: 16 heads, chunks of up to 1100 tokens).
+//
+// What bounds it.  A token moves (2 heads + 2 kv heads) d 2 bytes; per SM and 128 tokens of one head that is
+// 128 KB, about 5900 cycles of HBM time at d = 128, against 2800 of tensor core and 5000 of shared-memory
+// bandwidth (the operands of the products, the copies, K~ and S).  A chunk takes 6300: shared memory, and the
+// chain K~^T V, S, Q K^T, K~, which leaves the copies little slack.  152 states x 1024 tokens 36.6 us (4.9 TB/s,
+// 34.0 with two parts); 24 sequences of up to 1100 tokens, 16 heads, 77.6; 1 x 20000 tokens, 32 heads, 212.
+//
+// S stays in tensor memory in fp32 (lane: row of k, column: column of v).  Each chunk it is read once with the
+// sums of the chunk before, and written back there and to shared memory as bf16.  Q S is read back, weighted by
+// a^{i+1}, and P V added to it, which leaves room for the sums of K~^T V.
 //
 // Masked rows of P are zero, and 0 times a NaN or an infinity in V is NaN: V is looked over when it
 // arrives, what is not finite becomes 0, and the first token it was seen at is noted per column; from
@@ -24,13 +32,14 @@
 // Few sequences leave most SMs idle, so a long one is cut into segments: first every segment but the last
 // gathers what its own tokens add to the state (K~^T V alone, weighted to the segment's end), then one pass
 // over the states turns these into what each segment begins with, and then all segments run at once.  It
-// costs a second read of K and V.
+// costs a second read of K and V (1 x 20000 tokens, 32 heads, whole: 500 us).
 //
 // An item is one (segment, sequence, kv head).  A CTA, one an SM, takes item after item: near the end of
 // one it asks for a block of the grid that has not started (clusterlaunchcontrol), so that the
 // copies of the next item run under the end of this one.  Warps: 0-3 P and the outputs (one row a
-// thread), 4-7 the state (one row a thread), 8-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and
+// thread), 4-7 the state (one row a thread), 4-11 K~, 12 MMA issue and tensor memory, 13 TMA loads of K and
 // V, 14 of Q (one thread issues a copy in about half a microsecond), 15 the look at V, 16 the items.
+// (K~ by warps 8-11 alone: 1 x 20000 218 us.  Copies sent to L2 a chunk ahead: 24 sequences 83 us against 80.)
 // The loops over column blocks are not unrolled and rare paths are short: the roles run at the same time, and
 // their code has to fit the instruction cache together (152 states x 1024 tokens took 52 us unrolled, 36 rolled up).
 #include <algorithm>
@@ -63,7 +72,8 @@ struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalf;
     // K~ is written and multiplied in pieces, as shared memory has no room for all of its middle and low parts beside
-    // the rest (it has where only they are needed).
+    // the rest (it has where nothing else is needed).  With V in one tile instead 1 x 20000 tokens take 232 us against
+    // 221, with the low parts over S 230.
     static constexpr int kPieces = kGather ? 1 : 2;
     static constexpr int kRows = kChunk / kPieces;
     static constexpr int kPart = kRows * 128;              // [rows of a piece][64 columns] of the middle or low parts
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         mbar_init(&bars->o_empty, 128);
         mbar_init(&bars->k_raw, 1);
         mbar_init(&bars->piece, 1);
-        mbar_init(&bars->kt_full, 128);
+        mbar_init(&bars->kt_full, 256);
         mbar_init(&bars->st_full, 128);
         mbar_init(&bars->u_full, 1);
         mbar_init(&bars->soon, 1);
@@ -338,9 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             for (int part = 0; part < 3; ++part) {
 #pragma unroll
                 for (int kk = 0; kk < L::kRows / 16; ++kk) {
-                    const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4), all = off + (uint64_t)((piece * L::kPart) >> 4);
-                    tc_mma_ew(part == 2 ? tmem + L::kColU : small, part == 0 ? ld + off : part == 1 ? md + off : hd + all,
-                              vd + all, idesc_u, first && kk == 0 && (part == 0 || (kGather && part == 2)) ? 0u : 1u);
+                    const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
+                    const uint64_t all = off + (uint64_t)((piece * L::kPart) >> 4);
+                    const uint64_t from = part == 0 ? ld + off : part == 1 ? md + off : hd + all;
+                    const bool zero = first && kk == 0 && (part == 0 || (kGather && part == 2));
+                    tc_mma_ew(part == 2 ? tmem + L::kColU : small, from, vd + all, idesc_u, zero ? 0u : 1u);
                 }
             }
         };
@@ -362,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                         }
                         tc_commit_ew(&bars->s_full);
                         if (h == g - 1) tc_commit_ew(&bars->k_raw);
-                        // Q S, once the state is in shared memory (K~^T V before has been read) and the outputs before are
+                        // Q S, once the state is in shared memory (and K~^T V before has been read), and the
+                        // outputs before have been read
                         if (h == 0) ok = mbar_wait_warp(&bars->st_full, cc & 1);
                         if (ok && ii > 0) ok = mbar_wait_warp(&bars->o_empty, (ii - 1) & 1);
                         if (!ok) break;
@@ -444,26 +457,98 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 mbar_arrive(&bars->v_clean[cc & 1]);
             }
         }
-    } else if (warp >= 8) {
-        // ---------------------------------------------------------------- K weighted: row r of the chunk
-        int cc = 0;
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------- the state (warps 4-7, row r of S), K weighted
+        const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool mine = r < D;
+        uint8_t* ss = smem + L::kOffS + r * 128;
+        const bool keeps = warp < 8;
+        int cc = 0, uc = 0;  // chunks; completed K~^T V that the state has waited for
+        // S <- f S + K~^T V, columns x .. x + 31 (gather: the sums of the high parts and of the others)
+        auto step = [&](uint32_t (&s)[32], int x, float f) {
+            uint32_t u[32];
+            tmem_ld32_async(tm + L::kColS + x, s);
+            tmem_ld32_async(tm + L::kColU + x, u);
+            tmem_wait_ld(s);
+            tmem_wait_ld(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), f, __uint_as_float(u[e])));
+        };
         for (const Item* it; (it = items.next(ok)); items.done()) {
             const int chunks = it->chunks, len = it->len;
             const float la = it->la;
+            float f = 1.f;  // the decay over the chunk before
+            if (kGather && keeps) {
+                tc_fence_before();
+                mbar_arrive(&bars->st_full);
+            }
             for (int c = 0; c < chunks && ok; ++c, ++cc) {
+                if (!kGather && keeps) {
+                    const float* from = it->begin;
+                    if (c > 0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
+                        ++uc;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    auto take = [&](uint32_t (&s)[32], int x) {  // kept, and as bf16 for Q S
+                        tmem_st32_nowait(tm + L::kColS + x, s);
+                        if (!mine) return;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                w[q] = pack_bf16x2(__uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
+                            const int chunk = (x + e) >> 3;
+                            *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    };
+                    if (c > 0) {
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t s[32];
+                            step(s, x, f);
+                            take(s, x);
+                        }
+                    } else {
+                        const bool there = mine && from;
+                        const float* row = from + (size_t)r * D;
+                        const bool wide = (reinterpret_cast<uintptr_t>(from) & 31u) == 0;
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t s[32];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                if (there)
+                                    load_32(row + x + e, s + e, wide);
+                                else
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) s[e + i] = 0u;
+                            }
+                            take(s, x);
+                        }
+                    }
+                    f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars->st_full);
+                }
                 const int n = min(kChunk, len - c * kChunk);
                 // weighted to the end of the chunk, or of the segment
                 const int left = kGather ? len - c * kChunk : n;
-                // a thread: a row of the piece, and of its 16-byte parts all or one half
-                constexpr int kParts = D / 8 / L::kPieces;
-                const int pr = r & (L::kRows - 1), first = r / L::kRows * kParts;
+                // a thread: of a row of the piece kParts of its 16-byte parts, kStep loads in flight together
+                constexpr int kParts = D / 8 * L::kRows / 256, kStep = kParts < 4 ? kParts : 4;
+                const int at_k = keeps ? 128 + r : r, pr = at_k & (L::kRows - 1), first = at_k / L::kRows * kParts;
 #pragma unroll 1
                 for (int piece = 0; piece < L::kPieces && ok; ++piece) {
                     if (kGather) {
                         // Not while the products of the chunk before run: with K~ written beside them (and two tiles of
                         // low parts) about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of
                         // its operands in place and its commits outstanding until the waits ran out; in turn it has not
-                        // been seen (5 10^6 calls), and is faster too.
+                        // been seen (5 10^6 calls), and was faster too.
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
                         if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
                     } else {  // (the first: it also means that the products of the chunk before are done)
@@ -476,16 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     uint8_t* mid = smem + L::kOffMid + pr * 128;
                     uint8_t* low = smem + L::kOffLow + pr * 128;
 #pragma unroll 1
-                    for (int i0 = first; i0 < first + kParts; i0 += 4) {
-                        uint4 in[4];  // four loads in flight together
+                    for (int i0 = first; i0 < first + kParts; i0 += kStep) {
+                        uint4 in[kStep];
                         const int half = i0 >> 3;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < kStep; ++i)
                             in[i] = row < n ? *reinterpret_cast<const uint4*>(
                                                   hi + half * kHalf + ((((i0 & 7) + i) ^ (row & 7)) << 4))
-                                            : make_uint4(0u, 0u, 0u, 0u);  // rows past the sequence's end are not its own
+                                            : make_uint4(0u, 0u, 0u, 0u);  // not the sequence's own
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kStep; ++i) {
                             const int at = (((i0 & 7) + i) ^ (row & 7)) << 4;
                             uint32_t x[4] = {in[i].x, in[i].y, in[i].z, in[i].w}, m[4], l[4];
 #pragma unroll
@@ -507,85 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     mbar_arrive(&bars->kt_full);
                 }
             }
-        }
-    } else if (warp >= 4) {
-        // ---------------------------------------------------------------- the state: row r of S
-        const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const bool mine = r < D;
-        uint8_t* ss = smem + L::kOffS + r * 128;
-        int uc = 0;  // completed K~^T V that this role has waited for
-        // S <- f S + K~^T V, columns x .. x + 31 (gather: the sums of the high parts and of the others)
-        auto step = [&](uint32_t (&s)[32], int x, float f) {
-            uint32_t u[32];
-            tmem_ld32_async(tm + L::kColS + x, s);
-            tmem_ld32_async(tm + L::kColU + x, u);
-            tmem_wait_ld(s);
-            tmem_wait_ld(u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), f, __uint_as_float(u[e])));
-        };
-        for (const Item* it; (it = items.next(ok)); items.done()) {
-            const int chunks = it->chunks, len = it->len;
-            const float la = it->la;
-            float f = 1.f;  // the decay over the chunk before
-            if (kGather) {
-                tc_fence_before();
-                mbar_arrive(&bars->st_full);
-            }
-            for (int c = 0; c < (kGather ? 0 : chunks); ++c) {
-                const float* from = it->begin;
-                if (c > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
-                    ++uc;
-                }
-                if (!ok) break;
-                tc_fence_after();
-                auto take = [&](uint32_t (&s)[32], int x) {  // kept, and as bf16 for Q S
-                    tmem_st32_nowait(tm + L::kColS + x, s);
-                    if (!mine) return;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = pack_bf16x2(__uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
-                        const int chunk = (x + e) >> 3;
-                        *reinterpret_cast<uint4*>(ss + (chunk >> 3) * (D * 128) + (((chunk & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                };
-                if (c > 0) {
-#pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t s[32];
-                        step(s, x, f);
-                        take(s, x);
-                    }
-                } else {
-                    const bool there = mine && from;
-                    const float* row = from + (size_t)r * D;
-                    const bool wide = (reinterpret_cast<uintptr_t>(from) & 31u) == 0;
-#pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t s[32];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (there)
-                                load_32(row + x + e, s + e, wide);
-                            else
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) s[e + i] = 0u;
-                        }
-                        take(s, x);
-                    }
-                }
-                f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
-                tmem_wait_st();
-                tc_fence_before();
-                fence_proxy_async_smem();
-                mbar_arrive(&bars->st_full);
-            }
-            if (chunks == 0) continue;
+            if (chunks == 0 || !keeps) continue;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
             ++uc;
             float* to = it->end;
@@ -802,8 +809,8 @@ template <int D>
 cudaError_t launch(const LinearArgs& a, void* workspace, cudaStream_t stream) {
     static OncePerDevice configured;
     const cudaError_t e = configured.run([] {
-        cudaError_t r = cudaFuncSetAttribute((const void*)linear_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Layout<D, false>::kSmem);
+        cudaError_t r = cudaFuncSetAttribute((const void*)linear_kernel<D, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, false>::kSmem);
         if (r == cudaSuccess)
             r = cudaFuncSetAttribute((const void*)linear_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Layout<D, true>::kSmem);
