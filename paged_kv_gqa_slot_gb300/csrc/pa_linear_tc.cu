@@ -45,8 +45,8 @@
 #include <algorithm>
 #include <climits>
 
-#include "pa_step.cuh"
 #include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {

@@ -22,10 +22,16 @@
 //
 // Base of the softmax: a stage is taken against the row's current base, 0 to begin with (P, O and the sums have
 // the range of fp32).  Only a stage whose sum passes 2^16, or a first one whose sum is below 2^-40, takes the
-// maximum; the base moves there, and O is rescaled where the maximum grew by more than 2^8.  P is rounded to bf16
-// and the normaliser sums the rounded values, so their rounding moves weight between keys but not its total.  Where
-// few keys can dominate (a tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts,
-// in the two halves of S_t.
+// maximum (at d = 128 so does any stage with a masked key); where it is more than 2^8 above the base, or in a first
+// stage far below it, the base moves there and O is rescaled.  P is rounded to bf16 and the normaliser sums the
+// rounded values, so their rounding moves weight between keys but not its total.  Where few keys can dominate (a
+// tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
+//
+// Measured: 1 x 16384 tokens (32 / 8 heads of 128) 651 us, 1.69 PFLOP/s; 48 prompts of up to 1300 tokens 219 us; 7 of
+// up to 2200 (24 / 8 heads of 64) 92 us.  Long prompts are bound by the tensor core, d = 64 by the softmax, short
+// prompts by what an item costs besides its stages and by masked stages, which are nearly half of them.
+// Also tried: two softmax threads a row (1 x 16384 969 us against 774 then), an issuing warp a tile (48 prompts 266
+// us against 260), both tiles half a stage apart (no gain).
 //
 // Masked keys have P = 0, and 0 times a NaN or an infinity in V is NaN.  So in the stages that hold a
 // key masked for some row, a warp looks V over before its product: what is not finite is replaced
@@ -37,8 +43,8 @@
 #include <climits>
 #include <cmath>
 
-#include "pa_step.cuh"
 #include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {
@@ -50,6 +56,7 @@ constexpr int kThreads = 384;
 constexpr int kHalf = kRows * 128;      // [128 rows][64 columns] bf16
 constexpr float kRescaleThreshold = 8.f;
 constexpr float kSumMost = 65536.f, kFirstSumLeast = 0x1p-40f;  // a stage's sum outside takes the maximum
+constexpr float kFirstLeast = -32.f;    // a first maximum below it becomes the base
 constexpr float kSplitScale = 2.f;      // |scale| sqrt(d) past this: P in two parts
 constexpr int kFewKeys = 128;           // a tile with a row of at most this many keys: the same
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -200,26 +207,87 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
         const int lim = pos - j * kKeys;
         const bool unmasked = __all_sync(0xffffffffu, lim >= kKeys - 1);
         uint32_t s0[32], s1[32], s2[32], s3[32];
-        float sum;
-        if (D == 128 && !kSplit && unmasked) {
-            // the usual stage, quarter by quarter, each loaded while the one before is worked on (1 x 16384: 703 us
-            // against 773; at d = 64, where the softmax bounds both tiles, 135 against 131)
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t w[32];
-            tmem_ld32(tm_s, s0);
-            tmem_ld32_async(tm_s + 32, s1);
-            quarter_w(s0, sl, -base, w, ls);
-            tmem_wait_ld(s1);
-            tmem_ld32_async(tm_s + 64, s2);
-            quarter_w(s1, sl, -base, w + 16, ls);
-            tmem_st32_nowait(tm_s, w);
-            tmem_wait_ld(s2);
-            tmem_ld32_async(tm_s + 96, s3);
-            quarter_w(s2, sl, -base, w, ls);
-            tmem_wait_ld(s3);
-            quarter_w(s3, sl, -base, w + 16, ls);
-            tmem_st32_nowait(tm_s + 32, w);
-            sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        float sum = 0.f;
+        // At d = 128, where the tensor core is to be kept busy, the usual stage is taken in quarters and all others in
+        // little code (the whole below for both: 48 prompts 226 us against 219, 1 x 16384 773 against 655).  At d = 64
+        // the softmax bounds the kernel, and loads and P of a stage run on without a wait between them (as at d = 128:
+        // 7 prompts 120 us against 92).
+        if constexpr (D == 128) {
+            bool done = false;
+            if (!kSplit && unmasked) {
+                // quarter by quarter, each loaded while the one before is worked on
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t w[32];
+                tmem_ld32(tm_s, s0);
+                tmem_ld32_async(tm_s + 32, s1);
+                quarter_w(s0, sl, -base, w, ls);
+                tmem_wait_ld(s1);
+                tmem_ld32_async(tm_s + 64, s2);
+                quarter_w(s1, sl, -base, w + 16, ls);
+                tmem_st32_nowait(tm_s, w);
+                tmem_wait_ld(s2);
+                tmem_ld32_async(tm_s + 96, s3);
+                quarter_w(s2, sl, -base, w, ls);
+                tmem_wait_ld(s3);
+                quarter_w(s3, sl, -base, w + 16, ls);
+                tmem_st32_nowait(tm_s + 32, w);
+                sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                done = true;
+            }
+            // a sum past 2^16, or a first one below 2^-40: once more against a new base
+            if (done && __any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast))) {
+                tmem_wait_st();  // the scores that P went over
+                tmem_st32_nowait(tm_s, s0);
+                tmem_st32_nowait(tm_s + 32, s1);
+                tmem_wait_st();
+                done = false;
+            }
+            if (!done) {
+                // the maximum first, so that P is written once
+                const float sgn = sl < 0.f ? -1.f : 1.f;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(tm_s + c, s);
+                    mx = fmaxf(mx, quarter_max(s, lim - c, sgn));
+                }
+                mx *= fabsf(sl);
+                // (a maximum that is no number leaves the base: the row's result is none either)
+                float f = 1.f;
+                if (fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (j == 0 && mx < kFirstLeast))) {
+                    f = fast_exp2(base - mx);
+                    base = mx;
+                }
+                // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
+                if (j > 0) {
+                    if (__any_sync(0xffffffffu, f != 1.f)) scale_o<D>(tm_o, f);
+                    l *= f;
+                }
+                float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                if (kSplit) {
+                    tmem_ld32_async(tm_s, s0);
+                    tmem_ld32_async(tm_s + 32, s1);
+                    tmem_ld32_async(tm_s + 64, s2);
+                    tmem_ld32_async(tm_s + 96, s3);
+                    tmem_wait_ld(s0);
+                    tmem_wait_ld(s1);
+                    tmem_wait_ld(s2);
+                    tmem_wait_ld(s3);
+                    quarter_p<false, true>(s0, lim, sl, -base, tm_s, ls);
+                    quarter_p<false, true>(s1, lim - 32, sl, -base, tm_s + 16, ls);
+                    quarter_p<false, true>(s2, lim - 64, sl, -base, tm_s + 32, ls);
+                    quarter_p<false, true>(s3, lim - 96, sl, -base, tm_s + 48, ls);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(tm_s + c, s);
+                        quarter_p<false, false>(s, lim - c, sl, -base, tm_s + c / 2, ls);
+                    }
+                }
+                sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            }
         } else {
             tmem_ld32_async(tm_s, s0);
             tmem_ld32_async(tm_s + 32, s1);
@@ -231,25 +299,26 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
             tmem_wait_ld(s3);
             sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
                            : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
-        }
-        // a sum past 2^16, or a first one below 2^-40: once more against a new base
-        if (__any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && pos >= 0 && sum < kFirstSumLeast))) {
-            const float sgn = sl < 0.f ? -1.f : 1.f;
-            const float mx = fabsf(sl) * fmaxf(fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn)),
-                                               fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn)));
-            // (a maximum that is no number leaves the base: the row's result is none either)
-            float f = 1.f;
-            if (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY) {
-                f = fast_exp2(base - mx);
-                base = mx;
+            // a sum past 2^16, or a first one below 2^-40: once more against a new base
+            if (__any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && pos >= 0 && sum < kFirstSumLeast))) {
+                const float sgn = sl < 0.f ? -1.f : 1.f;
+                const float m0 = fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn));
+                const float m1 = fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn));
+                const float mx = fabsf(sl) * fmaxf(m0, m1);
+                // (a maximum that is no number leaves the base: the row's result is none either)
+                float f = 1.f;
+                if (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY) {
+                    f = fast_exp2(base - mx);
+                    base = mx;
+                }
+                // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
+                if (j > 0) {
+                    if (__any_sync(0xffffffffu, f != 1.f)) scale_o<D>(tm_o, f);
+                    l *= f;
+                }
+                sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
+                               : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
             }
-            // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
-            if (j > 0) {
-                if (__any_sync(0xffffffffu, f != 1.f)) scale_o<D>(tm_o, f);
-                l *= f;
-            }
-            sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
-                           : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
         }
         l += sum;
         tmem_wait_st();

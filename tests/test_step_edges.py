@@ -53,6 +53,23 @@ def test_segments_end_in_any_order():
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_packed_scores_far_from_zero(d):
+    """All scores of a row near one value, from -180 to 180, in stages that every row sees whole and in others; and
+    keys that come by it in jumps.  (Exact operands: q and k have few bits, so the scores are those of the reference.)"""
+    n, scale = 600, 1 / 64
+    for steps in ([-180.0], [180.0], [-180.0, -150.0, 10.0, 12.0, 100.0], [100.0, 20.0, -60.0, 130.0, 128.0]):
+        q, k, v, cu = R.packed_rows([n, 150], 4, 2, d, 49, strided=False)
+        q[:] = 64.0 / d
+        level = torch.tensor(steps, device="cuda")[torch.arange(n + 150, device="cuda") * len(steps) // (n + 150)]
+        k[:] = (level[:, None, None] + torch.round(k.float())).bfloat16()
+        out = pa.pa_prefill_packed(q, k, v, cu, scale, n)
+        ref, size = R.packed(q, k, v, cu, scale)
+        check(out, ref, size, str(steps))
+    clean()
+
+
+@gpu
 @pytest.mark.parametrize("lens,d", [([640, 1], 128), ([3000], 128), ([640, 70], 64), ([2600], 64)])
 def test_the_state_keeps_32_bits(lens, d):
     """Its error's size against its own: the parts of k's weighted rows 2^-24, the exponents (up to 6 where a term
