@@ -27,8 +27,8 @@
 // rounded values, so their rounding moves weight between keys but not its total.  Where few keys can dominate (a
 // tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
 //
-// Measured: 1 x 16384 tokens (32 / 8 heads of 128) 651 us, 1.69 PFLOP/s; 48 prompts of up to 1300 tokens 219 us; 7 of
-// up to 2200 (24 / 8 heads of 64) 92 us.  Long prompts are bound by the tensor core, d = 64 by the softmax, short
+// Measured: 1 x 16384 tokens (32 / 8 heads of 128) 650 us, 1.69 PFLOP/s; 48 prompts of up to 1300 tokens 211 us; 7 of
+// up to 2200 (24 / 8 heads of 64) 82 us.  Long prompts are bound by the tensor core, d = 64 by the softmax, short
 // prompts by what an item costs besides its stages and by masked stages, which are nearly half of them.
 // Also tried: two softmax threads a row (1 x 16384 969 us against 774 then), an issuing warp a tile (48 prompts 266
 // us against 260), both tiles half a stage apart (no gain).
@@ -60,6 +60,7 @@ constexpr float kFirstLeast = -32.f;    // a first maximum below it becomes the 
 constexpr float kSplitScale = 2.f;      // |scale| sqrt(d) past this: P in two parts
 constexpr int kFewKeys = 128;           // a tile with a row of at most this many keys: the same
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kNoRow = INT_MAX;
 
 template <int D>
 struct Layout {
@@ -194,15 +195,24 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float f) {
 }
 
 // The softmax of one tile's rows, stage by stage (the first is number `sc` of the tile's); `pos` the row's own
-// key.  Returns false when a wait ran out.  tcgen05.ld / st are warp-collective, so every branch that leads to one
-// is the warp's.
+// key, kNoRow for a row past the sequence's end or the tile's heads: nothing of it is masked, it has no say in
+// what its warp does, and what it computes from whatever its Q holds is not stored.  (With all its keys masked its warp
+// took every stage as a masked one: 6 x 4000 tokens, group 3 at d = 128, 601 us against 382.)  Returns false when a
+// wait ran out.  tcgen05.ld / st are warp-collective, so every branch that leads to one is the warp's.
 template <int D, bool kSplit>
 __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n, int pos, float sl, uint32_t tm_s,
                                              uint32_t tm_o, float& l_out) {
+    const bool there = pos != kNoRow, none = D == 64 && !__any_sync(0xffffffffu, there);
     float base = 0.f, l = 0.f;  // P = 2^(score - base)
 #pragma unroll 1
     for (int j = 0; j < n; ++j, ++sc) {
         if (__any_sync(0xffffffffu, !mbar_wait(&bars->s_full[t], sc & 1))) return false;
+        // No row of the warp's is anybody's: P is what it is.  (At d = 64, where the code is larger, this spares short
+        // prompts the variant without masks: 256 x 48 tokens 58 us against 75.)
+        if (D == 64 && none) {
+            mbar_arrive(&bars->p_full[t]);
+            continue;
+        }
         tc_fence_after();
         const int lim = pos - j * kKeys;
         const bool unmasked = __all_sync(0xffffffffu, lim >= kKeys - 1);
@@ -235,7 +245,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 done = true;
             }
             // a sum past 2^16, or a first one below 2^-40: once more against a new base
-            if (done && __any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast))) {
+            if (done && __any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast)))) {
                 tmem_wait_st();  // the scores that P went over
                 tmem_st32_nowait(tm_s, s0);
                 tmem_st32_nowait(tm_s + 32, s1);
@@ -255,7 +265,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 mx *= fabsf(sl);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (j == 0 && mx < kFirstLeast))) {
+                if (there && fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (j == 0 && mx < kFirstLeast))) {
                     f = fast_exp2(base - mx);
                     base = mx;
                 }
@@ -300,14 +310,14 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
             sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
                            : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
             // a sum past 2^16, or a first one below 2^-40: once more against a new base
-            if (__any_sync(0xffffffffu, !(sum <= kSumMost) || (j == 0 && pos >= 0 && sum < kFirstSumLeast))) {
+            if (__any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast)))) {
                 const float sgn = sl < 0.f ? -1.f : 1.f;
                 const float m0 = fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn));
                 const float m1 = fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn));
                 const float mx = fabsf(sl) * fmaxf(m0, m1);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY) {
+                if (there && (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY)) {
                     f = fast_exp2(base - mx);
                     base = mx;
                 }
@@ -687,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             if (ntok == 0) continue;
             const int n = (first + ntok + kKeys - 1) / kKeys;
             const bool valid = qi < ntok;
-            const int pos = valid ? first + qi : -1;
+            const int pos = valid ? first + qi : kNoRow;
             float l = 0.f;
             if (a.split_all || first + 1 <= kFewKeys)
                 ok = softmax_rows<D, true>(bars, t, sc, n, pos, a.scale_log2, tm_s, tm_o, l);
@@ -758,13 +768,17 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
     }
 }
 
-// Heads of a group that one tile holds: the largest divisor of the group up to 16.  (Few heads a tile make
-// its token range long, which wastes the diagonal's stages; a divisor that does not divide 128 leaves
-// up to 11 of the 128 rows empty.)
+// Heads of a group that one tile holds: the largest divisor of the group up to 16, as few heads a tile make its token
+// range long and leave more of it empty (group 4: 187 prompts of up to 128 tokens 90 us with 4 heads a tile, 97
+// with 2, 173 with 1; 6 of up to 4000 483, 495, 511).  One that does not divide 128 leaves rows empty and
+// has its token ranges begin anywhere, so the power of two goes before it where it is more than half as large
+// (group 24, 8 against 12: 34 prompts of up to 700 tokens 63 us against 72, 256 of up to 48 45 against 43; but group
+// 12, 4 against 12: 64 against 71, 53 against 40).
 int tile_heads(int group) {
-    for (int th = std::min(group, 16); th > 1; --th)
-        if (group % th == 0) return th;
-    return 1;
+    int most = std::min(group, 16), two = 1;
+    while (group % most != 0) --most;
+    while (two < 16 && group % (2 * two) == 0) two *= 2;
+    return 2 * two > most ? two : most;
 }
 
 template <int D>
