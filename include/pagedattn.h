@@ -430,6 +430,18 @@ int pa_device_status(uint32_t *flags, int32_t clear, pa_stream_t stream);
 int pa_selftest_wait_timeout(uint64_t limit_cycles, pa_stream_t stream);
 
 /*
+ * pa_selftest_packed_pairs -- a check of how pa_prefill_packed finds its work.  Its blocks take over one another's
+ * work in an order that is the hardware's, so each finds the sequence of a pair of tiles from the pair's number, whatever
+ * it found before: the pairs of pair_tokens (2 .. 256) tokens of the sequences, counted one after another, those
+ * of a sequence from its end.  For each of pairs[0 .. n), one after another as one block would,
+ *   out            [n, 3] int32 first row and length of its sequence and the pair's first token, or -1, -1, -1 past the last
+ * cu_lens, num_tokens and max_len as in pa_prefill_packed, and reported alike.  Asynchronous on `stream`.
+ */
+int pa_selftest_packed_pairs(const int32_t *cu_lens, int32_t batch, int32_t num_tokens, int32_t max_len,
+                             int32_t pair_tokens, const int32_t *pairs, int32_t n, int32_t *out,
+                             pa_stream_t stream);
+
+/*
  * pa_decode_splitkv_noalloc -- split-KV decode and its log-sum-exp merge in one call that
  * allocates nothing and takes no workspace: out = pa_combine(pa_decode_splitkv(...)).
  * The pages have no counterpart of this call; it exists for callers that cannot allocate

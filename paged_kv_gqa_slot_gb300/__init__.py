@@ -28,7 +28,7 @@ import torch
 __all__ = ["PaPool", "PaPool8", "pa_kv_append8", "pa_decode8", "pa_prefill_chunked8", "pa_decode_weights",
            "pa_decode8_weights", "pa_weights_workspace_bytes", "pa_kv_evict", "pa_kv_append", "pa_kv_copy", "pa_decode", "pa_append_decode", "pa_decode_splitkv",
            "pa_combine", "pa_prefill_chunked",
-           "pa_device_status", "pa_selftest_wait_timeout", "pa_splitkv_workspace_bytes", "pa_decode_num_splits", "pa_splitkv_num_partitions",
+           "pa_device_status", "pa_selftest_wait_timeout", "pa_selftest_packed_pairs", "pa_splitkv_workspace_bytes", "pa_decode_num_splits", "pa_splitkv_num_partitions",
            "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes", "PagedAttnError",
            "pa_prefill_packed", "pa_kv_grow", "pa_kv_free", "pa_linear_decode", "pa_linear_prefill",
            "pa_linear_workspace_bytes", "BlockManager", "pa_kv_block_bytes", "pa_kv_budget_blocks",
@@ -42,7 +42,7 @@ EXPORTED_SYMBOLS = ("pa_kv_append8", "pa_decode8", "pa_prefill_chunked8", "pa_de
                     "pa_decode_splitkv", "pa_combine",
                     "pa_prefill_chunked", "pa_device_status", "pa_decode_num_splits", "pa_splitkv_num_partitions",
                     "pa_status_str", "pa_version", "pa_decode_splitkv_noalloc", "pa_noalloc_scratch_bytes",
-                    "pa_selftest_wait_timeout", "pa_prefill_packed", "pa_kv_grow", "pa_kv_free", "pa_linear_decode",
+                    "pa_selftest_wait_timeout", "pa_selftest_packed_pairs", "pa_prefill_packed", "pa_kv_grow", "pa_kv_free", "pa_linear_decode",
                     "pa_linear_prefill", "pa_linear_workspace_bytes",
                     "pa_kv_block_bytes", "pa_kv_budget_blocks", "pa_bm_create", "pa_bm_destroy", "pa_bm_admit", "pa_bm_admit_cow",
                     "pa_bm_commit", "pa_bm_release", "pa_bm_slots", "pa_bm_stats")
@@ -108,6 +108,7 @@ def library() -> ctypes.CDLL:
         "pa_kv_evict": (ctypes.c_int, [P, P, P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, P]),
         "pa_bm_evict": (ctypes.c_int, [P, ctypes.c_int64, P, I32]),
         "pa_prefill_packed": (ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, I32, I64, I64, I64, I32, F32, P, P]),
+        "pa_selftest_packed_pairs": (ctypes.c_int, [P, I32, I32, I32, I32, P, I32, P, P]),
         "pa_kv_grow": (ctypes.c_int, [P, I32, P, P, I32, P, I32, P, I32, P, P, P, P, P, P, P]),
         "pa_kv_free": (ctypes.c_int, [P, P, I32, I32, P, I32, P, P, P]),
         "pa_linear_decode": (ctypes.c_int, [P, I32, P, P, P, P, P, P, I32, I32, I32, I32, I64, I64, I64, F32, P, P]),
@@ -720,6 +721,17 @@ def pa_selftest_wait_timeout(limit_cycles: int = 2_000_000, stream=None) -> None
     """Make one bounded device wait run out (an mbarrier nothing arrives on); afterwards the
     device status has PA_DEV_TIMEOUT set.  Asynchronous on `stream`."""
     _check(library().pa_selftest_wait_timeout(int(limit_cycles), _stream(stream)), "pa_selftest_wait_timeout")
+
+
+def pa_selftest_packed_pairs(cu_lens: torch.Tensor, num_tokens: int, max_len: int, pair_tokens: int, pairs: torch.Tensor,
+                             stream=None) -> torch.Tensor:
+    """[n, 3] int32: for each of `pairs`, in turn, the first row and the length of its sequence and its first token, as a
+    block of pa_prefill_packed finds them; -1 past the last pair."""
+    d = cu_lens.get_device()
+    out = _new(cu_lens, (pairs.numel(), 3), _I32, stream)
+    _call("pa_selftest_packed_pairs", d, stream, _arg(cu_lens, _I32, "cu_lens", d), cu_lens.numel() - 1, int(num_tokens),
+          int(max_len), int(pair_tokens), _arg(pairs, _I32, "pairs", d), pairs.numel(), out.data_ptr())
+    return out
 
 
 def pa_decode_num_splits(batch: int, num_kv_heads: int, max_blocks: int) -> int:

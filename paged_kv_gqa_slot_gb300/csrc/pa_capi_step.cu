@@ -85,6 +85,23 @@ int pa_prefill_packed(const void* q, const void* k, const void* v, const int32_t
     return from_cuda(launch_prefill_packed(a, (cudaStream_t)stream));
 }
 
+int pa_selftest_packed_pairs(const int32_t* cu_lens, int32_t batch, int32_t num_tokens, int32_t max_len,
+                             int32_t pair_tokens, const int32_t* pairs, int32_t n, int32_t* out, pa_stream_t stream) {
+    if (batch <= 0 || batch > 65535 || num_tokens < 0 || max_len < 0 || pair_tokens < 2 || pair_tokens > 256 || n < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!array_ok(cu_lens, 4)) return PA_ERR_INVALID_ARG;
+    if (n == 0) return PA_OK;
+    if (!array_ok(pairs, 4) || !array_ok(out, 4)) return PA_ERR_INVALID_ARG;
+    PackedArgs a = {};
+    a.cu_lens = cu_lens;
+    a.batch = batch;
+    a.num_tokens = num_tokens;
+    a.max_len = max_len;
+    a.status = device_status_ptr();
+    if (!a.status) return PA_ERR_CUDA;
+    return from_cuda(launch_selftest_pairs(a, pair_tokens, pairs, n, out, (cudaStream_t)stream));
+}
+
 int pa_kv_grow(int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens, const int32_t* new_lens,
                int32_t batch, const int32_t* free_blocks, int32_t capacity, const int32_t* num_free,
                int32_t max_tokens, int32_t* seq_lens_out, int32_t* num_free_out, int32_t* cu_lens,

@@ -222,6 +222,8 @@ cudaError_t launch_evict(const EvictArgs& a, int batch, cudaStream_t stream);
 cudaError_t launch_grow(const GrowArgs& a, cudaStream_t stream);
 cudaError_t launch_free(const FreeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_packed(const PackedArgs& a, cudaStream_t stream);
+cudaError_t launch_selftest_pairs(const PackedArgs& a, int pair_tokens, const int32_t* pairs, int n, int32_t* out,
+                                  cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearArgs& a, cudaStream_t stream);
 cudaError_t launch_linear_prefill(const LinearArgs& a, void* workspace, cudaStream_t stream);
 // chunks of 128 tokens on the tensor cores

@@ -430,33 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == kItemWarp) {
             // ---------------------------------------------------------------- the items
-            // id = pair * subs + sub, the pairs of the sequences counted one after another; ids only rise, so the
-            // walk over the sequences (32 at a time, one a lane) goes on where it was
+            // id = pair * subs + sub
             unsigned id = blockIdx.x;
             uint32_t phase = 0;
-            int b0 = 0;
-            unsigned before = 0;  // pairs of the sequences before b0
+            PairWalk walk(a.p, 2 * a.tpt);
             bool reports = id == 0;
-            auto look = [&](int b, int& row, int& len) {  // sequence b's rows and pairs
-                row = len = 0;
-                if (b >= a.p.batch) return 0u;
-                const int c0 = a.p.cu_lens[b], c1 = a.p.cu_lens[b + 1];
-                const bool off = c0 < 0 || c1 < c0 || c1 > a.p.num_tokens;
-                if (off || c1 - c0 > a.p.max_len) atomicOr(a.p.status, kDevOutOfRange);
-                row = c0;
-                len = off ? 0 : min(c1 - c0, a.p.max_len);
-                return (unsigned)((len + 2 * a.tpt - 1) / (2 * a.tpt));
-            };
-            auto sums = [&](unsigned x) {
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned up = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += up;
-                }
-                return x;
-            };
-            int row, len;
-            unsigned mine = look(lane, row, len), upto = sums(mine);
             for (int n = 0; ok; ++n) {
                 bool there = true;
                 if (n > 0) {  // the last copies of the item before are on their way, and a slot is free
@@ -465,29 +443,25 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
                     if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
                 }
-                if (!ok) break;
-                reports |= there && id == 0;
-                const unsigned pair = id / (unsigned)a.subs, sub = id % (unsigned)a.subs;
-                while (there && pair >= before + __shfl_sync(0xffffffffu, upto, 31)) {
-                    before += __shfl_sync(0xffffffffu, upto, 31);
-                    b0 += 32;
-                    there = b0 < a.p.batch;  // past the last pair: there are no others
-                    if (there) {
-                        mine = look(b0 + lane, row, len);
-                        upto = sums(mine);
-                    }
-                }
                 Item* it = reinterpret_cast<Item*>(smem + L::kOffItem + (n & 1) * 64);
-                if (there && pair >= before + upto - mine && pair < before + upto) {  // the sequence's own lane
-                    it->row = row;
-                    it->len = len;
-                    // the longest pair of a sequence first
-                    it->tok0 = (int)(before + upto - 1 - pair) * 2 * a.tpt;
-                    it->head0 = (int)sub * a.th;
-                    it->kvh = it->head0 / (a.p.num_heads / a.p.num_kv_heads);
-                    it->none = 0;
-                    it->any_bad = 0;
+                while (ok && there) {  // (the grid has blocks past the last pair; they may come before others)
+                    reports |= id == 0;
+                    const unsigned pair = id / (unsigned)a.subs, sub = id % (unsigned)a.subs;
+                    if (walk.find(pair)) {
+                        if (walk.owns(pair)) {  // one lane
+                            it->row = walk.row;
+                            it->len = walk.len;
+                            it->tok0 = walk.first_token(pair);
+                            it->head0 = (int)sub * a.th;
+                            it->kvh = it->head0 / (a.p.num_heads / a.p.num_kv_heads);
+                            it->none = 0;
+                            it->any_bad = 0;
+                        }
+                        break;
+                    }
+                    there = take_block(&bars->reply, &bars->next, phase, id, ok);
                 }
+                if (!ok) break;
                 if (!there && lane == 0) it->none = 1;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->item_full[n & 1]);
@@ -495,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             }
             // (sequences behind the last pair that anybody took are looked at for their offsets, too)
             if (reports)
-                for (; b0 < a.p.batch; b0 += 32) look(b0 + lane, row, len);
+                for (int b = walk.b0 + 32; b < a.p.batch; b += 32) walk.look(b + lane);
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- TMA loads, in the order of use
             const uint32_t q_bytes = (uint32_t)(a.tpt * a.th * 128 * L::kHalves);
@@ -768,6 +742,21 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
     }
 }
 
+// What the warp of the items finds for each of `pairs`: [row, length, first token], or -1s past the last pair.
+__global__ void __launch_bounds__(32) pairs_kernel(const PackedArgs p, int tokens, const int32_t* pairs, int n, int32_t* out) {
+    PairWalk walk(p, tokens);
+    for (int i = 0; i < n; ++i) {
+        const unsigned pair = (unsigned)pairs[i];
+        if (!walk.find(pair)) {
+            if (threadIdx.x < 3) out[3 * i + threadIdx.x] = -1;
+        } else if (walk.owns(pair)) {
+            out[3 * i] = walk.row;
+            out[3 * i + 1] = walk.len;
+            out[3 * i + 2] = walk.first_token(pair);
+        }
+    }
+}
+
 // Heads of a group that one tile holds: the largest divisor of the group up to 16, as few heads a tile make its token
 // range long and leave more of it empty (group 4: 187 prompts of up to 128 tokens 90 us with 4 heads a tile, 97
 // with 2, 173 with 1; 6 of up to 4000 483, 495, 511).  One that does not divide 128 leaves rows empty and
@@ -822,6 +811,12 @@ cudaError_t launch(const PackedArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_prefill_packed(const PackedArgs& a, cudaStream_t stream) {
     return a.head_dim == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+cudaError_t launch_selftest_pairs(const PackedArgs& a, int pair_tokens, const int32_t* pairs, int n, int32_t* out,
+                                  cudaStream_t stream) {
+    pairs_kernel<<<1, 32, 0, stream>>>(a, pair_tokens, pairs, n, out);
+    return cudaGetLastError();
 }
 
 }  // namespace pa

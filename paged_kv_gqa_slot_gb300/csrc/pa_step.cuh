@@ -2,6 +2,7 @@
 #pragma once
 
 #include "pa_device.cuh"
+#include "pa_internal.h"
 
 namespace pa {
 
@@ -79,5 +80,63 @@ __device__ __forceinline__ bool take_block(uint4* reply, uint64_t* next, uint32_
     if (got) id = x;
     return got != 0;
 }
+
+// The pairs of tiles of a packed call, found by number: the pairs of the sequences are counted one after another, each
+// sequence's longest first.  A warp looks at 32 sequences at a time, one a lane, and goes on from where it was, as blocks
+// are mostly taken over in rising order.  Nothing promises that order: a pair that lies before is looked for from
+// the first sequence on.
+struct PairWalk {
+    const PackedArgs& p;
+    const int tokens;             // of a pair
+    int b0 = 0;                   // first of the sequences looked at
+    unsigned before = 0;          // pairs of those before them
+    unsigned mine = 0, upto = 0;  // the lane's sequence: its pairs, and those up to its end from b0 on
+    int row = 0, len = 0;         // its rows
+
+    __device__ __forceinline__ PairWalk(const PackedArgs& args, int pair_tokens) : p(args), tokens(pair_tokens) { look_at(0); }
+
+    // Sequence b's rows and pairs for the lane that asks.
+    __device__ __forceinline__ void look(int b) {
+        row = len = 0;
+        mine = 0;
+        if (b >= p.batch) return;
+        const int c0 = p.cu_lens[b], c1 = p.cu_lens[b + 1];
+        const bool off = c0 < 0 || c1 < c0 || c1 > p.num_tokens;
+        if (off || c1 - c0 > p.max_len) atomicOr(p.status, kDevOutOfRange);
+        row = c0;
+        len = off ? 0 : min(c1 - c0, p.max_len);
+        mine = (unsigned)((len + tokens - 1) / tokens);
+    }
+    __device__ __forceinline__ void look_at(int b) {
+        const int lane = threadIdx.x & 31;
+        b0 = b;
+        look(b + lane);
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned up = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += up;
+        }
+    }
+    // Looks at the sequence of pair `pair`, the same in every lane; false: it lies past the last.
+    __device__ __forceinline__ bool find(unsigned pair) {
+        if (pair < before) {
+            before = 0;
+            look_at(0);
+        }
+        for (;;) {
+            const unsigned all = __shfl_sync(0xffffffffu, upto, 31);
+            if (pair < before + all) return true;
+            if (b0 + 32 >= p.batch) return false;
+            before += all;
+            look_at(b0 + 32);
+        }
+    }
+    // Of the lane whose sequence it is, once it has been found.
+    __device__ __forceinline__ bool owns(unsigned pair) const {
+        return pair >= before + upto - mine && pair < before + upto;
+    }
+    __device__ __forceinline__ int first_token(unsigned pair) const { return (int)(before + upto - 1 - pair) * tokens; }
+};
 
 }  // namespace pa

@@ -1,0 +1,84 @@
+"""Packed prompts and linear attention at the limits of what they assume: the order that blocks come in, infinite
+scores, values at the ends of the range, states summed over long segments."""
+import math
+import random
+
+import pytest
+import torch
+
+import paged_kv_gqa_slot_gb300 as pa
+import step_ref as R
+from paged_kv_gqa_slot_gb300 import build as pbuild
+from test_packed import check, clean
+
+gpu = pytest.mark.gpu
+FAKE = 0x40000
+
+
+# ----------------------------------------------------------------------------- without a GPU
+@pytest.fixture(scope="module")
+def lib():
+    pbuild.build()
+    return pa.library()
+
+
+def test_pair_selftest_refusals(lib):
+    bad = pa.PA_ERR_INVALID_ARG
+    call = lambda cu=FAKE, b=2, t=100, m=50, per=64, p=FAKE, n=3, o=FAKE: (  # noqa: E731
+        lib.pa_selftest_packed_pairs(cu, b, t, m, per, p, n, o, None))
+    for name in ("cu", "p", "o"):
+        assert call(**{name: None}) == bad and call(**{name: FAKE + 2}) == bad, name
+    assert call(b=0) == bad and call(b=65536) == bad and call(t=-1) == bad and call(m=-1) == bad and call(n=-1) == bad
+    assert call(per=1) == bad and call(per=257) == bad and call(n=0, p=None, o=None) == pa.PA_OK
+
+
+# ----------------------------------------------------------------------------- the order of the blocks
+def pairs_of(cu, rows, most, per):
+    """Every pair of the sequences, in order: [first row, length, first token]."""
+    want = []
+    for a, b in zip(cu[:-1], cu[1:]):
+        if a < 0 or b < a or b > rows:
+            continue
+        n = min(b - a, most)
+        want += [[a, n, at] for at in reversed(range(0, n, per))]
+    return want
+
+
+@gpu
+@pytest.mark.parametrize("batch", [1, 2, 31, 32, 33, 64, 65, 200, 1000])
+def test_pairs_are_found_in_any_order(batch):
+    """Rising, falling and shuffled, with pairs past the last among them; sequences of no tokens at window ends too."""
+    rng = random.Random(batch)
+    for most, per in ((1, 2), (40, 64), (300, 84), (2000, 256)):
+        lens = [rng.choice([0, rng.randint(0, most), most]) for _ in range(batch)]
+        cu = [5]
+        for n in lens:
+            cu.append(cu[-1] + n)
+        rows = cu[-1] + 3
+        want = pairs_of(cu, rows, most, per)
+        n = len(want)
+        past = [n, n + 1, n + 77]
+        rising = list(range(n)) + past
+        orders = [rising, rising[::-1], past + rising]
+        for _ in range(3):
+            orders.append(rng.sample(rising, len(rising)))
+        jumps = [x for i in range(min(n, 40)) for x in (i, n - 1 - i, n + i)]
+        orders.append(jumps)
+        t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for order in orders:
+            if not order:
+                continue
+            got = pa.pa_selftest_packed_pairs(t, rows, most, per, torch.tensor(order, dtype=torch.int32, device="cuda"))
+            assert got.tolist() == [want[i] if i < n else [-1] * 3 for i in order], (most, per, order[:8])
+    clean()
+
+
+@gpu
+def test_pairs_of_sequences_that_are_skipped():
+    cu, rows = [0, 100, 60, 200, 900, 300, 300], 300  # the second and the fourth are no sequences
+    want = pairs_of(cu, rows, 120, 64)
+    assert [w[:2] for w in want] == [[0, 100], [0, 100], [60, 120], [60, 120]]
+    got = pa.pa_selftest_packed_pairs(torch.tensor(cu, dtype=torch.int32, device="cuda"), rows, 120, 64,
+                                      torch.tensor([3, 0, 4, 2, 1], dtype=torch.int32, device="cuda"))
+    assert got.tolist() == [want[3], want[0], [-1] * 3, want[2], want[1]]
+    assert pa.pa_device_status(clear=True) == pa.PA_DEV_OUT_OF_RANGE
