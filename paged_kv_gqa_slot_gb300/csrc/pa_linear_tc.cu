@@ -88,8 +88,10 @@ struct Layout {
     static constexpr int kOffTab = kOffItem + 128;     // [2][32] a^31 .. a^0
     static constexpr int kOffBad = kOffTab + 256;      // [2][D] first token of a column with a value that is not finite
     static constexpr int kSmem = kOffBad + 2 * D * 4;
-    // tensor memory: scores and P; the outputs; K~^T V (gather: of the high parts, and of the others); the state
-    static constexpr uint32_t kColP = 0, kColO = 128, kColU = kColO + D, kColU2 = kColU + D, kColS = kColU2;
+    // tensor memory: scores and P; the outputs; K~^T V; the state
+    static constexpr uint32_t kColP = 0, kColO = 128, kColU = kColO + D, kColS = kColU + D;
+    // gather: K~^T V of the high parts, by turns; what they add up to; K~^T V of the other parts
+    static constexpr uint32_t kColHigh[2] = {0, 128}, kColSum = 128 + D, kColSmall = kColSum + D;
     static constexpr int kTmemCols = 512;
 };
 static_assert(Layout<128, false>::kSmem <= 227 * 1024, "shared memory");
@@ -341,9 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         const uint64_t ld = smem_desc_sw128(smem_u32(smem + L::kOffLow), L::kPart, 1024);
         int cc = 0, ii = 0;  // chunks and chunks' heads so far
         // K~^T V over a piece of K~, V from where its chunk's tiles begin; `first`: from zero.  The small parts come
-        // first, or into sums of their own: the tensor core cuts every sum off to 24 bits.
+        // first, or into sums of their own: the tensor core cuts every sum off to 24 bits.  (So the high parts are summed
+        // over one chunk at most, also where a segment is gathered; what is cut off the small ones is 2^-8 of that.)
         auto issue_u = [&](int piece, uint64_t hd, uint64_t vd, bool first) {
-            const uint32_t small = tmem + (kGather ? L::kColU2 : L::kColU);
+            const uint32_t small = tmem + (kGather ? L::kColSmall : L::kColU);
+            const uint32_t high = tmem + (kGather ? (cc & 1) * L::kColHigh[1] : L::kColU);
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
 #pragma unroll
@@ -351,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     const uint64_t off = (uint64_t)((kk * 16 * 128) >> 4);
                     const uint64_t all = off + (uint64_t)((piece * L::kPart) >> 4);
                     const uint64_t from = part == 0 ? ld + off : part == 1 ? md + off : hd + all;
-                    const bool zero = first && kk == 0 && (part == 0 || (kGather && part == 2));
-                    tc_mma_ew(part == 2 ? tmem + L::kColU : small, from, vd + all, idesc_u, zero ? 0u : 1u);
+                    const bool zero = kk == 0 && ((first && part == 0) || (kGather && part == 2));
+                    tc_mma_ew(part == 2 ? high : small, from, vd + all, idesc_u, zero ? 0u : 1u);
                 }
             }
         };
@@ -464,11 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         uint8_t* ss = smem + L::kOffS + r * 128;
         const bool keeps = warp < 8;
         int cc = 0, uc = 0;  // chunks; completed K~^T V that the state has waited for
-        // S <- f S + K~^T V, columns x .. x + 31 (gather: the sums of the high parts and of the others)
-        auto step = [&](uint32_t (&s)[32], int x, float f) {
+        // S <- f S + K~^T V, columns x .. x + 31, of the columns s_at and u_at of tensor memory
+        auto step = [&](uint32_t (&s)[32], int x, float f, uint32_t s_at = L::kColS, uint32_t u_at = L::kColU) {
             uint32_t u[32];
-            tmem_ld32_async(tm + L::kColS + x, s);
-            tmem_ld32_async(tm + L::kColU + x, u);
+            tmem_ld32_async(tm + s_at + x, s);
+            tmem_ld32_async(tm + u_at + x, u);
             tmem_wait_ld(s);
             tmem_wait_ld(u);
 #pragma unroll
@@ -591,6 +595,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     fence_proxy_async_smem();
                     mbar_arrive(&bars->kt_full);
                 }
+                if (kGather && keeps && c > 0 && ok) {
+                    // The high parts of the chunk before, whose products are done, to the others, in fp32, while those of
+                    // this chunk run into the other columns.  (Summed in tensor memory over a segment of 128 chunks the state
+                    // fell short by 6.4e-5, every sum being cut off.)  The next arrival on kt_full gives them back.
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t s[32];
+                        if (c > 1)
+                            step(s, x, 1.f, L::kColSum, ((cc - 1) & 1) * L::kColHigh[1]);
+                        else
+                            tmem_ld32(tm + ((cc - 1) & 1) * L::kColHigh[1] + x, s);
+                        tmem_st32_nowait(tm + L::kColSum + x, s);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
             }
             if (chunks == 0 || !keeps) continue;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->u_full, uc & 1));
@@ -602,7 +623,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t s[32];
-                step(s, x, f);
+                if (!kGather) {
+                    step(s, x, f);
+                } else {
+                    step(s, x, 1.f, L::kColSmall, ((cc - 1) & 1) * L::kColHigh[1]);
+                    if (chunks > 1) {
+                        uint32_t sum[32];
+                        tmem_ld32(tm + L::kColSum + x, sum);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(sum[e]));
+                    }
+                }
                 if (mine) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) store_32(to + (size_t)r * D + x + e, s + e, wide);

@@ -82,3 +82,38 @@ def test_pairs_of_sequences_that_are_skipped():
                                       torch.tensor([3, 0, 4, 2, 1], dtype=torch.int32, device="cuda"))
     assert got.tolist() == [want[3], want[0], [-1] * 3, want[2], want[1]]
     assert pa.pa_device_status(clear=True) == pa.PA_DEV_OUT_OF_RANGE
+
+
+# ----------------------------------------------------------------------------- states summed for long
+def one_signed(n, heads, d, seed):
+    """k and v in [0.5, 1.5), so that every error of a sum that is always of one sign adds up."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return ((torch.rand(n, heads, d, device="cuda", generator=gen) + 0.5).bfloat16() for _ in range(2))
+
+
+def off_by(state, k, v, log_decay):
+    """The state's relative errors against 64 bits, which has every term of one sign."""
+    n = k.shape[0]
+    rest = torch.exp(log_decay.double() * (n - 1 - torch.arange(n, device="cuda", dtype=torch.float64)))
+    want = (k.double() * rest[:, None]).T @ v.double()
+    return (state.double() - want) / want
+
+
+@gpu
+@pytest.mark.parametrize("decay", [0.0])
+@pytest.mark.parametrize("n,heads,d", [(1 << 20, 1, 64), (20000, 75, 128), (20000, 200, 64), (9000, 32, 128)])
+def test_a_state_summed_over_many_chunks(n, heads, d, decay):
+    """Segments of 128, 79, all (one segment) and 6 to 9 chunks.  Errors of one sign: the 8 sums of a chunk in the tensor core,
+    cut off to 2^-23 of what there is so far, half of the chunk's on average, 2^-21; the decays' 2^-22; below 2^-20.  Errors of
+    either sign: up to 192 sums in fp32, 2^-24 of what there is so far, 0.58 of it root mean square each, six times
+    0.58 * 0.58 * 192^0.5 * 2^-24 < 2^-19: below 2^-18 with the others."""
+    k, v = one_signed(n, heads, d, 71)
+    q = torch.zeros(n, heads, d, device="cuda").bfloat16()
+    state = torch.full((1, heads, d, d), math.nan, device="cuda")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    log_decay = torch.full((heads,), decay, device="cuda")
+    pa.pa_linear_prefill(state, ints([0]), q, k, v, log_decay, ints([0, n]), ints([n]), 1.0, n)
+    for h in {0, heads // 2, heads - 1}:
+        off = off_by(state[0, h], k[:, h], v[:, h], log_decay[h])
+        assert abs(float(off.mean())) <= 2.0 ** -20 and float(off.abs().max()) <= 2.0 ** -18, h
+    clean()
