@@ -9,23 +9,16 @@
 // d = 128 from HBM take 36.4 us, 6.2 TB/s; 32 states 2.8 us inside a graph.
 #include <algorithm>
 
-#include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_step.cuh"
 
 namespace pa {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kMinLogDecay = -1e4f;
 // Chunks up to this long go token by token: with d = 128, 32 states x 6 tokens 8.6 us against 8.9 in one chunk of
 // pa_linear_tc.cu, 8 10.4 against 8.9; 152 states 8.8 against 9.5, 10.6 against 9.5; 2048 91 against 93, 108 against
 // 94; 512 states 20.6 against 27.7, 24.7 against 27.7.
 constexpr int kFewTokens = 6;
-
-// log2 of a head's decay; a NaN is taken as the lower end
-__device__ __forceinline__ float log2_decay(float log_decay) {
-    return fminf(fmaxf(log_decay, kMinLogDecay), 0.f) * kLog2e;
-}
 
 // What a sequence's state slot says: its state (null: padding, zero rows) and whether it begins at zero.
 __device__ __forceinline__ float* state_of(const LinearArgs& a, int b, int kvh, bool report) {
@@ -64,19 +57,32 @@ __global__ void __launch_bounds__(256) linear_decode_kernel(const LinearArgs a) 
 #pragma unroll
         for (int n = 0; n < N; ++n) s[n] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float decay = exp2f(log2_decay(a.log_decay[kvh]));
     if (tid < D) s_k[tid] = __bfloat162float(a.rows.k[b * a.rows.k_stride + (long long)kvh * D + tid]);
+    const Decay decay(in_range(a.log_decay[kvh]), 1.f);
     const uint2 vv = *reinterpret_cast<const uint2*>(a.rows.v + b * a.rows.v_stride + (long long)kvh * D + col);
     const float v0 = bf16_lo(vv.x), v1 = bf16_hi(vv.x), v2 = bf16_lo(vv.y), v3 = bf16_hi(vv.y);
     __syncthreads();
+    const float x = decay.x;
+    if (decay.near) {  // (one loop that chooses in every term: 2048 states 42.1 us against 41.4)
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const float k = s_k[r + n * R];
-        s[n].x = fmaf(s[n].x, decay, k * v0);
-        s[n].y = fmaf(s[n].y, decay, k * v1);
-        s[n].z = fmaf(s[n].z, decay, k * v2);
-        s[n].w = fmaf(s[n].w, decay, k * v3);
-        *reinterpret_cast<float4*>(st + (size_t)(r + n * R) * D + col) = s[n];
+        for (int n = 0; n < N; ++n) {
+            const float k = s_k[r + n * R];
+            s[n].x = fmaf(k, v0, fmaf(s[n].x, x, s[n].x));
+            s[n].y = fmaf(k, v1, fmaf(s[n].y, x, s[n].y));
+            s[n].z = fmaf(k, v2, fmaf(s[n].z, x, s[n].z));
+            s[n].w = fmaf(k, v3, fmaf(s[n].w, x, s[n].w));
+            *reinterpret_cast<float4*>(st + (size_t)(r + n * R) * D + col) = s[n];
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const float k = s_k[r + n * R];
+            s[n].x = fmaf(s[n].x, x, k * v0);
+            s[n].y = fmaf(s[n].y, x, k * v1);
+            s[n].z = fmaf(s[n].z, x, k * v2);
+            s[n].w = fmaf(s[n].w, x, k * v3);
+            *reinterpret_cast<float4*>(st + (size_t)(r + n * R) * D + col) = s[n];
+        }
     }
     for (int h = 0; h < g; ++h) {
         if (tid < D)
@@ -123,18 +129,23 @@ __global__ void __launch_bounds__(D) linear_step_kernel(const LinearArgs a) {
     const int n = min(c1 - c0, p.max_len);
     if (n == 0) return;
     float* st = state_of(a, b, kvh, report);
-    const float decay = exp2f(log2_decay(a.log_decay[kvh]));
     float s[D];
 #pragma unroll
     for (int i = 0; i < D; ++i) s[i] = st && len > c1 - c0 ? st[(size_t)i * D + col] : 0.f;
+    const Decay decay(in_range(a.log_decay[kvh]), 1.f);  // (before the loads of S: 2048 states x 6 tokens 92.7 us, behind them 91.8)
     for (int t = 0; t < n; ++t) {
         const long long row = c0 + t;
         __syncthreads();
         s_k[col] = __bfloat162float(p.k[row * p.k_stride + (long long)kvh * D + col]);
         const float v = __bfloat162float(p.v[row * p.v_stride + (long long)kvh * D + col]);
         __syncthreads();
+        if (decay.near) {
 #pragma unroll
-        for (int i = 0; i < D; ++i) s[i] = fmaf(s[i], decay, s_k[i] * v);
+            for (int i = 0; i < D; ++i) s[i] = fmaf(s_k[i], v, fmaf(s[i], decay.x, s[i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < D; ++i) s[i] = fmaf(s[i], decay.x, s_k[i] * v);
+        }
         for (int h = kvh * g; h < (kvh + 1) * g; ++h) {
             __syncthreads();
             s_q[col] = __bfloat162float(p.q[row * p.q_stride + (long long)h * D + col]);

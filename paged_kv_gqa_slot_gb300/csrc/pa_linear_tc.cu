@@ -55,15 +55,13 @@ constexpr int kChunk = 128;
 constexpr int kThreads = 544;
 constexpr int kMmaWarp = 12, kLoadWarp = 13, kQLoadWarp = 14, kCleanWarp = 15, kItemWarp = 16;
 constexpr int kHalf = kChunk * 128;  // [128 rows][64 columns] bf16
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kMinLogDecay = -1e4f;
 
 // One item: what its roles need.  chunks < 0: there is none, the CTA is done; 0: padding, zero rows.
 struct Item {
     const float* begin;  // the state it begins with (null: zero)
     float* end;          // where its last state goes (null: nowhere)
     int row, len, chunks, kvh;
-    float la;            // log2 of the decay
+    float ld, la;        // the log decay, natural and to base 2
     int any_bad;         // a value of V was not finite
 };
 
@@ -133,11 +131,6 @@ __device__ __forceinline__ Rows rows_of(const LinearArgs& l, int b) {
     r.bad |= r.len > 0 && (c1 - c0 > p.max_len || r.slot >= l.num_slots);
     return r;
 }
-// log2 of a head's decay (a NaN is taken as the lower end)
-__device__ __forceinline__ float log2_decay(float log_decay) {
-    return fminf(fmaxf(log_decay, kMinLogDecay), 0.f) * kLog2e;
-}
-
 // d = (a0 * b0, a1 * b1), each rounded to nearest even
 __device__ __forceinline__ void mul_x2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
     asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
@@ -233,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (ok && n > 1) ok = __all_sync(0xffffffffu, mbar_wait(&bars->item_empty[n & 1], ((n >> 1) & 1) ^ 1));
                 if (ok) there = take_block(&bars->reply, &bars->next, phase, id, ok);
             }
-            Item it = {nullptr, nullptr, 0, 0, -1, 0, 0.f, 0};
+            Item it = {nullptr, nullptr, 0, 0, -1, 0, 0.f, 0.f, 0};
             while (ok && there) {
                 const int kvh = (int)(id % (unsigned)p.num_kv_heads), sb = (int)(id / (unsigned)p.num_kv_heads);
                 const int b = sb % p.batch, seg = sb / p.batch;
@@ -249,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     it.len = min(w.len - first * kChunk, chunks * kChunk);
                     it.chunks = pad ? 0 : chunks;
                     it.kvh = kvh;
-                    it.la = log2_decay(a.l.log_decay[kvh]);
+                    it.ld = in_range(a.l.log_decay[kvh]);
+                    it.la = it.ld * kLog2e;
                     if (!pad) {
                         float* state = a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * dd;
                         // (the first of several segments begins with a copy: the last may end before it starts)
@@ -468,20 +462,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         uint8_t* ss = smem + L::kOffS + r * 128;
         const bool keeps = warp < 8;
         int cc = 0, uc = 0;  // chunks; completed K~^T V that the state has waited for
-        // S <- f S + K~^T V, columns x .. x + 31, of the columns s_at and u_at of tensor memory
-        auto step = [&](uint32_t (&s)[32], int x, float f, uint32_t s_at = L::kColS, uint32_t u_at = L::kColU) {
-            uint32_t u[32];
+        // S (at s_at) and K~^T V (at u_at), columns x .. x + 31
+        auto both = [&](uint32_t (&s)[32], uint32_t (&u)[32], int x, uint32_t s_at, uint32_t u_at) {
             tmem_ld32_async(tm + s_at + x, s);
             tmem_ld32_async(tm + u_at + x, u);
             tmem_wait_ld(s);
             tmem_wait_ld(u);
+        };
+        auto sum = [&](uint32_t (&s)[32], int x, uint32_t s_at, uint32_t u_at) {  // S <- S + K~^T V
+            uint32_t u[32];
+            both(s, u, x, s_at, u_at);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), f, __uint_as_float(u[e])));
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(u[e]));
+        };
+        auto step = [&](uint32_t (&s)[32], int x, const Decay& f) {  // S <- f S + K~^T V
+            uint32_t u[32];
+            both(s, u, x, L::kColS, L::kColU);
+            if (f.near) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]), y0, y1;
+                    fma_x2(y0, y1, s0, s1, f.x, f.x, __uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+                    add_x2(s0, s1, y0, y1);
+                    s[e] = __float_as_uint(s0);
+                    s[e + 1] = __float_as_uint(s1);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), f.x, __uint_as_float(u[e])));
+            }
         };
         for (const Item* it; (it = items.next(ok)); items.done()) {
             const int chunks = it->chunks, len = it->len;
             const float la = it->la;
-            float f = 1.f;  // the decay over the chunk before
+            Decay f(it->ld, (float)kChunk);  // over the chunk before
             if (kGather && keeps) {
                 tc_fence_before();
                 mbar_arrive(&bars->st_full);
@@ -534,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                             take(s, x);
                         }
                     }
-                    f = fast_exp2((float)min(kChunk, len - c * kChunk) * la);
+                    if (len - c * kChunk < kChunk) f = Decay(it->ld, (float)(len - c * kChunk));  // the last
                     tmem_wait_st();
                     tc_fence_before();
                     fence_proxy_async_smem();
@@ -604,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     for (int x = 0; x < D; x += 32) {
                         uint32_t s[32];
                         if (c > 1)
-                            step(s, x, 1.f, L::kColSum, ((cc - 1) & 1) * L::kColHigh[1]);
+                            sum(s, x, L::kColSum, ((cc - 1) & 1) * L::kColHigh[1]);
                         else
                             tmem_ld32(tm + ((cc - 1) & 1) * L::kColHigh[1] + x, s);
                         tmem_st32_nowait(tm + L::kColSum + x, s);
@@ -626,13 +641,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 if (!kGather) {
                     step(s, x, f);
                 } else {
-                    step(s, x, 1.f, L::kColSmall, ((cc - 1) & 1) * L::kColHigh[1]);
+                    sum(s, x, L::kColSmall, ((cc - 1) & 1) * L::kColHigh[1]);
                     if (chunks > 1) {
-                        uint32_t sum[32];
-                        tmem_ld32(tm + L::kColSum + x, sum);
+                        uint32_t before[32];
+                        tmem_ld32(tm + L::kColSum + x, before);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(sum[e]));
+                            s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(before[e]));
                     }
                 }
                 if (mine) {
@@ -791,7 +806,8 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const TcArgs a) {
     const Rows w = rows_of(a.l, b);
     const int all = (w.len + kChunk - 1) / kChunk, n = (all + a.seg_chunks - 1) / a.seg_chunks - 1;
     if (n <= 0 || w.slot < 0 || w.slot >= a.l.num_slots) return;
-    const float f = fast_exp2((float)(a.seg_chunks * kChunk) * log2_decay(a.l.log_decay[kvh]));
+    const Decay f(in_range(a.l.log_decay[kvh]), (float)(a.seg_chunks * kChunk));
+    auto next = [&](float s, float x) { return fmaf(s, f.x, x) + (f.near ? s : 0.f); };
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!w.fresh) s = reinterpret_cast<const float4*>(a.l.state + ((size_t)w.slot * p.num_kv_heads + kvh) * D * D)[at];
     float4* seg = reinterpret_cast<float4*>(a.segments + ((size_t)b * a.segs * p.num_kv_heads + kvh) * D * D) + at;
@@ -807,10 +823,10 @@ __global__ void __launch_bounds__(256) linear_carry_kernel(const TcArgs a) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (i0 + i >= n) break;
-            s.x = fmaf(s.x, f, x[i].x);
-            s.y = fmaf(s.y, f, x[i].y);
-            s.z = fmaf(s.z, f, x[i].z);
-            s.w = fmaf(s.w, f, x[i].w);
+            s.x = next(s.x, x[i].x);
+            s.y = next(s.y, x[i].y);
+            s.z = next(s.z, x[i].z);
+            s.w = next(s.w, x[i].w);
             seg[(size_t)(i0 + i) * step] = s;
         }
     }

@@ -59,7 +59,6 @@ constexpr float kSumMost = 65536.f, kFirstSumLeast = 0x1p-40f;  // a stage's sum
 constexpr float kFirstLeast = -32.f;    // a first maximum below it becomes the base
 constexpr float kSplitScale = 2.f;      // |scale| sqrt(d) past this: P in two parts
 constexpr int kFewKeys = 128;           // a tile with a row of at most this many keys: the same
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kNoRow = INT_MAX;
 
 template <int D>

@@ -6,6 +6,34 @@
 
 namespace pa {
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A head's log decay as given, in its range (a NaN is taken as the lower end).
+__device__ __forceinline__ float in_range(float log_decay) { return fminf(fmaxf(log_decay, -1e4f), 0.f); }
+
+// A state's decay over n tokens, a^n = e^(n log_decay).  A state decays again and again, so the rounding of a factor near
+// one would add up (one token at a time with log decay -1e-5, after 4000 tokens: 1.5e-4 by a factor from exp2f, 2.7e-5
+// by one rounded to nearest).  There x = a^n - 1, to its own last bits, and S a^n is S + S x.
+struct Decay {
+    float x;
+    bool near;
+    __device__ __forceinline__ Decay(float log_decay, float n) {
+        const float t = log_decay * n;
+        near = t > -0.5f;
+        // e^t - 1 = t + t^2/2! + .. + t^9/9! + .., for t in (-1/2, 0] with what is left out below 2^-30 of it (without a
+        // branch, which would hold up the loads around it)
+        float p = 1.f / 362880.f;
+        p = fmaf(p, t, 1.f / 40320.f);
+        p = fmaf(p, t, 1.f / 5040.f);
+        p = fmaf(p, t, 1.f / 720.f);
+        p = fmaf(p, t, 1.f / 120.f);
+        p = fmaf(p, t, 1.f / 24.f);
+        p = fmaf(p, t, 1.f / 6.f);
+        p = fmaf(p, t, 0.5f);
+        x = near ? fmaf(p, t * t, t) : exp2f(t * kLog2e);
+    }
+};
+
 // 4-D tiled load of a tile of packed rows (strided_map): heads from `head`, rows from `row`, column halves from
 // `half`.
 __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, int head, int row, int half,

@@ -100,12 +100,12 @@ def off_by(state, k, v, log_decay):
 
 
 @gpu
-@pytest.mark.parametrize("decay", [0.0])
+@pytest.mark.parametrize("decay", [0.0, -1e-5, -1e-3])
 @pytest.mark.parametrize("n,heads,d", [(1 << 20, 1, 64), (20000, 75, 128), (20000, 200, 64), (9000, 32, 128)])
 def test_a_state_summed_over_many_chunks(n, heads, d, decay):
     """Segments of 128, 79, all (one segment) and 6 to 9 chunks.  Errors of one sign: the 8 sums of a chunk in the tensor core,
-    cut off to 2^-23 of what there is so far, half of the chunk's on average, 2^-21; the decays' 2^-22; below 2^-20.  Errors of
-    either sign: up to 192 sums in fp32, 2^-24 of what there is so far, 0.58 of it root mean square each, six times
+    cut off to 2^-23 of what there is so far, half of the chunk's on average, 2^-21; the decays' 2^-22, and of their exponents 3 * 2^-24 of what is 1.44 on average, less
+    than 2^-22; below 2^-20.  Errors of either sign: up to 192 sums in fp32, 2^-24 of what there is so far, 0.58 of it root mean square each, six times
     0.58 * 0.58 * 192^0.5 * 2^-24 < 2^-19: below 2^-18 with the others."""
     k, v = one_signed(n, heads, d, 71)
     q = torch.zeros(n, heads, d, device="cuda").bfloat16()
@@ -116,4 +116,27 @@ def test_a_state_summed_over_many_chunks(n, heads, d, decay):
     for h in {0, heads // 2, heads - 1}:
         off = off_by(state[0, h], k[:, h], v[:, h], log_decay[h])
         assert abs(float(off.mean())) <= 2.0 ** -20 and float(off.abs().max()) <= 2.0 ** -18, h
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("step", [1, 5])
+@pytest.mark.parametrize("decay", [0.0, -1e-5, -1e-3, -0.3, -0.6, -3.0])
+def test_a_state_carried_token_by_token(decay, step):
+    """2000 tokens by calls for one and for five.  Errors of one sign: a's, which over the tokens that count make
+    1 / (1 - a) of it: of a - 1, 2^-23 of that, 2^-23; from exp2f (a < 0.61) 2^-22 a / (1 - a) < 2^-21; below 2^-20.  Errors of
+    either sign: two roundings a token, 4000 at most that count, six times 0.58 * 0.58 * 4000^0.5 * 2^-24 < 2^-17."""
+    n, d = 2000, 64
+    k, v = one_signed(n, 1, d, 72)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    state, slot, cu = torch.full((1, 1, d, d), math.nan, device="cuda"), ints([0]), ints([0, step])
+    log_decay = torch.full((1,), decay, device="cuda")
+    for t in range(0, n, step):
+        rows, lens = slice(t, t + step), ints([t + step])
+        if step == 1:
+            pa.pa_linear_decode(state, slot, k[rows], k[rows], v[rows], log_decay, lens, 1.0)
+        else:
+            pa.pa_linear_prefill(state, slot, k[rows], k[rows], v[rows], log_decay, cu, lens, 1.0, step)
+    off = off_by(state[0, 0], k[:, 0], v[:, 0], log_decay[0])
+    assert abs(float(off.mean())) <= 2.0 ** -20 and float(off.abs().max()) <= 2.0 ** -17
     clean()
