@@ -21,9 +21,10 @@
 // first altogether was no faster: 7 prompts at d = 64 94 us against 92, 48 prompts 219 against 224).
 //
 // Base of the softmax: a stage is taken against the row's current base, 0 to begin with (P, O and the sums have
-// the range of fp32).  Only a stage whose sum passes 2^16, or a first one whose sum is below 2^-40, takes the
+// the range of fp32).  Only a stage whose sum passes 2^16, or a row's first one whose sum is below 2^-40, takes the
 // maximum (at d = 128 so does any stage with a masked key); where it is more than 2^8 above the base, or in a first
-// stage far below it, the base moves there and O is rescaled.  P is rounded to bf16 and the normaliser sums the
+// stage far below it, the base moves there and O is rescaled.  (A row's first stage is the first in which a key has any
+// weight: those before may hold scores of -inf alone.)  P is rounded to bf16 and the normaliser sums the
 // rounded values, so their rounding moves weight between keys but not its total.  Where few keys can dominate (a
 // tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
 //
@@ -244,7 +245,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 done = true;
             }
             // a sum past 2^16, or a first one below 2^-40: once more against a new base
-            if (done && __any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast)))) {
+            if (done && __any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (l == 0.f && sum < kFirstSumLeast)))) {
                 tmem_wait_st();  // the scores that P went over
                 tmem_st32_nowait(tm_s, s0);
                 tmem_st32_nowait(tm_s + 32, s1);
@@ -264,8 +265,8 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 mx *= fabsf(sl);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (there && fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (j == 0 && mx < kFirstLeast))) {
-                    f = fast_exp2(base - mx);
+                if (there && fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (l == 0.f && mx < kFirstLeast))) {
+                    f = l == 0.f ? 1.f : fast_exp2(base - mx);
                     base = mx;
                 }
                 // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
@@ -309,15 +310,15 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
             sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
                            : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
             // a sum past 2^16, or a first one below 2^-40: once more against a new base
-            if (__any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (j == 0 && sum < kFirstSumLeast)))) {
+            if (__any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (l == 0.f && sum < kFirstSumLeast)))) {
                 const float sgn = sl < 0.f ? -1.f : 1.f;
                 const float m0 = fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn));
                 const float m1 = fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn));
                 const float mx = fabsf(sl) * fmaxf(m0, m1);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (there && (j == 0 ? fabsf(mx) < INFINITY : mx > base + kRescaleThreshold && mx < INFINITY)) {
-                    f = fast_exp2(base - mx);
+                if (there && fabsf(mx) < INFINITY && (l == 0.f || mx > base + kRescaleThreshold)) {
+                    f = l == 0.f ? 1.f : fast_exp2(base - mx);
                     base = mx;
                 }
                 // S_t(j) was issued after P_t V (j-1) and is complete, so O may be changed
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_kernel(const __grid_consta
             ++ic;
             if (!ok) continue;
             tc_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = 1.f / l;  // (l = 0 where every score is -inf: 0 / 0, a NaN as the definition has it)
             const bool any_bad = it->any_bad != 0;
             __nv_bfloat16* dst = a.p.out + ((size_t)(it->row + first + qi) * a.p.num_heads + it->head0 + hh) * D;
             // Two neighbouring lanes store 64 bytes of one row together, then of the other's: half the lines a

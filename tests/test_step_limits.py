@@ -140,3 +140,41 @@ def test_a_state_carried_token_by_token(decay, step):
     off = off_by(state[0, 0], k[:, 0], v[:, 0], log_decay[0])
     assert abs(float(off.mean())) <= 2.0 ** -20 and float(off.abs().max()) <= 2.0 ** -17
     clean()
+
+
+# ----------------------------------------------------------------------------- infinite scores
+@gpu
+@pytest.mark.parametrize("heads,kvh,d", [(8, 2, 128), (3, 3, 128), (8, 2, 64), (10, 2, 64)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_infinite_scores_are_what_the_definition_makes_them(bad, heads, kvh, d):
+    """A key of score +inf makes its rows NaN, one of score -inf has no weight, and a row whose every score is -inf is NaN:
+    rows that see the value are compared like all others."""
+    lens = [200, 300, 97]
+    for at in (0, 1, 31, 127, 128, 140, 199, 200, 230, 499, 500, 540, 596):
+        q, k, v, cu = R.packed_rows(lens, heads, kvh, d, 81)
+        k[at, 0, 3] = bad
+        ref, size = R.packed(q, k, v, cu, 0.1)
+        check(pa.pa_prefill_packed(q, k, v, cu, 0.1, 300), ref, size, f"k {at}")
+        q, k, v, cu = R.packed_rows(lens, heads, kvh, d, 82)
+        q[at, 1, 0] = bad
+        ref, size = R.packed(q, k, v, cu, 0.1)
+        check(pa.pa_prefill_packed(q, k, v, cu, 0.1, 300), ref, size, f"q {at}")
+    clean()
+
+
+@gpu
+@pytest.mark.parametrize("heads,kvh,d", [(4, 2, 128), (1, 1, 128), (4, 2, 64), (3, 1, 64)])
+@pytest.mark.parametrize("none", [1, 127, 128, 129, 300])
+def test_keys_behind_scores_of_minus_infinity(none, heads, kvh, d):
+    """A sequence's first keys have scores of -inf: its first rows are NaN, and the others are those of the keys behind, however
+    low or high these are (first stages that hold no weight at all, too)."""
+    lens = [none + 290, 20]
+    for level in (0.0, -170.0, 60.0):
+        q, k, v, cu = R.packed_rows(lens, heads, kvh, d, 83, strided=False)
+        q[:] = 64.0 / d
+        k[:] = (level + torch.round(k.float())).bfloat16()
+        k[:none, :, 1] = -math.inf
+        ref, size = R.packed(q, k, v, cu, 1 / 64)
+        assert bool(torch.isnan(ref[:none]).all()) and not bool(torch.isnan(ref[none:]).any())
+        check(pa.pa_prefill_packed(q, k, v, cu, 1 / 64, lens[0]), ref, size, f"level {level}")
+    clean()
