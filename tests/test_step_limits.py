@@ -178,3 +178,21 @@ def test_keys_behind_scores_of_minus_infinity(none, heads, kvh, d):
         assert bool(torch.isnan(ref[:none]).all()) and not bool(torch.isnan(ref[none:]).any())
         check(pa.pa_prefill_packed(q, k, v, cu, 1 / 64, lens[0]), ref, size, f"level {level}")
     clean()
+
+
+@gpu
+@pytest.mark.parametrize("heads,kvh,d", [(4, 2, 128), (1, 1, 128), (4, 2, 64), (3, 1, 64)])
+@pytest.mark.parametrize("level", [6.1875, 5.0, 0.0, -9.5, -25.0, -100.0])
+def test_values_at_the_ends_of_the_range(level, heads, kvh, d):
+    """v of 2^111 and of 2^-100 under scores that are all alike (sums of 900 weights of up to 2^8 stay below 2^17 of them):
+    the results of v of 1, times that."""
+    n = 900
+    q, k, v, cu = R.packed_rows([n, 70], heads, kvh, d, 84, strided=False)
+    q[:] = 64.0 / d
+    k[:] = level
+    v[:] = v.abs() * 0.25 + 0.75
+    ref, size = R.packed(q, k, v, cu, 1 / 64)
+    for power in (111, -100):
+        out = pa.pa_prefill_packed(q, k, (v.double() * 2.0 ** power).bfloat16(), cu, 1 / 64, n)
+        check(out.double() * 2.0 ** -power, ref, size, f"2^{power}")
+    clean()
