@@ -22,9 +22,10 @@
 //
 // Base of the softmax: a stage is taken against the row's current base, 2^8 to begin with.  Only a stage whose sum passes
 // 2^8 of it, or a row's first one whose sum is below 2^-16 of it, takes the maximum (at d = 128 so does any stage with a
-// masked key); where that is above the base (2^8 above it where the sum did not pass), or in a first stage far below it,
-// the base moves there and O is rescaled.  So P stays below 2^8, as in the prefill over a pool, and sums of P V in fp32's
-// range for V up to 2^100 and down to 2^-100.  (A row's first stage is the first in which a key has any
+// masked key); where that is 2^(1/2) above the base (a sum that passes has one at least twice it), or in a first stage far
+// below it, the base moves there and O is rescaled.  (Kept until 2^8 above it in masked stages, for which the two need
+// telling apart: 48 prompts 236 us against 207.)  So P stays below 2^8, as in the prefill over a pool, and sums of P V in
+// fp32's range for V up to 2^100 and down to 2^-100.  (A row's first stage is the first in which a key has any
 // weight: those before may hold scores of -inf alone.)  P is rounded to bf16 and the normaliser sums the
 // rounded values, so their rounding moves weight between keys but not its total.  Where few keys can dominate (a
 // tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
@@ -57,7 +58,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10, kItemWarp = 11;
 constexpr int kThreads = 384;
 constexpr int kHalf = kRows * 128;      // [128 rows][64 columns] bf16
 constexpr float kBase = 8.f;            // the base to begin with
-constexpr float kRescaleThreshold = 8.f;
+constexpr float kRescaleThreshold = 0.5f;
 constexpr float kSumMost = 256.f, kFirstSumLeast = 0x1p-16f;  // a stage's sum outside takes the maximum
 constexpr float kFirstLeast = -8.f;     // a first maximum below it becomes the base
 constexpr float kSplitScale = 2.f;      // |scale| sqrt(d) past this: P in two parts
@@ -225,7 +226,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
         // the softmax bounds the kernel, and loads and P of a stage run on without a wait between them (as at d = 128:
         // 7 prompts 120 us against 92).
         if constexpr (D == 128) {
-            bool done = false, past = false;
+            bool done = false;
             if (!kSplit && unmasked) {
                 // quarter by quarter, each loaded while the one before is worked on
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
@@ -247,8 +248,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 done = true;
             }
             // a sum past 2^8, or a first one below 2^-16: once more against a new base
-            past = there && !(sum <= kSumMost);
-            if (done && __any_sync(0xffffffffu, past || (there && l == 0.f && sum < kFirstSumLeast))) {
+            if (done && __any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (l == 0.f && sum < kFirstSumLeast)))) {
                 tmem_wait_st();  // the scores that P went over
                 tmem_st32_nowait(tm_s, s0);
                 tmem_st32_nowait(tm_s + 32, s1);
@@ -268,8 +268,7 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
                 mx *= fabsf(sl);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (there && fabsf(mx) < INFINITY &&
-                    (mx > base + (past ? 0.f : kRescaleThreshold) || (l == 0.f && mx < kFirstLeast))) {
+                if (there && fabsf(mx) < INFINITY && (mx > base + kRescaleThreshold || (l == 0.f && mx < kFirstLeast))) {
                     f = l == 0.f ? 1.f : fast_exp2(base - mx);
                     base = mx;
                 }
@@ -314,15 +313,14 @@ __device__ __forceinline__ bool softmax_rows(Bars<D>* bars, int t, int sc, int n
             sum = unmasked ? stage_p<true, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s)
                            : stage_p<false, kSplit>(s0, s1, s2, s3, lim, sl, -base, tm_s);
             // a sum past 2^8, or a first one below 2^-16: once more against a new base
-            const bool past = there && !(sum <= kSumMost);
-            if (__any_sync(0xffffffffu, past || (there && l == 0.f && sum < kFirstSumLeast))) {
+            if (__any_sync(0xffffffffu, there && (!(sum <= kSumMost) || (l == 0.f && sum < kFirstSumLeast)))) {
                 const float sgn = sl < 0.f ? -1.f : 1.f;
                 const float m0 = fmaxf(quarter_max(s0, lim, sgn), quarter_max(s1, lim - 32, sgn));
                 const float m1 = fmaxf(quarter_max(s2, lim - 64, sgn), quarter_max(s3, lim - 96, sgn));
                 const float mx = fabsf(sl) * fmaxf(m0, m1);
                 // (a maximum that is no number leaves the base: the row's result is none either)
                 float f = 1.f;
-                if (there && fabsf(mx) < INFINITY && (l == 0.f || mx > base + (past ? 0.f : kRescaleThreshold))) {
+                if (there && fabsf(mx) < INFINITY && (l == 0.f || mx > base + kRescaleThreshold)) {
                     f = l == 0.f ? 1.f : fast_exp2(base - mx);
                     base = mx;
                 }
