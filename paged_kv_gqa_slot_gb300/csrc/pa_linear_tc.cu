@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         for (const Item* it; (it = items.next(ok)); items.done()) {
             const int chunks = it->chunks, len = it->len;
             const float la = it->la;
-            Decay f(it->ld, (float)kChunk);  // over the chunk before
+            Decay f(0.f, 0.f);  // over the chunk before
             if (kGather && keeps) {
                 tc_fence_before();
                 mbar_arrive(&bars->st_full);
@@ -549,11 +549,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                             take(s, x);
                         }
                     }
-                    if (len - c * kChunk < kChunk) f = Decay(it->ld, (float)(len - c * kChunk));  // the last
                     tmem_wait_st();
                     tc_fence_before();
                     fence_proxy_async_smem();
                     mbar_arrive(&bars->st_full);
+                    if (c == 0 || len - c * kChunk < kChunk) f = Decay(it->ld, (float)min(kChunk, len - c * kChunk));
                 }
                 const int n = min(kChunk, len - c * kChunk);
                 // weighted to the end of the chunk, or of the segment
