@@ -5,8 +5,8 @@
 //
 // Decode moves 8 d^2 bytes of state a (sequence, kv head) for about 5 d^2 flops: bound by HBM.  A CTA
 // holds one state (or a slice of its columns, when there are few) in registers: read once, updated,
-// written once, and every query head of the group is multiplied against the registers.  2048 states at
-// d = 128 from HBM take 36.4 us, 6.2 TB/s; 32 states 2.8 us inside a graph.
+// written once, and every query head of the group is multiplied against the registers.  2048 states from HBM take
+// 36.5 us at d = 128, 6.2 TB/s, 12.0 at d = 64, 5.7 TB/s; 32 states 3.1 and 2.1 us inside a graph.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -15,9 +15,14 @@
 namespace pa {
 namespace {
 
-// Chunks up to this long go token by token: with d = 128, 32 states x 6 tokens 8.6 us against 8.9 in one chunk of
-// pa_linear_tc.cu, 8 10.4 against 8.9; 152 states 8.8 against 9.5, 10.6 against 9.5; 2048 91 against 93, 108 against
-// 94; 512 states 20.6 against 27.7, 24.7 against 27.7.
+// Chunks up to this long go token by token, in fp32 throughout.  us of 6 and of 8 tokens against one chunk of
+// pa_linear_tc.cu, a query head a state and (in brackets) four, inputs in L2 where they fit:
+//   d = 128   32 states 8.6, 10.4 : 9.5 (16.8, 21.3 : 15.3)     512 20.4, 24.7 : 30.5 (38.4, 48.6 : 53.6)
+//             152 9.0, 10.7 : 10.0 (17.2, 21.8 : 15.9)          2048 89.8, 106 : 103 (157, 196 : 185)
+//   d = 64    32 states 5.9, 7.3 : 6.1 (11.8, 15.0 : 10.0)      512 8.8, 10.2 : 16.9 (15.6, 19.9 : 32.7)
+//             152 6.2, 7.5 : 6.7 (11.9, 15.4 : 10.8)            2048 16.7, 20.0 : 50.9 (30.2, 44.4 : 107)
+// Six is where the two cross for d = 128; groups of four with few states would change over at five, and at d = 64
+// many states at 12 to 16 tokens.
 constexpr int kFewTokens = 6;
 
 // What a sequence's state slot says: its state (null: padding, zero rows) and whether it begins at zero.
@@ -178,8 +183,11 @@ cudaError_t launch(K kernel, dim3 grid, int threads, const LinearArgs& a, cudaSt
 template <int D>
 cudaError_t decode(const LinearArgs& a, cudaStream_t stream) {
     const int kvh = a.rows.num_kv_heads;
-    // Columns are split over CTAs while the states alone leave SMs idle: 32 states 2.7 us against 3.4 whole, 128 3.9
-    // against 4.4; from one an SM on they are not: 152 3.9 split, 3.3 whole, 256 5.3 and 4.7 (in L2, d = 128).
+    // Columns are split over CTAs while the states alone leave SMs idle.  us split and whole, in L2, a query head a state and
+    // (in brackets) four:
+    //   d = 128   8 states 2.0, 2.9 (3.1, 4.2)   32 2.8, 3.3 (4.1, 4.6)   128 4.0, 4.4 (5.6, 5.8)   152 3.9, 3.2 (5.6, 4.5)
+    //   d = 64    8 states 1.8, 1.9 (3.0, 2.8)   32 2.0, 1.9 (3.3, 2.9)   128 2.9, 2.6 (4.9, 3.9)   152 2.2, 2.2 (3.7, 3.0)
+    // (at d = 64 a state is small enough for one CTA: whole costs no more there, and up to 1.2 us less)
     const long long states = (long long)kvh * a.rows.batch;
     if (states < device_info().num_sms)
         return launch(linear_decode_kernel<D, D / 4>, dim3(kvh * 4, a.rows.batch), 256, a, stream);

@@ -11,15 +11,18 @@
 //
 // Rounding.  P and S enter their products as bf16, one rounding of every term, as the outputs are bf16.  What is
 // added to S stays there, so K~ enters as three bf16 parts, all 24 bits of it; and since the tensor core cuts its
-// sums off instead of rounding them, K~^T V is summed from zero, the small parts first, and added to a^n S by the
-// threads in fp32.  The state is then within 2.5e-7 of 64 bits (two parts 2.4e-6; three, added to S by the tensor
-// core, 1.0e-6: 16 heads, chunks of up to 1100 tokens).
+// sums off instead of rounding them, K~^T V is summed from zero in every chunk, the small parts first, and added to
+// a^n S by the threads in fp32.  The state is then within 2.5e-7 of 64 bits (two parts 2.4e-6; three, added to S by the
+// tensor core, 1.0e-6: 24 sequences of up to 1100 tokens, 16 heads).  Where nothing decays and all terms have one sign it
+// is within 9.3e-7 after 2^20 tokens, 8192 sums of fp32 later, with a mean error of 1e-9.
 //
 // What bounds it.  A token moves (2 heads + 2 kv heads) d 2 bytes; per SM and 128 tokens of one head that is
 // 128 KB, about 5900 cycles of HBM time at d = 128, against 2800 of tensor core and 5000 of shared-memory
 // bandwidth (the operands of the products, the copies, K~ and S).  A chunk takes 6300: shared memory, and the
-// chain K~^T V, S, Q K^T, K~, which leaves the copies little slack.  152 states x 1024 tokens 36.6 us (4.9 TB/s,
-// 34.0 with two parts); 24 sequences of up to 1100 tokens, 16 heads, 77.6; 1 x 20000 tokens, 32 heads, 212.
+// chain K~^T V, S, Q K^T, K~, which leaves the copies little slack; and items run in the caller's order, so that the
+// longest may begin last (24 ragged: by a replay of the listed lengths about a quarter).  152 states x 1024 tokens
+// 38.0 us (4.7 TB/s); 24 sequences of up to 1100 tokens, 16 heads, 77.5; 1 x 20000 tokens, 32 heads, 213.  At d = 64 25,
+// 41 and 143.
 //
 // S stays in tensor memory in fp32 (lane: row of k, column: column of v).  Each chunk it is read once with the
 // sums of the chunk before, and written back there and to shared memory as bf16.  Q S is read back, weighted by
@@ -95,6 +98,18 @@ struct Layout {
 static_assert(Layout<128, false>::kSmem <= 227 * 1024, "shared memory");
 static_assert(sizeof(Item) <= 64, "item");
 
+// A barrier is waited for by the parity of its phase, so a phase may be over only once all who wait for the one before
+// have seen that.  Each has behind it, therefore, something that they do after their wait:
+//   k_full, v_full        the tile is loaded again after k_empty, v_empty: commits of the products that take K~ and V, issued
+//                         after kt_full (which all who wait for k_full or k_raw arrive on) and v_clean
+//   q_full, q_empty       one another: a copy, then the commit of the product that reads it
+//   s_full, qs_full, o_full  committed after p_full of the head before, or of this one, which those who wait arrive on
+//   p_full, o_empty       arrived on after s_full and o_full of the same head, committed by the warp that waits
+//   k_raw, piece          committed by the warp that has waited for kt_full, which those who wait for them arrive on
+//   kt_full, st_full      arrived on after k_raw, piece and u_full, committed by the warp that waits for these two
+//   u_full                committed after st_full of its chunk (gather: of its item)
+//   item_full, item_empty, soon, next  one another: two items, and a block is asked for after soon of the item before
+// So it is safe that the first piece of K~ is written while Q S runs and the second while P V runs.
 struct Bars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2], q_full, q_empty;
     uint64_t s_full, qs_full, p_full, o_full, o_empty;  // scores, Q S, P with Q S weighted, outputs ready; outputs read
@@ -564,10 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll 1
                 for (int piece = 0; piece < L::kPieces && ok; ++piece) {
                     if (kGather) {
-                        // Not while the products of the chunk before run: with K~ written beside them (and two tiles of
-                        // low parts) about one chunk in 10^5 never came to its end, both SMs of a pair at once, all of
-                        // its operands in place and its commits outstanding until the waits ran out; in turn it has not
-                        // been seen (5 10^6 calls), and was faster too.
+                        // Not before the products of the chunk before are done.  kt_full is waited for by parity, and K
+                        // has two tiles: without this wait both could be weighted, and two phases of kt_full be over,
+                        // while the issuing warp still waited for a V that came late; it then waited for a phase that its
+                        // own commits had to bring about.  (An earlier form, with room for the low parts of both tiles,
+                        // did so for about one chunk in 10^5, until the waits ran out.  In turn is faster, too.)
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[cc & 1], (cc >> 1) & 1));
                         if (ok && cc > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_raw, (cc - 1) & 1));
                     } else {  // (the first: it also means that the products of the chunk before are done)

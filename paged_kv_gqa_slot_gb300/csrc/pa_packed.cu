@@ -30,9 +30,10 @@
 // rounded values, so their rounding moves weight between keys but not its total.  Where few keys can dominate (a
 // tile with a row of at most 128 keys, or |scale| sqrt(d) > 2) P enters as two bf16 parts, in the two halves of S_t.
 //
-// Measured: 1 x 16384 tokens (32 / 8 heads of 128) 650 us, 1.69 PFLOP/s; 48 prompts of up to 1300 tokens 211 us; 7 of
-// up to 2200 (24 / 8 heads of 64) 82 us.  Long prompts are bound by the tensor core, d = 64 by the softmax, short
-// prompts by what an item costs besides its stages and by masked stages, which are nearly half of them.
+// Measured: 1 x 16384 tokens (16 / 2 heads of 128) 650 us, 1.69 PFLOP/s; 48 prompts of up to 1300 tokens (32 / 8 heads
+// of 128) 213 us; 7 of up to 2200 (24 / 8 heads of 64) 82 us.  Long prompts are bound by the tensor core, d = 64 by the
+// softmax, short prompts by what an item costs besides its stages and by masked stages, one of the 3.9 that an item of
+// the 48 has: they read their scores twice, and work through quarters that no row of the warp sees.
 // Also tried: two softmax threads a row (1 x 16384 969 us against 774 then), an issuing warp a tile (48 prompts 266
 // us against 260), both tiles half a stage apart (no gain).
 //
@@ -90,6 +91,10 @@ struct Item {
 };
 static_assert(sizeof(Item) <= 64, "item");
 
+// A barrier is waited for by the parity of its phase, so a phase may be over only once all who wait for the one before
+// have seen that: behind each lies something that they do after their wait (a tile is loaded again after the commits,
+// and the arrival of the warp that looks at V, that empty it; S_t, O_t and Q_t change hands in turn; an item's slot is
+// written again after every warp has given it back).
 template <int D>
 struct Bars {
     uint64_t q_full[2], q_empty[2], k_full[Layout<D>::kKSlots], k_empty[Layout<D>::kKSlots], v_full[Layout<D>::kVSlots],
