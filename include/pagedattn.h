@@ -323,8 +323,10 @@ int pa_prefill_chunked8(const pa_pool8 *pool, const void *q, const int32_t *cu_q
  *   out            [num_tokens, num_heads, head_dim] bf16, contiguous, 16-byte aligned; rows outside
  *                  every sequence stay as they are.  It overlaps none of the inputs
  * A sequence whose rows are not within [0, num_tokens] is skipped and sets PA_DEV_OUT_OF_RANGE.  A
- * NaN or an infinity in K or V concerns the rows that see its key alone, in V its column alone.
- * head_dim 64 or 128, any group size, batch <= 65535; arithmetic as pa_prefill_chunked.
+ * NaN or an infinity in K or V concerns the rows that see its key alone, in V its column alone; a
+ * score of +inf makes its row NaN, one of -inf gives its key no weight, and a row of nothing else is NaN.
+ * head_dim 64 or 128, any group size, batch <= 65535; arithmetic as pa_prefill_chunked (weights of up to
+ * 2^8, summed with v in fp32: |v| from 2^-100 to 2^100 keeps within its range).
  */
 int pa_prefill_packed(const void *q, const void *k, const void *v, const int32_t *cu_lens, int32_t batch,
                       int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -373,9 +375,10 @@ int pa_kv_free(const int32_t *ids, const int32_t *counts, int32_t rows, int32_t 
                int32_t capacity, const int32_t *num_free, int32_t *num_free_out, pa_stream_t stream);
 
 /*
- * pa_linear_decode, pa_linear_prefill -- linear attention with a decay for each head, as the layers
- * between the full-attention ones of a hybrid stack compute it ("Qwen3.5": 3 of every 4 layers, with a
- * per-request recurrent state).  With a = exp(log_decay[h]) of kv head h, over a sequence's tokens t,
+ * pa_linear_decode, pa_linear_prefill -- linear attention with a fixed decay for each head and a state for
+ * each request (the family of retention and lightning attention).  It is not the recurrence of the pages'
+ * hybrid stack ("Qwen3.5"), whose gated delta rule decays by a gate of every token and takes what the state
+ * holds for a key out of it before adding.  With a = exp(log_decay[h]) of kv head h, over a sequence's tokens t,
  *   S_t = a S_{t-1} + k_t v_t^T  (head_dim x head_dim),   o_t = scale q_t^T S_t,
  * query head i reading the state of kv head i / (num_heads / num_kv_heads).  The state lives in
  *   state          [num_slots, num_kv_heads, head_dim (of k), head_dim (of v)] fp32, 16-byte aligned,
@@ -392,10 +395,12 @@ int pa_kv_free(const int32_t *ids, const int32_t *counts, int32_t rows, int32_t 
  * pa_linear_prefill: rows cu_q_lens[b] .. cu_q_lens[b+1] are its newest tokens, any number; none leaves the
  * state as it is.  Rows outside every sequence stay as they are; rows past max_chunk, a sequence with
  * fewer tokens than rows and one whose rows are not within [0, num_tokens] as in pa_prefill_packed.
- * Both keep S in fp32 throughout; the prefill's products take q, k and v as they are, the scores and S
- * (where q reads it) as bf16, and k's weighted rows (where S gathers them) in full, as three bf16
- * parts.  A NaN or an infinity in a row of v concerns its column from that row on, which may turn NaN
- * as a whole.
+ * Both keep S in fp32 throughout.  A call with max_chunk up to 6 goes token by token and computes in fp32 alone,
+ * as pa_linear_decode; a longer one takes 128 tokens at a time, in products of q, k and v as they are, the scores
+ * and S (where q reads it) as bf16, and k's weighted rows (where S gathers them) in full, as three bf16
+ * parts.  So a sequence's outputs may differ in their last bits with the max_chunk of its batch; its state is
+ * right to 32 bits either way.  A NaN or an infinity in a row of v concerns its column from that row on, in one of k its
+ * row of the state and the outputs from there on; either may turn NaN as a whole.
  *   workspace      pa_linear_workspace_bytes(...) bytes, 16-byte aligned (may be NULL where that is 0),
  *                  not shared by calls that may run at the same time; nothing in it outlives the call
  * head_dim 64 or 128, any group size, batch <= 65535.

@@ -11,10 +11,10 @@ pa_decode8, pa_prefill_chunked8; pa_decode_weights / pa_decode8_weights and pa_k
 eviction by accumulated attention weight.  Tensors must be CUDA,
 contiguous, and of the dtypes the header states (bf16 data, int32 tables,
 int64 slot mapping, fp32 split-KV workspace).  Calls are asynchronous on the
-given stream (default: torch's current stream).  For a hybrid stack's step: pa_prefill_packed
+given stream (default: torch's current stream).  For a step of full and linear attention: pa_prefill_packed
 (cold prompts, rows strided as a fused projection leaves them), pa_kv_grow and pa_kv_free (tables,
 lengths and slots built on the GPU from a free list) and pa_linear_decode / pa_linear_prefill
-(linear attention with a decay for each head).
+(linear attention with a fixed decay for each head).
 """
 from __future__ import annotations
 
@@ -557,7 +557,7 @@ def pa_kv_evict(block_tables: torch.Tensor, seq_lens: torch.Tensor, weights: tor
     return new_tables, new_lens, new_weights, evicted, num
 
 
-# ----------------------------------------------------------------------------- a hybrid stack's step
+# ----------------------------------------------------------------------------- a step of full and linear attention
 def _strided(t: torch.Tensor, heads: int, dim: int, name: str, device: int) -> Tuple[int, int]:
     """Address and row stride of bf16 rows [heads, dim] on the call's device: each row contiguous, the
     rows any multiple of 8 elements apart (a view of a fused projection)."""
