@@ -585,6 +585,11 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _most(n) -> int:
+    """An upper bound as int32: larger ones mean the same as the largest (and negative ones are refused as such)."""
+    return max(-1, min(int(n), 0x7fffffff))
+
+
 def _packed(q, k, v, out, stream):
     """Check the rows of a packed call; (device, rows, heads, kv heads, dim, addresses, strides, out)."""
     shape, kshape = q.shape, k.shape
@@ -610,7 +615,7 @@ def pa_prefill_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_lens
     k and v [rows, num_kv_heads, head_dim] are sequence b.  Rows may be strided views."""
     d, rows, heads, kvh, dim, p, s, out = _packed(q, k, v, out, stream)
     _call("pa_prefill_packed", d, stream, *p, _arg(cu_lens, _I32, "cu_lens", d), cu_lens.numel() - 1, rows, heads, kvh,
-          dim, *s, int(max_len), float(scale), _arg(out, _BF16, "out", d))
+          dim, *s, _most(max_len), float(scale), _arg(out, _BF16, "out", d))
     return out
 
 
@@ -681,7 +686,7 @@ def pa_linear_decode(state: torch.Tensor, state_slots: torch.Tensor, q: torch.Te
 
 
 def pa_linear_workspace_bytes(batch: int, num_kv_heads: int, head_dim: int, max_chunk: int) -> int:
-    return int(library().pa_linear_workspace_bytes(batch, num_kv_heads, head_dim, max_chunk))
+    return int(library().pa_linear_workspace_bytes(batch, num_kv_heads, head_dim, _most(max_chunk)))
 
 
 def pa_linear_prefill(state: torch.Tensor, state_slots: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -703,7 +708,7 @@ def pa_linear_prefill(state: torch.Tensor, state_slots: torch.Tensor, q: torch.T
     elif workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace: need {need} bytes, got {workspace.numel() * workspace.element_size()}")
     _call("pa_linear_prefill", d, stream, st, state.shape[0], slots, *p, decay, _arg(cu_q_lens, _I32, "cu_q_lens", d),
-          lens, B, rows, heads, kvh, dim, *s, int(max_chunk), float(scale),
+          lens, B, rows, heads, kvh, dim, *s, _most(max_chunk), float(scale),
           _arg(workspace, workspace.dtype, "workspace", d) or None, _arg(out, _BF16, "out", d))
     return out
 

@@ -9,6 +9,7 @@ import torch
 import paged_kv_gqa_slot_gb300 as pa
 import step_ref as R
 from paged_kv_gqa_slot_gb300 import build as pbuild
+from test_linear import Case
 from test_packed import check, clean
 
 gpu = pytest.mark.gpu
@@ -196,3 +197,21 @@ def test_values_at_the_ends_of_the_range(level, heads, kvh, d):
         out = pa.pa_prefill_packed(q, k, (v.double() * 2.0 ** power).bfloat16(), cu, 1 / 64, n)
         check(out.double() * 2.0 ** -power, ref, size, f"2^{power}")
     clean()
+
+
+# ----------------------------------------------------------------------------- bounds that int32 does not hold
+@gpu
+@pytest.mark.parametrize("most", [1 << 31, 1 << 32, (1 << 32) + 5, (1 << 63) - 1])
+def test_bounds_past_int32_are_upper_bounds_like_others(most):
+    lens = [300, 0, 41]
+    q, k, v, cu = R.packed_rows(lens, 4, 2, 64, 85)
+    ref, size = R.packed(q, k, v, cu, 0.1)
+    check(pa.pa_prefill_packed(q, k, v, cu, 0.1, most), ref, size)
+    assert pa.pa_linear_workspace_bytes(1, 2, 64, most) == pa.pa_linear_workspace_bytes(1, 2, 64, 2 ** 31 - 1) > 0
+    c = Case(86, lens, 4, 2, 64, fresh=(2,))
+    c.check(lambda: c.prefill(most=most))
+    for refused in (-1, -(1 << 32)):
+        with pytest.raises(pa.PagedAttnError):
+            pa.pa_prefill_packed(q, k, v, cu, 0.1, refused)
+        with pytest.raises(pa.PagedAttnError):
+            c.prefill(most=refused)
